@@ -141,8 +141,8 @@ using namespace moe;
 
 namespace {
 
-constexpr int kKinds = 8;
-enum Kind { K_ROUTER = 0, K_FFN = 1, K_COMBINE = 2, K_GEMM_GU = 3, K_GEMM_DN = 4, K_GATHER = 5, K_FFN_MISS = 6 };
+constexpr int kKinds = 10;
+enum Kind { K_ROUTER = 0, K_FFN = 1, K_COMBINE = 2, K_GEMM_GU = 3, K_GEMM_DN = 4, K_GATHER = 5, K_FFN_MISS = 6 };  // and KvKind
 constexpr double kHostWaitLimitS = 10.0;  // longest the host waits for the routing of one call
 // Rounds of ready-word source values kept in pinned memory. A round's entry is
 // rewritten kEpochRing calls later, long after its copies ran: every call
@@ -211,6 +211,8 @@ struct moe_ctx {
     unsigned* err_host = nullptr;   // mapped pinned word that kernels report expired waits into
     unsigned* err_dev = nullptr;
     uint32_t err_generation = 0;  // bumped whenever a kernel reported an expired wait
+    KvState* kv = nullptr;        // the cache calls' workspace and error word, made by the first of them
+    std::mutex kv_mu;
     long fail_copy_at = -1;  // test hook: the n-th miss copy from now reports failure
     long copies_issued = 0;
     // timeline diagnostics (see TraceLaunch)
@@ -479,6 +481,20 @@ struct Prof {
         C->prof.push_back(r);
     }
 };
+
+}  // namespace
+
+void* moe::ctx_launch_begin(moe_ctx* C, int kind, double bytes, double flops, cudaStream_t s) {
+    return new (std::nothrow) Prof(C, s, kind, bytes, flops);
+}
+void moe::ctx_launch_end(void* rec) { delete static_cast<Prof*>(rec); }
+bool moe::ctx_profiling(const moe_ctx* C) { return C->profiling; }
+void moe::ctx_count_launch(moe_ctx* C) { ++C->launches; }
+int moe::ctx_device(const moe_ctx* C) { return C->device; }
+KvState*& moe::ctx_kv(moe_ctx* C) { return C->kv; }
+std::mutex& moe::ctx_kv_mutex(moe_ctx* C) { return C->kv_mu; }
+
+namespace {
 
 void drain_prof(moe_ctx* C) {
     for (ProfRec& r : C->prof) {
@@ -1437,6 +1453,7 @@ extern "C" void moe_ctx_destroy(moe_ctx* C) {
         cudaFree(C->trace_spans);
     }
     for (cudaEvent_t e : C->timing_pool) cudaEventDestroy(e);
+    kv_state_destroy(C->kv);
     cudaFree(C->staging);
     cudaFreeHost(C->err_host);
     cudaEventDestroy(C->staging_free);

@@ -1,0 +1,233 @@
+// libmoe C ABI: the 4-bit key/value cache and the attention over it.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <new>
+
+#include "kv_internal.h"
+
+using namespace moe;
+
+#define CUDA_TRY(call)                                                                                 \
+    do {                                                                                               \
+        cudaError_t e_ = (call);                                                                       \
+        if (e_ != cudaSuccess)                                                                         \
+            return set_error(MOE_ECUDA, "%s failed: %s (%s:%d)", #call, cudaGetErrorString(e_), __FILE__, \
+                             __LINE__);                                                                \
+    } while (0)
+
+namespace moe {
+
+// What the cache calls of a context keep: a mapped word that kernels note bad
+// slots and page ids in.
+struct KvState {
+    unsigned* bad_host = nullptr;
+    unsigned* bad_dev = nullptr;
+};
+
+void kv_state_destroy(KvState* st) {
+    if (!st) return;
+    cudaFreeHost(st->bad_host);
+    delete st;
+}
+
+}  // namespace moe
+
+namespace {
+
+bool shape_ok(const moe_kv_cache* c) {
+    return c && c->n_kv_heads >= 1 && c->n_kv_heads <= 65536 &&
+           (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256) && c->page_tokens >= 16 &&
+           c->page_tokens <= 256 && !(c->page_tokens & (c->page_tokens - 1)) && c->n_pages >= 1 &&
+           (int64_t)c->n_pages * c->page_tokens < (int64_t)1 << 31;
+}
+
+moe_status check_cache(const char* who, const moe_kv_cache* c) {
+    if (!shape_ok(c))
+        return set_error(MOE_EINVAL, "%s: bad cache (n_kv_heads >= 1, head_dim 64, 128 or 256, page_tokens 16 to 256 "
+                         "and a power of two, n_pages >= 1, n_pages * page_tokens < 2^31)", who);
+    if (!c->pages || (reinterpret_cast<uintptr_t>(c->pages) & 15))
+        return set_error(MOE_EINVAL, "%s: pages must be a 16-byte aligned device pointer", who);
+    return MOE_OK;
+}
+
+KvCache view(const moe_kv_cache* c) {
+    KvCache v;
+    v.pages = static_cast<uint8_t*>(c->pages);
+    v.H = c->n_kv_heads;
+    v.P = c->page_tokens;
+    v.page_shift = 0;
+    while ((1 << v.page_shift) < v.P) ++v.page_shift;
+    v.n_pages = c->n_pages;
+    v.n_slots = (unsigned)c->n_pages * (unsigned)c->page_tokens;
+    return v;
+}
+
+int type_size(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
+
+bool rows_ok(const void* p, int64_t ts, int64_t hs, moe_dtype t) {
+    const int64_t per = 16 / type_size(t);
+    return !(reinterpret_cast<uintptr_t>(p) & 15) && ts % per == 0 && hs % per == 0;
+}
+
+// The context's cache state, made by its first cache call. Held under the context's mutex.
+moe_status state_of(moe_ctx* C, KvState** out) {
+    KvState*& st = ctx_kv(C);
+    if (!st) {
+        KvState* n = new (std::nothrow) KvState();
+        if (!n) return set_error(MOE_ENOMEM, "out of host memory");
+        if (cudaHostAlloc(&n->bad_host, sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
+            cudaHostGetDevicePointer(&n->bad_dev, n->bad_host, 0) != cudaSuccess) {
+            cudaGetLastError();
+            kv_state_destroy(n);
+            return set_error(MOE_ENOMEM, "cache state allocation failed");
+        }
+        *n->bad_host = 0;
+        st = n;
+    }
+    *out = st;
+    return MOE_OK;
+}
+
+// Counts a launch; with profiling on, times it.
+struct Launch {
+    void* rec = nullptr;
+    Launch(moe_ctx* C, int kind, double bytes, double flops, cudaStream_t s) {
+        if (ctx_profiling(C))
+            rec = ctx_launch_begin(C, kind, bytes, flops, s);
+        else
+            ctx_count_launch(C);
+    }
+    ~Launch() {
+        if (rec) ctx_launch_end(rec);
+    }
+};
+
+moe_status rows_call(const char* who, moe_ctx* C, const moe_kv_cache* cache, const void* k, int64_t kt, int64_t kh,
+                     const void* v, int64_t vt, int64_t vh, moe_dtype dtype, const int32_t* slots, int32_t n_tokens,
+                     bool append, void* stream) {
+    if (!C) return set_error(MOE_EINVAL, "%s: ctx is NULL", who);
+    moe_status st = check_cache(who, cache);
+    if (st != MOE_OK) return st;
+    if (dtype != MOE_F32 && dtype != MOE_F16 && dtype != MOE_BF16)
+        return set_error(MOE_EINVAL, "%s: dtype %d (MOE_F32, MOE_F16 or MOE_BF16)", who, (int)dtype);
+    if (n_tokens < 0) return set_error(MOE_EINVAL, "%s: n_tokens = %d", who, n_tokens);
+    if ((int64_t)n_tokens * cache->n_kv_heads >= (int64_t)1 << 31)
+        return set_error(MOE_EINVAL, "%s: n_tokens * n_kv_heads must be below 2^31", who);
+    if (n_tokens == 0) return MOE_OK;
+    if (!k || !v || !slots) return set_error(MOE_EINVAL, "%s: NULL argument", who);
+    if (!rows_ok(k, kt, kh, dtype) || !rows_ok(v, vt, vh, dtype))
+        return set_error(MOE_EINVAL, "%s: rows of k and v must start on 16-byte boundaries", who);
+    CUDA_TRY(cudaSetDevice(ctx_device(C)));
+    std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
+    KvState* S;
+    if ((st = state_of(C, &S)) != MOE_OK) return st;
+    KvRows a{};
+    a.c = view(cache);
+    a.slots = slots;
+    a.n = (unsigned)n_tokens * (unsigned)cache->n_kv_heads;
+    a.by_head = FastDiv((uint32_t)cache->n_kv_heads);
+    if (append) {
+        a.k_in = k;
+        a.v_in = v;
+    } else {
+        a.k_out = const_cast<void*>(k);
+        a.v_out = const_cast<void*>(v);
+    }
+    a.kt = kt, a.kh = kh, a.vt = vt, a.vh = vh;
+    a.bad = S->bad_dev;
+    const int d = cache->head_dim;
+    const double bytes = (double)a.n * 2 * d * (type_size(dtype) + 0.5625) + 4.0 * n_tokens;
+    cudaStream_t s = (cudaStream_t)stream;
+    Launch l(C, append ? K_KV_APPEND : K_KV_READ, bytes, 0, s);
+    CUDA_TRY(append ? launch_kv_append(a, d, dtype, s) : launch_kv_read(a, d, dtype, s));
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" size_t moe_kv_cache_bytes(const moe_kv_cache* c) {
+    if (!shape_ok(c)) return 0;
+    return (size_t)c->n_pages * c->n_kv_heads * (c->page_tokens / kKvBlock) * kv_record_bytes(c->head_dim);
+}
+
+extern "C" moe_status moe_kv_append(moe_ctx* C, const moe_kv_cache* cache, const void* k, int64_t kt, int64_t kh,
+                                    const void* v, int64_t vt, int64_t vh, moe_dtype dtype, const int32_t* slots,
+                                    int32_t n_tokens, void* stream) {
+    return rows_call("moe_kv_append", C, cache, k, kt, kh, v, vt, vh, dtype, slots, n_tokens, true, stream);
+}
+
+extern "C" moe_status moe_kv_read(moe_ctx* C, const moe_kv_cache* cache, const int32_t* slots, int32_t n_tokens,
+                                  void* k, int64_t kt, int64_t kh, void* v, int64_t vt, int64_t vh, moe_dtype dtype,
+                                  void* stream) {
+    return rows_call("moe_kv_read", C, cache, k, kt, kh, v, vt, vh, dtype, slots, n_tokens, false, stream);
+}
+
+extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const moe_kv_attend_args* p,
+                                    void* stream) {
+    const char* who = "moe_kv_attend";
+    if (!C || !p) return set_error(MOE_EINVAL, "%s: NULL argument", who);
+    moe_status st = check_cache(who, cache);
+    if (st != MOE_OK) return st;
+    if (p->dtype != MOE_F16 && p->dtype != MOE_BF16)
+        return set_error(MOE_EINVAL, "%s: dtype %d (MOE_F16 or MOE_BF16)", who, (int)p->dtype);
+    if (p->batch < 0 || p->n_q < 0 || p->max_pages < 0 || p->max_q < 0 || p->max_len < 0 || p->window < 0 ||
+        (p->causal != 0 && p->causal != 1) || !isfinite(p->scale))
+        return set_error(MOE_EINVAL, "%s: batch, n_q, max_pages, max_q, max_len and window must not be negative, causal "
+                         "0 or 1 and scale finite", who);
+    if (p->n_heads < 1 || p->n_heads % cache->n_kv_heads)
+        return set_error(MOE_EINVAL, "%s: n_heads = %d must be a multiple of n_kv_heads = %d", who, p->n_heads,
+                         cache->n_kv_heads);
+    if ((int64_t)p->max_pages * cache->page_tokens >= (int64_t)1 << 31 ||
+        (int64_t)p->n_q * p->n_heads >= (int64_t)1 << 31)
+        return set_error(MOE_EINVAL, "%s: max_pages * page_tokens and n_q * n_heads must be below 2^31", who);
+    if (p->n_q == 0) return MOE_OK;
+    if (p->batch == 0) return set_error(MOE_EINVAL, "%s: n_q = %d rows of no sequence", who, p->n_q);
+    if (!p->q_start && p->n_q % p->batch)
+        return set_error(MOE_EINVAL, "%s: without q_start, n_q = %d must be a multiple of batch = %d", who, p->n_q,
+                         p->batch);
+    if (!p->q || !p->out || !p->kv_len || (p->max_pages && !p->page_table))
+        return set_error(MOE_EINVAL, "%s: NULL argument", who);
+    if (!rows_ok(p->q, p->q_token_stride, p->q_head_stride, p->dtype) ||
+        !rows_ok(p->out, p->out_token_stride, p->out_head_stride, p->dtype))
+        return set_error(MOE_EINVAL, "%s: rows of q and out must start on 16-byte boundaries", who);
+    CUDA_TRY(cudaSetDevice(ctx_device(C)));
+    std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
+    KvState* S;
+    if ((st = state_of(C, &S)) != MOE_OK) return st;
+    KvAttend a{};
+    a.c = view(cache);
+    a.q = p->q;
+    a.out = p->out;
+    a.lse = p->lse;
+    a.qt = p->q_token_stride, a.qh = p->q_head_stride, a.ot = p->out_token_stride, a.oh = p->out_head_stride;
+    a.table = p->page_table;
+    a.table_stride = p->page_table_stride;
+    a.kv_len = p->kv_len;
+    a.q_start = p->q_start;
+    a.B = p->batch, a.n_q = p->n_q, a.Hq = p->n_heads, a.G = p->n_heads / cache->n_kv_heads, a.max_pages = p->max_pages;
+    a.T = p->q_start ? 0 : p->n_q / p->batch;
+    a.causal = p->causal;
+    // a window no shorter than any sequence hides nothing
+    a.window = (int64_t)p->window >= (int64_t)p->max_pages * cache->page_tokens ? 0 : p->window;
+    a.scale_log2 = p->scale * 1.4426950408889634f;
+    a.bad = S->bad_dev;
+    const int d = cache->head_dim;
+    cudaStream_t s = (cudaStream_t)stream;
+    const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
+    Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
+             4.0 * p->n_q * len * p->n_heads * d, s);
+    CUDA_TRY(launch_kv_attend(a, d, p->dtype, s));
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_kv_check(moe_ctx* C) {
+    if (!C) return set_error(MOE_EINVAL, "moe_kv_check: ctx is NULL");
+    std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
+    KvState* S = ctx_kv(C);
+    if (S && *(volatile unsigned*)S->bad_host) {
+        *(volatile unsigned*)S->bad_host = 0;
+        return set_error(MOE_EINVAL, "an earlier cache call met a slot or page id outside its cache");
+    }
+    return MOE_OK;
+}

@@ -10,6 +10,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <vector>
 
 #include "../../include/moe.h"
@@ -345,5 +346,21 @@ size_t pf_part_floats(int d, int inter0);
 // launch when tiles are split; *launched (if given) gets the launch count.
 cudaError_t launch_pf_gemm(const PfArgs& a, int phase, const void* b0, const void* b1, const int rows[2],
                            cudaStream_t s, int* launched = nullptr);
+
+// ---- what the cache calls (kv_api.cu) use of a context --------------------------
+
+enum KvKind { K_KV_APPEND = 7, K_KV_READ = 8, K_KV_ATTEND = 9 };  // kernel kinds, after those of api.cu
+
+struct KvState;  // kv_api.cu
+void kv_state_destroy(KvState* st);
+
+int ctx_device(const moe_ctx* C);
+KvState*& ctx_kv(moe_ctx* C);
+std::mutex& ctx_kv_mutex(moe_ctx* C);  // held by a cache call while it enqueues
+bool ctx_profiling(const moe_ctx* C);
+void ctx_count_launch(moe_ctx* C);
+// With profiling on: counts a launch and records its start (end) on s.
+void* ctx_launch_begin(moe_ctx* C, int kind, double bytes, double flops, cudaStream_t s);
+void ctx_launch_end(void* rec);
 
 }  // namespace moe

@@ -476,6 +476,117 @@ moe_status moe_layer_create_streamed(moe_ctx* ctx, const moe_shapes* shapes, con
  * Errors: MOE_EINVAL (NULL layer, n < 0), MOE_ESTATE (not a streamed layer). */
 moe_status moe_layer_prefetch(moe_layer* layer, int32_t n, int32_t* queued);
 
+/* ---- key/value cache in 4 bits, and attention over it ---------------------- */
+
+/* The attention that runs beside the MoE layer in a decoder layer ([P1] §2.5:
+ * split-K/V decode attention, sliding-window and full layers), over a cache of
+ * keys and values held as the experts' weights are: 4-bit affine in groups of
+ * 64, here along head_dim, 4.5 bits an element in all.
+ *
+ * The cache is a buffer of pages that the caller owns. A page holds
+ * page_tokens tokens of every kv head, as [kv head][block of 16 tokens][record].
+ * A record (18 * head_dim bytes) holds, for its 16 tokens in order:
+ *   K codes: head_dim/2 bytes per token;  V codes: likewise;
+ *   K affine: head_dim/64 words per token, fp16 scale | fp16 bias << 16;
+ *   V affine: likewise.
+ * With NG = head_dim/64 groups, 32-bit word i * NG + j of a token's codes holds
+ * elements 8i .. 8i+7 of group j, nibble n (bits 4n..4n+3) element
+ * {0, 2, 4, 6, 1, 3, 5, 7}[n] of them. An element's value is scale * code + bias.
+ * Token t of a sequence lies in page page_table[t / page_tokens], at place
+ * t % page_tokens. New pages need no initialisation: places past a sequence's
+ * length are never used, whatever bytes they hold. Several caches (one per
+ * layer, say) are several buffers; the calls keep no state of a cache. */
+typedef struct {
+    int32_t n_kv_heads;  /* >= 1 */
+    int32_t head_dim;    /* 64, 128 or 256 */
+    int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+    int32_t n_pages;     /* >= 1; n_pages * page_tokens < 2^31 */
+    void* pages;         /* device, moe_kv_cache_bytes() bytes, 16-byte aligned */
+} moe_kv_cache;
+
+typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 } moe_dtype;
+
+/* Bytes of a cache's pages: n_pages * page_tokens * n_kv_heads * head_dim *
+ * 9/8. 0 if the shape is not a valid one (pages is not looked at). */
+size_t moe_kv_cache_bytes(const moe_kv_cache* cache);
+
+/* Quantise n_tokens rows of keys and values into the cache. Row t, kv head h
+ * starts at k + t * k_token_stride + h * k_head_stride (in elements; any
+ * stride, zero and negative ones among them, whose rows start on 16-byte
+ * boundaries), head_dim contiguous elements of `dtype`; v likewise. Token t
+ * goes to slot slots[t] = page * page_tokens + place; a negative slot skips
+ * the token. Slots of one call are distinct: two rows for one slot leave a
+ * mixture of both there.
+ * Per group of 64 elements, in fp32 (x clamped to +-65504, what fp16 scales
+ * can span):  bias = min(x) rounded down to fp16;  scale = (max(x) - bias) / 15
+ * rounded up to fp16;  code = (x - bias) / scale rounded to the nearest
+ * integer, ties to even (0 where scale is 0). So 0 <= code <= 15 without
+ * clamping, and |value - x| <= scale / 2. A NaN makes its group's 64 values NaN.
+ * k, v, slots: device. Asynchronous on `stream`; no synchronisation, no
+ * allocation. A slot past the cache's end is skipped and noted (moe_kv_check).
+ * Errors: MOE_EINVAL (NULL, shape, type, alignment, n_tokens < 0), MOE_ECUDA. */
+moe_status moe_kv_append(moe_ctx* ctx, const moe_kv_cache* cache, const void* k, int64_t k_token_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                         moe_dtype dtype, const int32_t* slots, int32_t n_tokens, void* stream);
+
+/* Read n_tokens rows back: the values scale * code + bias (one fp32 fused
+ * multiply-add, rounded once to `dtype`), laid out as for moe_kv_append. A
+ * token whose slot is negative reads as zeros, one whose slot lies past the
+ * cache's end too, and is noted. Errors: as moe_kv_append. */
+moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const int32_t* slots, int32_t n_tokens, void* k,
+                       int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
+                       int64_t v_head_stride, moe_dtype dtype, void* stream);
+
+/* Attention of new tokens over the cache. Sequence b has n_b new tokens, rows
+ * q_start[b] .. q_start[b+1] of q (ascending from 0; NULL: n_q / batch rows each), the last of
+ * the kv_len[b] tokens that the cache holds of it (append them first): new
+ * token i sits at position p = kv_len[b] - n_b + i and sees the keys j with
+ * 0 <= j < kv_len[b], j <= p if causal, and j > p - window if window > 0.
+ * Query head h reads kv head h / (n_heads / n_kv_heads).
+ *   out[i][h] = sum_j w_j V_j,  w = softmax over the seen j of scale * q_ih . K_j
+ *   lse[i][h] = ln sum_j exp(scale * q_ih . K_j)
+ * A token that sees nothing (an empty sequence, a position below 0) gets
+ * out = 0, lse = -inf. Softmax statistics and sums are fp32. Keys, values and
+ * probabilities enter the tensor cores in fp16 or exact integer codes, queries
+ * as fp16 scaled by a power of two per row (exact for all but elements under
+ * 2^-14 of the row's largest). Repeating a call on the same data gives the same bits. */
+typedef struct {
+    const void* q; /* device, [n_q][n_heads][head_dim] of dtype (MOE_F16 or MOE_BF16), head_dim contiguous,
+                      rows on 16-byte boundaries; strides in elements */
+    int64_t q_token_stride, q_head_stride;
+    void* out; /* device, same shape and type */
+    int64_t out_token_stride, out_head_stride;
+    float* lse;                 /* device f32 [n_q][n_heads], or NULL */
+    const int32_t* page_table;  /* device [batch][max_pages], rows page_table_stride entries apart */
+    int64_t page_table_stride;
+    const int32_t* kv_len;      /* device [batch]; a length past max_pages * page_tokens counts as that */
+    const int32_t* q_start;     /* device [batch + 1], or NULL */
+    int32_t batch, n_q, n_heads, max_pages;
+    int32_t max_q;   /* largest n_b, as the caller knows it on the host: it chooses the kernel, no result depends on it */
+    int32_t max_len; /* likewise the largest kv_len, or 0 for max_pages * page_tokens */
+    int32_t causal;  /* 0 or 1 */
+    int32_t window;  /* 0: none */
+    float scale;
+    moe_dtype dtype;
+} moe_kv_attend_args;
+
+/* Asynchronous on `stream`, no synchronisation. The context owns a workspace
+ * for partial results: its first call on a context allocates it (make it
+ * before any stream capture), and calls on several streams of one context are
+ * ordered after one another on the device where they use it. Replays of a
+ * captured call must not run at the same time as other attention calls of the
+ * context. Several host threads may call. A page id outside the cache hides
+ * that page's keys and is noted (moe_kv_check).
+ * Errors: MOE_EINVAL, MOE_ENOMEM (workspace), MOE_ECUDA, MOE_ETIMEOUT (a
+ * bounded device wait expired in an earlier call). */
+moe_status moe_kv_attend(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_attend_args* args, void* stream);
+
+/* MOE_EINVAL if a finished moe_kv_* call of the context met a slot or page id
+ * outside its cache since the last check (each was skipped), MOE_ETIMEOUT if
+ * a bounded device wait expired, else MOE_OK. Does not wait: synchronise
+ * first for an answer on the calls enqueued so far. */
+moe_status moe_kv_check(moe_ctx* ctx);
+
 /* ---- diagnostics -------------------------------------------------------- */
 
 const char* moe_status_str(moe_status s);
@@ -488,7 +599,7 @@ const char* moe_last_error(void);
  * hit), 2 combine, 3 prefill grouped GEMM gate/up, 4 prefill grouped GEMM
  * down, 5 prefill token-row conversion to fp16, 6 decode expert FFN over the
  * experts copied in by the call (its duration includes the wait for the
- * copies). Returns launches, total
+ * copies), 7 moe_kv_append, 8 moe_kv_read, 9 moe_kv_attend. Returns launches, total
  * milliseconds and the algorithmic bytes and flops of those launches. Waits
  * for the events. */
 moe_status moe_ctx_set_profiling(moe_ctx* ctx, int32_t on);
@@ -496,7 +607,7 @@ moe_status moe_ctx_kernel_times(moe_ctx* ctx, int32_t kind, uint64_t* launches, 
                                 double* bytes, double* flops);
 moe_status moe_ctx_reset_kernel_times(moe_ctx* ctx);
 
-/* Number of kernels the context's layers have launched since its creation
+/* Number of kernels the context's layers and cache calls have launched since its creation
  * (every launch is counted, profiling or not). */
 moe_status moe_ctx_launches(moe_ctx* ctx, uint64_t* out);
 
