@@ -1,4 +1,28 @@
-// Attention over the 4-bit cache: one warp per new token and query head.
+// Attention of few query columns over the 4-bit cache (decode steps): the cache
+// is read once, the codes go to the tensor cores as they are.
+//
+// Columns are (new token, query head of the kv head) pairs, 8 * NT to a tile; a
+// segment is (sequence, kv head, column tile), its keys in blocks of 16 (one
+// record each). All segments' blocks are laid end to end and cut into equal
+// ranges, one per CTA, so ragged batches and single long sequences alike keep
+// every SM reading; a segment cut between CTAs is joined from fp32 partial
+// results by the CTA that finishes it last, in CTA order.
+//
+// Within a CTA each of 8 warps takes every eighth chunk (4,608 bytes: 64, 32 or
+// 16 tokens for head_dim 64, 128, 256) and owns a ring of bulk copies into
+// shared memory, so no barrier but a piece's final merge is shared.
+//
+// Per chunk, with mma.sync m16n8k16 (fp16 inputs, fp32 sums):
+//   scores  z[token][col] = c[col] * sum_g (s_tg * (codes . q)_g + b_tg * X_g[col])
+//     where X_g is q's sum over group g. A nibble masked in place is an fp16
+//     subnormal, code * 2^-24 (or * 2^-20 for the high nibble of a byte, whose
+//     query element is divided by 16), so one AND makes two exact operands.
+//   weights p = 2^(z - m), m a bound that moves only when some z passes it by 8
+//     (so p <= 2^8), the sums then rescaled.
+//   output  o[dim][col] = sum_t code_td * (p s_tg f_g) + sum_t p b_tg: the scale
+//     goes into the weights, one fp16 operand per group, f_g a power of two that keeps
+//     it within fp16's range whatever the values' magnitude. Rounding the
+//     weights to fp16 (2^-11) is the one rounding beyond fp32 here.
 #include <cuda_bf16.h>
 
 #include "kv_internal.h"
@@ -8,117 +32,736 @@ namespace moe {
 
 namespace {
 
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kChunkBytes = 4608;
+constexpr float kLazy = 8.0f;  // how far a score may pass the bound before it moves (log2)
+
+template <int D, int NT>
+struct Shape {
+    static constexpr int NG = D / 64, W = D / 32;  // groups; code words of a row that one lane of four holds
+    static constexpr int kRec = kv_record_bytes(D);
+    static constexpr int SB = kChunkBytes / kRec;  // blocks of a chunk
+    static constexpr int NC = 8 * NT;
+    static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;  // per SM
+    static constexpr int kStages = kCtas == 2 ? 2 : D == 256 && NT == 2 ? 2 : 3;
+    static constexpr int kCol = D + 4;  // floats of a column in the merge buffer
+    static constexpr int kRing = kWarps * kStages * kChunkBytes;
+    static constexpr int kMerge = kWarps * NC * kCol * 4;
+    static constexpr int kSmall = (2 * kWarps * NC + 2 * NC) * 4;
+    static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + 128;
+    static constexpr int kSlot = NC * (D + 2);  // floats of one partial result: m[NC], l[NC], o[NC][D]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 affine_of(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// N consecutive 32-bit words of shared memory
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = ptx::lds_u4(a + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+    } else {
+        w[0] = ptx::lds_u32(a);
+    }
+}
+
 template <class T>
-__device__ __forceinline__ float to_f(T x);
+__device__ __forceinline__ float2 unpack2(uint32_t w);
 template <>
-__device__ __forceinline__ float to_f<__half>(__half x) {
-    return __half2float(x);
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return affine_of(w);
 }
 template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) {
-    return __bfloat162float(x);
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-template <class T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) {
-    return __float2half_rn(x);
+
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
 }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-    return __float2bfloat16_rn(x);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// One sequence as the schedule sees it.
+struct Seq {
+    int first, n, len, lo_blk, per, nct;  // first q row, new tokens, keys, first block seen, units per segment, column tiles
+    bool any;                             // some key is seen
+};
+
+__device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
+    Seq s;
+    if (a.q_start) {
+        s.first = __ldg(a.q_start + b);
+        s.n = __ldg(a.q_start + b + 1) - s.first;
+    } else {
+        s.first = b * a.T;
+        s.n = a.T;
+    }
+    s.len = max(0, min(__ldg(a.kv_len + b), a.max_pages << a.c.page_shift));
+    const int pos0 = s.len - s.n;
+    const int lo = a.window && pos0 >= a.window ? pos0 - a.window + 1 : 0;
+    s.lo_blk = lo >> 4;
+    const int nblk = ((s.len + 15) >> 4) - s.lo_blk;
+    s.any = s.len > 0;
+    s.per = max(1, nblk);
+    s.nct = s.n > 0 ? (int)(((int64_t)s.n * a.G + NC - 1) / NC) : 0;
+    return s;
+}
+
+__device__ __forceinline__ int64_t units_of(const KvAttend& a, const Seq& s) { return (int64_t)s.per * a.c.H * s.nct; }
+
+// A walk over the CTA's range of units, piece by piece (a piece: the part of
+// one segment that the range holds).
+struct Walk {
+    int64_t w, w1, ex;  // position, end, and where sequence b's units start
+    int b;
+    Seq s;
+    int h, ct, blk0, nb;  // piece: kv head, column tile, first block (of the segment) and blocks
+    int64_t seg0;         // flat start of the piece's segment
+    int rot;              // chunks before this piece, mod kWarps
+    int64_t quota;        // units of a CTA
+
+    __device__ __forceinline__ bool done() const { return w >= w1; }
+    __device__ __forceinline__ void piece(const KvAttend& a, int NC) {
+        if (w >= w1) return;
+        int64_t u = units_of(a, s);
+        while (w >= ex + u) {
+            ex += u;
+            s = seq_of(a, ++b, NC);
+            u = units_of(a, s);
+        }
+        const int64_t r = w - ex;
+        const unsigned seg = (unsigned)(r / s.per);
+        blk0 = (int)(r - (int64_t)seg * s.per);
+        h = (int)(seg / (unsigned)s.nct);
+        ct = (int)(seg - (unsigned)h * (unsigned)s.nct);
+        seg0 = w - blk0;
+        nb = (int)min((int64_t)(s.per - blk0), w1 - w);
+    }
+    template <int SB>
+    __device__ __forceinline__ void next(const KvAttend& a, int NC) {
+        rot = (rot + (nb + SB - 1) / SB) % kWarps;
+        w += nb;
+        piece(a, NC);
+    }
+};
+
+template <int D, int NT, class T>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
+    kv_decode_kernel(const __grid_constant__ KvAttend a) {
+    using S = Shape<D, NT>;
+    constexpr int NG = S::NG, W = S::W, SB = S::SB, NC = S::NC, kRec = S::kRec, kStages = S::kStages;
+    extern __shared__ __align__(128) unsigned char smem[];
+    unsigned char* ring = smem;
+    float* merge = reinterpret_cast<float*>(smem + S::kRing);
+    float* sm_m = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [kWarps][NC]
+    float* sm_l = sm_m + kWarps * NC;
+    float* sm_w = sm_l + kWarps * NC;  // [2][NC]: the merged m and l
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_w + 2 * NC);
+    int64_t* scan = reinterpret_cast<int64_t*>(bars + kWarps * kStages);  // kWarps sums, then the start: flat, sequence
+    int* flag = reinterpret_cast<int*>(scan + kWarps + 2);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (lane < kStages) ptx::mbar_init(bars + warp * kStages + lane, 1);
+    ptx::fence_mbar_init();
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+
+    // ---- the CTA's range ----
+    Walk wk;
+    {
+        int64_t total = 0, ex = 0, u = 0;
+        for (int base = 0; base < a.B; base += kThreads) {
+            const int b = base + tid;
+            u = b < a.B ? units_of(a, seq_of(a, b, NC)) : 0;
+            int64_t inc = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(kFull, inc, o);
+                if (lane >= o) inc += x;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            ex = total + inc - u;
+            for (int i = 0; i < kWarps; ++i) {
+                if (i < warp) ex += scan[i];
+                total += scan[i];
+            }
+        }
+        const int64_t quota = max((int64_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
+        wk.w = quota * blockIdx.x;
+        wk.w1 = min(total, wk.w + quota);
+        if (wk.w >= total) return;
+        if (a.B > kThreads) {  // again, for the chunk that holds the start
+            int64_t run = 0;
+            for (int base = 0; base < a.B; base += kThreads) {
+                const int b = base + tid;
+                const int64_t v = b < a.B ? units_of(a, seq_of(a, b, NC)) : 0;
+                int64_t inc = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(kFull, inc, o);
+                    if (lane >= o) inc += x;
+                }
+                __syncthreads();
+                if (lane == 31) scan[warp] = inc;
+                __syncthreads();
+                int64_t e = run + inc - v;
+                for (int i = 0; i < kWarps; ++i) {
+                    if (i < warp) e += scan[i];
+                    run += scan[i];
+                }
+                if (e <= wk.w && wk.w < e + v) scan[kWarps] = e, scan[kWarps + 1] = b;
+            }
+        } else if (ex <= wk.w && wk.w < ex + u) {
+            scan[kWarps] = ex, scan[kWarps + 1] = tid;
+        }
+        __syncthreads();
+        wk.ex = scan[kWarps];
+        wk.b = (int)scan[kWarps + 1];
+        wk.s = seq_of(a, wk.b, NC);
+        wk.rot = 0;
+        wk.quota = quota;
+        wk.piece(a, NC);
+    }
+
+    // ---- loads: this warp's chunks, kStages ahead ----
+    Walk ld = wk;
+    int ld_c = (warp - ld.rot) & (kWarps - 1);  // next chunk of ld's piece
+    uint32_t ld_n = 0, use_n = 0;               // chunks issued and used
+    uint32_t valid = 0;                         // per stage, 4 bits: blocks that were loaded
+    bool dead = false;                          // a wait expired
+    uint64_t* mybars = bars + warp * kStages;
+    const uint32_t ring0 = ptx::smem_addr(ring) + warp * kStages * kChunkBytes;
+    auto issue = [&]() {
+        while (!ld.done() && (!ld.s.any || ld_c * SB >= ld.nb)) {
+            ld.template next<SB>(a, NC);
+            ld_c = (warp - ld.rot) & (kWarps - 1);
+        }
+        if (ld.done() || dead) return;
+        const int st = (int)(ld_n % kStages);
+        const int blk = ld.s.lo_blk + ld.blk0 + ld_c * SB + lane;  // of the sequence, for lane < SB
+        bool ok = lane < SB && ld_c * SB + lane < ld.nb;
+        int page = 0;
+        if (ok) {
+            const int tok = blk << 4;
+            page = __ldg(a.table + (int64_t)ld.b * a.table_stride + (tok >> a.c.page_shift));
+            if ((unsigned)page >= (unsigned)a.c.n_pages) {
+                *(volatile unsigned*)a.bad = 1u;
+                ok = false;
+            }
+        }
+        const unsigned v = __ballot_sync(kFull, ok);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(mybars + st, __popc(v) * kRec);
+        __syncwarp();
+        if (ok) {
+            const int in = (blk << 4) & (a.c.P - 1);
+            const uint8_t* src =
+                a.c.pages + (((size_t)page * a.c.H + ld.h) * (a.c.P >> 4) + (in >> 4)) * (size_t)kRec;
+            ptx::bulk_g2s(ring + (warp * kStages + st) * kChunkBytes + lane * kRec, src, kRec, mybars + st);
+        }
+        valid = (valid & ~(15u << (4 * st))) | (v << (4 * st));
+        ++ld_n;
+        ld_c += kWarps;
+    };
+    for (int i = 0; i < kStages; ++i) issue();
+
+    // row g of a score tile holds token pi(g) of its half block; see below
+    const int pg = g ^ ((g >> 1) & 1);
+
+    uint32_t qf[NT][W][4];
+    float cz[NT][2], X[NT][NG][2];
+    int hi_c[NT][2], lo_c[NT][2];
+    int q_b = -1, q_h = 0, q_ct = 0;
+
+    for (; !wk.done(); wk.template next<SB>(a, NC)) {
+        const int ncols = min(NC, wk.s.n * a.G - wk.ct * NC);
+        const int c0 = wk.ct * NC;
+        if (wk.b != q_b || wk.h != q_h || wk.ct != q_ct) {
+            q_b = wk.b, q_h = wk.h, q_ct = wk.ct;
+            // ---- queries: column g of each n-tile, scaled to a largest element in [2^10, 2^11) ----
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int c = nt * 8 + g;
+                uint32_t raw[W][4];
+                const bool in = c < ncols;
+                const int i = (c0 + c) / a.G, hq = (c0 + c) - i * a.G;
+                const T* qp = static_cast<const T*>(a.q) + (int64_t)(wk.s.first + i) * a.qt +
+                              (int64_t)(wk.h * a.G + hq) * a.qh;
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    const int w = t * W + k;
+                    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(qp + (w % NG) * 64 + (w / NG) * 8))
+                                       : make_uint4(0, 0, 0, 0);
+                    raw[k][0] = v.x, raw[k][1] = v.y, raw[k][2] = v.z, raw[k][3] = v.w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<T>(raw[k][e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
+                ex = top == 0.0f || ex == 128 ? 10 : min(max(ex, -100), 110);
+                const float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
+                float xs[NG] = {};
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = unpack2<T>(raw[k][e]);
+                        const float sc = (e & 1) ? f * 0.0625f : f;  // pairs 1 and 3 meet codes times 16
+                        const uint32_t p = pack_h2(v.x * sc, v.y * sc);
+                        qf[nt][k][e] = p;
+                        const float2 r = affine_of(p);
+                        xs[k % NG] += (r.x + r.y) * ((e & 1) ? 16.0f : 1.0f);
+                    }
+                }
+                const float back = a.scale_log2 * __uint_as_float((uint32_t)(127 - 10 + ex) << 23) * 16777216.0f;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    xs[j] += __shfl_xor_sync(kFull, xs[j], 1);
+                    xs[j] += __shfl_xor_sync(kFull, xs[j], 2);
+                    X[nt][j][0] = __shfl_sync(kFull, xs[j], 8 * t) * 0x1p-24f;
+                    X[nt][j][1] = __shfl_sync(kFull, xs[j], 8 * t + 4) * 0x1p-24f;
+                }
+                cz[nt][0] = __shfl_sync(kFull, back, 8 * t);
+                cz[nt][1] = __shfl_sync(kFull, back, 8 * t + 4);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // keys [lo_c, hi_c) that column 2t + e sees
+                    const int cc = nt * 8 + 2 * t + e;
+                    const int pos = wk.s.len - wk.s.n + (c0 + cc) / a.G;
+                    hi_c[nt][e] = cc < ncols ? (a.causal ? min(wk.s.len, pos + 1) : wk.s.len) : 0;
+                    lo_c[nt][e] = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+                }
+            }
+        }
+        // tokens [all_lo, all_hi) are seen by every column of the tile
+        const int pos_first = wk.s.len - wk.s.n + c0 / a.G, pos_last = wk.s.len - wk.s.n + (c0 + ncols - 1) / a.G;
+        const int all_hi = a.causal ? min(wk.s.len, pos_first + 1) : wk.s.len;
+        const int all_lo = a.window && pos_last >= a.window ? pos_last - a.window + 1 : 0;
+
+        float o[NT][D / 16][4], bacc[NT][NG][2], m[NT][2], l[NT][2], f[NG], lim[NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) bacc[nt][j][0] = bacc[nt][j][1] = 0.0f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) f[j] = 1.0f, lim[j] = 0.0f;
+
+        for (int c = (warp - wk.rot) & (kWarps - 1); wk.s.any && c * SB < wk.nb; c += kWarps) {
+            const int st = (int)(use_n % kStages);
+            if (!dead && !ptx::mbar_wait_bounded(mybars + st, (use_n / kStages) & 1, nullptr)) {
+                dead = true;
+                if (lane == 0) *(volatile unsigned*)a.err = 1024u;
+            }
+            dead = __any_sync(kFull, dead);
+            if (dead) break;
+            const uint32_t base = ring0 + st * kChunkBytes;
+            const unsigned v = (valid >> (4 * st)) & 15u;
+            const int tok0 = (wk.s.lo_blk + wk.blk0 + c * SB) << 4;
+            const bool whole = v == (1u << SB) - 1 && tok0 >= all_lo && tok0 + 16 * SB <= all_hi;
+
+            float z[SB][NT][4];
+            uint32_t va[SB][2][NG];  // value affine words of tokens pi(g), pi(g) + 8
+#pragma unroll
+            for (int sb = 0; sb < SB; ++sb) {
+                const uint32_t rec = base + sb * kRec;
+                uint32_t kw[2][W], ka[2][NG];
+                lds_words<W>(rec + pg * (D / 2) + t * W * 4, kw[0]);
+                lds_words<W>(rec + (pg + 8) * (D / 2) + t * W * 4, kw[1]);
+                lds_words<NG>(rec + kv_k_affine(D) + pg * NG * 4, ka[0]);
+                lds_words<NG>(rec + kv_k_affine(D) + (pg + 8) * NG * 4, ka[1]);
+                lds_words<NG>(rec + kv_v_affine(D) + pg * NG * 4, va[sb][0]);
+                lds_words<NG>(rec + kv_v_affine(D) + (pg + 8) * NG * 4, va[sb][1]);
+                float acc[NG][NT][4];
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    const uint32_t x0 = kw[0][k], x1 = kw[1][k], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(acc[k % NG][nt], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                            qf[nt][k][0], qf[nt][k][1]);
+                        mma(acc[k % NG][nt], y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u,
+                            qf[nt][k][2], qf[nt][k][3]);
+                    }
+                }
+                float zz[NT][4] = {};
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const float2 r0 = affine_of(ka[0][j]), r1 = affine_of(ka[1][j]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        zz[nt][0] = fmaf(r0.x, acc[j][nt][0], fmaf(r0.y, X[nt][j][0], zz[nt][0]));
+                        zz[nt][1] = fmaf(r0.x, acc[j][nt][1], fmaf(r0.y, X[nt][j][1], zz[nt][1]));
+                        zz[nt][2] = fmaf(r1.x, acc[j][nt][2], fmaf(r1.y, X[nt][j][0], zz[nt][2]));
+                        zz[nt][3] = fmaf(r1.x, acc[j][nt][3], fmaf(r1.y, X[nt][j][1], zz[nt][3]));
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[sb][nt][e] = zz[nt][e] * cz[nt][e & 1];
+            }
+            if (!whole) {
+#pragma unroll
+                for (int sb = 0; sb < SB; ++sb) {
+                    const int tk = tok0 + sb * 16 + pg;
+                    const bool in = (v >> sb) & 1;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = tk + (e & 2) * 4;
+                            if (!in || k < lo_c[nt][e & 1] || k >= hi_c[nt][e & 1]) z[sb][nt][e] = -INFINITY;
+                        }
+                    // places that no column sees hold anything: their scale must not move f
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (!in || tk + 8 * r >= wk.s.len)
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) va[sb][r][j] = 0;
+                }
+            }
+            // does a score or a scale pass its bound?
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+#pragma unroll
+                    for (int sb = 1; sb < SB; ++sb) top = fmaxf(top, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
+                    over |= top > m[nt][e] + kLazy;
+                }
+            float smax[NG];
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                smax[j] = 0.0f;
+#pragma unroll
+                for (int sb = 0; sb < SB; ++sb)
+                    smax[j] = fmaxf(smax[j], fmaxf(affine_of(va[sb][0][j]).x, affine_of(va[sb][1][j]).x));
+                over |= smax[j] > lim[j];
+            }
+            if (__any_sync(kFull, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = m[nt][e];
+#pragma unroll
+                        for (int sb = 0; sb < SB; ++sb) top = fmaxf(top, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                        const float sc = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - top);
+                        m[nt][e] = top;
+                        l[nt][e] *= sc;
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) bacc[nt][j][e] *= sc;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= sc, o[nt][i][e + 2] *= sc;
+                    }
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    float top = smax[j];
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                    if (top > lim[j]) {  // the same in every lane
+                        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -24), 15);
+                        const float nf = __uint_as_float((uint32_t)(127 - ex) << 23);
+                        lim[j] = 16.0f * __uint_as_float((uint32_t)(127 + ex) << 23);
+                        const float sc = nf / f[j];
+                        f[j] = nf;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[nt][j * 4 + i][e] *= sc;
+                    }
+                }
+            }
+            float ms[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                ms[nt][0] = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+                ms[nt][1] = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+            }
+#pragma unroll
+            for (int sb = 0; sb < SB; ++sb) {
+                const uint32_t rec = base + sb * kRec;
+                // tokens pi(2t), pi(2t+1), and the same plus 8: k index 2t, 2t+1, 2t+8, 2t+9 of the product
+                uint32_t vw[4][NG];
+                const int ta = (2 * t) ^ (t & 1), tb = (2 * t + 1) ^ (t & 1);
+                lds_words<NG>(rec + kv_v_codes(D) + ta * (D / 2) + g * NG * 4, vw[0]);
+                lds_words<NG>(rec + kv_v_codes(D) + tb * (D / 2) + g * NG * 4, vw[1]);
+                lds_words<NG>(rec + kv_v_codes(D) + (ta + 8) * (D / 2) + g * NG * 4, vw[2]);
+                lds_words<NG>(rec + kv_v_codes(D) + (tb + 8) * (D / 2) + g * NG * 4, vw[3]);
+                float p[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[nt][e] = ex2(z[sb][nt][e] - ms[nt][e & 1]);
+                        l[nt][e & 1] += p[nt][e];
+                    }
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const float2 r0 = affine_of(va[sb][0][j]), r1 = affine_of(va[sb][1][j]);
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w0 = p[nt][0] * (r0.x * f[j]), w1 = p[nt][1] * (r0.x * f[j]);
+                        float w2 = p[nt][2] * (r1.x * f[j]), w3 = p[nt][3] * (r1.x * f[j]);
+                        float d0 = p[nt][0] * r0.y, d1 = p[nt][1] * r0.y, d2 = p[nt][2] * r1.y, d3 = p[nt][3] * r1.y;
+                        if (!whole) {  // an unseen value may be NaN or infinite
+                            if (z[sb][nt][0] == -INFINITY) w0 = d0 = 0.0f;
+                            if (z[sb][nt][1] == -INFINITY) w1 = d1 = 0.0f;
+                            if (z[sb][nt][2] == -INFINITY) w2 = d2 = 0.0f;
+                            if (z[sb][nt][3] == -INFINITY) w3 = d3 = 0.0f;
+                        }
+                        pb[nt][0] = transpose8x8(pack_h2(w0, w1));
+                        pb[nt][1] = transpose8x8(pack_h2(w2, w3));
+                        bacc[nt][j][0] += d0 + d2;
+                        bacc[nt][j][1] += d1 + d3;
+                    }
+                    // two tokens' nibbles side by side: low halves hold elements 0, 2, 4, 6, high halves 1, 3, 5, 7
+                    const uint32_t u0 = __byte_perm(vw[0][j], vw[1][j], 0x5410);
+                    const uint32_t h0 = __byte_perm(vw[0][j], vw[1][j], 0x7632);
+                    const uint32_t u1 = __byte_perm(vw[2][j], vw[3][j], 0x5410);
+                    const uint32_t h1 = __byte_perm(vw[2][j], vw[3][j], 0x7632);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(o[nt][j * 4 + 0], u0 & 0x000F000Fu, h0 & 0x000F000Fu, u1 & 0x000F000Fu, h1 & 0x000F000Fu,
+                            pb[nt][0], pb[nt][1]);
+                        mma(o[nt][j * 4 + 1], u0 & 0x00F000F0u, h0 & 0x00F000F0u, u1 & 0x00F000F0u, h1 & 0x00F000F0u,
+                            pb[nt][0], pb[nt][1]);
+                        mma(o[nt][j * 4 + 2], (u0 >> 8) & 0x000F000Fu, (h0 >> 8) & 0x000F000Fu, (u1 >> 8) & 0x000F000Fu,
+                            (h1 >> 8) & 0x000F000Fu, pb[nt][0], pb[nt][1]);
+                        mma(o[nt][j * 4 + 3], (u0 >> 8) & 0x00F000F0u, (h0 >> 8) & 0x00F000F0u, (u1 >> 8) & 0x00F000F0u,
+                            (h1 >> 8) & 0x00F000F0u, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            ++use_n;
+            __syncwarp();
+            issue();
+        }
+
+        // ---- merge the warps ----
+        // o[nt][4j + i][e]: dim 64j + 8g + 2i + (e >> 1), column 8nt + 2t + (e & 1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], x);
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) bacc[nt][j][e] += __shfl_xor_sync(kFull, bacc[nt][j][e], x);
+                }
+                if (g == 0) {
+                    sm_m[warp * NC + nt * 8 + 2 * t + e] = m[nt][e];
+                    sm_l[warp * NC + nt * 8 + 2 * t + e] = l[nt][e];
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = nt * 8 + 2 * t + e;
+                float M = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i * NC + col]);
+                const float wt = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - M);
+                float* dst = merge + (warp * NC + col) * S::kCol + 8 * g;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const float s1 = 16777216.0f / f[j], bb = bacc[nt][j][e];
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float sc = (i & 1) ? s1 * 0.0625f : s1;
+                        y[2 * i] = wt * fmaf(o[nt][j * 4 + i][e], sc, bb);
+                        y[2 * i + 1] = wt * fmaf(o[nt][j * 4 + i][e + 2], sc, bb);
+                    }
+                    if (wt == 0.0f)  // nothing seen by this warp
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+                    *reinterpret_cast<float4*>(dst + 64 * j) = make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<float4*>(dst + 64 * j + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        if (tid < NC) {
+            float M = -INFINITY, L = 0.0f;
+            for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i * NC + tid]);
+            for (int i = 0; i < kWarps; ++i) {
+                const float mi = sm_m[i * NC + tid];
+                if (mi != -INFINITY) L += sm_l[i * NC + tid] * ex2(mi - M);
+            }
+            sm_w[tid] = M;
+            sm_w[NC + tid] = L;
+        }
+        __syncthreads();
+
+        const int64_t seg1 = wk.seg0 + wk.s.per;
+        const int cta0 = (int)(wk.seg0 / wk.quota), cta1 = (int)((seg1 - 1) / wk.quota);
+        // writes columns' results; o4(col, dim) gives four sums, M and L the column's statistics
+        auto put = [&](int col, int dim, float4 x) {
+            const int i = (c0 + col) / a.G, hq = wk.h * a.G + (c0 + col) - i * a.G;
+            const float L = sm_w[NC + col];
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+            store4(static_cast<T*>(a.out) + (int64_t)(wk.s.first + i) * a.ot + (int64_t)hq * a.oh + dim, x);
+            if (a.lse && dim == 0)
+                a.lse[(int64_t)(wk.s.first + i) * a.Hq + hq] =
+                    L == 0.0f ? -INFINITY : 0.6931471805599453f * (sm_w[col] + log2f(L));
+        };
+        float* slot = a.part + (size_t)(2 * blockIdx.x + (wk.blk0 == 0 ? 1 : 0)) * S::kSlot;
+        for (int x = tid; x < ncols * (D / 4); x += kThreads) {
+            const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
+            float4 y = *reinterpret_cast<const float4*>(merge + col * S::kCol + dim);
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(merge + (i * NC + col) * S::kCol + dim);
+                y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
+            }
+            if (cta0 == cta1)
+                put(col, dim, y);
+            else
+                __stcg(reinterpret_cast<float4*>(slot + 2 * NC + col * D + dim), y);
+        }
+        if (cta0 != cta1) {
+            // ---- a segment cut between CTAs: the last to finish joins the parts ----
+            if (tid < 2 * NC) __stcg(slot + tid, sm_w[tid]);
+            __threadfence();
+            __syncthreads();
+            const int parts = cta1 - cta0 + 1;
+            if (tid == 0) {
+                const unsigned old = atomicAdd(a.counters + cta0, 1u);
+                *flag = old == (unsigned)parts - 1;
+                if (*flag) a.counters[cta0] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (*flag) {
+                auto part = [&](int p) {  // part p: the segment's start lies in CTA cta0's second slot
+                    return a.part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * S::kSlot;
+                };
+                // per column: the largest m, then the sum of l, by one warp each
+                for (int col = warp; col < NC; col += kWarps) {
+                    float M = -INFINITY, L = 0.0f;
+                    for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(part(p) + col));
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+                    for (int p = lane; p < parts; p += 32) {
+                        const float mi = __ldcg(part(p) + col);
+                        if (mi != -INFINITY) L += __ldcg(part(p) + NC + col) * ex2(mi - M);
+                    }
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
+                    if (lane == 0) sm_w[col] = M, sm_w[NC + col] = L;
+                }
+                __syncthreads();
+                for (int x = tid; x < ncols * (D / 4); x += kThreads) {
+                    const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
+                    const float M = sm_w[col];
+                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int p = 0; p < parts; ++p) {
+                        const float mi = __ldcg(part(p) + col);
+                        const float4 q = __ldcg(reinterpret_cast<const float4*>(part(p) + 2 * NC + col * D + dim));
+                        const float wt = mi == -INFINITY ? 0.0f : ex2(mi - M);
+                        y.x = fmaf(wt, q.x, y.x), y.y = fmaf(wt, q.y, y.y), y.z = fmaf(wt, q.z, y.z), y.w = fmaf(wt, q.w, y.w);
+                    }
+                    put(col, dim, y);
+                }
+            }
+        }
+        __syncthreads();  // merge and sm_* are free again
+    }
+    // a warp that gave up lets the copies already issued land before the CTA can exit
+    if (dead)
+        for (; use_n < ld_n; ++use_n) ptx::mbar_wait_bounded(mybars + use_n % kStages, (use_n / kStages) & 1, nullptr);
+}
+
+template <int D, int NT, class T>
+cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s) {
+    using S = Shape<D, NT>;
+    auto kernel = kv_decode_kernel<D, NT, T>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(dim3(S::kCtas * sms), dim3(kThreads), S::kSmem, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(128) kv_attend_kernel(const __grid_constant__ KvAttend a) {
-    constexpr int NG = D / 64;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (w >= (int64_t)a.n_q * a.Hq) return;
-    const int row = (int)(w / a.Hq), hq = (int)(w % a.Hq), h = hq / a.G;
-    int b = 0, n = a.T, first = 0;
-    if (a.q_start) {
-        int hi = a.B - 1;
-        while (b < hi) {  // the last sequence that starts at or before the row
-            const int mid = (b + hi + 1) >> 1;
-            if (a.q_start[mid] <= row)
-                b = mid;
-            else
-                hi = mid - 1;
-        }
-        first = a.q_start[b];
-        n = a.q_start[b + 1] - first;
-    } else {
-        b = row / a.T;
-        first = b * a.T;
-    }
-    const int len = min(a.kv_len[b], a.max_pages << a.c.page_shift);
-    const int pos = len - n + (row - first);
-    const int hi = a.causal ? min(len, pos + 1) : len;
-    const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-    // lane: words lane, lane + 32, ... of the row (8 elements each)
-    constexpr int W = D / 8;
-    const bool act = lane < W;
-    float q[8], acc[8] = {};
-    const int i = lane / NG, g = lane % NG;
-    const T* qp = static_cast<const T*>(a.q) + (int64_t)row * a.qt + (int64_t)hq * a.qh + g * 64 + i * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = act ? to_f<T>(qp[e]) * a.scale_log2 : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    for (int j = lo; j < hi; ++j) {
-        const int page = a.table[(int64_t)b * a.table_stride + (j >> a.c.page_shift)];
-        if ((unsigned)page >= (unsigned)a.c.n_pages) {
-            *(volatile unsigned*)a.bad = 1u;
-            continue;
-        }
-        const int place = j & (a.c.P - 1), r = place & 15;
-        const uint8_t* rec = a.c.pages + (((size_t)page * a.c.H + h) * (a.c.P >> 4) + (place >> 4)) * kv_record_bytes(D);
-        float z = 0.0f, v[8];
-        if (act) {
-            const uint32_t kw = reinterpret_cast<const uint32_t*>(rec)[r * W + lane];
-            const uint32_t vw = reinterpret_cast<const uint32_t*>(rec + kv_v_codes(D))[r * W + lane];
-            const __half2 ka = *reinterpret_cast<const __half2*>(rec + kv_k_affine(D) + (r * NG + g) * 4);
-            const __half2 va = *reinterpret_cast<const __half2*>(rec + kv_v_affine(D) + (r * NG + g) * 4);
-            const float2 kf = __half22float2(ka), vf = __half22float2(va);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int nb = 4 * ((e & 1) * 4 + (e >> 1));
-                z = fmaf(q[e], fmaf(kf.x, (float)((kw >> nb) & 15u), kf.y), z);
-                v[e] = fmaf(vf.x, (float)((vw >> nb) & 15u), vf.y);
-            }
-        }
-#pragma unroll
-        for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
-        const float mn = fmaxf(m, z);
-        const float c = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(z - mn);
-        l = fmaf(l, c, p);
-        m = mn;
-        if (act) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], c, p * v[e]);
-        }
-    }
-    if (act) {
-        T* op = static_cast<T*>(a.out) + (int64_t)row * a.ot + (int64_t)hq * a.oh + g * 64 + i * 8;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) op[e] = from_f<T>(acc[e] * inv);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+cudaError_t launch_decode_cols(const KvAttend& a, int cols, int sms, cudaStream_t s) {
+    return cols <= 8 ? launch_decode<D, 1, T>(a, sms, s) : launch_decode<D, 2, T>(a, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, cudaStream_t s) {
-    const unsigned grid = (unsigned)(((int64_t)a.n_q * a.Hq + 3) / 4);
+cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s) {
     const bool bf = t == MOE_BF16;
     if (d == 64)
-        bf ? kv_attend_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(a) : kv_attend_kernel<64, __half><<<grid, 128, 0, s>>>(a);
-    else if (d == 128)
-        bf ? kv_attend_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(a) : kv_attend_kernel<128, __half><<<grid, 128, 0, s>>>(a);
-    else
-        bf ? kv_attend_kernel<256, __nv_bfloat16><<<grid, 128, 0, s>>>(a) : kv_attend_kernel<256, __half><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+        return bf ? launch_decode_cols<64, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<64, __half>(a, cols, sms, s);
+    if (d == 128)
+        return bf ? launch_decode_cols<128, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<128, __half>(a, cols, sms, s);
+    return bf ? launch_decode_cols<256, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<256, __half>(a, cols, sms, s);
 }
 
 }  // namespace moe

@@ -18,17 +18,69 @@ using namespace moe;
 
 namespace moe {
 
-// What the cache calls of a context keep: a mapped word that kernels note bad
-// slots and page ids in.
+// What the cache calls of a context keep: mapped words in which kernels note
+// bad slots and page ids [0] and expired waits [1], and the attention's
+// workspace, with the stream of the last call that uses it and an event behind
+// that call.
 struct KvState {
     unsigned* bad_host = nullptr;
     unsigned* bad_dev = nullptr;
+    int sms = 0;
+    unsigned char* ws = nullptr;
+    cudaEvent_t ws_done = nullptr;
+    cudaStream_t ws_stream = nullptr;
+    bool ws_used = false;
 };
 
 void kv_state_destroy(KvState* st) {
     if (!st) return;
     cudaFreeHost(st->bad_host);
+    cudaFree(st->ws);
+    if (st->ws_done) cudaEventDestroy(st->ws_done);
     delete st;
+}
+
+constexpr size_t kCounterBytes = 4096;  // a counter for each of up to 1,024 CTAs
+
+// The workspace of an attention call, made by the first of them.
+moe_status ensure_workspace(KvState* S, int device) {
+    if (S->ws) return MOE_OK;
+    int sms = 0;
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
+    if ((size_t)sms * kKvMaxCtas * sizeof(unsigned) > kCounterBytes)
+        return set_error(MOE_ECUDA, "moe_kv_attend: %d SMs are more than it is made for", sms);
+    const size_t bytes = kCounterBytes + (size_t)sms * kKvMaxCtas * kKvPartFloats * sizeof(float);
+    if (!S->ws_done) CUDA_TRY(cudaEventCreateWithFlags(&S->ws_done, cudaEventDisableTiming));
+    unsigned char* p = nullptr;
+    if (cudaMalloc(&p, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return set_error(MOE_ENOMEM, "moe_kv_attend: workspace of %zu bytes failed", bytes);
+    }
+    if (cudaMemset(p, 0, kCounterBytes) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
+        cudaFree(p);
+        return set_error(MOE_ECUDA, "moe_kv_attend: clearing the workspace failed: %s", cudaGetErrorString(cudaGetLastError()));
+    }
+    S->sms = sms;
+    S->ws = p;
+    return MOE_OK;
+}
+
+// Orders a call on s behind the last call that used the workspace on another
+// stream. A call being captured records no event outside its graph.
+moe_status workspace_begin(KvState* S, cudaStream_t s, bool* capturing) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    CUDA_TRY(cudaStreamIsCapturing(s, &cs));
+    *capturing = cs != cudaStreamCaptureStatusNone;
+    if (!*capturing && S->ws_used && S->ws_stream != s) CUDA_TRY(cudaStreamWaitEvent(s, S->ws_done, 0));
+    return MOE_OK;
+}
+
+moe_status workspace_end(KvState* S, cudaStream_t s, bool capturing) {
+    if (capturing) return MOE_OK;
+    CUDA_TRY(cudaEventRecord(S->ws_done, s));
+    S->ws_stream = s;
+    S->ws_used = true;
+    return MOE_OK;
 }
 
 }  // namespace moe
@@ -76,17 +128,29 @@ moe_status state_of(moe_ctx* C, KvState** out) {
     if (!st) {
         KvState* n = new (std::nothrow) KvState();
         if (!n) return set_error(MOE_ENOMEM, "out of host memory");
-        if (cudaHostAlloc(&n->bad_host, sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
+        if (cudaHostAlloc(&n->bad_host, 2 * sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
             cudaHostGetDevicePointer(&n->bad_dev, n->bad_host, 0) != cudaSuccess) {
             cudaGetLastError();
             kv_state_destroy(n);
             return set_error(MOE_ENOMEM, "cache state allocation failed");
         }
-        *n->bad_host = 0;
+        n->bad_host[0] = n->bad_host[1] = 0;
         st = n;
     }
     *out = st;
     return MOE_OK;
+}
+
+// A kernel gave up on a wait: its counters may be off, so they are cleared
+// before the next call.
+moe_status expired(KvState* S) {
+    S->bad_host[1] = 0;
+    if (S->ws) {
+        cudaDeviceSynchronize();
+        cudaMemset(S->ws, 0, kCounterBytes);
+        cudaDeviceSynchronize();
+    }
+    return set_error(MOE_ETIMEOUT, "a bounded device wait expired in an earlier attention call");
 }
 
 // Counts a launch; with profiling on, times it.
@@ -212,19 +276,29 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.window = (int64_t)p->window >= (int64_t)p->max_pages * cache->page_tokens ? 0 : p->window;
     a.scale_log2 = p->scale * 1.4426950408889634f;
     a.bad = S->bad_dev;
+    a.err = S->bad_dev + 1;
+    if (*(volatile unsigned*)(S->bad_host + 1)) return expired(S);
+    if ((st = ensure_workspace(S, ctx_device(C))) != MOE_OK) return st;
+    a.counters = reinterpret_cast<unsigned*>(S->ws);
+    a.part = reinterpret_cast<float*>(S->ws + kCounterBytes);
+    a.min_units = 32;
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
+    bool capturing;
+    if ((st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
     const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
-    CUDA_TRY(launch_kv_attend(a, d, p->dtype, s));
-    return MOE_OK;
+    const int64_t cols = (int64_t)p->max_q * a.G;
+    CUDA_TRY(launch_kv_attend(a, d, p->dtype, (int)(cols < 1 << 20 ? cols : 1 << 20), S->sms, s));
+    return workspace_end(S, s, capturing);
 }
 
 extern "C" moe_status moe_kv_check(moe_ctx* C) {
     if (!C) return set_error(MOE_EINVAL, "moe_kv_check: ctx is NULL");
     std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
     KvState* S = ctx_kv(C);
+    if (S && *(volatile unsigned*)(S->bad_host + 1)) return expired(S);
     if (S && *(volatile unsigned*)S->bad_host) {
         *(volatile unsigned*)S->bad_host = 0;
         return set_error(MOE_EINVAL, "an earlier cache call met a slot or page id outside its cache");

@@ -69,8 +69,18 @@ struct KvAttend {
     int causal, window;
     float scale_log2;  // scale * log2(e)
     unsigned* bad;
+    unsigned* err;  // mapped word: a bounded wait expired
+    // workspace of segments cut between CTAs: a counter per CTA (zero between
+    // calls) and two partial results per CTA
+    unsigned* counters;
+    float* part;
+    int min_units;  // fewest blocks of 16 tokens that a CTA takes
 };
 
-cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, cudaStream_t s);
+constexpr int kKvMaxCtas = 2;                       // resident CTAs per SM of any of the kernels
+constexpr size_t kKvPartFloats = 2 * 16 * (256 + 2);  // partial results of one CTA, at most
+
+// cols: query columns (new tokens * query heads per kv head) of a sequence, as the caller knows them
+cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s);
 
 }  // namespace moe
