@@ -19,10 +19,11 @@
 //     query element is divided by 16), so one AND makes two exact operands.
 //   weights p = 2^(z - m), m a bound that moves only when some z passes it by 8
 //     (so p <= 2^8), the sums then rescaled.
-//   output  o[dim][col] = sum_t code_td * (p s_tg f_g) + sum_t p b_tg: the scale
-//     goes into the weights, one fp16 operand per group, f_g a power of two that keeps
-//     it within fp16's range whatever the values' magnitude. Rounding the
-//     weights to fp16 (2^-11) is the one rounding beyond fp32 here.
+//   output  o[dim][col] = sum_t code_td * (p f s_tg) + sum_t p f b_tg: the scale
+//     goes into the weights, one fp16 operand per group; f is a power of two, part of the
+//     exponent's bound, that brings the largest scale near 1 so that weights stay within
+//     fp16's range whatever the values' magnitude. Rounding the weights to fp16
+//     (2^-11) is the one rounding beyond fp32 here.
 #include <cuda_bf16.h>
 
 #include "kv_internal.h"
@@ -35,7 +36,8 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kChunkBytes = 4608;
-constexpr float kLazy = 8.0f;  // how far a score may pass the bound before it moves (log2)
+constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it moves (log2)
+constexpr float kNone = -3e38f;  // the bound before any score
 
 template <int D, int NT>
 struct Shape {
@@ -48,8 +50,8 @@ struct Shape {
     static constexpr int kCol = D + 4;  // floats of a column in the merge buffer
     static constexpr int kRing = kWarps * kStages * kChunkBytes;
     static constexpr int kMerge = kWarps * NC * kCol * 4;
-    static constexpr int kSmall = (2 * kWarps * NC + 2 * NC) * 4;
-    static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + 128;
+    static constexpr int kSmall = (4 * kWarps * NC + 2 * NC) * 4;
+    static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + 96 + kWarps * 2 * 112;
     static constexpr int kSlot = NC * (D + 2);  // floats of one partial result: m[NC], l[NC], o[NC][D]
 };
 
@@ -117,10 +119,15 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// n / d, by 32-bit division where it will do.
+__device__ __forceinline__ int64_t quot(int64_t n, int64_t d) {
+    if ((uint64_t)(n | d) >> 32) return n / d;
+    return (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
 // One sequence as the schedule sees it.
 struct Seq {
-    int first, n, len, lo_blk, per, nct;  // first q row, new tokens, keys, first block seen, units per segment, column tiles
-    bool any;                             // some key is seen
+    int first, n, len, lo_blk, per, nct;  // first q row, new tokens, keys, first block seen, blocks of a segment, column tiles
 };
 
 __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
@@ -134,52 +141,74 @@ __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
     }
     s.len = max(0, min(__ldg(a.kv_len + b), a.max_pages << a.c.page_shift));
     const int pos0 = s.len - s.n;
-    const int lo = a.window && pos0 >= a.window ? pos0 - a.window + 1 : 0;
-    s.lo_blk = lo >> 4;
-    const int nblk = ((s.len + 15) >> 4) - s.lo_blk;
-    s.any = s.len > 0;
-    s.per = max(1, nblk);
-    s.nct = s.n > 0 ? (int)(((int64_t)s.n * a.G + NC - 1) / NC) : 0;
+    s.lo_blk = (a.window && pos0 >= a.window ? pos0 - a.window + 1 : 0) >> 4;
+    s.per = max(1, ((s.len + 15) >> 4) - s.lo_blk);  // a segment without keys is one unit: its rows become zeros
+    s.nct = s.n > 0 ? (int)quot((int64_t)s.n * a.G + NC - 1, NC) : 0;
     return s;
 }
 
-__device__ __forceinline__ int64_t units_of(const KvAttend& a, const Seq& s) { return (int64_t)s.per * a.c.H * s.nct; }
+// Units of a segment: its blocks, rounded up to whole ranges where every range is one CTA's and one segment's.
+__device__ __forceinline__ int64_t units_of(const KvAttend& a, const Seq& s, int64_t pad) {
+    return (pad ? quot(s.per + pad - 1, pad) * pad : s.per) * a.c.H * s.nct;
+}
 
 // A walk over the CTA's range of units, piece by piece (a piece: the part of
-// one segment that the range holds).
+// one segment that the range holds). Kept in shared memory, one copy per warp
+// for its loads and one for its arithmetic: they are looked at between pieces
+// only, and the registers are needed for sums.
 struct Walk {
-    int64_t w, w1, ex;  // position, end, and where sequence b's units start
-    int b;
+    int64_t w, w1, ex;    // position, end, and where sequence b's units start
+    int64_t seg0, quota;  // where the piece's segment starts; units of a CTA
+    int64_t pad;          // quota where segments are padded to it, else 0
     Seq s;
-    int h, ct, blk0, nb;  // piece: kv head, column tile, first block (of the segment) and blocks
-    int64_t seg0;         // flat start of the piece's segment
-    int rot;              // chunks before this piece, mod kWarps
-    int64_t quota;        // units of a CTA
+    int b, h, ct, blk0, nb;  // sequence, kv head, column tile, first block (of the segment) and blocks
+    int rot;                 // chunks before this piece, mod kWarps
 
     __device__ __forceinline__ bool done() const { return w >= w1; }
     __device__ __forceinline__ void piece(const KvAttend& a, int NC) {
         if (w >= w1) return;
-        int64_t u = units_of(a, s);
+        int64_t u = units_of(a, s, pad);
         while (w >= ex + u) {
             ex += u;
             s = seq_of(a, ++b, NC);
-            u = units_of(a, s);
+            u = units_of(a, s, pad);
         }
-        const int64_t r = w - ex;
-        const unsigned seg = (unsigned)(r / s.per);
-        blk0 = (int)(r - (int64_t)seg * s.per);
-        h = (int)(seg / (unsigned)s.nct);
-        ct = (int)(seg - (unsigned)h * (unsigned)s.nct);
+        const int64_t per = pad ? quot(s.per + pad - 1, pad) * pad : s.per;
+        const int64_t seg = quot(w - ex, per);
+        blk0 = (int)(w - ex - seg * per);
+        h = (int)((uint32_t)seg / (uint32_t)s.nct);
+        ct = (int)((uint32_t)seg - (uint32_t)h * (uint32_t)s.nct);
         seg0 = w - blk0;
         nb = (int)min((int64_t)(s.per - blk0), w1 - w);
     }
     template <int SB>
     __device__ __forceinline__ void next(const KvAttend& a, int NC) {
         rot = (rot + (nb + SB - 1) / SB) % kWarps;
-        w += nb;
+        w = pad ? w1 : w + nb;
         piece(a, NC);
     }
 };
+
+// Exclusive and total sums of u over the block's threads; scratch: kWarps words.
+__device__ __forceinline__ int64_t block_scan(int64_t u, int64_t* scratch, int warp, int lane, int64_t* total) {
+    int64_t inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int64_t ex = inc - u, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) ex += scratch[i];
+        sum += scratch[i];
+    }
+    *total = sum;
+    return ex;
+}
 
 template <int D, int NT, class T>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
@@ -192,9 +221,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     float* sm_m = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [kWarps][NC]
     float* sm_l = sm_m + kWarps * NC;
     float* sm_w = sm_l + kWarps * NC;  // [2][NC]: the merged m and l
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_w + 2 * NC);
+    int2* sm_see = reinterpret_cast<int2*>(sm_w + 2 * NC);  // [kWarps][NC]: the keys [x, y) that a column sees
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_see + kWarps * NC);
     int64_t* scan = reinterpret_cast<int64_t*>(bars + kWarps * kStages);  // kWarps sums, then the start: flat, sequence
-    int* flag = reinterpret_cast<int*>(scan + kWarps + 2);
+    Walk* walks = reinterpret_cast<Walk*>(scan + kWarps + 2);              // [kWarps][2]
+    int* flag = reinterpret_cast<int*>(walks + 2 * kWarps);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (lane < kStages) ptx::mbar_init(bars + warp * kStages + lane, 1);
@@ -203,183 +234,192 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     ptx::pdl_launch_dependents();
 
     // ---- the CTA's range ----
-    Walk wk;
+    Walk& wk = walks[2 * warp];
+    Walk& lw = walks[2 * warp + 1];
     {
-        int64_t total = 0, ex = 0, u = 0;
+        const bool one = a.B <= kThreads;
+        int64_t total = 0, padded = 0, ex = 0, ex_pad = 0, u = 0, u_pad = 0;
         for (int base = 0; base < a.B; base += kThreads) {
             const int b = base + tid;
-            u = b < a.B ? units_of(a, seq_of(a, b, NC)) : 0;
-            int64_t inc = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(kFull, inc, o);
-                if (lane >= o) inc += x;
+            u = u_pad = 0;
+            if (b < a.B) {
+                const Seq s = seq_of(a, b, NC);
+                u = units_of(a, s, 0);
+                u_pad = units_of(a, s, a.min_units);
             }
-            __syncthreads();
-            if (lane == 31) scan[warp] = inc;
-            __syncthreads();
-            ex = total + inc - u;
-            for (int i = 0; i < kWarps; ++i) {
-                if (i < warp) ex += scan[i];
-                total += scan[i];
-            }
+            int64_t sum, sum_pad;
+            ex = block_scan(u, scan, warp, lane, &sum);
+            ex_pad = block_scan(u_pad, scan, warp, lane, &sum_pad);
+            total += sum, padded += sum_pad;
         }
-        const int64_t quota = max((int64_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
-        wk.w = quota * blockIdx.x;
-        wk.w1 = min(total, wk.w + quota);
-        if (wk.w >= total) return;
-        if (a.B > kThreads) {  // again, for the chunk that holds the start
+        // few short segments: a CTA each, or several where one has more than min_units blocks; else equal ranges
+        const bool pad = padded <= (int64_t)a.min_units * gridDim.x;
+        const int64_t quota = pad ? a.min_units : quot(total + gridDim.x - 1, gridDim.x);
+        if (pad) total = padded, ex = ex_pad, u = u_pad;
+        const int64_t w = quota * blockIdx.x;
+        if (w >= total) return;
+        if (!one) {  // again, for the sequence that holds the start
             int64_t run = 0;
             for (int base = 0; base < a.B; base += kThreads) {
                 const int b = base + tid;
-                const int64_t v = b < a.B ? units_of(a, seq_of(a, b, NC)) : 0;
-                int64_t inc = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t x = __shfl_up_sync(kFull, inc, o);
-                    if (lane >= o) inc += x;
-                }
-                __syncthreads();
-                if (lane == 31) scan[warp] = inc;
-                __syncthreads();
-                int64_t e = run + inc - v;
-                for (int i = 0; i < kWarps; ++i) {
-                    if (i < warp) e += scan[i];
-                    run += scan[i];
-                }
-                if (e <= wk.w && wk.w < e + v) scan[kWarps] = e, scan[kWarps + 1] = b;
+                const int64_t v = b < a.B ? units_of(a, seq_of(a, b, NC), pad ? quota : 0) : 0;
+                int64_t sum;
+                const int64_t e = run + block_scan(v, scan, warp, lane, &sum);
+                run += sum;
+                if (e <= w && w < e + v) scan[kWarps] = e, scan[kWarps + 1] = b;
             }
-        } else if (ex <= wk.w && wk.w < ex + u) {
+        } else if (ex <= w && w < ex + u) {
             scan[kWarps] = ex, scan[kWarps + 1] = tid;
         }
         __syncthreads();
-        wk.ex = scan[kWarps];
-        wk.b = (int)scan[kWarps + 1];
-        wk.s = seq_of(a, wk.b, NC);
-        wk.rot = 0;
-        wk.quota = quota;
-        wk.piece(a, NC);
+        Walk x;
+        x.w = w;
+        x.w1 = min(total, w + quota);
+        x.quota = quota;
+        x.pad = pad ? quota : 0;
+        x.ex = scan[kWarps];
+        x.b = (int)scan[kWarps + 1];
+        x.s = seq_of(a, x.b, NC);
+        x.rot = 0;
+        x.piece(a, NC);
+        if (lane < 2) walks[2 * warp + lane] = x;
+        __syncwarp();
     }
 
-    // ---- loads: this warp's chunks, kStages ahead ----
-    Walk ld = wk;
-    int ld_c = (warp - ld.rot) & (kWarps - 1);  // next chunk of ld's piece
-    uint32_t ld_n = 0, use_n = 0;               // chunks issued and used
-    uint32_t valid = 0;                         // per stage, 4 bits: blocks that were loaded
-    bool dead = false;                          // a wait expired
-    uint64_t* mybars = bars + warp * kStages;
-    const uint32_t ring0 = ptx::smem_addr(ring) + warp * kStages * kChunkBytes;
-    auto issue = [&]() {
-        while (!ld.done() && (!ld.s.any || ld_c * SB >= ld.nb)) {
-            ld.template next<SB>(a, NC);
-            ld_c = (warp - ld.rot) & (kWarps - 1);
+    // ---- loads: this warp's chunks, kStages ahead, and the page of the one after ----
+    uint32_t ld_n = 0, use_n = 0;  // chunks issued and used
+    uint32_t valid = 0;            // per stage, 4 bits: blocks that were loaded
+    bool dead = false;             // a wait expired
+    uint64_t* const mybars = bars + warp * kStages;
+    unsigned char* const myring = ring + warp * kStages * kChunkBytes;
+    int ld_c, ld_nb, ld_blk, ld_page = 0;  // next chunk; its piece's blocks and first block; this lane's page
+    const int32_t* ld_table;
+    const uint8_t* ld_head;
+    bool ld_more;
+    auto load_piece = [&]() {
+        ld_more = !lw.done();
+        ld_c = (warp - lw.rot) & (kWarps - 1);
+        ld_nb = lw.s.len > 0 ? lw.nb : 0;
+        ld_blk = lw.s.lo_blk + lw.blk0;
+        ld_table = a.table + (int64_t)lw.b * a.table_stride;
+        ld_head = a.c.pages + (size_t)lw.h * (a.c.P >> 4) * kRec;
+    };
+    auto find = [&]() {  // moves on to a piece with a chunk for this warp, and fetches its page id
+        while (ld_more && ld_c * SB >= ld_nb) {
+            Walk x = lw;
+            x.template next<SB>(a, NC);
+            __syncwarp();
+            if (lane == 0) lw = x;
+            __syncwarp();
+            load_piece();
         }
-        if (ld.done() || dead) return;
+        const int i = ld_c * SB + lane;
+        if (ld_more && lane < SB && i < ld_nb) ld_page = __ldg(ld_table + ((ld_blk + i) >> (a.c.page_shift - 4)));
+    };
+    auto issue = [&]() {
+        if (!ld_more || dead) return;
         const int st = (int)(ld_n % kStages);
-        const int blk = ld.s.lo_blk + ld.blk0 + ld_c * SB + lane;  // of the sequence, for lane < SB
-        bool ok = lane < SB && ld_c * SB + lane < ld.nb;
-        int page = 0;
-        if (ok) {
-            const int tok = blk << 4;
-            page = __ldg(a.table + (int64_t)ld.b * a.table_stride + (tok >> a.c.page_shift));
-            if ((unsigned)page >= (unsigned)a.c.n_pages) {
-                *(volatile unsigned*)a.bad = 1u;
-                ok = false;
-            }
+        const int i = ld_c * SB + lane;
+        bool ok = lane < SB && i < ld_nb;
+        if (ok && (unsigned)ld_page >= (unsigned)a.c.n_pages) {
+            *(volatile unsigned*)a.bad = 1u;
+            ok = false;
         }
         const unsigned v = __ballot_sync(kFull, ok);
         if (lane == 0) ptx::mbar_arrive_expect_tx(mybars + st, __popc(v) * kRec);
         __syncwarp();
         if (ok) {
-            const int in = (blk << 4) & (a.c.P - 1);
-            const uint8_t* src =
-                a.c.pages + (((size_t)page * a.c.H + ld.h) * (a.c.P >> 4) + (in >> 4)) * (size_t)kRec;
-            ptx::bulk_g2s(ring + (warp * kStages + st) * kChunkBytes + lane * kRec, src, kRec, mybars + st);
+            const int in = (ld_blk + i) & ((a.c.P >> 4) - 1);
+            ptx::bulk_g2s(myring + st * kChunkBytes + lane * kRec,
+                          ld_head + ((size_t)ld_page * a.c.H * (a.c.P >> 4) + in) * kRec, kRec, mybars + st);
         }
         valid = (valid & ~(15u << (4 * st))) | (v << (4 * st));
         ++ld_n;
         ld_c += kWarps;
+        find();
     };
+    load_piece();
+    find();
+#pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue();
 
-    // row g of a score tile holds token pi(g) of its half block; see below
+    // row g of a score tile holds token pi(g) of its half block: 0 1 3 2 4 5 7 6, so that the
+    // four lanes of a value fragment read rows of both parities (half as many bank conflicts)
     const int pg = g ^ ((g >> 1) & 1);
 
     uint32_t qf[NT][W][4];
     float cz[NT][2], X[NT][NG][2];
-    int hi_c[NT][2], lo_c[NT][2];
-    int q_b = -1, q_h = 0, q_ct = 0;
 
-    for (; !wk.done(); wk.template next<SB>(a, NC)) {
-        const int ncols = min(NC, wk.s.n * a.G - wk.ct * NC);
-        const int c0 = wk.ct * NC;
-        if (wk.b != q_b || wk.h != q_h || wk.ct != q_ct) {
-            q_b = wk.b, q_h = wk.h, q_ct = wk.ct;
-            // ---- queries: column g of each n-tile, scaled to a largest element in [2^10, 2^11) ----
+#pragma unroll 1
+    while (!wk.done()) {
+        const int c0 = wk.ct * NC, len = wk.s.len, nb = len > 0 ? wk.nb : 0, blk0 = wk.s.lo_blk + wk.blk0;
+        const int ncols = min(NC, wk.s.n * a.G - c0);
+        int all_lo, all_hi;  // the keys that every column of the tile sees
+        {
+            const int pos = len - wk.s.n + (int)a.by_g.div(c0 + lane);
+            int hi = a.causal ? min(len, pos + 1) : len, lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+            all_lo = __reduce_max_sync(kFull, lane < ncols ? lo : 0);
+            all_hi = __reduce_min_sync(kFull, lane < ncols ? hi : len);
+            if (lane < NC) sm_see[warp * NC + lane] = make_int2(lo, lane < ncols ? hi : 0);
+            __syncwarp();
+        }
+        // ---- queries: column g of each n-tile, scaled to a largest element in [2^10, 2^11) ----
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int c = nt * 8 + g;
-                uint32_t raw[W][4];
-                const bool in = c < ncols;
-                const int i = (c0 + c) / a.G, hq = (c0 + c) - i * a.G;
-                const T* qp = static_cast<const T*>(a.q) + (int64_t)(wk.s.first + i) * a.qt +
-                              (int64_t)(wk.h * a.G + hq) * a.qh;
-                float top = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int c = nt * 8 + g;
+            uint32_t raw[W][4];
+            const bool in = c < ncols;
+            const int i = (int)a.by_g.div(c0 + c), hq = (c0 + c) - i * a.G;
+            const T* qp =
+                static_cast<const T*>(a.q) + (int64_t)(wk.s.first + i) * a.qt + (int64_t)(wk.h * a.G + hq) * a.qh;
+            float top = 0.0f;
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
-                    const int w = t * W + k;
-                    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(qp + (w % NG) * 64 + (w / NG) * 8))
-                                       : make_uint4(0, 0, 0, 0);
-                    raw[k][0] = v.x, raw[k][1] = v.y, raw[k][2] = v.z, raw[k][3] = v.w;
+            for (int k = 0; k < W; ++k) {
+                const int w = t * W + k;
+                const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(qp + (w % NG) * 64 + (w / NG) * 8))
+                                   : make_uint4(0, 0, 0, 0);
+                raw[k][0] = v.x, raw[k][1] = v.y, raw[k][2] = v.z, raw[k][3] = v.w;
+            }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<T>(raw[k][e]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
+            for (int k = 0; k < W; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack2<T>(raw[k][e]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-                int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
-                ex = top == 0.0f || ex == 128 ? 10 : min(max(ex, -100), 110);
-                const float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
-                float xs[NG] = {};
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
+            ex = top == 0.0f || ex == 128 ? 10 : min(max(ex, -100), 110);
+            const float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
+            float xs[NG] = {};
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
+            for (int k = 0; k < W; ++k) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 v = unpack2<T>(raw[k][e]);
-                        const float sc = (e & 1) ? f * 0.0625f : f;  // pairs 1 and 3 meet codes times 16
-                        const uint32_t p = pack_h2(v.x * sc, v.y * sc);
-                        qf[nt][k][e] = p;
-                        const float2 r = affine_of(p);
-                        xs[k % NG] += (r.x + r.y) * ((e & 1) ? 16.0f : 1.0f);
-                    }
-                }
-                const float back = a.scale_log2 * __uint_as_float((uint32_t)(127 - 10 + ex) << 23) * 16777216.0f;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    xs[j] += __shfl_xor_sync(kFull, xs[j], 1);
-                    xs[j] += __shfl_xor_sync(kFull, xs[j], 2);
-                    X[nt][j][0] = __shfl_sync(kFull, xs[j], 8 * t) * 0x1p-24f;
-                    X[nt][j][1] = __shfl_sync(kFull, xs[j], 8 * t + 4) * 0x1p-24f;
-                }
-                cz[nt][0] = __shfl_sync(kFull, back, 8 * t);
-                cz[nt][1] = __shfl_sync(kFull, back, 8 * t + 4);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // keys [lo_c, hi_c) that column 2t + e sees
-                    const int cc = nt * 8 + 2 * t + e;
-                    const int pos = wk.s.len - wk.s.n + (c0 + cc) / a.G;
-                    hi_c[nt][e] = cc < ncols ? (a.causal ? min(wk.s.len, pos + 1) : wk.s.len) : 0;
-                    lo_c[nt][e] = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = unpack2<T>(raw[k][e]);
+                    const float sc = (e & 1) ? f * 0.0625f : f;  // pairs 1 and 3 meet codes times 16
+                    const uint32_t p = pack_h2(v.x * sc, v.y * sc);
+                    qf[nt][k][e] = p;
+                    const float2 r = affine_of(p);
+                    xs[k % NG] += (r.x + r.y) * ((e & 1) ? 16.0f : 1.0f);
                 }
             }
+            const float back = a.scale_log2 * __uint_as_float((uint32_t)(127 - 10 + ex) << 23) * 16777216.0f;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                xs[j] += __shfl_xor_sync(kFull, xs[j], 1);
+                xs[j] += __shfl_xor_sync(kFull, xs[j], 2);
+                X[nt][j][0] = __shfl_sync(kFull, xs[j], 8 * t) * 0x1p-24f;
+                X[nt][j][1] = __shfl_sync(kFull, xs[j], 8 * t + 4) * 0x1p-24f;
+            }
+            cz[nt][0] = __shfl_sync(kFull, back, 8 * t);
+            cz[nt][1] = __shfl_sync(kFull, back, 8 * t + 4);
         }
-        // tokens [all_lo, all_hi) are seen by every column of the tile
-        const int pos_first = wk.s.len - wk.s.n + c0 / a.G, pos_last = wk.s.len - wk.s.n + (c0 + ncols - 1) / a.G;
-        const int all_hi = a.causal ? min(wk.s.len, pos_first + 1) : wk.s.len;
-        const int all_lo = a.window && pos_last >= a.window ? pos_last - a.window + 1 : 0;
 
-        float o[NT][D / 16][4], bacc[NT][NG][2], m[NT][2], l[NT][2], f[NG], lim[NG];
+        // The sums hold 2^(z - me): me = m - lf, m within kLazy of the largest z so far, 2^lf the
+        // factor that keeps weight times scale within fp16's range. lim: the largest scale 2^lf serves.
+        float o[NT][D / 16][4], bacc[NT][NG][2], thr[NT][2], me[NT][2], l[NT][2], lim = 0.0f, lf = 24.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -388,13 +428,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
 #pragma unroll
             for (int j = 0; j < NG; ++j) bacc[nt][j][0] = bacc[nt][j][1] = 0.0f;
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.0f;
-        }
 #pragma unroll
-        for (int j = 0; j < NG; ++j) f[j] = 1.0f, lim[j] = 0.0f;
+            for (int e = 0; e < 2; ++e) thr[nt][e] = me[nt][e] = kNone, l[nt][e] = 0.0f;
+        }
 
-        for (int c = (warp - wk.rot) & (kWarps - 1); wk.s.any && c * SB < wk.nb; c += kWarps) {
+#pragma unroll 1
+        for (int c = (warp - wk.rot) & (kWarps - 1); c * SB < nb; c += kWarps) {
             const int st = (int)(use_n % kStages);
             if (!dead && !ptx::mbar_wait_bounded(mybars + st, (use_n / kStages) & 1, nullptr)) {
                 dead = true;
@@ -402,9 +441,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
             }
             dead = __any_sync(kFull, dead);
             if (dead) break;
-            const uint32_t base = ring0 + st * kChunkBytes;
+            const uint32_t base = ptx::smem_addr(myring) + st * kChunkBytes;
             const unsigned v = (valid >> (4 * st)) & 15u;
-            const int tok0 = (wk.s.lo_blk + wk.blk0 + c * SB) << 4;
+            const int tok0 = (blk0 + c * SB) << 4;
             const bool whole = v == (1u << SB) - 1 && tok0 >= all_lo && tok0 + 16 * SB <= all_hi;
 
             float z[SB][NT][4];
@@ -437,22 +476,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                             qf[nt][k][2], qf[nt][k][3]);
                     }
                 }
-                float zz[NT][4] = {};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[sb][nt][e] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     const float2 r0 = affine_of(ka[0][j]), r1 = affine_of(ka[1][j]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        zz[nt][0] = fmaf(r0.x, acc[j][nt][0], fmaf(r0.y, X[nt][j][0], zz[nt][0]));
-                        zz[nt][1] = fmaf(r0.x, acc[j][nt][1], fmaf(r0.y, X[nt][j][1], zz[nt][1]));
-                        zz[nt][2] = fmaf(r1.x, acc[j][nt][2], fmaf(r1.y, X[nt][j][0], zz[nt][2]));
-                        zz[nt][3] = fmaf(r1.x, acc[j][nt][3], fmaf(r1.y, X[nt][j][1], zz[nt][3]));
+                        z[sb][nt][0] = fmaf(r0.x, acc[j][nt][0], fmaf(r0.y, X[nt][j][0], z[sb][nt][0]));
+                        z[sb][nt][1] = fmaf(r0.x, acc[j][nt][1], fmaf(r0.y, X[nt][j][1], z[sb][nt][1]));
+                        z[sb][nt][2] = fmaf(r1.x, acc[j][nt][2], fmaf(r1.y, X[nt][j][0], z[sb][nt][2]));
+                        z[sb][nt][3] = fmaf(r1.x, acc[j][nt][3], fmaf(r1.y, X[nt][j][1], z[sb][nt][3]));
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[sb][nt][e] = zz[nt][e] * cz[nt][e & 1];
+                    for (int e = 0; e < 4; ++e) z[sb][nt][e] *= cz[nt][e & 1];
             }
             if (!whole) {
 #pragma unroll
@@ -464,12 +506,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int k = tk + (e & 2) * 4;
-                            if (!in || k < lo_c[nt][e & 1] || k >= hi_c[nt][e & 1]) z[sb][nt][e] = -INFINITY;
+                            const int2 see = sm_see[warp * NC + nt * 8 + 2 * t + (e & 1)];
+                            if (!in || k < see.x || k >= see.y) z[sb][nt][e] = -INFINITY;
                         }
-                    // places that no column sees hold anything: their scale must not move f
+                    // places past the sequence's end hold anything: their scale must not move lf
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        if (!in || tk + 8 * r >= wk.s.len)
+                        if (!in || tk + 8 * r >= len)
 #pragma unroll
                             for (int j = 0; j < NG; ++j) va[sb][r][j] = 0;
                 }
@@ -483,60 +526,45 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     float top = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
 #pragma unroll
                     for (int sb = 1; sb < SB; ++sb) top = fmaxf(top, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
-                    over |= top > m[nt][e] + kLazy;
+                    over |= top > thr[nt][e];
                 }
-            float smax[NG];
+            __half2 sm = __float2half2_rn(0.0f);
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                smax[j] = 0.0f;
+            for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-                for (int sb = 0; sb < SB; ++sb)
-                    smax[j] = fmaxf(smax[j], fmaxf(affine_of(va[sb][0][j]).x, affine_of(va[sb][1][j]).x));
-                over |= smax[j] > lim[j];
-            }
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+                        sm = __hmax2(sm, *reinterpret_cast<const __half2*>(&va[sb][r][j]));
+            const float smax = __low2float(sm);
+            over |= smax > lim;
             if (__any_sync(kFull, over)) {
+                float top = smax;
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+                if (top > lim) {  // the same in every lane
+                    const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -24), 15);
+                    lf = (float)-ex;
+                    lim = __uint_as_float((uint32_t)(127 + 4 + ex) << 23);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = m[nt][e];
+                        float mx = thr[nt][e] - kLazy;
 #pragma unroll
-                        for (int sb = 0; sb < SB; ++sb) top = fmaxf(top, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
+                        for (int sb = 0; sb < SB; ++sb) mx = fmaxf(mx, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-                        const float sc = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - top);
-                        m[nt][e] = top;
+                        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+                        const float sc = ex2(me[nt][e] - (mx - lf));
+                        thr[nt][e] = mx + kLazy;
+                        me[nt][e] = mx - lf;
                         l[nt][e] *= sc;
 #pragma unroll
                         for (int j = 0; j < NG; ++j) bacc[nt][j][e] *= sc;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) o[nt][i][e] *= sc, o[nt][i][e + 2] *= sc;
                     }
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    float top = smax[j];
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-                    if (top > lim[j]) {  // the same in every lane
-                        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -24), 15);
-                        const float nf = __uint_as_float((uint32_t)(127 - ex) << 23);
-                        lim[j] = 16.0f * __uint_as_float((uint32_t)(127 + ex) << 23);
-                        const float sc = nf / f[j];
-                        f[j] = nf;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) o[nt][j * 4 + i][e] *= sc;
-                    }
-                }
-            }
-            float ms[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                ms[nt][0] = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-                ms[nt][1] = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
             }
 #pragma unroll
             for (int sb = 0; sb < SB; ++sb) {
@@ -553,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[nt][e] = ex2(z[sb][nt][e] - ms[nt][e & 1]);
+                        p[nt][e] = ex2(z[sb][nt][e] - me[nt][e & 1]);
                         l[nt][e & 1] += p[nt][e];
                     }
 #pragma unroll
@@ -562,19 +590,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float w0 = p[nt][0] * (r0.x * f[j]), w1 = p[nt][1] * (r0.x * f[j]);
-                        float w2 = p[nt][2] * (r1.x * f[j]), w3 = p[nt][3] * (r1.x * f[j]);
-                        float d0 = p[nt][0] * r0.y, d1 = p[nt][1] * r0.y, d2 = p[nt][2] * r1.y, d3 = p[nt][3] * r1.y;
-                        if (!whole) {  // an unseen value may be NaN or infinite
-                            if (z[sb][nt][0] == -INFINITY) w0 = d0 = 0.0f;
-                            if (z[sb][nt][1] == -INFINITY) w1 = d1 = 0.0f;
-                            if (z[sb][nt][2] == -INFINITY) w2 = d2 = 0.0f;
-                            if (z[sb][nt][3] == -INFINITY) w3 = d3 = 0.0f;
+                        float w0 = p[nt][0] * r0.x, w1 = p[nt][1] * r0.x, w2 = p[nt][2] * r1.x, w3 = p[nt][3] * r1.x;
+                        if (whole) {
+                            bacc[nt][j][0] = fmaf(p[nt][0], r0.y, fmaf(p[nt][2], r1.y, bacc[nt][j][0]));
+                            bacc[nt][j][1] = fmaf(p[nt][1], r0.y, fmaf(p[nt][3], r1.y, bacc[nt][j][1]));
+                        } else {  // an unseen value may be NaN or infinite
+                            const float n = -INFINITY;
+                            if (z[sb][nt][0] == n) w0 = 0.0f; else bacc[nt][j][0] = fmaf(p[nt][0], r0.y, bacc[nt][j][0]);
+                            if (z[sb][nt][1] == n) w1 = 0.0f; else bacc[nt][j][1] = fmaf(p[nt][1], r0.y, bacc[nt][j][1]);
+                            if (z[sb][nt][2] == n) w2 = 0.0f; else bacc[nt][j][0] = fmaf(p[nt][2], r1.y, bacc[nt][j][0]);
+                            if (z[sb][nt][3] == n) w3 = 0.0f; else bacc[nt][j][1] = fmaf(p[nt][3], r1.y, bacc[nt][j][1]);
                         }
                         pb[nt][0] = transpose8x8(pack_h2(w0, w1));
                         pb[nt][1] = transpose8x8(pack_h2(w2, w3));
-                        bacc[nt][j][0] += d0 + d2;
-                        bacc[nt][j][1] += d1 + d3;
                     }
                     // two tokens' nibbles side by side: low halves hold elements 0, 2, 4, 6, high halves 1, 3, 5, 7
                     const uint32_t u0 = __byte_perm(vw[0][j], vw[1][j], 0x5410);
@@ -600,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
 
         // ---- merge the warps ----
-        // o[nt][4j + i][e]: dim 64j + 8g + 2i + (e >> 1), column 8nt + 2t + (e & 1)
+        // o[nt][4j + i][e]: dim 64j + 8g + 2i + (e >> 1), column 8nt + 2t + (e & 1), in units of 2^-24
+        // (odd i: 2^-20)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -612,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     for (int j = 0; j < NG; ++j) bacc[nt][j][e] += __shfl_xor_sync(kFull, bacc[nt][j][e], x);
                 }
                 if (g == 0) {
-                    sm_m[warp * NC + nt * 8 + 2 * t + e] = m[nt][e];
+                    sm_m[warp * NC + nt * 8 + 2 * t + e] = me[nt][e];
                     sm_l[warp * NC + nt * 8 + 2 * t + e] = l[nt][e];
                 }
             }
@@ -622,45 +651,37 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int col = nt * 8 + 2 * t + e;
-                float M = -INFINITY;
+                float M = kNone;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i * NC + col]);
-                const float wt = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - M);
+                const float wt = ex2(me[nt][e] - M);
                 float* dst = merge + (warp * NC + col) * S::kCol + 8 * g;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    const float s1 = 16777216.0f / f[j], bb = bacc[nt][j][e];
                     float y[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float sc = (i & 1) ? s1 * 0.0625f : s1;
-                        y[2 * i] = wt * fmaf(o[nt][j * 4 + i][e], sc, bb);
-                        y[2 * i + 1] = wt * fmaf(o[nt][j * 4 + i][e + 2], sc, bb);
+                        const float sc = (i & 1) ? 1048576.0f : 16777216.0f;
+                        y[2 * i] = wt * fmaf(o[nt][j * 4 + i][e], sc, bacc[nt][j][e]);
+                        y[2 * i + 1] = wt * fmaf(o[nt][j * 4 + i][e + 2], sc, bacc[nt][j][e]);
                     }
-                    if (wt == 0.0f)  // nothing seen by this warp
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
                     *reinterpret_cast<float4*>(dst + 64 * j) = make_float4(y[0], y[1], y[2], y[3]);
                     *reinterpret_cast<float4*>(dst + 64 * j + 4) = make_float4(y[4], y[5], y[6], y[7]);
                 }
             }
         if (tid < NC) {
-            float M = -INFINITY, L = 0.0f;
+            float M = kNone, L = 0.0f;
             for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i * NC + tid]);
-            for (int i = 0; i < kWarps; ++i) {
-                const float mi = sm_m[i * NC + tid];
-                if (mi != -INFINITY) L += sm_l[i * NC + tid] * ex2(mi - M);
-            }
+            for (int i = 0; i < kWarps; ++i) L += sm_l[i * NC + tid] * ex2(sm_m[i * NC + tid] - M);
             sm_w[tid] = M;
             sm_w[NC + tid] = L;
         }
         __syncthreads();
 
-        const int64_t seg1 = wk.seg0 + wk.s.per;
-        const int cta0 = (int)(wk.seg0 / wk.quota), cta1 = (int)((seg1 - 1) / wk.quota);
-        // writes columns' results; o4(col, dim) gives four sums, M and L the column's statistics
+        const int cta0 = (int)quot(wk.seg0, wk.quota), cta1 = (int)quot(wk.seg0 + wk.s.per - 1, wk.quota);
+        // writes four sums of a column, whose statistics are in sm_w
         auto put = [&](int col, int dim, float4 x) {
-            const int i = (c0 + col) / a.G, hq = wk.h * a.G + (c0 + col) - i * a.G;
+            const int i = (int)a.by_g.div(c0 + col), hq = wk.h * a.G + (c0 + col) - i * a.G;
             const float L = sm_w[NC + col];
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
@@ -700,16 +721,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 auto part = [&](int p) {  // part p: the segment's start lies in CTA cta0's second slot
                     return a.part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * S::kSlot;
                 };
-                // per column: the largest m, then the sum of l, by one warp each
+                // per column: the largest bound, then the sum of l, by one warp each
                 for (int col = warp; col < NC; col += kWarps) {
-                    float M = -INFINITY, L = 0.0f;
+                    float M = kNone, L = 0.0f;
                     for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(part(p) + col));
 #pragma unroll
                     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-                    for (int p = lane; p < parts; p += 32) {
-                        const float mi = __ldcg(part(p) + col);
-                        if (mi != -INFINITY) L += __ldcg(part(p) + NC + col) * ex2(mi - M);
-                    }
+                    for (int p = lane; p < parts; p += 32)
+                        L += __ldcg(part(p) + NC + col) * ex2(__ldcg(part(p) + col) - M);
 #pragma unroll
                     for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
                     if (lane == 0) sm_w[col] = M, sm_w[NC + col] = L;
@@ -719,18 +738,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
                     const float M = sm_w[col];
                     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
                     for (int p = 0; p < parts; ++p) {
-                        const float mi = __ldcg(part(p) + col);
                         const float4 q = __ldcg(reinterpret_cast<const float4*>(part(p) + 2 * NC + col * D + dim));
-                        const float wt = mi == -INFINITY ? 0.0f : ex2(mi - M);
+                        const float wt = ex2(__ldcg(part(p) + col) - M);
                         y.x = fmaf(wt, q.x, y.x), y.y = fmaf(wt, q.y, y.y), y.z = fmaf(wt, q.z, y.z), y.w = fmaf(wt, q.w, y.w);
                     }
                     put(col, dim, y);
                 }
             }
         }
-        __syncthreads();  // merge and sm_* are free again
+        {
+            Walk x = wk;
+            x.template next<SB>(a, NC);
+            __syncthreads();  // merge, sm_* and the walk are free again
+            if (lane == 0) wk = x;
+            __syncwarp();
+        }
     }
     // a warp that gave up lets the copies already issued land before the CTA can exit
     if (dead)

@@ -270,6 +270,7 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.kv_len = p->kv_len;
     a.q_start = p->q_start;
     a.B = p->batch, a.n_q = p->n_q, a.Hq = p->n_heads, a.G = p->n_heads / cache->n_kv_heads, a.max_pages = p->max_pages;
+    a.by_g = FastDiv((uint32_t)a.G);
     a.T = p->q_start ? 0 : p->n_q / p->batch;
     a.causal = p->causal;
     // a window no shorter than any sequence hides nothing

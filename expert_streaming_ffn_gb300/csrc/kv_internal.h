@@ -65,6 +65,7 @@ struct KvAttend {
     const int32_t* kv_len;
     const int32_t* q_start;  // or null
     int B, n_q, Hq, G, max_pages;
+    FastDiv by_g{1};  // / G
     int T;  // tokens per sequence when q_start is null
     int causal, window;
     float scale_log2;  // scale * log2(e)
