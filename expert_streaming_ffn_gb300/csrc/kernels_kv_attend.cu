@@ -38,6 +38,9 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kChunkBytes = 4608;
 constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it moves (log2)
 constexpr float kNone = -3e38f;  // the bound before any score
+constexpr int kPieceCost = 24;  // what a piece costs beside its blocks, in blocks
+
+constexpr int kPlanBytes = 2304;  // of the schedule and a flag, at least
 
 template <int D, int NT>
 struct Shape {
@@ -49,9 +52,11 @@ struct Shape {
     static constexpr int kStages = kCtas == 2 ? 2 : D == 256 && NT == 2 ? 2 : 3;
     static constexpr int kCol = D + 4;  // floats of a column in the merge buffer
     static constexpr int kRing = kWarps * kStages * kChunkBytes;
-    static constexpr int kMerge = kWarps * NC * kCol * 4;
-    static constexpr int kSmall = (4 * kWarps * NC + 2 * NC) * 4;
-    static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + 96 + kWarps * 2 * 112;
+    static constexpr int kMaxGrid = 160 * kCtas;
+    // the merge buffer also holds the statistics of a split segment's parts
+    static constexpr int kMerge = kWarps * kCol > 2 * kMaxGrid ? kWarps * NC * kCol * 4 : 2 * kMaxGrid * NC * 4;
+    static constexpr int kSmall = (4 * kWarps * NC + 2 * NC + 4 * NC + 2 * (NG + 1) * NC + 2 * NT * W * 128) * 4;
+    static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + kPlanBytes;
     static constexpr int kSlot = NC * (D + 2);  // floats of one partial result: m[NC], l[NC], o[NC][D]
 };
 
@@ -147,67 +152,221 @@ __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
     return s;
 }
 
-// Units of a segment: its blocks, rounded up to whole ranges where every range is one CTA's and one segment's.
-__device__ __forceinline__ int64_t units_of(const KvAttend& a, const Seq& s, int64_t pad) {
-    return (pad ? quot(s.per + pad - 1, pad) * pad : s.per) * a.c.H * s.nct;
-}
-
-// A walk over the CTA's range of units, piece by piece (a piece: the part of
-// one segment that the range holds). Kept in shared memory, one copy per warp
-// for its loads and one for its arithmetic: they are looked at between pieces
-// only, and the registers are needed for sums.
-struct Walk {
-    int64_t w, w1, ex;    // position, end, and where sequence b's units start
-    int64_t seg0, quota;  // where the piece's segment starts; units of a CTA
-    int64_t pad;          // quota where segments are padded to it, else 0
-    Seq s;
-    int b, h, ct, blk0, nb;  // sequence, kv head, column tile, first block (of the segment) and blocks
-    int rot;                 // chunks before this piece, mod kWarps
-
-    __device__ __forceinline__ bool done() const { return w >= w1; }
-    __device__ __forceinline__ void piece(const KvAttend& a, int NC) {
-        if (w >= w1) return;
-        int64_t u = units_of(a, s, pad);
-        while (w >= ex + u) {
-            ex += u;
-            s = seq_of(a, ++b, NC);
-            u = units_of(a, s, pad);
-        }
-        const int64_t per = pad ? quot(s.per + pad - 1, pad) * pad : s.per;
-        const int64_t seg = quot(w - ex, per);
-        blk0 = (int)(w - ex - seg * per);
-        h = (int)((uint32_t)seg / (uint32_t)s.nct);
-        ct = (int)((uint32_t)seg - (uint32_t)h * (uint32_t)s.nct);
-        seg0 = w - blk0;
-        nb = (int)min((int64_t)(s.per - blk0), w1 - w);
-    }
-    template <int SB>
-    __device__ __forceinline__ void next(const KvAttend& a, int NC) {
-        rot = (rot + (nb + SB - 1) / SB) % kWarps;
-        w = pad ? w1 : w + nb;
-        piece(a, NC);
+// How the segments' blocks are cut into the CTAs' ranges. Either (pad) a range
+// holds one segment's blocks at most, a segment taking whole ranges; or segments
+// lie end to end, each with kPieceCost units before its blocks for what a piece
+// costs beside them.
+struct Cut {
+    int64_t quota, total;
+    int lead;  // units before a segment's blocks
+    bool pad;
+    __device__ __forceinline__ int64_t seg_units(int per) const {
+        return pad ? quot(per + quota - 1, quota) * quota : per + lead;
     }
 };
 
-// Exclusive and total sums of u over the block's threads; scratch: kWarps words.
-__device__ __forceinline__ int64_t block_scan(int64_t u, int64_t* scratch, int warp, int lane, int64_t* total) {
-    int64_t inc = u;
+// A piece: the part of a segment that a CTA's range holds.
+struct Piece {
+    int first, n, len;   // the sequence: first q row, new tokens, keys
+    int b, h, c0;        // sequence, kv head, first column
+    int blk, nb;         // first block (of the sequence) and blocks; nb = 0 where there are no keys
+    int cta0, parts;     // the segment's first CTA, and how many share it
+    int start;           // 1: the piece holds the segment's first block
+    int rot;             // which warp takes its first chunk
+    int all_lo, all_hi;  // the keys that every column sees
+};
+
+constexpr int kPieces = 32;  // pieces of one list
+
+// What a block knows of the schedule, in shared memory.
+struct Plan {
+    int64_t scan[kWarps];
+    int2 most[kWarps];
+    Cut cut;
+    int64_t w, w1;     // the CTA's range
+    int64_t ex;        // where sequence b's units start
+    int b, seg;        // the next piece's sequence, and its segment there
+    Seq s;             // that sequence
+    int count, more;   // pieces of the list; whether another list follows
+    Piece piece[kPieces];
+};
+
+static_assert(sizeof(Plan) + 4 <= kPlanBytes);
+
+// Cuts U blocks in Sg segments of at most `most` blocks into ranges for the grid.
+__device__ __forceinline__ Cut make_cut(const KvAttend& a, int64_t U, int64_t Sg, int most) {
+    Cut c;
+    const int grid = gridDim.x;
+    c.lead = kPieceCost;
+    c.total = U + Sg * kPieceCost;
+    c.quota = quot(c.total + grid - 1, grid);
+    c.pad = false;
+    if (Sg <= grid) {  // fewer segments than CTAs: the same number of whole CTAs for each, unless that is too uneven
+        const int per = (int)((uint32_t)grid / (uint32_t)max((int)Sg, 1));
+        const int each = max(a.min_units, (int)((uint32_t)(most + per - 1) / (uint32_t)per));
+        if (each <= max((int64_t)a.min_units, c.quota + kPieceCost)) c.quota = each, c.lead = 0, c.pad = true;
+    }
+    return c;
+}
+
+template <class I>
+__device__ __forceinline__ I warp_inclusive(I x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += x;
+        const I y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
     }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    int64_t ex = inc - u, sum = 0;
+    return x;
+}
+
+// The CTA's range, and the sequence and segment that it starts in. False: the
+// range is empty. Up to 32 sequences, each warp works it out by itself and
+// warp 0 writes it down; the block is not synchronised.
+template <int NC>
+__device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, int warp, int lane) {
+    const int H = a.c.H;
+    if (a.B <= 32) {
+        Seq s{};
+        if (lane < a.B) s = seq_of(a, lane, NC);
+        const int64_t segs = (int64_t)H * s.nct;
+        int64_t U = segs * s.per, Sg = segs;
+        const int most = __reduce_max_sync(kFull, s.nct ? s.per : 0);
+        if (a.B > 1) {
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) ex += scratch[i];
-        sum += scratch[i];
+            for (int o = 16; o; o >>= 1) {
+                U += __shfl_xor_sync(kFull, U, o);
+                Sg += __shfl_xor_sync(kFull, Sg, o);
+            }
+        } else {
+            U = __shfl_sync(kFull, U, 0), Sg = __shfl_sync(kFull, Sg, 0);
+        }
+        Cut c = make_cut(a, U, Sg, most);
+        const int64_t v = lane < a.B ? c.seg_units(s.per) * segs : 0;
+        const int64_t inc = a.B > 1 ? warp_inclusive(v, lane) : v, e = inc - v;
+        c.total = __shfl_sync(kFull, inc, a.B > 1 ? 31 : 0);
+        const int64_t w = c.quota * blockIdx.x;
+        if (w >= c.total) return false;
+        if (warp == 0 && e <= w && w < e + v) {
+            P.cut = c;
+            P.w = w;
+            P.w1 = min(c.total, w + c.quota);
+            P.ex = e;
+            P.b = lane;
+            P.seg = (int)quot(w - e, c.seg_units(s.per));
+            P.s = s;
+        }
+        __syncwarp();
+        return true;
     }
-    *total = sum;
-    return ex;
+    int64_t U = 0, Sg = 0;
+    int most = 0;
+    for (int b = tid; b < a.B; b += kThreads) {
+        const Seq s = seq_of(a, b, NC);
+        const int64_t segs = (int64_t)H * s.nct;
+        U += segs * s.per, Sg += segs;
+        if (s.nct) most = max(most, s.per);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        U += __shfl_xor_sync(kFull, U, o);
+        Sg += __shfl_xor_sync(kFull, Sg, o);
+    }
+    most = __reduce_max_sync(kFull, most);
+    if (lane == 0) P.scan[warp] = U, P.most[warp] = make_int2(most, (int)min(Sg, (int64_t)1 << 30));
+    __syncthreads();
+    U = 0, Sg = 0, most = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) U += P.scan[i], most = max(most, P.most[i].x), Sg += P.most[i].y;
+    Cut c = make_cut(a, U, Sg, most);
+    const int64_t w = c.quota * blockIdx.x;
+    int64_t run = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + tid;
+        Seq s{};
+        if (b < a.B) s = seq_of(a, b, NC);
+        const int64_t v = b < a.B ? c.seg_units(s.per) * H * s.nct : 0;
+        const int64_t inc = warp_inclusive(v, lane);
+        __syncthreads();
+        if (lane == 31) P.scan[warp] = inc;
+        __syncthreads();
+        int64_t e = run + inc - v;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) e += P.scan[i];
+            run += P.scan[i];
+        }
+        if (e <= w && w < e + v) {
+            P.ex = e;
+            P.b = b;
+            P.seg = (int)quot(w - e, c.seg_units(s.per));
+            P.s = s;
+        }
+    }
+    if (w >= run) return false;
+    if (tid == 0) {
+        c.total = run;
+        P.cut = c;
+        P.w = w;
+        P.w1 = min(run, w + c.quota);
+    }
+    __syncthreads();
+    return true;
+}
+
+// The next list of pieces, by one warp: lane p looks at the p-th segment from the list's first.
+template <int NC, int SB>
+__device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane) {
+    const Cut c = P.cut;
+    int b = P.b;
+    int64_t e = P.ex, seg = (int64_t)P.seg + lane;
+    Seq s = P.s;
+    int64_t u = c.seg_units(s.per), n = (int64_t)a.c.H * s.nct;
+    while (seg >= n && b + 1 < a.B && e + n * u < P.w1) {
+        seg -= n;
+        e += n * u;
+        s = seq_of(a, ++b, NC);
+        u = c.seg_units(s.per);
+        n = (int64_t)a.c.H * s.nct;
+    }
+    const int64_t at = e + seg * u + c.lead;  // the segment's first block
+    const bool in = seg < n && at - c.lead < P.w1;
+    const int lo = in ? (int)max((int64_t)0, min(P.w - at, (int64_t)s.per)) : 0;
+    const int hi = in ? (int)max((int64_t)0, min(P.w1 - at, (int64_t)s.per)) : 0;
+    const bool some = hi > lo;
+    const unsigned who = __ballot_sync(kFull, some);
+    const int nb = some && s.len > 0 ? hi - lo : 0;
+    int chunks = (nb + SB - 1) / SB, rot = chunks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, rot, o);
+        if (lane >= o) rot += x;
+    }
+    if (some) {
+        Piece p;
+        p.first = s.first, p.n = s.n, p.len = s.len;
+        p.b = b;
+        p.h = (int)((uint32_t)seg / (uint32_t)s.nct);
+        p.c0 = (int)((uint32_t)seg - (uint32_t)p.h * (uint32_t)s.nct) * NC;
+        p.blk = s.lo_blk + lo;
+        p.nb = nb;
+        p.cta0 = (int)quot(at, c.quota);
+        p.parts = (int)quot(at + s.per - 1, c.quota) - p.cta0 + 1;
+        p.start = lo == 0;
+        p.rot = (rot - chunks) & (kWarps - 1);
+        const int pos0 = s.len - s.n, first = pos0 + (int)a.by_g.div(p.c0);
+        const int last = pos0 + (int)a.by_g.div(min(p.c0 + NC, s.n * a.G) - 1);
+        p.all_hi = a.causal ? min(s.len, first + 1) : s.len;
+        p.all_lo = a.window && last >= a.window ? last - a.window + 1 : 0;
+        P.piece[__popc(who & ((1u << lane) - 1))] = p;
+    }
+    // the next list starts at the segment behind lane 31's
+    const bool more = __shfl_sync(kFull, in && at + s.per < P.w1, 31);
+    __syncwarp();
+    if (lane == 31) {
+        P.b = b, P.ex = e, P.seg = (int)seg + 1, P.s = s;
+        P.more = more;
+    }
+    if (lane == 0) P.count = __popc(who);
 }
 
 template <int D, int NT, class T>
@@ -218,106 +377,53 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* ring = smem;
     float* merge = reinterpret_cast<float*>(smem + S::kRing);
-    float* sm_m = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [kWarps][NC]
-    float* sm_l = sm_m + kWarps * NC;
-    float* sm_w = sm_l + kWarps * NC;  // [2][NC]: the merged m and l
-    int2* sm_see = reinterpret_cast<int2*>(sm_w + 2 * NC);  // [kWarps][NC]: the keys [x, y) that a column sees
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_see + kWarps * NC);
-    int64_t* scan = reinterpret_cast<int64_t*>(bars + kWarps * kStages);  // kWarps sums, then the start: flat, sequence
-    Walk* walks = reinterpret_cast<Walk*>(scan + kWarps + 2);              // [kWarps][2]
-    int* flag = reinterpret_cast<int*>(walks + 2 * kWarps);
+    float* sm_stat = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [2][2][kWarps][NC]: by piece parity, bounds and sums
+    float* sm_w = sm_stat + 4 * kWarps * NC;  // [2][NC]: the merged bound and sum
+    int2* sm_see = reinterpret_cast<int2*>(sm_w + 2 * NC);            // [2][NC]: the keys [x, y) that a column sees
+    float* sm_x = reinterpret_cast<float*>(sm_see + 2 * NC);           // [2][NG + 1][NC]: X_g, then cz (below)
+    uint32_t* sm_q = reinterpret_cast<uint32_t*>(sm_x + 2 * (NG + 1) * NC);  // [2][NT][W][32][4]: query fragments
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_q + 2 * NT * W * 128);
+    Plan& plan = *reinterpret_cast<Plan*>(bars + kWarps * kStages);
+    int* flag = reinterpret_cast<int*>(&plan + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (lane < kStages) ptx::mbar_init(bars + warp * kStages + lane, 1);
     ptx::fence_mbar_init();
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
+    if (!make_plan<NC>(a, plan, tid, warp, lane)) return;
 
-    // ---- the CTA's range ----
-    Walk& wk = walks[2 * warp];
-    Walk& lw = walks[2 * warp + 1];
-    {
-        const bool one = a.B <= kThreads;
-        int64_t total = 0, padded = 0, ex = 0, ex_pad = 0, u = 0, u_pad = 0;
-        for (int base = 0; base < a.B; base += kThreads) {
-            const int b = base + tid;
-            u = u_pad = 0;
-            if (b < a.B) {
-                const Seq s = seq_of(a, b, NC);
-                u = units_of(a, s, 0);
-                u_pad = units_of(a, s, a.min_units);
-            }
-            int64_t sum, sum_pad;
-            ex = block_scan(u, scan, warp, lane, &sum);
-            ex_pad = block_scan(u_pad, scan, warp, lane, &sum_pad);
-            total += sum, padded += sum_pad;
-        }
-        // few short segments: a CTA each, or several where one has more than min_units blocks; else equal ranges
-        const bool pad = padded <= (int64_t)a.min_units * gridDim.x;
-        const int64_t quota = pad ? a.min_units : quot(total + gridDim.x - 1, gridDim.x);
-        if (pad) total = padded, ex = ex_pad, u = u_pad;
-        const int64_t w = quota * blockIdx.x;
-        if (w >= total) return;
-        if (!one) {  // again, for the sequence that holds the start
-            int64_t run = 0;
-            for (int base = 0; base < a.B; base += kThreads) {
-                const int b = base + tid;
-                const int64_t v = b < a.B ? units_of(a, seq_of(a, b, NC), pad ? quota : 0) : 0;
-                int64_t sum;
-                const int64_t e = run + block_scan(v, scan, warp, lane, &sum);
-                run += sum;
-                if (e <= w && w < e + v) scan[kWarps] = e, scan[kWarps + 1] = b;
-            }
-        } else if (ex <= w && w < ex + u) {
-            scan[kWarps] = ex, scan[kWarps + 1] = tid;
-        }
-        __syncthreads();
-        Walk x;
-        x.w = w;
-        x.w1 = min(total, w + quota);
-        x.quota = quota;
-        x.pad = pad ? quota : 0;
-        x.ex = scan[kWarps];
-        x.b = (int)scan[kWarps + 1];
-        x.s = seq_of(a, x.b, NC);
-        x.rot = 0;
-        x.piece(a, NC);
-        if (lane < 2) walks[2 * warp + lane] = x;
-        __syncwarp();
-    }
-
-    // ---- loads: this warp's chunks, kStages ahead, and the page of the one after ----
     uint32_t ld_n = 0, use_n = 0;  // chunks issued and used
     uint32_t valid = 0;            // per stage, 4 bits: blocks that were loaded
     bool dead = false;             // a wait expired
+    int parity = 0;
     uint64_t* const mybars = bars + warp * kStages;
     unsigned char* const myring = ring + warp * kStages * kChunkBytes;
-    int ld_c, ld_nb, ld_blk, ld_page = 0;  // next chunk; its piece's blocks and first block; this lane's page
-    const int32_t* ld_table;
-    const uint8_t* ld_head;
-    bool ld_more;
-    auto load_piece = [&]() {
-        ld_more = !lw.done();
-        ld_c = (warp - lw.rot) & (kWarps - 1);
-        ld_nb = lw.s.len > 0 ? lw.nb : 0;
-        ld_blk = lw.s.lo_blk + lw.blk0;
-        ld_table = a.table + (int64_t)lw.b * a.table_stride;
-        ld_head = a.c.pages + (size_t)lw.h * (a.c.P >> 4) * kRec;
-    };
+
+#pragma unroll 1
+  for (;;) {  // lists of pieces
+    if (warp == 0) list_pieces<NC, SB>(a, plan, lane);
+    __syncthreads();
+    const int count = plan.count;
+
+    // ---- loads: this warp's chunks, kStages ahead, and the page of the one after ----
+    int ld_p = -1, ld_c = 0, ld_nb = 0, ld_blk = 0, ld_page = 0;  // piece, next chunk; its blocks and first block; this lane's page
+    const int32_t* ld_table = nullptr;
+    const uint8_t* ld_head = nullptr;
     auto find = [&]() {  // moves on to a piece with a chunk for this warp, and fetches its page id
-        while (ld_more && ld_c * SB >= ld_nb) {
-            Walk x = lw;
-            x.template next<SB>(a, NC);
-            __syncwarp();
-            if (lane == 0) lw = x;
-            __syncwarp();
-            load_piece();
+        while (ld_c * SB >= ld_nb && ++ld_p < count) {
+            const Piece& p = plan.piece[ld_p];
+            ld_c = (warp - p.rot) & (kWarps - 1);
+            ld_nb = p.nb;
+            ld_blk = p.blk;
+            ld_table = a.table + (int64_t)p.b * a.table_stride;
+            ld_head = a.c.pages + (size_t)p.h * (a.c.P >> 4) * kRec;
         }
         const int i = ld_c * SB + lane;
-        if (ld_more && lane < SB && i < ld_nb) ld_page = __ldg(ld_table + ((ld_blk + i) >> (a.c.page_shift - 4)));
+        if (ld_p < count && lane < SB && i < ld_nb) ld_page = __ldg(ld_table + ((ld_blk + i) >> (a.c.page_shift - 4)));
     };
     auto issue = [&]() {
-        if (!ld_more || dead) return;
+        if (ld_p >= count || dead) return;
         const int st = (int)(ld_n % kStages);
         const int i = ld_c * SB + lane;
         bool ok = lane < SB && i < ld_nb;
@@ -338,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         ld_c += kWarps;
         find();
     };
-    load_piece();
     find();
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue();
@@ -347,78 +452,81 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     // four lanes of a value fragment read rows of both parities (half as many bank conflicts)
     const int pg = g ^ ((g >> 1) & 1);
 
-    uint32_t qf[NT][W][4];
-    float cz[NT][2], X[NT][NG][2];
-
-#pragma unroll 1
-    while (!wk.done()) {
-        const int c0 = wk.ct * NC, len = wk.s.len, nb = len > 0 ? wk.nb : 0, blk0 = wk.s.lo_blk + wk.blk0;
-        const int ncols = min(NC, wk.s.n * a.G - c0);
-        int all_lo, all_hi;  // the keys that every column of the tile sees
-        {
-            const int pos = len - wk.s.n + (int)a.by_g.div(c0 + lane);
-            int hi = a.causal ? min(len, pos + 1) : len, lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-            all_lo = __reduce_max_sync(kFull, lane < ncols ? lo : 0);
-            all_hi = __reduce_min_sync(kFull, lane < ncols ? hi : len);
-            if (lane < NC) sm_see[warp * NC + lane] = make_int2(lo, lane < ncols ? hi : 0);
-            __syncwarp();
-        }
-        // ---- queries: column g of each n-tile, scaled to a largest element in [2^10, 2^11) ----
+    // ---- a piece's queries: fp16 fragments in shared memory, each warp NT of its columns ----
+    // A row is scaled by a power of two to a largest element in [2^10, 2^11), and by the sign
+    // of the scale; pairs 1 and 3 of a word are divided by 16 to meet codes times 16.
+    auto prepare_q = [&](int i, int par) {
+        const Piece& p = plan.piece[i];
+        constexpr int E = D / 32;  // elements of a lane
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int c = nt * 8 + g;
-            uint32_t raw[W][4];
-            const bool in = c < ncols;
-            const int i = (int)a.by_g.div(c0 + c), hq = (c0 + c) - i * a.G;
-            const T* qp =
-                static_cast<const T*>(a.q) + (int64_t)(wk.s.first + i) * a.qt + (int64_t)(wk.h * a.G + hq) * a.qh;
+            const int c = p.c0 + nt * 8 + warp, tk = (int)a.by_g.div(c), hq = c - tk * a.G;
+            const bool in = tk < p.n;
+            uint32_t raw[E / 2] = {};
+            if (in) {
+                const T* qp = static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt +
+                              (int64_t)(p.h * a.G + hq) * a.qh + lane * E;
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) raw[k] = __ldg(reinterpret_cast<const unsigned*>(qp) + k);
+            }
             float top = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const int w = t * W + k;
-                const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(qp + (w % NG) * 64 + (w / NG) * 8))
-                                   : make_uint4(0, 0, 0, 0);
-                raw[k][0] = v.x, raw[k][1] = v.y, raw[k][2] = v.z, raw[k][3] = v.w;
+            for (int k = 0; k < E / 2; ++k) {
+                const float2 f = unpack2<T>(raw[k]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack2<T>(raw[k][e]);
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            // non-negative floats compare as integers
+            top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
             int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
             ex = top == 0.0f || ex == 128 ? 10 : min(max(ex, -100), 110);
-            const float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
-            float xs[NG] = {};
+            float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
+            if (a.scale_log2 <= 0.0f) f = a.scale_log2 < 0.0f ? -f : 0.0f;
+            float xs = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = unpack2<T>(raw[k][e]);
-                    const float sc = (e & 1) ? f * 0.0625f : f;  // pairs 1 and 3 meet codes times 16
-                    const uint32_t p = pack_h2(v.x * sc, v.y * sc);
-                    qf[nt][k][e] = p;
-                    const float2 r = affine_of(p);
-                    xs[k % NG] += (r.x + r.y) * ((e & 1) ? 16.0f : 1.0f);
-                }
+            for (int k = 0; k < E / 2; ++k) {
+                const int dim = lane * E + 2 * k, j = dim >> 6, w = ((dim & 63) >> 3) * NG + j, e = (dim & 7) >> 1;
+                const float2 v = unpack2<T>(raw[k]);
+                const float sc = (e & 1) ? f * 0.0625f : f;
+                const uint32_t h = pack_h2(v.x * sc, v.y * sc);
+                const float2 y = affine_of(h);
+                xs += (y.x + y.y) * ((e & 1) ? 16.0f : 1.0f);
+                // word w = t * W + k of the row: fragment k of lane (g = column, t)
+                sm_q[((par * NT + nt) * W + w % W) * 128 + (warp * 4 + w / W) * 4 + e] = h;
             }
-            const float back = a.scale_log2 * __uint_as_float((uint32_t)(127 - 10 + ex) << 23) * 16777216.0f;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                xs[j] += __shfl_xor_sync(kFull, xs[j], 1);
-                xs[j] += __shfl_xor_sync(kFull, xs[j], 2);
-                X[nt][j][0] = __shfl_sync(kFull, xs[j], 8 * t) * 0x1p-24f;
-                X[nt][j][1] = __shfl_sync(kFull, xs[j], 8 * t + 4) * 0x1p-24f;
+            for (int o = 32 / NG / 2; o; o >>= 1) xs += __shfl_xor_sync(kFull, xs, o);
+            float* sx = sm_x + par * (NG + 1) * NC + nt * 8 + warp;
+            if (lane % (32 / NG) == 0) sx[lane / (32 / NG) * NC] = xs * 0x1p-24f;
+            if (lane == 0) {
+                sx[NG * NC] = a.scale_log2 == 0.0f ? 1.0f
+                                                   : fabsf(a.scale_log2) *
+                                                         __uint_as_float((uint32_t)(127 - 10 + ex) << 23) * 16777216.0f;
+                const int pos = p.len - p.n + tk;
+                sm_see[par * NC + nt * 8 + warp] =
+                    make_int2(a.window && pos >= a.window ? pos - a.window + 1 : 0,
+                              in ? (a.causal ? min(p.len, pos + 1) : p.len) : 0);
             }
-            cz[nt][0] = __shfl_sync(kFull, back, 8 * t);
-            cz[nt][1] = __shfl_sync(kFull, back, 8 * t + 4);
+        }
+    };
+    if (count) prepare_q(0, parity);
+    __syncthreads();
+
+#pragma unroll 1
+    for (int ip = 0; ip < count; ++ip, parity ^= 1) {
+        const Piece& pc = plan.piece[ip];
+        const int nb = pc.nb, blk0 = pc.blk;
+        const float* const sx = sm_x + parity * (NG + 1) * NC + 2 * t;
+        const uint32_t sq = ptx::smem_addr(sm_q + parity * NT * W * 128 + lane * 4);
+        float cz[NT][2];  // scores are cz times the sums below, cz > 0
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 v = *reinterpret_cast<const float2*>(sx + NG * NC + nt * 8);
+            cz[nt][0] = v.x, cz[nt][1] = v.y;
         }
 
-        // The sums hold 2^(z - me): me = m - lf, m within kLazy of the largest z so far, 2^lf the
-        // factor that keeps weight times scale within fp16's range. lim: the largest scale 2^lf serves.
+        // The sums hold 2^(cz z - me): me = m - lf, m within kLazy of the largest cz z so far, 2^lf the
+        // factor that keeps weight times scale within fp16's range. thr: the z that passes the bound; lim: the largest
+        // scale that 2^lf serves.
         float o[NT][D / 16][4], bacc[NT][NG][2], thr[NT][2], me[NT][2], l[NT][2], lim = 0.0f, lf = 24.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -433,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
 
 #pragma unroll 1
-        for (int c = (warp - wk.rot) & (kWarps - 1); c * SB < nb; c += kWarps) {
+        for (int c = (warp - pc.rot) & (kWarps - 1); c * SB < nb; c += kWarps) {
             const int st = (int)(use_n % kStages);
             if (!dead && !ptx::mbar_wait_bounded(mybars + st, (use_n / kStages) & 1, nullptr)) {
                 dead = true;
@@ -444,14 +552,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
             const uint32_t base = ptx::smem_addr(myring) + st * kChunkBytes;
             const unsigned v = (valid >> (4 * st)) & 15u;
             const int tok0 = (blk0 + c * SB) << 4;
-            const bool whole = v == (1u << SB) - 1 && tok0 >= all_lo && tok0 + 16 * SB <= all_hi;
+            const bool whole = v == (1u << SB) - 1 && tok0 >= pc.all_lo && tok0 + 16 * SB <= pc.all_hi;
 
+            // the query fragments and X come from shared memory once a chunk: held in registers they
+            // would not leave room for two CTAs
+            uint4 qf[NT][W];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < W; ++k) qf[nt][k] = ptx::lds_u4(sq + (nt * W + k) * 512);
             float z[SB][NT][4];
             uint32_t va[SB][2][NG];  // value affine words of tokens pi(g), pi(g) + 8
 #pragma unroll
             for (int sb = 0; sb < SB; ++sb) {
                 const uint32_t rec = base + sb * kRec;
                 uint32_t kw[2][W], ka[2][NG];
+                float2 X[NT][NG];
                 lds_words<W>(rec + pg * (D / 2) + t * W * 4, kw[0]);
                 lds_words<W>(rec + (pg + 8) * (D / 2) + t * W * 4, kw[1]);
                 lds_words<NG>(rec + kv_k_affine(D) + pg * NG * 4, ka[0]);
@@ -471,11 +587,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma(acc[k % NG][nt], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u,
-                            qf[nt][k][0], qf[nt][k][1]);
+                            qf[nt][k].x, qf[nt][k].y);
                         mma(acc[k % NG][nt], y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u,
-                            qf[nt][k][2], qf[nt][k][3]);
+                            qf[nt][k].z, qf[nt][k].w);
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) X[nt][j] = *reinterpret_cast<const float2*>(sx + j * NC + nt * 8);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -485,16 +605,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     const float2 r0 = affine_of(ka[0][j]), r1 = affine_of(ka[1][j]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        z[sb][nt][0] = fmaf(r0.x, acc[j][nt][0], fmaf(r0.y, X[nt][j][0], z[sb][nt][0]));
-                        z[sb][nt][1] = fmaf(r0.x, acc[j][nt][1], fmaf(r0.y, X[nt][j][1], z[sb][nt][1]));
-                        z[sb][nt][2] = fmaf(r1.x, acc[j][nt][2], fmaf(r1.y, X[nt][j][0], z[sb][nt][2]));
-                        z[sb][nt][3] = fmaf(r1.x, acc[j][nt][3], fmaf(r1.y, X[nt][j][1], z[sb][nt][3]));
+                        z[sb][nt][0] = fmaf(r0.x, acc[j][nt][0], fmaf(r0.y, X[nt][j].x, z[sb][nt][0]));
+                        z[sb][nt][1] = fmaf(r0.x, acc[j][nt][1], fmaf(r0.y, X[nt][j].y, z[sb][nt][1]));
+                        z[sb][nt][2] = fmaf(r1.x, acc[j][nt][2], fmaf(r1.y, X[nt][j].x, z[sb][nt][2]));
+                        z[sb][nt][3] = fmaf(r1.x, acc[j][nt][3], fmaf(r1.y, X[nt][j].y, z[sb][nt][3]));
                     }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[sb][nt][e] *= cz[nt][e & 1];
             }
             if (!whole) {
 #pragma unroll
@@ -506,13 +622,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int k = tk + (e & 2) * 4;
-                            const int2 see = sm_see[warp * NC + nt * 8 + 2 * t + (e & 1)];
+                            const int2 see = sm_see[parity * NC + nt * 8 + 2 * t + (e & 1)];
                             if (!in || k < see.x || k >= see.y) z[sb][nt][e] = -INFINITY;
                         }
                     // places past the sequence's end hold anything: their scale must not move lf
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        if (!in || tk + 8 * r >= len)
+                        if (!in || tk + 8 * r >= pc.len)
 #pragma unroll
                             for (int j = 0; j < NG; ++j) va[sb][r][j] = 0;
                 }
@@ -551,13 +667,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = thr[nt][e] - kLazy;
+                        float mx = kNone;
 #pragma unroll
                         for (int sb = 0; sb < SB; ++sb) mx = fmaxf(mx, fmaxf(z[sb][nt][e], z[sb][nt][e + 2]));
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+                        mx = fmaxf(thr[nt][e] == kNone ? kNone : fmaf(thr[nt][e], cz[nt][e], -kLazy),
+                                   mx == kNone ? kNone : mx * cz[nt][e]);
                         const float sc = ex2(me[nt][e] - (mx - lf));
-                        thr[nt][e] = mx + kLazy;
+                        thr[nt][e] = mx == kNone ? kNone : (mx + kLazy) / cz[nt][e];
                         me[nt][e] = mx - lf;
                         l[nt][e] *= sc;
 #pragma unroll
@@ -581,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[nt][e] = ex2(z[sb][nt][e] - me[nt][e & 1]);
+                        p[nt][e] = ex2(fmaf(z[sb][nt][e], cz[nt][e & 1], -me[nt][e & 1]));
                         l[nt][e & 1] += p[nt][e];
                     }
 #pragma unroll
@@ -627,6 +745,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
             issue();
         }
 
+        if (ip + 1 < count) prepare_q(ip + 1, parity ^ 1);
+        float* sm_m = sm_stat + parity * 2 * kWarps * NC;  // [kWarps][NC]
+        float* sm_l = sm_m + kWarps * NC;
         // ---- merge the warps ----
         // o[nt][4j + i][e]: dim 64j + 8g + 2i + (e >> 1), column 8nt + 2t + (e & 1), in units of 2^-24
         // (odd i: 2^-20)
@@ -678,19 +799,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
         __syncthreads();
 
-        const int cta0 = (int)quot(wk.seg0, wk.quota), cta1 = (int)quot(wk.seg0 + wk.s.per - 1, wk.quota);
+        const int cta0 = pc.cta0, parts = pc.parts, c0 = pc.c0, ncols = min(NC, pc.n * a.G - c0);
         // writes four sums of a column, whose statistics are in sm_w
         auto put = [&](int col, int dim, float4 x) {
-            const int i = (int)a.by_g.div(c0 + col), hq = wk.h * a.G + (c0 + col) - i * a.G;
+            const int i = (int)a.by_g.div(c0 + col), hq = pc.h * a.G + (c0 + col) - i * a.G;
             const float L = sm_w[NC + col];
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-            store4(static_cast<T*>(a.out) + (int64_t)(wk.s.first + i) * a.ot + (int64_t)hq * a.oh + dim, x);
+            store4(static_cast<T*>(a.out) + (int64_t)(pc.first + i) * a.ot + (int64_t)hq * a.oh + dim, x);
             if (a.lse && dim == 0)
-                a.lse[(int64_t)(wk.s.first + i) * a.Hq + hq] =
+                a.lse[(int64_t)(pc.first + i) * a.Hq + hq] =
                     L == 0.0f ? -INFINITY : 0.6931471805599453f * (sm_w[col] + log2f(L));
         };
-        float* slot = a.part + (size_t)(2 * blockIdx.x + (wk.blk0 == 0 ? 1 : 0)) * S::kSlot;
+        float* slot = a.part + (size_t)(2 * blockIdx.x + pc.start) * S::kSlot;
         for (int x = tid; x < ncols * (D / 4); x += kThreads) {
             const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
             float4 y = *reinterpret_cast<const float4*>(merge + col * S::kCol + dim);
@@ -699,17 +820,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 const float4 q = *reinterpret_cast<const float4*>(merge + (i * NC + col) * S::kCol + dim);
                 y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
             }
-            if (cta0 == cta1)
+            if (parts == 1)
                 put(col, dim, y);
             else
                 __stcg(reinterpret_cast<float4*>(slot + 2 * NC + col * D + dim), y);
         }
-        if (cta0 != cta1) {
+        if (parts > 1) {
             // ---- a segment cut between CTAs: the last to finish joins the parts ----
             if (tid < 2 * NC) __stcg(slot + tid, sm_w[tid]);
             __threadfence();
             __syncthreads();
-            const int parts = cta1 - cta0 + 1;
             if (tid == 0) {
                 const unsigned old = atomicAdd(a.counters + cta0, 1u);
                 *flag = old == (unsigned)parts - 1;
@@ -721,14 +841,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 auto part = [&](int p) {  // part p: the segment's start lies in CTA cta0's second slot
                     return a.part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * S::kSlot;
                 };
-                // per column: the largest bound, then the sum of l, by one warp each
+                // every part's statistics at once, then its columns' weights in their place
+                float* st = merge;  // [parts][2][NC]
+                for (int x = tid; x < parts * 2 * NC; x += kThreads) st[x] = __ldcg(part(x / (2 * NC)) + x % (2 * NC));
+                __syncthreads();
                 for (int col = warp; col < NC; col += kWarps) {
                     float M = kNone, L = 0.0f;
-                    for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(part(p) + col));
+                    for (int p = lane; p < parts; p += 32) M = fmaxf(M, st[p * 2 * NC + col]);
 #pragma unroll
                     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-                    for (int p = lane; p < parts; p += 32)
-                        L += __ldcg(part(p) + NC + col) * ex2(__ldcg(part(p) + col) - M);
+                    for (int p = lane; p < parts; p += 32) {
+                        const float wt = ex2(st[p * 2 * NC + col] - M);
+                        L += st[p * 2 * NC + NC + col] * wt;
+                        st[p * 2 * NC + col] = wt;
+                    }
 #pragma unroll
                     for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
                     if (lane == 0) sm_w[col] = M, sm_w[NC + col] = L;
@@ -736,26 +862,30 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 __syncthreads();
                 for (int x = tid; x < ncols * (D / 4); x += kThreads) {
                     const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
-                    const float M = sm_w[col];
                     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int p = 0; p < parts; ++p) {
-                        const float4 q = __ldcg(reinterpret_cast<const float4*>(part(p) + 2 * NC + col * D + dim));
-                        const float wt = ex2(__ldcg(part(p) + col) - M);
-                        y.x = fmaf(wt, q.x, y.x), y.y = fmaf(wt, q.y, y.y), y.z = fmaf(wt, q.z, y.z), y.w = fmaf(wt, q.w, y.w);
+                    constexpr int kAhead = 6;  // loads in flight
+                    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+                        float4 q[kAhead];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            if (p0 + i < parts)
+                                q[i] = __ldcg(reinterpret_cast<const float4*>(part(p0 + i) + 2 * NC + col * D + dim));
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            if (p0 + i < parts) {
+                                const float wt = st[(p0 + i) * 2 * NC + col];
+                                y.x = fmaf(wt, q[i].x, y.x), y.y = fmaf(wt, q[i].y, y.y);
+                                y.z = fmaf(wt, q[i].z, y.z), y.w = fmaf(wt, q[i].w, y.w);
+                            }
                     }
                     put(col, dim, y);
                 }
             }
         }
-        {
-            Walk x = wk;
-            x.template next<SB>(a, NC);
-            __syncthreads();  // merge, sm_* and the walk are free again
-            if (lane == 0) wk = x;
-            __syncwarp();
-        }
     }
+    if (!plan.more) break;
+    __syncthreads();  // the list is read no more
+  }
     // a warp that gave up lets the copies already issued land before the CTA can exit
     if (dead)
         for (; use_n < ld_n; ++use_n) ptx::mbar_wait_bounded(mybars + use_n % kStages, (use_n / kStages) & 1, nullptr);
@@ -768,7 +898,7 @@ cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s) {
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = launch_config(dim3(S::kCtas * sms), dim3(kThreads), S::kSmem, s, true, &attr);
+    const cudaLaunchConfig_t cfg = launch_config(dim3(min(S::kCtas * sms, S::kMaxGrid)), dim3(kThreads), S::kSmem, s, true, &attr);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
