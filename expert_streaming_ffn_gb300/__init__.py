@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -136,9 +137,9 @@ SIGNATURES = [
     ("moe_layer_set_prefetch", _i32, [_vp, _i32]),
     ("moe_layer_prefetch_stats", _i32, [_vp, _P(ctypes.c_uint64), _P(ctypes.c_uint64)]),
     ("moe_kv_cache_bytes", _sz, [_P(moe_kv_cache)]),
-    ("moe_kv_append", _i32, [_vp, _P(moe_kv_cache), _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _vp, _i32, _vp]),
-    ("moe_kv_read", _i32, [_vp, _P(moe_kv_cache), _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _vp]),
-    ("moe_kv_attend", _i32, [_vp, _P(moe_kv_cache), _P(moe_kv_attend_args), _vp]),
+    ("moe_kv_append", _i32, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _vp, _i32, _vp]),
+    ("moe_kv_read", _i32, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _vp]),
+    ("moe_kv_attend", _i32, [_vp, _vp, _vp, _vp]),
     ("moe_kv_check", _i32, [_vp]),
 ]
 
@@ -502,46 +503,50 @@ def moe_layer_prefetch(layer: int, n: int) -> int:
 # key/value cache in 4 bits, and attention over it
 
 _KV_TYPES: dict = {}  # torch dtype -> moe_dtype, filled by the first use of torch
+_torch = None
+_kv_attend_pack = struct.Struct("@PqqPqqPPqPP8ifi").pack  # the fields of moe_kv_attend_args, in order
 
 
-def _kv_type(dtype) -> int:
-    if not _KV_TYPES:
+def _kv_torch():
+    global _torch
+    if _torch is None:
         import torch
 
         _KV_TYPES.update({torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16})
+        _torch = torch
+    return _torch
+
+
+def _kv_type(dtype) -> int:
     t = _KV_TYPES.get(dtype)
     if t is None:
         raise ValueError(f"expected float32, float16 or bfloat16, got {dtype}")
     return t
 
 
-def _kv_rows(t, what: str, heads: int, cache: moe_kv_cache):
-    """(pointer, token stride, head stride) of a [tokens][heads][head_dim] CUDA tensor."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.head_dim or t.get_device() != cache.device:
-        raise ValueError(f"{what}: expected a CUDA tensor [tokens][{heads}][{cache.head_dim}] on the cache's device, "
-                         f"got {tuple(t.shape)} on {t.device}")
+def _kv_rows(t, what: str, n: int, heads: int, cache: moe_kv_cache):
+    """(pointer, token stride, head stride) of a [n][heads][head_dim] CUDA tensor."""
+    if t.shape != (n, heads, cache.dim) or t.get_device() != cache.device:
+        raise ValueError(f"{what}: expected a CUDA tensor {[n, heads, cache.dim]} on the cache's device, got "
+                         f"{list(t.shape)} on {t.device}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), st if t.shape[0] > 1 else 0, sh if heads > 1 else 0
+    return t.data_ptr(), st if n > 1 else 0, sh if heads > 1 else 0
 
 
 def _kv_ints(t, what: str, shape, cache: moe_kv_cache) -> int:
     """Device pointer of an int32 CUDA tensor of that shape, contiguous in its last dimension."""
-    import torch
-
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.get_device() != cache.device or \
-            (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what}: expected int32 {shape} on the cache's device, contiguous in its last dimension, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype != _torch.int32 or t.shape != shape or t.get_device() != cache.device or \
+            (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: expected int32 {list(shape)} on the cache's device, contiguous in its last "
+                         f"dimension, got {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _kv_stream(stream, cache: moe_kv_cache):
     if stream is None:
-        import torch
-
-        return torch._C._cuda_getCurrentRawStream(cache.device)
+        return _torch._C._cuda_getCurrentRawStream(cache.device)
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -553,8 +558,7 @@ def moe_kv_cache_bytes(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages
 def moe_kv_make_cache(pages, n_kv_heads: int, head_dim: int, page_tokens: int) -> moe_kv_cache:
     """The cache held in `pages`, a contiguous CUDA uint8 tensor whose first
     dimension is the pages (moe_kv_cache_bytes in all). Keeps the tensor alive."""
-    import torch
-
+    torch = _kv_torch()
     if not pages.is_cuda or not pages.is_contiguous() or pages.dtype != torch.uint8 or pages.dim() < 1:
         raise ValueError("pages: expected a contiguous CUDA uint8 tensor")
     c = moe_kv_cache(n_kv_heads, head_dim, page_tokens, pages.shape[0], pages.data_ptr())
@@ -562,7 +566,8 @@ def moe_kv_make_cache(pages, n_kv_heads: int, head_dim: int, page_tokens: int) -
     if want == 0 or pages.numel() != want:
         raise ValueError(f"pages: {pages.numel()} bytes for {pages.shape[0]} pages of {page_tokens} tokens, {n_kv_heads} "
                          f"kv heads of {head_dim}: expected {want or 'another shape'}")
-    c.tensor, c.device = pages, pages.get_device()
+    # what the calls need of it: the tensor kept alive, and fields that ctypes would be slow to read
+    c.tensor, c.device, c.heads, c.dim, c.ptr = pages, pages.get_device(), n_kv_heads, head_dim, ctypes.addressof(c)
     return c
 
 
@@ -578,32 +583,32 @@ def moe_kv_new_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: 
 def moe_kv_append(ctx: int, cache: moe_kv_cache, k, v, slots, stream=None) -> None:
     """Quantise the rows k, v (CUDA [n][kv heads][head_dim], f32, f16 or bf16, any token and head strides) into
     the cache at slots (CUDA int32 [n]; page * page_tokens + place, negative = skip)."""
-    kp, kt, kh = _kv_rows(k, "k", cache.n_kv_heads, cache)
-    vp, vt, vh = _kv_rows(v, "v", cache.n_kv_heads, cache)
     n = k.shape[0]
-    if v.shape[0] != n or v.dtype != k.dtype:
-        raise ValueError("k and v: expected as many rows of the same type")
-    _check(load().moe_kv_append(ctx, cache, kp, kt, kh, vp, vt, vh, _kv_type(k.dtype),
-                                _kv_ints(slots, "slots", (n,), cache), n, _kv_stream(stream, cache)), "moe_kv_append")
+    kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
+    vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)
+    if v.dtype != k.dtype:
+        raise ValueError("k and v: expected the same type")
+    _check((_lib or load()).moe_kv_append(ctx, cache.ptr, kp, kt, kh, vp, vt, vh, _kv_type(k.dtype),
+                                          _kv_ints(slots, "slots", (n,), cache), n, _kv_stream(stream, cache)),
+           "moe_kv_append")
 
 
 def moe_kv_read(ctx: int, cache: moe_kv_cache, slots, dtype=None, k=None, v=None, stream=None):
     """The rows at slots (CUDA int32 [n]), as (k, v) [n][kv heads][head_dim] of dtype (bf16 unless k and v are
     given); zeros where a slot is negative."""
-    import torch
-
     n = slots.shape[0]
-    shape = (n, cache.n_kv_heads, cache.head_dim)
     if k is None or v is None:
-        dtype = dtype or (k if k is not None else v if v is not None else torch.empty(0, dtype=torch.bfloat16)).dtype
-        k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
-    kp, kt, kh = _kv_rows(k, "k", cache.n_kv_heads, cache)
-    vp, vt, vh = _kv_rows(v, "v", cache.n_kv_heads, cache)
-    if k.shape[0] != n or v.shape[0] != n or v.dtype != k.dtype:
-        raise ValueError("k and v: expected as many rows as slots, of the same type")
-    _check(load().moe_kv_read(ctx, cache, _kv_ints(slots, "slots", (n,), cache), n, kp, kt, kh, vp, vt, vh,
-                              _kv_type(k.dtype), _kv_stream(stream, cache)), "moe_kv_read")
+        given = k if k is not None else v
+        dtype = given.dtype if given is not None else dtype or _torch.bfloat16
+        shape = (n, cache.heads, cache.dim)
+        k = _torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
+        v = _torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
+    kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
+    vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)
+    if v.dtype != k.dtype:
+        raise ValueError("k and v: expected the same type")
+    _check((_lib or load()).moe_kv_read(ctx, cache.ptr, _kv_ints(slots, "slots", (n,), cache), n, kp, kt, kh, vp, vt, vh,
+                                        _kv_type(k.dtype), _kv_stream(stream, cache)), "moe_kv_read")
     return k, v
 
 
@@ -614,32 +619,29 @@ def moe_kv_attend(ctx: int, cache: moe_kv_cache, q, page_table, kv_len, q_start=
     int32 [batch + 1], or None for n_q / batch tokens each. max_q: the most new tokens of one sequence, known
     on the host (default: the mean). scale: 1/sqrt(head_dim) by default. Returns out; lse (f32 [n_q][heads]),
     if given, is filled."""
-    import torch
-
-    B = kv_len.shape[0]
-    n, heads = q.shape[0], q.shape[1]
-    qp, qt, qh = _kv_rows(q, "q", heads, cache)
+    B, (n, heads) = kv_len.shape[0], q.shape[:2]
+    qp, qt, qh = _kv_rows(q, "q", n, heads, cache)
     if out is None:
-        out = torch.empty((n, heads, cache.head_dim), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out: expected q's shape and type")
-    op, ot, oh = _kv_rows(out, "out", heads, cache)
-    lp = None
+        out = _torch.empty((n, heads, cache.dim), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise ValueError("out: expected q's type")
+    op, ot, oh = _kv_rows(out, "out", n, heads, cache)
+    lp = 0
     if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (n, heads) or not lse.is_contiguous() or \
+        if lse.dtype != _torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous() or \
                 lse.get_device() != cache.device:
-            raise ValueError(f"lse: expected a contiguous float32 CUDA tensor {(n, heads)}")
+            raise ValueError(f"lse: expected a contiguous float32 CUDA tensor {[n, heads]}")
         lp = lse.data_ptr()
     if page_table.dim() != 2:
         raise ValueError("page_table: expected [batch][max pages]")
     pages = page_table.shape[1]
-    a = moe_kv_attend_args(
+    args = _kv_attend_pack(
         qp, qt, qh, op, ot, oh, lp, _kv_ints(page_table, "page_table", (B, pages), cache), page_table.stride(0),
         _kv_ints(kv_len, "kv_len", (B,), cache),
-        None if q_start is None else _kv_ints(q_start, "q_start", (B + 1,), cache),
+        0 if q_start is None else _kv_ints(q_start, "q_start", (B + 1,), cache),
         B, n, heads, pages, -(-n // max(B, 1)) if max_q is None else max_q, max_len, causal, window,
-        cache.head_dim ** -0.5 if scale is None else scale, _kv_type(q.dtype))
-    _check(load().moe_kv_attend(ctx, cache, a, _kv_stream(stream, cache)), "moe_kv_attend")
+        cache.dim ** -0.5 if scale is None else scale, _kv_type(q.dtype))
+    _check((_lib or load()).moe_kv_attend(ctx, cache.ptr, args, _kv_stream(stream, cache)), "moe_kv_attend")
     return out
 
 

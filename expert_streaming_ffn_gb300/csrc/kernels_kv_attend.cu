@@ -5,8 +5,10 @@
 // segment is (sequence, kv head, column tile), its keys in blocks of 16 (one
 // record each). All segments' blocks are laid end to end and cut into equal
 // ranges, one per CTA, so ragged batches and single long sequences alike keep
-// every SM reading; a segment cut between CTAs is joined from fp32 partial
-// results by the CTA that finishes it last, in CTA order.
+// every SM reading; the fp32 partial results of a segment cut between CTAs are
+// joined by a second kernel, in CTA order. (A join by the CTA that finishes last, in this
+// kernel, took 5 us against 2.5, and its registers spilled the main loop's: 71 us against 43
+// at 131,071 keys of 8 heads.)
 //
 // Within a CTA each of 8 warps takes every eighth chunk (4,608 bytes: 64, 32 or
 // 16 tokens for head_dim 64, 128, 256) and owns a ring of bulk copies into
@@ -40,7 +42,7 @@ constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it 
 constexpr float kNone = -3e38f;  // the bound before any score
 constexpr int kPieceCost = 24;  // what a piece costs beside its blocks, in blocks
 
-constexpr int kPlanBytes = 2304;  // of the schedule and a flag, at least
+constexpr int kPlanBytes = 2304;  // of the schedule, at least
 
 template <int D, int NT>
 struct Shape {
@@ -53,10 +55,10 @@ struct Shape {
     static constexpr int kCol = D + 4;  // floats of a column in the merge buffer
     static constexpr int kRing = kWarps * kStages * kChunkBytes;
     static constexpr int kMaxGrid = 160 * kCtas;
-    // the merge buffer also holds the statistics of a split segment's parts
-    static constexpr int kMerge = kWarps * kCol > 2 * kMaxGrid ? kWarps * NC * kCol * 4 : 2 * kMaxGrid * NC * 4;
+    static constexpr int kMerge = kWarps * NC * kCol * 4;
     static constexpr int kSmall = (4 * kWarps * NC + 2 * NC + 4 * NC + 2 * (NG + 1) * NC + 2 * NT * W * 128) * 4;
     static constexpr size_t kSmem = kRing + kMerge + kSmall + kWarps * kStages * 8 + kPlanBytes;
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM share its 228 KB, 1 KB of each taken by the system");
     static constexpr int kSlot = NC * (D + 2);  // floats of one partial result: m[NC], l[NC], o[NC][D]
 };
 
@@ -138,8 +140,8 @@ struct Seq {
 __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
     Seq s;
     if (a.q_start) {
-        s.first = __ldg(a.q_start + b);
-        s.n = __ldg(a.q_start + b + 1) - s.first;
+        s.first = min(max(__ldg(a.q_start + b), 0), a.n_q);  // within q whatever q_start holds
+        s.n = min(__ldg(a.q_start + b + 1), a.n_q) - s.first;
     } else {
         s.first = b * a.T;
         s.n = a.T;
@@ -168,12 +170,14 @@ struct Cut {
 // A piece: the part of a segment that a CTA's range holds.
 struct Piece {
     int first, n, len;   // the sequence: first q row, new tokens, keys
-    int b, h, c0;        // sequence, kv head, first column
+    int h, c0;           // kv head, first column
     int blk, nb;         // first block (of the sequence) and blocks; nb = 0 where there are no keys
-    int cta0, parts;     // the segment's first CTA, and how many share it
+    int parts;           // how many CTAs share the segment
     int start;           // 1: the piece holds the segment's first block
     int rot;             // which warp takes its first chunk
     int all_lo, all_hi;  // the keys that every column sees
+    const int32_t* table;  // the sequence's page ids
+    const uint8_t* head;   // the head's records of page 0
 };
 
 constexpr int kPieces = 32;  // pieces of one list
@@ -191,7 +195,7 @@ struct Plan {
     Piece piece[kPieces];
 };
 
-static_assert(sizeof(Plan) + 4 <= kPlanBytes);
+static_assert(sizeof(Plan) <= kPlanBytes);
 
 // Cuts U blocks in Sg segments of at most `most` blocks into ranges for the grid.
 __device__ __forceinline__ Cut make_cut(const KvAttend& a, int64_t U, int64_t Sg, int most) {
@@ -314,7 +318,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
 }
 
 // The next list of pieces, by one warp: lane p looks at the p-th segment from the list's first.
-template <int NC, int SB>
+template <int NC, int SB, int kRec>
 __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane) {
     const Cut c = P.cut;
     int b = P.b;
@@ -344,18 +348,18 @@ __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane
     if (some) {
         Piece p;
         p.first = s.first, p.n = s.n, p.len = s.len;
-        p.b = b;
         p.h = (int)((uint32_t)seg / (uint32_t)s.nct);
         p.c0 = (int)((uint32_t)seg - (uint32_t)p.h * (uint32_t)s.nct) * NC;
         p.blk = s.lo_blk + lo;
         p.nb = nb;
-        p.cta0 = (int)quot(at, c.quota);
-        p.parts = (int)quot(at + s.per - 1, c.quota) - p.cta0 + 1;
+        p.parts = (int)quot(at + s.per - 1, c.quota) - (int)quot(at, c.quota) + 1;
         p.start = lo == 0;
         p.rot = (rot - chunks) & (kWarps - 1);
         const int pos0 = s.len - s.n, first = pos0 + (int)a.by_g.div(p.c0);
         const int last = pos0 + (int)a.by_g.div(min(p.c0 + NC, s.n * a.G) - 1);
         p.all_hi = a.causal ? min(s.len, first + 1) : s.len;
+        p.table = a.table + (int64_t)b * a.table_stride;
+        p.head = a.c.pages + (size_t)p.h * (a.c.P >> 4) * kRec;
         p.all_lo = a.window && last >= a.window ? last - a.window + 1 : 0;
         P.piece[__popc(who & ((1u << lane) - 1))] = p;
     }
@@ -367,6 +371,19 @@ __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane
         P.more = more;
     }
     if (lane == 0) P.count = __popc(who);
+}
+
+// Four sums of a column (its segment: first q row, kv head, first column), with
+// its bound and sum of weights, to the output.
+template <class T>
+__device__ __forceinline__ void put_out(const KvAttend& a, int first, int h, int c0, int col, int dim, float4 x, float m,
+                                        float l) {
+    const int i = (int)a.by_g.div(c0 + col), hq = h * a.G + (c0 + col) - i * a.G;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+    store4(static_cast<T*>(a.out) + (int64_t)(first + i) * a.ot + (int64_t)hq * a.oh + dim, x);
+    if (a.lse && dim == 0)
+        a.lse[(int64_t)(first + i) * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
 
 template <int D, int NT, class T>
@@ -384,49 +401,44 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     uint32_t* sm_q = reinterpret_cast<uint32_t*>(sm_x + 2 * (NG + 1) * NC);  // [2][NT][W][32][4]: query fragments
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm_q + 2 * NT * W * 128);
     Plan& plan = *reinterpret_cast<Plan*>(bars + kWarps * kStages);
-    int* flag = reinterpret_cast<int*>(&plan + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (lane < kStages) ptx::mbar_init(bars + warp * kStages + lane, 1);
     ptx::fence_mbar_init();
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
+    if (tid == 0 && a.join) a.join[blockIdx.x].parts = 0;
     if (!make_plan<NC>(a, plan, tid, warp, lane)) return;
 
-    uint32_t ld_n = 0, use_n = 0;  // chunks issued and used
-    uint32_t valid = 0;            // per stage, 4 bits: blocks that were loaded
-    bool dead = false;             // a wait expired
+    uint32_t use_n = 0;  // chunks used
+    uint32_t valid = 0;  // per stage, 4 bits: the blocks that were asked for; bit 16 + stage: in flight
+    bool dead = false;   // a wait expired
     int parity = 0;
     uint64_t* const mybars = bars + warp * kStages;
     unsigned char* const myring = ring + warp * kStages * kChunkBytes;
 
 #pragma unroll 1
   for (;;) {  // lists of pieces
-    if (warp == 0) list_pieces<NC, SB>(a, plan, lane);
+    if (warp == 0) list_pieces<NC, SB, kRec>(a, plan, lane);
     __syncthreads();
     const int count = plan.count;
 
     // ---- loads: this warp's chunks, kStages ahead, and the page of the one after ----
-    int ld_p = -1, ld_c = 0, ld_nb = 0, ld_blk = 0, ld_page = 0;  // piece, next chunk; its blocks and first block; this lane's page
-    const int32_t* ld_table = nullptr;
-    const uint8_t* ld_head = nullptr;
+    int ld_p = -1, ld_c = 1 << 20, ld_page = 0;  // piece, next chunk, this lane's page of it
     auto find = [&]() {  // moves on to a piece with a chunk for this warp, and fetches its page id
-        while (ld_c * SB >= ld_nb && ++ld_p < count) {
+        while ((ld_p < 0 || ld_c * SB >= plan.piece[ld_p].nb) && ++ld_p < count)
+            ld_c = (warp - plan.piece[ld_p].rot) & (kWarps - 1);
+        if (ld_p < count) {
             const Piece& p = plan.piece[ld_p];
-            ld_c = (warp - p.rot) & (kWarps - 1);
-            ld_nb = p.nb;
-            ld_blk = p.blk;
-            ld_table = a.table + (int64_t)p.b * a.table_stride;
-            ld_head = a.c.pages + (size_t)p.h * (a.c.P >> 4) * kRec;
+            const int i = ld_c * SB + lane;
+            if (lane < SB && i < p.nb) ld_page = __ldg(p.table + ((p.blk + i) >> (a.c.page_shift - 4)));
         }
-        const int i = ld_c * SB + lane;
-        if (ld_p < count && lane < SB && i < ld_nb) ld_page = __ldg(ld_table + ((ld_blk + i) >> (a.c.page_shift - 4)));
     };
-    auto issue = [&]() {
+    auto issue = [&](int st) {
         if (ld_p >= count || dead) return;
-        const int st = (int)(ld_n % kStages);
+        const Piece& p = plan.piece[ld_p];
         const int i = ld_c * SB + lane;
-        bool ok = lane < SB && i < ld_nb;
+        bool ok = lane < SB && i < p.nb;
         if (ok && (unsigned)ld_page >= (unsigned)a.c.n_pages) {
             *(volatile unsigned*)a.bad = 1u;
             ok = false;
@@ -435,40 +447,46 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         if (lane == 0) ptx::mbar_arrive_expect_tx(mybars + st, __popc(v) * kRec);
         __syncwarp();
         if (ok) {
-            const int in = (ld_blk + i) & ((a.c.P >> 4) - 1);
+            const int in = (p.blk + i) & ((a.c.P >> 4) - 1);
             ptx::bulk_g2s(myring + st * kChunkBytes + lane * kRec,
-                          ld_head + ((size_t)ld_page * a.c.H * (a.c.P >> 4) + in) * kRec, kRec, mybars + st);
+                          p.head + ((size_t)ld_page * a.c.H * (a.c.P >> 4) + in) * kRec, kRec, mybars + st);
         }
-        valid = (valid & ~(15u << (4 * st))) | (v << (4 * st));
-        ++ld_n;
+        valid = (valid & ~(15u << (4 * st))) | (v << (4 * st)) | (65536u << st);
         ld_c += kWarps;
         find();
     };
-    find();
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue();
 
     // row g of a score tile holds token pi(g) of its half block: 0 1 3 2 4 5 7 6, so that the
     // four lanes of a value fragment read rows of both parities (half as many bank conflicts)
     const int pg = g ^ ((g >> 1) & 1);
 
     // ---- a piece's queries: fp16 fragments in shared memory, each warp NT of its columns ----
-    // A row is scaled by a power of two to a largest element in [2^10, 2^11), and by the sign
-    // of the scale; pairs 1 and 3 of a word are divided by 16 to meet codes times 16.
-    auto prepare_q = [&](int i, int par) {
+    constexpr int E = D / 32;  // elements of a lane
+    struct RawQ {
+        uint32_t w[NT][E / 2];
+    };
+    auto fetch_q = [&](int i) {
         const Piece& p = plan.piece[i];
-        constexpr int E = D / 32;  // elements of a lane
+        RawQ r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c = p.c0 + nt * 8 + warp, tk = (int)a.by_g.div(c), hq = c - tk * a.G;
-            const bool in = tk < p.n;
-            uint32_t raw[E / 2] = {};
-            if (in) {
-                const T* qp = static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt +
-                              (int64_t)(p.h * a.G + hq) * a.qh + lane * E;
+            const unsigned* qp = reinterpret_cast<const unsigned*>(
+                static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt + (int64_t)(p.h * a.G + hq) * a.qh + lane * E);
 #pragma unroll
-                for (int k = 0; k < E / 2; ++k) raw[k] = __ldg(reinterpret_cast<const unsigned*>(qp) + k);
-            }
+            for (int k = 0; k < E / 2; ++k) r.w[nt][k] = tk < p.n ? __ldg(qp + k) : 0u;
+        }
+        return r;
+    };
+    // A row is scaled by a power of two to a largest element in [2^10, 2^11), and by the sign
+    // of the scale; pairs 1 and 3 of a word are divided by 16 to meet codes times 16.
+    auto prepare_q = [&](int i, int par, const RawQ& r) {
+        const Piece& p = plan.piece[i];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int tk = (int)a.by_g.div(p.c0 + nt * 8 + warp);
+            const bool in = tk < p.n;
+            const uint32_t(&raw)[E / 2] = r.w[nt];
             float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < E / 2; ++k) {
@@ -508,7 +526,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
             }
         }
     };
-    if (count) prepare_q(0, parity);
+    // the first queries are asked for ahead of the cache, or they would queue behind it
+    RawQ first_q{};
+    if (count) first_q = fetch_q(0);
+    find();
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) issue((int)((use_n + i) % kStages));
+    if (count) prepare_q(0, parity, first_q);
     __syncthreads();
 
 #pragma unroll 1
@@ -741,11 +765,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 }
             }
             ++use_n;
+            valid &= ~(65536u << st);
             __syncwarp();
-            issue();
+            issue(st);
         }
 
-        if (ip + 1 < count) prepare_q(ip + 1, parity ^ 1);
+        if (ip + 1 < count) prepare_q(ip + 1, parity ^ 1, fetch_q(ip + 1));
         float* sm_m = sm_stat + parity * 2 * kWarps * NC;  // [kWarps][NC]
         float* sm_l = sm_m + kWarps * NC;
         // ---- merge the warps ----
@@ -799,18 +824,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
         __syncthreads();
 
-        const int cta0 = pc.cta0, parts = pc.parts, c0 = pc.c0, ncols = min(NC, pc.n * a.G - c0);
-        // writes four sums of a column, whose statistics are in sm_w
-        auto put = [&](int col, int dim, float4 x) {
-            const int i = (int)a.by_g.div(c0 + col), hq = pc.h * a.G + (c0 + col) - i * a.G;
-            const float L = sm_w[NC + col];
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-            store4(static_cast<T*>(a.out) + (int64_t)(pc.first + i) * a.ot + (int64_t)hq * a.oh + dim, x);
-            if (a.lse && dim == 0)
-                a.lse[(int64_t)(pc.first + i) * a.Hq + hq] =
-                    L == 0.0f ? -INFINITY : 0.6931471805599453f * (sm_w[col] + log2f(L));
-        };
+        const int parts = pc.parts, ncols = min(NC, pc.n * a.G - pc.c0);
         float* slot = a.part + (size_t)(2 * blockIdx.x + pc.start) * S::kSlot;
         for (int x = tid; x < ncols * (D / 4); x += kThreads) {
             const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
@@ -821,66 +835,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                 y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
             }
             if (parts == 1)
-                put(col, dim, y);
+                put_out<T>(a, pc.first, pc.h, pc.c0, col, dim, y, sm_w[col], sm_w[NC + col]);
             else
                 __stcg(reinterpret_cast<float4*>(slot + 2 * NC + col * D + dim), y);
         }
-        if (parts > 1) {
-            // ---- a segment cut between CTAs: the last to finish joins the parts ----
+        if (parts > 1) {  // a segment cut between CTAs: kv_join_kernel adds its parts
             if (tid < 2 * NC) __stcg(slot + tid, sm_w[tid]);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const unsigned old = atomicAdd(a.counters + cta0, 1u);
-                *flag = old == (unsigned)parts - 1;
-                if (*flag) a.counters[cta0] = 0;
-                __threadfence();
-            }
-            __syncthreads();
-            if (*flag) {
-                auto part = [&](int p) {  // part p: the segment's start lies in CTA cta0's second slot
-                    return a.part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * S::kSlot;
-                };
-                // every part's statistics at once, then its columns' weights in their place
-                float* st = merge;  // [parts][2][NC]
-                for (int x = tid; x < parts * 2 * NC; x += kThreads) st[x] = __ldcg(part(x / (2 * NC)) + x % (2 * NC));
-                __syncthreads();
-                for (int col = warp; col < NC; col += kWarps) {
-                    float M = kNone, L = 0.0f;
-                    for (int p = lane; p < parts; p += 32) M = fmaxf(M, st[p * 2 * NC + col]);
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-                    for (int p = lane; p < parts; p += 32) {
-                        const float wt = ex2(st[p * 2 * NC + col] - M);
-                        L += st[p * 2 * NC + NC + col] * wt;
-                        st[p * 2 * NC + col] = wt;
-                    }
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
-                    if (lane == 0) sm_w[col] = M, sm_w[NC + col] = L;
-                }
-                __syncthreads();
-                for (int x = tid; x < ncols * (D / 4); x += kThreads) {
-                    const int col = x / (D / 4), dim = (x % (D / 4)) * 4;
-                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    constexpr int kAhead = 6;  // loads in flight
-                    for (int p0 = 0; p0 < parts; p0 += kAhead) {
-                        float4 q[kAhead];
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i)
-                            if (p0 + i < parts)
-                                q[i] = __ldcg(reinterpret_cast<const float4*>(part(p0 + i) + 2 * NC + col * D + dim));
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i)
-                            if (p0 + i < parts) {
-                                const float wt = st[(p0 + i) * 2 * NC + col];
-                                y.x = fmaf(wt, q[i].x, y.x), y.y = fmaf(wt, q[i].y, y.y);
-                                y.z = fmaf(wt, q[i].z, y.z), y.w = fmaf(wt, q[i].w, y.w);
-                            }
-                    }
-                    put(col, dim, y);
-                }
-            }
+            if (pc.start && tid == 0 && a.join) a.join[blockIdx.x] = KvJoin{parts, pc.first, pc.h, pc.c0, ncols};
         }
     }
     if (!plan.more) break;
@@ -888,34 +849,97 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
   }
     // a warp that gave up lets the copies already issued land before the CTA can exit
     if (dead)
-        for (; use_n < ld_n; ++use_n) ptx::mbar_wait_bounded(mybars + use_n % kStages, (use_n / kStages) & 1, nullptr);
+        for (uint32_t n = use_n; n < use_n + kStages; ++n)
+            if (valid >> (16 + n % kStages) & 1) ptx::mbar_wait_bounded(mybars + n % kStages, (n / kStages) & 1, nullptr);
+}
+
+// Adds the parts of the segment that starts in the range of CTA blockIdx.x and
+// does not end there, if there is one: block y takes column y, D/4 threads times
+// 1024/D groups of parts. Part 0 lies in that CTA's second slot, part p in the first
+// slot of the p-th CTA after it.
+template <int D, int NT, class T>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ KvAttend a) {
+    using S = Shape<D, NT>;
+    constexpr int NC = S::NC, kLanes = D / 4, kGroups = kThreads / kLanes;
+    __shared__ float w[S::kMaxGrid];
+    __shared__ float4 sum[kThreads];
+    __shared__ float warp_m[kWarps], warp_l[kWarps];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const KvJoin j = a.join[blockIdx.x];
+    const int tid = threadIdx.x, col = blockIdx.y;
+    if (col >= j.cols || j.parts == 0) return;
+    const float* p0 = a.part + (size_t)(2 * blockIdx.x + 1) * S::kSlot;
+    auto part = [&](int p) { return p0 + (p == 0 ? 0 : (2 * p - 1) * S::kSlot); };
+    // weights: 2^(bound - largest bound)
+    float M = kNone;
+    for (int p = tid; p < j.parts; p += kThreads) M = fmaxf(M, w[p] = part(p)[col]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+    if ((tid & 31) == 0) warp_m[tid >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, warp_m[i]);
+    float L = 0.0f;
+    for (int p = tid; p < j.parts; p += kThreads) {
+        w[p] = ex2(w[p] - M);
+        L += part(p)[NC + col] * w[p];
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(kFull, L, x);
+    if ((tid & 31) == 0) warp_l[tid >> 5] = L;
+    __syncthreads();
+    const int dim = tid % kLanes * 4, grp = tid / kLanes;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int p = grp; p < j.parts; p += kGroups) {
+        const float4 q = *reinterpret_cast<const float4*>(part(p) + 2 * NC + col * D + dim);
+        y.x = fmaf(w[p], q.x, y.x), y.y = fmaf(w[p], q.y, y.y), y.z = fmaf(w[p], q.z, y.z), y.w = fmaf(w[p], q.w, y.w);
+    }
+    sum[tid] = y;
+    __syncthreads();
+    if (grp) return;
+    L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) L += warp_l[i];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 q = sum[i * kLanes + tid];
+        y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
+    }
+    put_out<T>(a, j.first, j.h, j.c0, col, dim, y, M, L);
 }
 
 template <int D, int NT, class T>
-cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s) {
+cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s, int* launched) {
     using S = Shape<D, NT>;
     auto kernel = kv_decode_kernel<D, NT, T>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = launch_config(dim3(min(S::kCtas * sms, S::kMaxGrid)), dim3(kThreads), S::kSmem, s, true, &attr);
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    const int grid = min(S::kCtas * sms, S::kMaxGrid);
+    const cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(kThreads), S::kSmem, s, true, &attr);
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess || !a.join) return e;
+    *launched = 2;
+    const cudaLaunchConfig_t jcfg = launch_config(dim3(grid, S::NC), dim3(kThreads), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&jcfg, kv_join_kernel<D, NT, T>, a);
 }
 
 template <int D, class T>
-cudaError_t launch_decode_cols(const KvAttend& a, int cols, int sms, cudaStream_t s) {
-    return cols <= 8 ? launch_decode<D, 1, T>(a, sms, s) : launch_decode<D, 2, T>(a, sms, s);
+cudaError_t launch_decode_cols(const KvAttend& a, int cols, int sms, cudaStream_t s, int* launched) {
+    return cols <= 8 ? launch_decode<D, 1, T>(a, sms, s, launched) : launch_decode<D, 2, T>(a, sms, s, launched);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s) {
+cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s, int* launched) {
     const bool bf = t == MOE_BF16;
     if (d == 64)
-        return bf ? launch_decode_cols<64, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<64, __half>(a, cols, sms, s);
+        return bf ? launch_decode_cols<64, __nv_bfloat16>(a, cols, sms, s, launched) : launch_decode_cols<64, __half>(a, cols, sms, s, launched);
     if (d == 128)
-        return bf ? launch_decode_cols<128, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<128, __half>(a, cols, sms, s);
-    return bf ? launch_decode_cols<256, __nv_bfloat16>(a, cols, sms, s) : launch_decode_cols<256, __half>(a, cols, sms, s);
+        return bf ? launch_decode_cols<128, __nv_bfloat16>(a, cols, sms, s, launched) : launch_decode_cols<128, __half>(a, cols, sms, s, launched);
+    return bf ? launch_decode_cols<256, __nv_bfloat16>(a, cols, sms, s, launched) : launch_decode_cols<256, __half>(a, cols, sms, s, launched);
 }
 
 }  // namespace moe

@@ -40,25 +40,21 @@ void kv_state_destroy(KvState* st) {
     delete st;
 }
 
-constexpr size_t kCounterBytes = 4096;  // a counter for each of up to 1,024 CTAs
+constexpr size_t kJoinBytes = 1024 * sizeof(KvJoin);  // for up to 1,024 CTAs
 
 // The workspace of an attention call, made by the first of them.
 moe_status ensure_workspace(KvState* S, int device) {
     if (S->ws) return MOE_OK;
     int sms = 0;
     CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
-    if ((size_t)sms * kKvMaxCtas * sizeof(unsigned) > kCounterBytes)
+    if ((size_t)sms * kKvMaxCtas * sizeof(KvJoin) > kJoinBytes)
         return set_error(MOE_ECUDA, "moe_kv_attend: %d SMs are more than it is made for", sms);
-    const size_t bytes = kCounterBytes + (size_t)sms * kKvMaxCtas * kKvPartFloats * sizeof(float);
+    const size_t bytes = kJoinBytes + (size_t)sms * kKvMaxCtas * kKvPartFloats * sizeof(float);
     if (!S->ws_done) CUDA_TRY(cudaEventCreateWithFlags(&S->ws_done, cudaEventDisableTiming));
     unsigned char* p = nullptr;
     if (cudaMalloc(&p, bytes) != cudaSuccess) {
         cudaGetLastError();
         return set_error(MOE_ENOMEM, "moe_kv_attend: workspace of %zu bytes failed", bytes);
-    }
-    if (cudaMemset(p, 0, kCounterBytes) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
-        cudaFree(p);
-        return set_error(MOE_ECUDA, "moe_kv_attend: clearing the workspace failed: %s", cudaGetErrorString(cudaGetLastError()));
     }
     S->sms = sms;
     S->ws = p;
@@ -141,15 +137,8 @@ moe_status state_of(moe_ctx* C, KvState** out) {
     return MOE_OK;
 }
 
-// A kernel gave up on a wait: its counters may be off, so they are cleared
-// before the next call.
 moe_status expired(KvState* S) {
     S->bad_host[1] = 0;
-    if (S->ws) {
-        cudaDeviceSynchronize();
-        cudaMemset(S->ws, 0, kCounterBytes);
-        cudaDeviceSynchronize();
-    }
     return set_error(MOE_ETIMEOUT, "a bounded device wait expired in an earlier attention call");
 }
 
@@ -280,18 +269,24 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.err = S->bad_dev + 1;
     if (*(volatile unsigned*)(S->bad_host + 1)) return expired(S);
     if ((st = ensure_workspace(S, ctx_device(C))) != MOE_OK) return st;
-    a.counters = reinterpret_cast<unsigned*>(S->ws);
-    a.part = reinterpret_cast<float*>(S->ws + kCounterBytes);
+    a.part = reinterpret_cast<float*>(S->ws + kJoinBytes);
     a.min_units = 32;
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
-    bool capturing;
-    if ((st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
+    // few short segments are never cut between CTAs: such a call leaves the workspace alone
+    const int64_t blocks = (int64_t)p->max_pages * cache->page_tokens / kKvBlock;
+    const int64_t segs = ((int64_t)p->n_q * a.G / 8 + p->batch) * cache->n_kv_heads;
+    const bool shared = blocks > a.min_units || segs > S->sms;
+    if (shared) a.join = reinterpret_cast<KvJoin*>(S->ws);
+    bool capturing = true;
+    if (shared && (st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
     const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
     const int64_t cols = (int64_t)p->max_q * a.G;
-    CUDA_TRY(launch_kv_attend(a, d, p->dtype, (int)(cols < 1 << 20 ? cols : 1 << 20), S->sms, s));
+    int launched = 1;
+    CUDA_TRY(launch_kv_attend(a, d, p->dtype, (int)(cols < 1 << 20 ? cols : 1 << 20), S->sms, s, &launched));
+    for (; launched > 1; --launched) ctx_count_launch(C);  // the first is counted already
     return workspace_end(S, s, capturing);
 }
 

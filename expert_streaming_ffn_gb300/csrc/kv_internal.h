@@ -54,6 +54,12 @@ struct KvRows {
 cudaError_t launch_kv_append(const KvRows& a, int d, moe_dtype t, cudaStream_t s);
 cudaError_t launch_kv_read(const KvRows& a, int d, moe_dtype t, cudaStream_t s);
 
+// A segment cut between CTAs (parts = 0: none): how many have a part, its first
+// q row, kv head, first column and columns.
+struct KvJoin {
+    int parts, first, h, c0, cols;
+};
+
 struct KvAttend {
     KvCache c;
     const void* q;
@@ -71,9 +77,9 @@ struct KvAttend {
     float scale_log2;  // scale * log2(e)
     unsigned* bad;
     unsigned* err;  // mapped word: a bounded wait expired
-    // workspace of segments cut between CTAs: a counter per CTA (zero between
-    // calls) and two partial results per CTA
-    unsigned* counters;
+    // workspace of segments cut between CTAs: per CTA the segment that starts in its
+    // range and ends in another's, and two partial results; null: none can be cut
+    KvJoin* join;
     float* part;
     int min_units;  // fewest blocks of 16 tokens that a CTA takes
 };
@@ -81,7 +87,7 @@ struct KvAttend {
 constexpr int kKvMaxCtas = 2;                       // resident CTAs per SM of any of the kernels
 constexpr size_t kKvPartFloats = 2 * 16 * (256 + 2);  // partial results of one CTA, at most
 
-// cols: query columns (new tokens * query heads per kv head) of a sequence, as the caller knows them
-cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s);
+// *launched gets the number of kernels. cols: query columns (new tokens * query heads per kv head) of a sequence, as the caller knows them
+cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s, int* launched);
 
 }  // namespace moe
