@@ -140,13 +140,13 @@ struct Seq {
 __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
     Seq s;
     if (a.q_start) {
-        s.first = min(max(__ldg(a.q_start + b), 0), a.n_q);  // within q whatever q_start holds
-        s.n = min(__ldg(a.q_start + b + 1), a.n_q) - s.first;
+        s.first = min(max(*(a.q_start + b), 0), a.n_q);  // within q whatever q_start holds
+        s.n = min(*(a.q_start + b + 1), a.n_q) - s.first;
     } else {
         s.first = b * a.T;
         s.n = a.T;
     }
-    s.len = max(0, min(__ldg(a.kv_len + b), a.max_pages << a.c.page_shift));
+    s.len = max(0, min(*(a.kv_len + b), a.max_pages << a.c.page_shift));
     const int pos0 = s.len - s.n;
     s.lo_blk = (a.window && pos0 >= a.window ? pos0 - a.window + 1 : 0) >> 4;
     s.per = max(1, ((s.len + 15) >> 4) - s.lo_blk);  // a segment without keys is one unit: its rows become zeros
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         if (ld_p < count) {
             const Piece& p = plan.piece[ld_p];
             const int i = ld_c * SB + lane;
-            if (lane < SB && i < p.nb) ld_page = __ldg(p.table + ((p.blk + i) >> (a.c.page_shift - 4)));
+            if (lane < SB && i < p.nb) ld_page = *(p.table + ((p.blk + i) >> (a.c.page_shift - 4)));
         }
     };
     auto issue = [&](int st) {
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
             const unsigned* qp = reinterpret_cast<const unsigned*>(
                 static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt + (int64_t)(p.h * a.G + hq) * a.qh + lane * E);
 #pragma unroll
-            for (int k = 0; k < E / 2; ++k) r.w[nt][k] = tk < p.n ? __ldg(qp + k) : 0u;
+            for (int k = 0; k < E / 2; ++k) r.w[nt][k] = tk < p.n ? *(qp + k) : 0u;
         }
         return r;
     };

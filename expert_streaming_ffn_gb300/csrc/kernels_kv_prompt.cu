@@ -1,0 +1,803 @@
+// Attention of many query rows over the 4-bit cache (prompts), on the
+// 5th-generation tensor cores.
+//
+// A CTA holds 256 query rows (two tiles of 128; one tile for head_dim 256),
+// rows being (new token, query head) pairs of one kv head, so a key tile is
+// dequantised once for all of them. Per key tile of 128 (64 for head_dim 256):
+//   four warps dequantise K, then V, from global memory (the next tile's words
+//     already in registers) to fp16 in shared memory, 128-byte swizzled; V is used
+//     as it lies, [key][dim], as an operand whose rows run along dim;
+//   one thread issues S = Q K^T into tensor memory and, later, O += P V with P
+//     from tensor memory, where it takes the place of S;
+//   four warps per tile, a row a thread, turn S into P = 2^(c s - m), fp16. The
+//     bound m moves only when a score passes it by 8 (P <= 2^8), and then O is
+//     rescaled in tensor memory; so S is read once.
+// With two tiles, one's softmax runs under the other's products; with one tile
+// (head_dim 256, whose O takes half of tensor memory) S has two buffers instead.
+// Few rows: the keys are split over CTAs, fp32 partial results joined by a
+// second kernel.
+//
+// Rounding beyond fp32: K and V values, P and Q (scaled by a power of two per row)
+// to fp16.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kv_internal.h"
+#include "ptx.cuh"
+#include "tc_operand.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr float kLazy = 8.0f;
+constexpr float kNone = -3e38f;
+constexpr int kPoison = 64;  // NaN values noted exactly; more are taken as a range
+
+template <int D>
+struct PShape {
+    static constexpr int NG = D / 64;
+    static constexpr int MT = D <= 128 ? 2 : 1;    // row tiles
+    static constexpr int NS = MT == 2 ? 1 : 2;     // S buffers of a row tile
+    static constexpr int KT = D <= 128 ? 128 : 64; // keys of a tile
+    static constexpr int kRows = 128 * MT;
+    static constexpr int kRec = kv_record_bytes(D);
+    static constexpr int kSoftWarps = 4 * MT, kWarpDq = kSoftWarps, kWarpMma = kSoftWarps + 4;
+    // Two row tiles: four warpgroups (the last one issues; three of its warps idle), whose
+    // registers are shared out anew, 2 * 176 + 112 + 48 = 4 * 128. One: three warps a scheduler at
+    // most, 168 registers each, as they are.
+    static constexpr bool kShare = MT == 2;
+    static constexpr int kThreads = kShare ? 512 : 32 * (kSoftWarps + 5);
+    static constexpr int kQBytes = 128 * D * 2;  // one row tile
+    static constexpr int kTile = KT * D * 2;     // K or V
+    static constexpr int kStages = 2;
+    static constexpr int kColO = MT * NS * KT;   // tensor memory: S buffers, then O
+    static constexpr int kSmem = 1024 + MT * kQBytes + 2 * kStages * kTile + 1024;
+    static constexpr int kSlot = kRows * (D + 2);  // floats of a partial result: o[row][D], then m and l
+};
+
+struct Bars {
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    int abort;
+    int n_poison, poison_lo, poison_hi;
+    int poison[kPoison];  // key * 4 + group
+    uint4 hide[8];        // of tiles j mod 8: keys (bits) whose page is outside the cache
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+    return pack_h2(x, y);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+#define R8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+#define W8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+
+// 32 lanes x 32 columns of tensor memory, thread i lane (base + i)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : W8(v, 0), W8(v, 8), W8(v, 16), W8(v, 24)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::R8(v, 0),
+        R8(v, 8), R8(v, 16), R8(v, 24), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an operand [k][n] whose n runs along the 128-byte rows: chunks of
+// 64 n lie n_stride bytes apart, groups of eight k 1024.
+__device__ __forceinline__ uint64_t sw128_desc_n(uint32_t saddr, uint32_t n_stride) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(n_stride >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Two fp32 operations in one.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 f2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// What a CTA works on.
+struct Work {
+    int first, n, len, b;  // the sequence: first q row, new tokens, keys, index
+    int h, row0;           // kv head, first of its rows
+    int k0, tiles;         // first key, and key tiles of this split
+    bool any;              // there is such a piece of work
+};
+
+template <int D>
+__device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
+    using S = PShape<D>;
+    // block: (row tile over all sequences, kv head, split), splits of a tile side by side
+    const unsigned split = blockIdx.x % (unsigned)a.splits, x = blockIdx.x / (unsigned)a.splits;
+    const unsigned h = x % (unsigned)a.c.H;
+    int want = (int)(x / (unsigned)a.c.H);
+    Work w{};
+    w.h = (int)h;
+    for (int base = 0; base < a.B; base += 32) {
+        const int b = base + lane;
+        int first = 0, n = 0, cnt = 0;
+        if (b < a.B) {
+            if (a.q_start) {
+                first = min(max(*(a.q_start + b), 0), a.n_q);  // within q whatever q_start holds
+                n = min(*(a.q_start + b + 1), a.n_q) - first;
+            } else {
+                first = b * a.T, n = a.T;
+            }
+            if (n > 0) cnt = (int)(((int64_t)n * a.G + S::kRows - 1) / S::kRows);
+        }
+        int inc = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const bool mine = want >= inc - cnt && want < inc;
+        const unsigned who = __ballot_sync(kFull, mine);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            w.b = base + src;
+            w.first = __shfl_sync(kFull, first, src);
+            w.n = __shfl_sync(kFull, n, src);
+            // the last rows first: they see the most keys
+            w.row0 = __shfl_sync(kFull, inc - 1 - want, src) * S::kRows;
+            w.any = true;
+            break;
+        }
+        want -= __shfl_sync(kFull, inc, 31);
+    }
+    if (!w.any) return w;
+    w.len = max(0, min(*(a.kv_len + w.b), a.max_pages << a.c.page_shift));
+    const int rows = min(S::kRows, w.n * a.G - w.row0);
+    const int p0 = w.len - w.n + (int)a.by_g.div(w.row0), p1 = w.len - w.n + (int)a.by_g.div(w.row0 + rows - 1);
+    const int lo = a.window && p0 >= a.window ? p0 - a.window + 1 : 0;
+    const int hi = a.causal ? min(w.len, p1 + 1) : w.len;
+    w.k0 = lo & ~15;
+    const int tiles = hi > w.k0 ? (hi - w.k0 + S::KT - 1) / S::KT : 0;
+    const int t0 = (int)((int64_t)tiles * split / a.splits), t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    w.k0 += t0 * S::KT;
+    w.tiles = t1 - t0;
+    return w;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttend a) {
+    using S = PShape<D>;
+    constexpr int NG = S::NG, MT = S::MT, NS = S::NS, KT = S::KT, kRec = S::kRec;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* const smem =
+        smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023);  // operand tiles on 1 KB
+    unsigned char* const sq = smem;                              // [MT][NG chunks of 64 dims][128 rows][128 bytes]
+    unsigned char* const sk = sq + MT * S::kQBytes;              // [stages][NG][KT][128 bytes]
+    unsigned char* const sv = sk + S::kStages * S::kTile;
+    Bars& B = *reinterpret_cast<Bars*>(sv + S::kStages * S::kTile);
+    static_assert(sizeof(Bars) <= 1024);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        ptx::mbar_init(&B.q_full, 32 * S::kSoftWarps);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&B.k_full[i], 128);
+            ptx::mbar_init(&B.v_full[i], 128);
+            ptx::mbar_init(&B.k_empty[i], 1);
+            ptx::mbar_init(&B.v_empty[i], 1);
+            ptx::mbar_init(&B.s_full[i], 1);
+            ptx::mbar_init(&B.p_full[i], 128);
+            ptx::mbar_init(&B.o_full[i], 1);
+        }
+        ptx::mbar_init(&B.drain, 1);
+        B.abort = 0;
+        B.n_poison = 0;
+        for (int i = 0; i < 8; ++i) B.hide[i] = make_uint4(0, 0, 0, 0);
+        B.poison_lo = 0x7FFFFFFF;
+        B.poison_hi = -1;
+    }
+    ptx::fence_mbar_init();
+    if (warp == S::kWarpMma) {
+        ptx::tmem_alloc(&B.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const Work w = find_work<D>(a, lane);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = B.tmem;
+    volatile int* const abortp = &B.abort;
+    auto give_up = [&](unsigned code) {
+        if (!*abortp) *(volatile unsigned*)a.err = code;
+        *abortp = 1;
+    };
+
+    if (!w.any) {
+    } else if (warp < S::kSoftWarps) {
+        if constexpr (S::kShare) more_registers<176>();
+        // ---------------- a row a thread: queries in, softmax, output ----------------
+        const int mt = warp >> 2, r = tid & 127;
+        const int row = w.row0 + mt * 128 + r;  // of the kv head's rows of this sequence
+        const bool in = row < w.n * a.G;
+        const int tk = in ? (int)a.by_g.div(row) : 0, hq = w.h * a.G + (in ? row - tk * a.G : 0);
+        const int pos = w.len - w.n + tk;
+        const int hi = !in ? 0 : a.causal ? min(w.len, pos + 1) : w.len;
+        const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+        float c;  // scores in base 2 are c times S, c > 0
+        {
+            const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(w.first + tk) * a.qt +
+                                                             (int64_t)hq * a.qh);
+            float top = 0.0f;
+            if (in)
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = *(qp + i);
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<T>(u[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+            int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
+            ex = top == 0.0f || ex == 128 ? 10 : min(max(ex, -100), 110);
+            float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
+            if (a.scale_log2 <= 0.0f) f = a.scale_log2 < 0.0f ? -f : 0.0f;
+            c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - 10 + ex) << 23);
+            const uint32_t dst = ptx::smem_addr(sq + mt * S::kQBytes) + r * 128;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 v = in ? *(qp + i) : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = unpack2<T>(u[e]);
+                    o[e] = pack_h2(x.x * f, x.y * f);
+                }
+                ptx::sts_u4(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&B.q_full);
+        }
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t t_o = tmem + lanes + S::kColO + mt * D;
+        float m = kNone, thr = kNone, l = 0.0f;  // bound, the S that passes it by kLazy, sum of weights
+        bool ok = true;
+        for (int j = 0; j < w.tiles; ++j) {
+            const int sb = MT == 2 ? mt : j & 1;  // S buffer, and its barriers
+            const uint32_t ph = MT == 2 ? j & 1 : (j >> 1) & 1;
+            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.s_full[sb], ph, abortp));
+            if (!ok) {
+                if (lane == 0) give_up(1u << 16);
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t t_s = tmem + lanes + sb * KT;
+            const int key0 = w.k0 + j * KT;
+            const uint4 hv = ptx::lds_u4(ptx::smem_addr(&B.hide[j & 7]));
+            const uint32_t hide[4] = {hv.x, hv.y, hv.z, hv.w};
+            const bool masked = !__all_sync(kFull, key0 >= lo && key0 + KT <= hi && !(hv.x | hv.y | hv.z | hv.w));
+            uint32_t p[KT / 2];
+            // rows that meet their first keys have no bound yet: a first pass finds their largest score
+            bool find = __any_sync(kFull, m == kNone && key0 < hi && key0 + KT > lo);
+            for (;;) {
+                float top = kNone;
+                uint64_t sum = f2(0.0f, 0.0f);
+                const uint64_t cc = f2(c, c), mm = f2(-m, -m);
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * q, s);
+                    ptx::tmem_ld_wait();
+                    if (masked) {
+                        const int k = key0 + 32 * q;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (k + i < lo || k + i >= hi || (hide[q] >> i & 1)) s[i] = 0xFF800000u;  // -inf
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                    if (!find) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 z = f2(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, mm));
+                            const float x = ex2(z.x), y = ex2(z.y);
+                            sum = add2(sum, f2(x, y));
+                            p[16 * q + i / 2] = pack_h2(x, y);
+                        }
+                    }
+                }
+                const bool over = top > thr;
+                if (!__any_sync(kFull, over)) {
+                    if (find) {
+                        find = false;
+                        continue;
+                    }
+                    const float2 x = f2(sum);
+                    l += x.x + x.y;
+                    break;
+                }
+                // some row of the warp passes its bound: its sums so far are rescaled, and the weights made again
+                find = false;
+                const float mn = over ? fmaxf(m, top * c) : m;
+                const float sc = over && m != kNone ? ex2(m - mn) : 1.0f;
+                if (j > 0 && __any_sync(kFull, sc != 1.0f)) {
+                    if (NS == 2) {  // the last product may still run
+                        ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[0], (j - 1) & 1, abortp));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                    }
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + 32 * q, o);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
+                        tmem_st32(t_o + 32 * q, o);
+                    }
+                }
+                l *= sc;
+                m = mn;
+                if (over) thr = fmaxf((mn + kLazy) / c, top);
+            }
+            if (!ok && lane == 0) give_up(1u << 20);
+            if (!ok) break;
+#pragma unroll
+            for (int q = 0; q < KT / 64; ++q) tmem_st32(t_s + 32 * q, p + 32 * q);
+            tmem_st_wait();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&B.p_full[sb]);
+        }
+        // ---- output ----
+        if (ok && w.tiles > 0) {
+            // o_full: once after the last product of a row tile (MT == 2), or after each (NS == 2)
+            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[mt], NS == 2 ? (w.tiles - 1) & 1 : 0, abortp));
+            if (!ok && lane == 0) give_up(1u << 17);
+            ptx::tc_fence_after();
+        }
+        // NaN values are kept out of the products, where a weight of zero would spread them:
+        // the rows that see one are NaN in its group
+        unsigned nan = 0;
+        if (const int np = *(volatile int*)&B.n_poison) {
+            for (int i = 0; i < min(np, kPoison); ++i) {
+                const int e = B.poison[i], k = e >> 2;
+                if (k >= lo && k < hi) nan |= 1u << (e & 3);
+            }
+            if (np > kPoison && B.poison_lo < hi && B.poison_hi >= lo) nan = 15u;
+        }
+        float* const slot = a.part + (size_t)blockIdx.x * S::kSlot;
+        if (ok) {
+            const bool whole = a.splits == 1;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                if (w.tiles > 0) {
+                    tmem_ld32(t_o + 32 * q, o);
+                    ptx::tmem_ld_wait();
+                }
+                const bool bad = nan >> (q / 2) & 1;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (w.tiles == 0 || l == 0.0f)
+                        o[i] = 0;
+                    else if (bad)
+                        o[i] = 0x7FC00000u;
+                if (in && whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)(w.first + tk) * a.ot +
+                                                          (int64_t)hq * a.oh + 32 * q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = pack2<T>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                        dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else if (in) {
+                    uint4* dst = reinterpret_cast<uint4*>(slot + (size_t)(mt * 128 + r) * D + 32 * q);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) __stcg(dst + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+                }
+            }
+            if (in && whole) {
+                if (a.lse) a.lse[(int64_t)(w.first + tk) * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+            } else if (in) {
+                __stcg(slot + (size_t)S::kRows * D + mt * 128 + r, m);
+                __stcg(slot + (size_t)S::kRows * (D + 1) + mt * 128 + r, l);
+            }
+        }
+    } else if (warp < S::kWarpMma) {
+        if constexpr (S::kShare) fewer_registers<112>();
+        // ---------------- dequantisation ----------------
+        // A row's code bytes are kChunks pieces of 16; thread: piece t % kChunks of row t / kChunks, and so on
+        constexpr int kChunks = D / 32, kPerIt = 128 / kChunks, kIts = KT / kPerIt;
+        const int t = tid - 32 * S::kWarpDq, piece = t % kChunks, r0 = t / kChunks;
+        const int32_t* const table = a.table + (int64_t)w.b * a.table_stride;
+        const uint8_t* const head = a.c.pages + (size_t)w.h * (a.c.P >> 4) * kRec;
+        const size_t page_bytes = (size_t)a.c.H * (a.c.P >> 4) * kRec;
+        int64_t at[kIts];  // of each of this thread's rows: the record's offset, or -1
+        uint4 kw[kIts], vw[kIts];
+        uint32_t ka[kIts][NG], va[kIts][NG];
+        auto places = [&](int j) {
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int key = w.k0 + j * KT + it * kPerIt + r0;
+                at[it] = -1;
+                if (key < w.len) {
+                    const int page = *(table + (key >> a.c.page_shift));
+                    if ((unsigned)page < (unsigned)a.c.n_pages)
+                        at[it] = (int64_t)page * page_bytes + (size_t)((key & (a.c.P - 1)) >> 4) * kRec;
+                    else
+                        *(volatile unsigned*)a.bad = 1u;
+                }
+            }
+        };
+        // side 0: keys, 1: values; rows that are not there read as zeros
+        auto fetch = [&](int j, int side, uint4 (&cw)[kIts], uint32_t (&aw)[kIts][NG]) {
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int key = w.k0 + j * KT + it * kPerIt + r0, r = key & 15;
+                cw[it] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) aw[it][g] = 0;
+                if (at[it] >= 0) {
+                    const uint8_t* rec = head + at[it];
+                    cw[it] = *(reinterpret_cast<const uint4*>(rec + (side ? kv_v_codes(D) : 0) + r * (D / 2)) + piece);
+                    const uint32_t* ap = reinterpret_cast<const uint32_t*>(rec + (side ? kv_v_affine(D) : kv_k_affine(D))) + r * NG;
+                    if constexpr (NG == 4) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(ap);
+                        aw[it][0] = x.x, aw[it][1] = x.y, aw[it][2] = x.z, aw[it][3] = x.w;
+                    } else if constexpr (NG == 2) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(ap);
+                        aw[it][0] = x.x, aw[it][1] = x.y;
+                    } else {
+                        aw[it][0] = *(ap);
+                    }
+                }
+            }
+        };
+        // keys of tile j that are not there, for the softmax to leave out; and room for tile j + 2's, eight
+        // tiles after its last use (the softmax is behind by three at most)
+        auto note = [&](int j) {
+            if (t == 0) B.hide[(j + 2) & 7] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int r = it * kPerIt + r0;
+                if (at[it] < 0 && piece == 0 && w.k0 + j * KT + r < w.len)
+                    atomicOr(reinterpret_cast<unsigned*>(&B.hide[j & 7]) + (r >> 5), 1u << (r & 31));
+            }
+        };
+        auto put = [&](int j, int side, unsigned char* tile, const uint4 (&cw)[kIts], uint32_t (&aw)[kIts][NG]) {
+            const uint32_t base = ptx::smem_addr(tile);
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int r = it * kPerIt + r0;
+                if (side) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        if ((aw[it][g] & 0x7C00u) == 0x7C00u || (aw[it][g] & 0x7C000000u) == 0x7C000000u) {
+                            aw[it][g] = 0;
+                            if (piece == 0) {
+                                const int key = w.k0 + j * KT + r, k = atomicAdd(&B.n_poison, 1);
+                                if (k < kPoison) B.poison[k] = key * 4 + g;
+                                atomicMin(&B.poison_lo, key);
+                                atomicMax(&B.poison_hi, key);
+                            }
+                        }
+                }
+                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {  // word 4 piece + x: elements 8i .. 8i+7 of group g
+                    const int g = (4 * piece + x) % NG, i = (4 * piece + x) / NG;
+                    const uint32_t af = NG == 1 ? aw[it][0] : NG == 4 ? aw[it][x] : aw[it][x & 1];
+                    const __half2 s2 = __half2half2(__ushort_as_half((unsigned short)(af & 0xFFFFu)));
+                    const __half2 b2 = __half2half2(__ushort_as_half((unsigned short)(af >> 16)));
+                    ptx::sts_u4(base + g * (KT * 128) + r * 128 + ((i ^ (r & 7)) << 4), dequant8(words[x], s2, b2));
+                }
+            }
+        };
+        if (w.tiles > 0) {
+            places(0);
+            fetch(0, 0, kw, ka);
+            fetch(0, 1, vw, va);
+        }
+        bool ok = true;
+        for (int j = 0; j < w.tiles && ok; ++j) {
+            const int st = j & 1;
+            const uint32_t ph = ((j >> 1) & 1) ^ 1;
+            const bool more = j + 1 < w.tiles;
+            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.k_empty[st], ph, abortp));
+            if (!ok) break;
+            note(j);
+            if (more) places(j + 1);
+            put(j, 0, sk + st * S::kTile, kw, ka);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&B.k_full[st]);
+            if (more) fetch(j + 1, 0, kw, ka);
+            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.v_empty[st], ph, abortp));
+            if (!ok) break;
+            put(j, 1, sv + st * S::kTile, vw, va);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&B.v_full[st]);
+            if (more) fetch(j + 1, 1, vw, va);
+        }
+        if (!ok && lane == 0) give_up(1u << 18);
+    } else {
+        if constexpr (S::kShare) fewer_registers<48>();
+      if (warp == S::kWarpMma && lane == 0 && w.tiles > 0) {
+        // ---------------- MMA issue ----------------
+        const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
+        const uint64_t dq = sw128_desc(ptx::smem_addr(sq)), dk = sw128_desc(ptx::smem_addr(sk));
+        const uint64_t dv = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
+        auto qk = [&](int mt, int sb, int st) {  // S[sb] = Q[mt] K[st]^T
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const int chunk = k >> 2, in = k & 3;
+                ptx::mma_f16_ss(tmem + sb * KT, dq + ((mt * S::kQBytes + chunk * (128 * 128) + in * 32) >> 4),
+                                dk + ((st * S::kTile + chunk * (KT * 128) + in * 32) >> 4), id_s, k > 0);
+            }
+        };
+        auto pv = [&](int mt, int sb, int st, int j) {  // O[mt] += P[sb] V[st]
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+                mma_f16_ts(tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, dv + ((st * S::kTile + k * 2048) >> 4), id_o,
+                           j > 0 || k > 0);
+        };
+        auto wait = [&](uint64_t* bar, uint32_t ph) { return ptx::mbar_wait_bounded(bar, ph, abortp); };
+        bool ok = wait(&B.q_full, 0);
+        // every commit's arrival is waited for by somebody, so none can reach a CTA that has ended
+        auto scores = [&](int j) {  // K of tile j is there
+            const int st = j & 1;
+            if (!wait(&B.k_full[st], (j >> 1) & 1)) return false;
+            ptx::tc_fence_after();
+            return true;
+        };
+        if (MT == 2) {
+            ok = ok && scores(0);
+            if (ok) {
+                for (int mt = 0; mt < 2; ++mt) {
+                    qk(mt, mt, 0);
+                    ptx::mma_commit(&B.s_full[mt]);
+                }
+                if (w.tiles > 2) ptx::mma_commit(&B.k_empty[0]);
+            }
+            for (int j = 0; j < w.tiles && ok; ++j) {
+                const int st = j & 1, nx = (j + 1) & 1;
+                for (int mt = 0; mt < 2 && ok; ++mt) {
+                    ok = wait(&B.p_full[mt], j & 1);
+                    if (mt == 0) ok = ok && wait(&B.v_full[st], (j >> 1) & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    pv(mt, mt, st, j);
+                    if (j + 1 < w.tiles) {
+                        if (mt == 0) ok = scores(j + 1);
+                        if (!ok) break;
+                        qk(mt, mt, nx);
+                        ptx::mma_commit(&B.s_full[mt]);
+                    } else {
+                        ptx::mma_commit(&B.o_full[mt]);
+                    }
+                }
+                if (!ok) break;
+                if (j + 2 < w.tiles) ptx::mma_commit(&B.v_empty[st]);
+                if (j + 3 < w.tiles) ptx::mma_commit(&B.k_empty[nx]);
+            }
+        } else {
+            auto next = [&](int j) {  // S of tile j into buffer j & 1
+                if (!scores(j)) return false;
+                qk(0, j & 1, j & 1);
+                ptx::mma_commit(&B.s_full[j & 1]);
+                if (j + 2 < w.tiles) ptx::mma_commit(&B.k_empty[j & 1]);
+                return true;
+            };
+            for (int j = 0; j < min(2, w.tiles) && ok; ++j) ok = next(j);
+            for (int j = 0; j < w.tiles && ok; ++j) {
+                const int st = j & 1;
+                ok = wait(&B.p_full[st], (j >> 1) & 1) && wait(&B.v_full[st], (j >> 1) & 1);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                pv(0, st, st, j);
+                ptx::mma_commit(&B.o_full[0]);
+                if (j + 2 < w.tiles) {
+                    ptx::mma_commit(&B.v_empty[st]);
+                    ok = next(j + 2);
+                }
+            }
+        }
+        if (!ok) {
+            give_up(1u << 19);
+            ptx::mma_commit(&B.drain);  // what was issued finishes before tensor memory is given back
+            ptx::mbar_wait_bounded(&B.drain, 0, nullptr);
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == S::kWarpMma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Adds the splits of a row tile's partial results; block (tile and kv head, row
+// group of 8): a warp a row.
+template <int D, class T>
+__global__ void __launch_bounds__(256) kv_prompt_join_kernel(const __grid_constant__ KvAttend a) {
+    using S = PShape<D>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    // the work of split 0 of this block's tile
+    const unsigned x = blockIdx.x / (S::kRows / 8), r = blockIdx.x % (S::kRows / 8) * 8 + warp;
+    const unsigned h = x % (unsigned)a.c.H;
+    int want = (int)(x / (unsigned)a.c.H), first = 0, row0 = -1, nn = 0;
+    for (int base = 0; base < a.B; base += 32) {
+        const int b = base + lane;
+        int f = 0, n = 0, cnt = 0;
+        if (b < a.B) {
+            if (a.q_start) {
+                f = min(max(*(a.q_start + b), 0), a.n_q);
+                n = min(*(a.q_start + b + 1), a.n_q) - f;
+            } else {
+                f = b * a.T, n = a.T;
+            }
+            if (n > 0) cnt = (int)(((int64_t)n * a.G + S::kRows - 1) / S::kRows);
+        }
+        int inc = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned who = __ballot_sync(kFull, want >= inc - cnt && want < inc);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            first = __shfl_sync(kFull, f, src);
+            nn = __shfl_sync(kFull, n, src);
+            row0 = __shfl_sync(kFull, inc - 1 - want, src) * S::kRows;
+            break;
+        }
+        want -= __shfl_sync(kFull, inc, 31);
+    }
+    if (row0 < 0) return;
+    const int row = row0 + (int)r;
+    if (row >= nn * a.G) return;
+    const int tk = (int)a.by_g.div(row), hq = (int)h * a.G + row - tk * a.G;
+    const float* p0 = a.part + (size_t)x * a.splits * S::kSlot;
+    float M = kNone, L = 0.0f;
+    for (int p = lane; p < a.splits; p += 32) M = fmaxf(M, p0[(size_t)p * S::kSlot + (size_t)S::kRows * D + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    constexpr int E = D / 32;
+    float y[E] = {};
+#pragma unroll 4
+    for (int p = 0; p < a.splits; ++p) {
+        const float* s = p0 + (size_t)p * S::kSlot;
+        const float wt = ex2(s[(size_t)S::kRows * D + r] - M);
+        L = fmaf(wt, s[(size_t)S::kRows * (D + 1) + r], L);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(s + (size_t)r * D + lane * E + e);
+            y[e] = fmaf(wt, v.x, y[e]), y[e + 1] = fmaf(wt, v.y, y[e + 1]);
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + (int64_t)(first + tk) * a.ot + (int64_t)hq * a.oh + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(y[e] * inv, y[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[(int64_t)(first + tk) * a.Hq + hq] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
+}
+
+// Row tiles of a call, at most: the sequences' remainders are known on the device only.
+int64_t row_tiles(const KvAttend& a, int rows) {
+    return a.q_start ? (int64_t)a.n_q * a.G / rows + a.B : (int64_t)a.B * (((int64_t)a.T * a.G + rows - 1) / rows);
+}
+
+template <int D, class T>
+cudaError_t launch_prompt(KvAttend a, int max_len, int sms, cudaStream_t s, int* launched) {
+    using S = PShape<D>;
+    const int64_t work = row_tiles(a, S::kRows) * a.c.H;
+    auto kernel = kv_prompt_kernel<D, T>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
+    if (e != cudaSuccess) return e;
+    // too few to fill the GPU: the keys are split, four tiles of them to a CTA at least
+    a.splits = 1;
+    if (a.part && work < sms) {
+        const int64_t most = (max_len + 4 * S::KT - 1) / (4 * S::KT);
+        a.splits = (int)std::max<int64_t>(1, std::min(sms / work, most));
+    }
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(work * a.splits)), dim3(S::kThreads), S::kSmem, s, true, &attr);
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    *launched = 2;
+    const cudaLaunchConfig_t jcfg = launch_config(dim3((unsigned)(work * (S::kRows / 8))), dim3(256), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&jcfg, kv_prompt_join_kernel<D, T>, a);
+}
+
+}  // namespace
+
+bool kv_prompt_splits(const KvAttend& a, int d, int sms) {
+    return row_tiles(a, d == 256 ? PShape<256>::kRows : PShape<128>::kRows) * a.c.H < sms;
+}
+
+cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int max_len, int sms, cudaStream_t s, int* launched) {
+    const bool bf = t == MOE_BF16;
+    if (d == 64)
+        return bf ? launch_prompt<64, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<64, __half>(a, max_len, sms, s, launched);
+    if (d == 128)
+        return bf ? launch_prompt<128, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<128, __half>(a, max_len, sms, s, launched);
+    return bf ? launch_prompt<256, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<256, __half>(a, max_len, sms, s, launched);
+}
+
+}  // namespace moe

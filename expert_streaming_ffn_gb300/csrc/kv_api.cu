@@ -40,6 +40,9 @@ void kv_state_destroy(KvState* st) {
     delete st;
 }
 
+// Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel takes.
+constexpr int kDecodeCols = 16;
+
 constexpr size_t kJoinBytes = 1024 * sizeof(KvJoin);  // for up to 1,024 CTAs
 
 // The workspace of an attention call, made by the first of them.
@@ -49,7 +52,7 @@ moe_status ensure_workspace(KvState* S, int device) {
     CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
     if ((size_t)sms * kKvMaxCtas * sizeof(KvJoin) > kJoinBytes)
         return set_error(MOE_ECUDA, "moe_kv_attend: %d SMs are more than it is made for", sms);
-    const size_t bytes = kJoinBytes + (size_t)sms * kKvMaxCtas * kKvPartFloats * sizeof(float);
+    const size_t bytes = kJoinBytes + (size_t)sms * kKvPartFloats * sizeof(float);
     if (!S->ws_done) CUDA_TRY(cudaEventCreateWithFlags(&S->ws_done, cudaEventDisableTiming));
     unsigned char* p = nullptr;
     if (cudaMalloc(&p, bytes) != cudaSuccess) {
@@ -273,19 +276,22 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.min_units = 32;
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
+    const bool prompt = (int64_t)p->max_q * a.G > kDecodeCols;
     // few short segments are never cut between CTAs: such a call leaves the workspace alone
     const int64_t blocks = (int64_t)p->max_pages * cache->page_tokens / kKvBlock;
     const int64_t segs = ((int64_t)p->n_q * a.G / 8 + p->batch) * cache->n_kv_heads;
-    const bool shared = blocks > a.min_units || segs > S->sms;
+    const bool shared = prompt ? kv_prompt_splits(a, d, S->sms) : blocks > a.min_units || segs > S->sms;
     if (shared) a.join = reinterpret_cast<KvJoin*>(S->ws);
+    if (!shared) a.part = prompt ? nullptr : a.part;
     bool capturing = true;
     if (shared && (st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
     const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
-    const int64_t cols = (int64_t)p->max_q * a.G;
     int launched = 1;
-    CUDA_TRY(launch_kv_attend(a, d, p->dtype, (int)(cols < 1 << 20 ? cols : 1 << 20), S->sms, s, &launched));
+    const int cap = p->max_pages * cache->page_tokens;
+    CUDA_TRY(prompt ? launch_kv_prompt(a, d, p->dtype, p->max_len ? (p->max_len < cap ? p->max_len : cap) : cap, S->sms, s, &launched)
+                    : launch_kv_attend(a, d, p->dtype, p->max_q * a.G, S->sms, s, &launched));
     for (; launched > 1; --launched) ctx_count_launch(C);  // the first is counted already
     return workspace_end(S, s, capturing);
 }

@@ -81,13 +81,20 @@ struct KvAttend {
     // range and ends in another's, and two partial results; null: none can be cut
     KvJoin* join;
     float* part;
+    int splits;     // prompts: CTAs that share a row tile's keys
     int min_units;  // fewest blocks of 16 tokens that a CTA takes
 };
 
-constexpr int kKvMaxCtas = 2;                       // resident CTAs per SM of any of the kernels
-constexpr size_t kKvPartFloats = 2 * 16 * (256 + 2);  // partial results of one CTA, at most
+constexpr int kKvMaxCtas = 2;  // resident CTAs per SM of any of the kernels
+// Floats of partial results per SM: one row tile's of the prompt kernel, 256 rows of
+// 128 elements and two statistics; the decode kernel needs less.
+constexpr size_t kKvPartFloats = 256 * (128 + 2);
 
 // *launched gets the number of kernels. cols: query columns (new tokens * query heads per kv head) of a sequence, as the caller knows them
 cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s, int* launched);
+
+// The same for many columns a sequence. kv_prompt_splits: whether it may use the workspace.
+bool kv_prompt_splits(const KvAttend& a, int d, int sms);
+cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int max_len, int sms, cudaStream_t s, int* launched);
 
 }  // namespace moe
