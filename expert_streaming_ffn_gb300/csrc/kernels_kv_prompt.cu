@@ -9,9 +9,9 @@
 //     as it lies, [key][dim], as an operand whose rows run along dim;
 //   one thread issues S = Q K^T into tensor memory and, later, O += P V with P
 //     from tensor memory, where it takes the place of S;
-//   four warps per tile, a row a thread, turn S into P = 2^(c s - m), fp16. The
-//     bound m moves only when a score passes it by 8 (P <= 2^8), and then O is
-//     rescaled in tensor memory; so S is read once.
+//   four warps per tile, a row a thread, turn S into P = 2^(c s - m), fp16, in two
+//     halves, so that O += P V starts on the first. The bound m moves only when a
+//     score passes it by 8 (P <= 2^8), and then O is rescaled in tensor memory.
 // With two tiles, one's softmax runs under the other's products; with one tile
 // (head_dim 256, whose O takes half of tensor memory) S has two buffers instead.
 // Few rows: the keys are split over CTAs, fp32 partial results joined by a
@@ -44,12 +44,14 @@ struct PShape {
     static constexpr int KT = D <= 128 ? 128 : 64; // keys of a tile
     static constexpr int kRows = 128 * MT;
     static constexpr int kRec = kv_record_bytes(D);
-    static constexpr int kSoftWarps = 4 * MT, kWarpDq = kSoftWarps, kWarpMma = kSoftWarps + 4;
-    // Two row tiles: four warpgroups (the last one issues; three of its warps idle), whose
-    // registers are shared out anew, 2 * 176 + 112 + 48 = 4 * 128. One: three warps a scheduler at
-    // most, 168 registers each, as they are.
+    // Warp 0 issues (its warpgroup's other three idle), warps 4 to 7 dequantise, the rest are the
+    // softmax's. The issuing warp comes first as the scheduler prefers older warps: as the last one
+    // it took 110 ns to issue a product of 35 ns.
+    static constexpr int kWarpMma = 0, kWarpDq = 4, kWarpSoft = 8, kSoftWarps = 4 * MT;
+    static constexpr int kThreads = 32 * (kWarpSoft + kSoftWarps);
+    // With two row tiles the warpgroups share the registers out anew, 56 + 104 + 2 * 176 = 4 * 128;
+    // with one there are 168 for each thread.
     static constexpr bool kShare = MT == 2;
-    static constexpr int kThreads = kShare ? 512 : 32 * (kSoftWarps + 5);
     static constexpr int kQBytes = 128 * D * 2;  // one row tile
     static constexpr int kTile = KT * D * 2;     // K or V
     static constexpr int kStages = 2;
@@ -59,7 +61,7 @@ struct PShape {
 };
 
 struct Bars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], drain;
     uint32_t tmem;
     int abort;
     int n_poison, poison_lo, poison_hi;
@@ -102,7 +104,7 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
 #define W8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
 
 // 32 lanes x 32 columns of tensor memory, thread i lane (base + i)
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -116,6 +118,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::R8(v, 0),
         R8(v, 8), R8(v, 16), R8(v, 24), "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::R8(v, 0),
+        R8(v, 8), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : W8(v, 0) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::R8(v, 0), "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -251,7 +266,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             ptx::mbar_init(&B.k_empty[i], 1);
             ptx::mbar_init(&B.v_empty[i], 1);
             ptx::mbar_init(&B.s_full[i], 1);
-            ptx::mbar_init(&B.p_full[i], 128);
+            for (int h = 0; h < 2; ++h) ptx::mbar_init(&B.p_full[i][h], 128);
             ptx::mbar_init(&B.o_full[i], 1);
         }
         ptx::mbar_init(&B.drain, 1);
@@ -280,10 +295,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
     };
 
     if (!w.any) {
-    } else if (warp < S::kSoftWarps) {
+    } else if (warp >= S::kWarpSoft) {
         if constexpr (S::kShare) more_registers<176>();
         // ---------------- a row a thread: queries in, softmax, output ----------------
-        const int mt = warp >> 2, r = tid & 127;
+        const int mt = (warp - S::kWarpSoft) >> 2, r = tid & 127;
         const int row = w.row0 + mt * 128 + r;  // of the kv head's rows of this sequence
         const bool in = row < w.n * a.G;
         const int tk = in ? (int)a.by_g.div(row) : 0, hq = w.h * a.G + (in ? row - tk * a.G : 0);
@@ -345,77 +360,67 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             const uint4 hv = ptx::lds_u4(ptx::smem_addr(&B.hide[j & 7]));
             const uint32_t hide[4] = {hv.x, hv.y, hv.z, hv.w};
             const bool masked = !__all_sync(kFull, key0 >= lo && key0 + KT <= hi && !(hv.x | hv.y | hv.z | hv.w));
-            uint32_t p[KT / 2];
-            // rows that meet their first keys have no bound yet: a first pass finds their largest score
-            bool find = __any_sync(kFull, m == kNone && key0 < hi && key0 + KT > lo);
-            for (;;) {
-                float top = kNone;
-                uint64_t sum = f2(0.0f, 0.0f);
-                const uint64_t cc = f2(c, c), mm = f2(-m, -m);
+            uint32_t s[KT];
 #pragma unroll
-                for (int q = 0; q < KT / 32; ++q) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + 32 * q, s);
-                    ptx::tmem_ld_wait();
-                    if (masked) {
-                        const int k = key0 + 32 * q;
+            for (int q = 0; q < KT / 32; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
+            ptx::tmem_ld_wait();
+            if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (k + i < lo || k + i >= hi || (hide[q] >> i & 1)) s[i] = 0xFF800000u;  // -inf
-                    }
+                for (int i = 0; i < KT; ++i)
+                    if (key0 + i < lo || key0 + i >= hi || (hide[i / 32] >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
+            }
+            float top = kNone;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                    if (!find) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 z = f2(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, mm));
-                            const float x = ex2(z.x), y = ex2(z.y);
-                            sum = add2(sum, f2(x, y));
-                            p[16 * q + i / 2] = pack_h2(x, y);
-                        }
-                    }
-                }
-                const bool over = top > thr;
-                if (!__any_sync(kFull, over)) {
-                    if (find) {
-                        find = false;
-                        continue;
-                    }
-                    const float2 x = f2(sum);
-                    l += x.x + x.y;
-                    break;
-                }
-                // some row of the warp passes its bound: its sums so far are rescaled, and the weights made again
-                find = false;
+            for (int i = 0; i < KT; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+            const bool over = top > thr;
+            if (__any_sync(kFull, over)) {
+                // some row of the warp passes its bound: its sums so far are rescaled
                 const float mn = over ? fmaxf(m, top * c) : m;
                 const float sc = over && m != kNone ? ex2(m - mn) : 1.0f;
                 if (j > 0 && __any_sync(kFull, sc != 1.0f)) {
                     if (NS == 2) {  // the last product may still run
                         ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[0], (j - 1) & 1, abortp));
-                        if (!ok) break;
+                        if (!ok) {
+                            if (lane == 0) give_up(1u << 20);
+                            break;
+                        }
                         ptx::tc_fence_after();
                     }
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + 32 * q, o);
+#pragma unroll 1
+                    for (int q = 0; q < D / 8; ++q) {  // few at a time: the scores are in registers
+                        uint32_t o[8];
+                        tmem_ld8(t_o + 8 * q, o);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
-                        tmem_st32(t_o + 32 * q, o);
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
+                        tmem_st8(t_o + 8 * q, o);
                     }
                 }
                 l *= sc;
                 m = mn;
                 if (over) thr = fmaxf((mn + kLazy) / c, top);
             }
-            if (!ok && lane == 0) give_up(1u << 20);
-            if (!ok) break;
+            uint64_t sum = f2(0.0f, 0.0f);
+            const uint64_t cc = f2(c, c), mm = f2(-m, -m);
 #pragma unroll
-            for (int q = 0; q < KT / 64; ++q) tmem_st32(t_s + 32 * q, p + 32 * q);
-            tmem_st_wait();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&B.p_full[sb]);
+            for (int q = 0; q < 2; ++q) {  // in halves, so that the product with V starts on the first
+#pragma unroll
+                for (int i = q * (KT / 2); i < (q + 1) * (KT / 2); i += 2) {
+                    const float2 z = f2(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, mm));
+                    const float x = ex2(z.x), y = ex2(z.y);
+                    sum = add2(sum, f2(x, y));
+                    s[i / 2] = pack_h2(x, y);
+                }
+                if constexpr (KT == 128)
+                    tmem_st32(t_s + 32 * q, s + 32 * q);
+                else
+                    tmem_st16(t_s + 16 * q, s + 16 * q);
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&B.p_full[sb][q]);
+            }
+            const float2 x = f2(sum);
+            l += x.x + x.y;
         }
         // ---- output ----
         if (ok && w.tiles > 0) {
@@ -476,8 +481,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 __stcg(slot + (size_t)S::kRows * (D + 1) + mt * 128 + r, l);
             }
         }
-    } else if (warp < S::kWarpMma) {
-        if constexpr (S::kShare) fewer_registers<112>();
+    } else if (warp >= S::kWarpDq) {
+        if constexpr (S::kShare) fewer_registers<104>();
         // ---------------- dequantisation ----------------
         // A row's code bytes are kChunks pieces of 16; thread: piece t % kChunks of row t / kChunks, and so on
         constexpr int kChunks = D / 32, kPerIt = 128 / kChunks, kIts = KT / kPerIt;
@@ -593,24 +598,26 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         if (!ok && lane == 0) give_up(1u << 18);
     } else {
-        if constexpr (S::kShare) fewer_registers<48>();
+        if constexpr (S::kShare) fewer_registers<56>();
       if (warp == S::kWarpMma && lane == 0 && w.tiles > 0) {
         // ---------------- MMA issue ----------------
         const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
-        const uint64_t dq = sw128_desc(ptx::smem_addr(sq)), dk = sw128_desc(ptx::smem_addr(sk));
-        const uint64_t dv = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
+        // descriptors: the low words hold the address, in 16-byte units, and never carry
+        const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq)), dk0 = sw128_desc(ptx::smem_addr(sk));
+        const uint64_t dv0 = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
+        auto at = [](uint64_t d, uint32_t bytes) { return (d & ~0xFFFFFFFFull) | ((uint32_t)d + (bytes >> 4)); };
         auto qk = [&](int mt, int sb, int st) {  // S[sb] = Q[mt] K[st]^T
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const int chunk = k >> 2, in = k & 3;
-                ptx::mma_f16_ss(tmem + sb * KT, dq + ((mt * S::kQBytes + chunk * (128 * 128) + in * 32) >> 4),
-                                dk + ((st * S::kTile + chunk * (KT * 128) + in * 32) >> 4), id_s, k > 0);
+                ptx::mma_f16_ss(tmem + sb * KT, at(dq0, mt * S::kQBytes + chunk * (128 * 128) + in * 32),
+                                at(dk0, st * S::kTile + chunk * (KT * 128) + in * 32), id_s, k > 0);
             }
         };
-        auto pv = [&](int mt, int sb, int st, int j) {  // O[mt] += P[sb] V[st]
+        auto pv = [&](int mt, int sb, int st, int j, int half) {  // O[mt] += P[sb] V[st], over half the keys
 #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-                mma_f16_ts(tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, dv + ((st * S::kTile + k * 2048) >> 4), id_o,
+            for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
+                mma_f16_ts(tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, at(dv0, st * S::kTile + k * 2048), id_o,
                            j > 0 || k > 0);
         };
         auto wait = [&](uint64_t* bar, uint32_t ph) { return ptx::mbar_wait_bounded(bar, ph, abortp); };
@@ -634,11 +641,15 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             for (int j = 0; j < w.tiles && ok; ++j) {
                 const int st = j & 1, nx = (j + 1) & 1;
                 for (int mt = 0; mt < 2 && ok; ++mt) {
-                    ok = wait(&B.p_full[mt], j & 1);
-                    if (mt == 0) ok = ok && wait(&B.v_full[st], (j >> 1) & 1);
+                    if (mt == 0) ok = wait(&B.v_full[st], (j >> 1) & 1);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && wait(&B.p_full[mt][half], j & 1);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        pv(mt, mt, st, j, half);
+                    }
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    pv(mt, mt, st, j);
                     if (j + 1 < w.tiles) {
                         if (mt == 0) ok = scores(j + 1);
                         if (!ok) break;
@@ -663,10 +674,15 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             for (int j = 0; j < min(2, w.tiles) && ok; ++j) ok = next(j);
             for (int j = 0; j < w.tiles && ok; ++j) {
                 const int st = j & 1;
-                ok = wait(&B.p_full[st], (j >> 1) & 1) && wait(&B.v_full[st], (j >> 1) & 1);
+                ok = wait(&B.v_full[st], (j >> 1) & 1);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && wait(&B.p_full[st][half], (j >> 1) & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    pv(0, st, st, j, half);
+                }
                 if (!ok) break;
-                ptx::tc_fence_after();
-                pv(0, st, st, j);
                 ptx::mma_commit(&B.o_full[0]);
                 if (j + 2 < w.tiles) {
                     ptx::mma_commit(&B.v_empty[st]);
