@@ -134,12 +134,31 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The products, issued by the one lane whose `one` is set while the whole warp comes along: with
+// the operands the same in every lane they are worked out in uniform registers, and a product
+// costs its issuer far less than inside a branch that one lane takes alone.
+// D[tmem] (+)= A[smem] * B[smem]^T, and D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_addr(bar)),
+        "r"(one)
         : "memory");
 }
 
@@ -256,7 +275,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
     unsigned char* const sv = sk + S::kStages * S::kTile;
     Bars& B = *reinterpret_cast<Bars*>(sv + S::kStages * S::kTile);
     static_assert(sizeof(Bars) <= 1024);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's index from lane 0, so that the compiler knows it to be the same in all lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
         ptx::mbar_init(&B.q_full, 32 * S::kSoftWarps);
@@ -287,14 +307,16 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = B.tmem;
+    constexpr uint32_t tmem = 0;  // all 512 columns were allocated: they start at 0, checked below
     volatile int* const abortp = &B.abort;
     auto give_up = [&](unsigned code) {
         if (!*abortp) *(volatile unsigned*)a.err = code;
         *abortp = 1;
     };
 
-    if (!w.any) {
+    const bool based = B.tmem == tmem;
+    if (!based && tid == 0) give_up(1u << 21);
+    if (!w.any || !based) {
     } else if (warp >= S::kWarpSoft) {
         if constexpr (S::kShare) more_registers<176>();
         // ---------------- a row a thread: queries in, softmax, output ----------------
@@ -424,8 +446,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         // ---- output ----
         if (ok && w.tiles > 0) {
-            // o_full: once after the last product of a row tile (MT == 2), or after each (NS == 2)
-            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[mt], NS == 2 ? (w.tiles - 1) & 1 : 0, abortp));
+            // o_full: once after the last product of a row tile (MT == 2), or after each (NS == 2; the last S
+            // says no more than that the third to last is done, so the last two phases are waited for in turn)
+            if (NS == 2 && w.tiles > 1) ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[0], w.tiles & 1, abortp));
+            ok = ok && __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[mt], NS == 2 ? (w.tiles - 1) & 1 : 0, abortp));
             if (!ok && lane == 0) give_up(1u << 17);
             ptx::tc_fence_after();
         }
@@ -599,109 +623,109 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         if (!ok && lane == 0) give_up(1u << 18);
     } else {
         if constexpr (S::kShare) fewer_registers<56>();
-      if (warp == S::kWarpMma && lane == 0 && w.tiles > 0) {
-        // ---------------- MMA issue ----------------
-        const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
-        // descriptors: the low words hold the address, in 16-byte units, and never carry
-        const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq)), dk0 = sw128_desc(ptx::smem_addr(sk));
-        const uint64_t dv0 = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
-        auto at = [](uint64_t d, uint32_t bytes) { return (d & ~0xFFFFFFFFull) | ((uint32_t)d + (bytes >> 4)); };
-        auto qk = [&](int mt, int sb, int st) {  // S[sb] = Q[mt] K[st]^T
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const int chunk = k >> 2, in = k & 3;
-                ptx::mma_f16_ss(tmem + sb * KT, at(dq0, mt * S::kQBytes + chunk * (128 * 128) + in * 32),
-                                at(dk0, st * S::kTile + chunk * (KT * 128) + in * 32), id_s, k > 0);
-            }
-        };
-        auto pv = [&](int mt, int sb, int st, int j, int half) {  // O[mt] += P[sb] V[st], over half the keys
-#pragma unroll
-            for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
-                mma_f16_ts(tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, at(dv0, st * S::kTile + k * 2048), id_o,
-                           j > 0 || k > 0);
-        };
-        auto wait = [&](uint64_t* bar, uint32_t ph) { return ptx::mbar_wait_bounded(bar, ph, abortp); };
-        bool ok = wait(&B.q_full, 0);
-        // every commit's arrival is waited for by somebody, so none can reach a CTA that has ended
-        auto scores = [&](int j) {  // K of tile j is there
-            const int st = j & 1;
-            if (!wait(&B.k_full[st], (j >> 1) & 1)) return false;
-            ptx::tc_fence_after();
-            return true;
-        };
-        if (MT == 2) {
-            ok = ok && scores(0);
-            if (ok) {
-                for (int mt = 0; mt < 2; ++mt) {
-                    qk(mt, mt, 0);
-                    ptx::mma_commit(&B.s_full[mt]);
-                }
-                if (w.tiles > 2) ptx::mma_commit(&B.k_empty[0]);
-            }
-            for (int j = 0; j < w.tiles && ok; ++j) {
-                const int st = j & 1, nx = (j + 1) & 1;
-                for (int mt = 0; mt < 2 && ok; ++mt) {
-                    if (mt == 0) ok = wait(&B.v_full[st], (j >> 1) & 1);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && wait(&B.p_full[mt][half], j & 1);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        pv(mt, mt, st, j, half);
-                    }
-                    if (!ok) break;
-                    if (j + 1 < w.tiles) {
-                        if (mt == 0) ok = scores(j + 1);
-                        if (!ok) break;
-                        qk(mt, mt, nx);
-                        ptx::mma_commit(&B.s_full[mt]);
-                    } else {
-                        ptx::mma_commit(&B.o_full[mt]);
-                    }
-                }
-                if (!ok) break;
-                if (j + 2 < w.tiles) ptx::mma_commit(&B.v_empty[st]);
-                if (j + 3 < w.tiles) ptx::mma_commit(&B.k_empty[nx]);
-            }
-        } else {
-            auto next = [&](int j) {  // S of tile j into buffer j & 1
-                if (!scores(j)) return false;
-                qk(0, j & 1, j & 1);
-                ptx::mma_commit(&B.s_full[j & 1]);
-                if (j + 2 < w.tiles) ptx::mma_commit(&B.k_empty[j & 1]);
-                return true;
+        if (warp == S::kWarpMma) {
+            // ---------------- MMA issue ----------------
+            const uint32_t one = lane == 0;
+            const int tiles = __shfl_sync(kFull, w.tiles, 0);
+            const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
+            // descriptors: the low words hold the address, in 16-byte units, and never carry
+            const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq));
+            const uint64_t dk0 = sw128_desc(ptx::smem_addr(sk));
+            const uint64_t dv0 = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
+            auto at = [](uint64_t d, uint32_t bytes) { return (d & ~0xFFFFFFFFull) | ((uint32_t)d + (bytes >> 4)); };
+            auto wait = [&](uint64_t* bar, uint32_t ph) {
+                const bool got = __all_sync(kFull, ptx::mbar_wait_bounded(bar, ph, abortp));
+                ptx::tc_fence_after();
+                return got;
             };
-            for (int j = 0; j < min(2, w.tiles) && ok; ++j) ok = next(j);
-            for (int j = 0; j < w.tiles && ok; ++j) {
-                const int st = j & 1;
-                ok = wait(&B.v_full[st], (j >> 1) & 1);
+            auto qk = [&](int mt, int sb, int st) {  // S[sb] = Q[mt] K[st]^T
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int chunk = k >> 2, in = k & 3;
+                    mma_ss(one, tmem + sb * KT, at(dq0, mt * S::kQBytes + chunk * (128 * 128) + in * 32),
+                           at(dk0, st * S::kTile + chunk * (KT * 128) + in * 32), id_s, k > 0);
+                }
+            };
+            // O[mt] += P[sb] V[st], over half the keys as soon as their weights are there
+            auto pv = [&](int mt, int sb, int st, int j, uint32_t ph) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    ok = ok && wait(&B.p_full[st][half], (j >> 1) & 1);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    pv(0, st, st, j, half);
+                    if (!wait(&B.p_full[sb][half], ph)) return false;
+#pragma unroll
+                    for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
+                        mma_ts(one, tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, at(dv0, st * S::kTile + k * 2048), id_o,
+                               j > 0 || k > 0);
                 }
-                if (!ok) break;
-                ptx::mma_commit(&B.o_full[0]);
-                if (j + 2 < w.tiles) {
-                    ptx::mma_commit(&B.v_empty[st]);
-                    ok = next(j + 2);
+                return true;
+            };
+            // Every commit's arrival is waited for by somebody, so none can reach a CTA that has ended.
+            bool ok = tiles > 0 && wait(&B.q_full, 0) && wait(&B.k_full[0], 0);
+            if (MT == 2) {
+                if (ok) {
+                    for (int mt = 0; mt < 2; ++mt) {
+                        qk(mt, mt, 0);
+                        commit(one, &B.s_full[mt]);
+                    }
+                    if (tiles > 2) commit(one, &B.k_empty[0]);
+                }
+                auto step = [&](int j, int st) {  // tile j, st = j & 1
+                    const uint32_t ph = (j >> 1) & 1;
+                    const bool more = j + 1 < tiles;
+                    if (!wait(&B.v_full[st], ph)) return false;
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        if (!pv(mt, mt, st, j, j & 1)) return false;
+                        if (more) {
+                            if (mt == 0 && !wait(&B.k_full[st ^ 1], ((j + 1) >> 1) & 1)) return false;
+                            qk(mt, mt, st ^ 1);
+                            commit(one, &B.s_full[mt]);
+                        } else {
+                            commit(one, &B.o_full[mt]);
+                        }
+                    }
+                    if (j + 2 < tiles) commit(one, &B.v_empty[st]);
+                    if (j + 3 < tiles) commit(one, &B.k_empty[st ^ 1]);
+                    return true;
+                };
+                for (int j = 0; j < tiles && ok; j += 2) {
+                    ok = step(j, 0);
+                    if (ok && j + 1 < tiles) ok = step(j + 1, 1);
+                }
+            } else {
+                auto scores = [&](int j, int st) {  // S of tile j into buffer st = j & 1
+                    if (!wait(&B.k_full[st], (j >> 1) & 1)) return false;
+                    qk(0, st, st);
+                    commit(one, &B.s_full[st]);
+                    if (j + 2 < tiles) commit(one, &B.k_empty[st]);
+                    return true;
+                };
+                auto step = [&](int j, int st) {
+                    const uint32_t ph = (j >> 1) & 1;
+                    if (!wait(&B.v_full[st], ph) || !pv(0, st, st, j, ph)) return false;
+                    commit(one, &B.o_full[0]);
+                    if (j + 2 >= tiles) return true;
+                    commit(one, &B.v_empty[st]);
+                    return scores(j + 2, st);
+                };
+                ok = ok && scores(0, 0);
+                if (ok && tiles > 1) ok = scores(1, 1);
+                for (int j = 0; j < tiles && ok; j += 2) {
+                    ok = step(j, 0);
+                    if (ok && j + 1 < tiles) ok = step(j + 1, 1);
                 }
             }
+            if (!ok && tiles > 0) {
+                if (one) give_up(1u << 19);
+                commit(one, &B.drain);  // what was issued finishes before tensor memory is given back
+                ptx::mbar_wait_bounded(&B.drain, 0, nullptr);
+            }
         }
-        if (!ok) {
-            give_up(1u << 19);
-            ptx::mma_commit(&B.drain);  // what was issued finishes before tensor memory is given back
-            ptx::mbar_wait_bounded(&B.drain, 0, nullptr);
-        }
-      }
     }
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == S::kWarpMma) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(B.tmem, 512);
     }
 }
 
