@@ -7,7 +7,7 @@
 //   four warps dequantise K, then V, from global memory (the next tile's words
 //     already in registers) to fp16 in shared memory, 128-byte swizzled; V is used
 //     as it lies, [key][dim], as an operand whose rows run along dim;
-//   one thread issues S = Q K^T into tensor memory and, later, O += P V with P
+//   two warps issue S = Q K^T into tensor memory and, later, O += P V with P
 //     from tensor memory, where it takes the place of S;
 //   four warps per tile, a row a thread, turn S into P = 2^(c s - m), fp16, in two
 //     halves, so that O += P V starts on the first. The bound m moves only when a
@@ -44,9 +44,9 @@ struct PShape {
     static constexpr int KT = D <= 128 ? 128 : 64; // keys of a tile
     static constexpr int kRows = 128 * MT;
     static constexpr int kRec = kv_record_bytes(D);
-    // Warp 0 issues (its warpgroup's other three idle), warps 4 to 7 dequantise, the rest are the
-    // softmax's. The issuing warp comes first as the scheduler prefers older warps: as the last one
-    // it took 110 ns to issue a product of 35 ns.
+    // Warps 0 and 1 issue (their warpgroup's other two idle), warps 4 to 7 dequantise, the rest are the
+    // softmax's. The issuing warps come first as the scheduler prefers older warps: as the CTA's last,
+    // one warp took 110 ns to issue a product of 38 ns.
     static constexpr int kWarpMma = 0, kWarpDq = 4, kWarpSoft = 8, kSoftWarps = 4 * MT;
     static constexpr int kThreads = 32 * (kWarpSoft + kSoftWarps);
     // With two row tiles the warpgroups share the registers out anew, 56 + 104 + 2 * 176 = 4 * 128;
@@ -61,7 +61,7 @@ struct PShape {
 };
 
 struct Bars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], drain;
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], s_free[2], drain[2];
     uint32_t tmem;
     int abort;
     int n_poison, poison_lo, poison_hi;
@@ -285,11 +285,12 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             ptx::mbar_init(&B.v_full[i], 128);
             ptx::mbar_init(&B.k_empty[i], 1);
             ptx::mbar_init(&B.v_empty[i], 1);
+            ptx::mbar_init(&B.s_free[i], 1);
+            ptx::mbar_init(&B.drain[i], 1);
             ptx::mbar_init(&B.s_full[i], 1);
             for (int h = 0; h < 2; ++h) ptx::mbar_init(&B.p_full[i][h], 128);
             ptx::mbar_init(&B.o_full[i], 1);
         }
-        ptx::mbar_init(&B.drain, 1);
         B.abort = 0;
         B.n_poison = 0;
         for (int i = 0; i < 8; ++i) B.hide[i] = make_uint4(0, 0, 0, 0);
@@ -514,21 +515,28 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         const int32_t* const table = a.table + (int64_t)w.b * a.table_stride;
         const uint8_t* const head = a.c.pages + (size_t)w.h * (a.c.P >> 4) * kRec;
         const size_t page_bytes = (size_t)a.c.H * (a.c.P >> 4) * kRec;
-        int64_t at[kIts];  // of each of this thread's rows: the record's offset, or -1
+        // Of each of this thread's rows of a tile: the page id, and the record's offset, -1 where there
+        // is none. The ids are asked for a tile before the records.
+        int32_t page[kIts];
+        int64_t at[kIts];
         uint4 kw[kIts], vw[kIts];
         uint32_t ka[kIts][NG], va[kIts][NG];
+        auto ask = [&](int j) {
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int key = w.k0 + j * KT + it * kPerIt + r0;
+                page[it] = key < w.len ? table[key >> a.c.page_shift] : -1;
+            }
+        };
         auto places = [&](int j) {
 #pragma unroll
             for (int it = 0; it < kIts; ++it) {
                 const int key = w.k0 + j * KT + it * kPerIt + r0;
                 at[it] = -1;
-                if (key < w.len) {
-                    const int page = *(table + (key >> a.c.page_shift));
-                    if ((unsigned)page < (unsigned)a.c.n_pages)
-                        at[it] = (int64_t)page * page_bytes + (size_t)((key & (a.c.P - 1)) >> 4) * kRec;
-                    else
-                        *(volatile unsigned*)a.bad = 1u;
-                }
+                if ((unsigned)page[it] < (unsigned)a.c.n_pages)
+                    at[it] = (int64_t)page[it] * page_bytes + (size_t)((key & (a.c.P - 1)) >> 4) * kRec;
+                else if (key < w.len)
+                    *(volatile unsigned*)a.bad = 1u;
             }
         };
         // side 0: keys, 1: values; rows that are not there read as zeros
@@ -596,9 +604,11 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
         };
         if (w.tiles > 0) {
+            ask(0);
             places(0);
             fetch(0, 0, kw, ka);
             fetch(0, 1, vw, va);
+            ask(1);
         }
         bool ok = true;
         for (int j = 0; j < w.tiles && ok; ++j) {
@@ -608,11 +618,14 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.k_empty[st], ph, abortp));
             if (!ok) break;
             note(j);
-            if (more) places(j + 1);
             put(j, 0, sk + st * S::kTile, kw, ka);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.k_full[st]);
-            if (more) fetch(j + 1, 0, kw, ka);
+            if (more) {
+                places(j + 1);
+                fetch(j + 1, 0, kw, ka);
+                ask(j + 2);
+            }
             ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.v_empty[st], ph, abortp));
             if (!ok) break;
             put(j, 1, sv + st * S::kTile, vw, va);
@@ -623,14 +636,16 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         if (!ok && lane == 0) give_up(1u << 18);
     } else {
         if constexpr (S::kShare) fewer_registers<56>();
-        if (warp == S::kWarpMma) {
+        if (warp < 2) {
             // ---------------- MMA issue ----------------
+            // One warp with two row tiles: a warp for each would have products of both kinds (Q K^T from
+            // shared memory, P V from tensor memory) alternate, and each change costs some 130 cycles
+            // (1.53 ms against 1.08 for 4,096 tokens behind 12,288). With one row tile S in one, O in another.
             const uint32_t one = lane == 0;
             const int tiles = __shfl_sync(kFull, w.tiles, 0);
             const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
             // descriptors: the low words hold the address, in 16-byte units, and never carry
-            const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq));
-            const uint64_t dk0 = sw128_desc(ptx::smem_addr(sk));
+            const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq)), dk0 = sw128_desc(ptx::smem_addr(sk));
             const uint64_t dv0 = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
             auto at = [](uint64_t d, uint32_t bytes) { return (d & ~0xFFFFFFFFull) | ((uint32_t)d + (bytes >> 4)); };
             auto wait = [&](uint64_t* bar, uint32_t ph) {
@@ -659,56 +674,61 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 return true;
             };
             // Every commit's arrival is waited for by somebody, so none can reach a CTA that has ended.
-            bool ok = tiles > 0 && wait(&B.q_full, 0) && wait(&B.k_full[0], 0);
-            if (MT == 2) {
-                if (ok) {
-                    for (int mt = 0; mt < 2; ++mt) {
-                        qk(mt, mt, 0);
-                        commit(one, &B.s_full[mt]);
-                    }
-                    if (tiles > 2) commit(one, &B.k_empty[0]);
-                }
+            bool ok = tiles > 0;
+            if (MT == 2 && warp == 0) {
+                auto scores = [&](int mt, int j, int st) {  // S[mt] of tile j
+                    qk(mt, mt, st);
+                    commit(one, &B.s_full[mt]);
+                    if (mt == 1 && j + 2 < tiles) commit(one, &B.k_empty[st]);
+                };
                 auto step = [&](int j, int st) {  // tile j, st = j & 1
-                    const uint32_t ph = (j >> 1) & 1;
                     const bool more = j + 1 < tiles;
-                    if (!wait(&B.v_full[st], ph)) return false;
+                    if (!wait(&B.v_full[st], (j >> 1) & 1) || (more && !wait(&B.k_full[st ^ 1], ((j + 1) >> 1) & 1)))
+                        return false;
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         if (!pv(mt, mt, st, j, j & 1)) return false;
-                        if (more) {
-                            if (mt == 0 && !wait(&B.k_full[st ^ 1], ((j + 1) >> 1) & 1)) return false;
-                            qk(mt, mt, st ^ 1);
-                            commit(one, &B.s_full[mt]);
-                        } else {
+                        if (more)
+                            scores(mt, j + 1, st ^ 1);
+                        else
                             commit(one, &B.o_full[mt]);
-                        }
                     }
                     if (j + 2 < tiles) commit(one, &B.v_empty[st]);
-                    if (j + 3 < tiles) commit(one, &B.k_empty[st ^ 1]);
                     return true;
                 };
+                ok = ok && wait(&B.q_full, 0) && wait(&B.k_full[0], 0);
+                if (ok)
+                    for (int mt = 0; mt < 2; ++mt) scores(mt, 0, 0);
                 for (int j = 0; j < tiles && ok; j += 2) {
                     ok = step(j, 0);
                     if (ok && j + 1 < tiles) ok = step(j + 1, 1);
                 }
-            } else {
-                auto scores = [&](int j, int st) {  // S of tile j into buffer st = j & 1
+            } else if (MT == 2) {
+            } else if (warp == 0) {
+                auto scores = [&](int j, int st) {  // S of tile j into buffer st = j & 1, once tile j - 2's P is used
+                    if (j >= 2 && !wait(&B.s_free[st], ((j >> 1) & 1) ^ 1)) return false;
                     if (!wait(&B.k_full[st], (j >> 1) & 1)) return false;
                     qk(0, st, st);
                     commit(one, &B.s_full[st]);
                     if (j + 2 < tiles) commit(one, &B.k_empty[st]);
                     return true;
                 };
+                ok = ok && wait(&B.q_full, 0);
+                for (int j = 0; j < tiles && ok; j += 2) {
+                    ok = scores(j, 0);
+                    if (ok && j + 1 < tiles) ok = scores(j + 1, 1);
+                }
+            } else {
                 auto step = [&](int j, int st) {
                     const uint32_t ph = (j >> 1) & 1;
                     if (!wait(&B.v_full[st], ph) || !pv(0, st, st, j, ph)) return false;
                     commit(one, &B.o_full[0]);
-                    if (j + 2 >= tiles) return true;
-                    commit(one, &B.v_empty[st]);
-                    return scores(j + 2, st);
+                    if (j + 2 < tiles) {
+                        commit(one, &B.v_empty[st]);
+                        commit(one, &B.s_free[st]);
+                    }
+                    return true;
                 };
-                ok = ok && scores(0, 0);
-                if (ok && tiles > 1) ok = scores(1, 1);
                 for (int j = 0; j < tiles && ok; j += 2) {
                     ok = step(j, 0);
                     if (ok && j + 1 < tiles) ok = step(j + 1, 1);
@@ -716,8 +736,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             if (!ok && tiles > 0) {
                 if (one) give_up(1u << 19);
-                commit(one, &B.drain);  // what was issued finishes before tensor memory is given back
-                ptx::mbar_wait_bounded(&B.drain, 0, nullptr);
+                commit(one, &B.drain[warp]);  // what was issued finishes before tensor memory is given back
+                ptx::mbar_wait_bounded(&B.drain[warp], 0, nullptr);
             }
         }
     }
