@@ -56,7 +56,7 @@ struct PShape {
     static constexpr int kTile = KT * D * 2;     // K or V
     static constexpr int kStages = 2;
     static constexpr int kColO = MT * NS * KT;   // tensor memory: S buffers, then O
-    static constexpr int kSmem = 1024 + MT * kQBytes + 2 * kStages * kTile + 1024;
+    static constexpr int kSmem = MT * kQBytes + 2 * kStages * kTile + 1024;
     static constexpr int kSlot = kRows * (D + 2);  // floats of a partial result: o[row][D], then m and l
 };
 
@@ -134,31 +134,21 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The products, issued by the one lane whose `one` is set while the whole warp comes along: with
-// the operands the same in every lane they are worked out in uniform registers, and a product
-// costs its issuer far less than inside a branch that one lane takes alone.
-// D[tmem] (+)= A[smem] * B[smem]^T, and D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-        : "memory");
+// 1 in one lane of a converged warp, always the same, 0 in the others. The whole warp goes
+// through the issuing loops and this lane issues: the products' operands are then worked out in uniform
+// registers. (One lane in a branch of its own, chosen by its number, took 1.62 ms where this takes 1.03.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_addr(bar)),
-        "r"(one)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -267,9 +257,8 @@ template <int D, class T>
 __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttend a) {
     using S = PShape<D>;
     constexpr int NG = S::NG, MT = S::MT, NS = S::NS, KT = S::KT, kRec = S::kRec;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* const smem =
-        smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023);  // operand tiles on 1 KB
+    // operand tiles lie on 1 KB; at a place the compiler knows, so that their descriptors are constants
+    extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const sq = smem;                              // [MT][NG chunks of 64 dims][128 rows][128 bytes]
     unsigned char* const sk = sq + MT * S::kQBytes;              // [stages][NG][KT][128 bytes]
     unsigned char* const sv = sk + S::kStages * S::kTile;
@@ -315,7 +304,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         *abortp = 1;
     };
 
-    const bool based = B.tmem == tmem;
+    const bool based = B.tmem == tmem && (ptx::smem_addr(smem) & 1023) == 0;
     if (!based && tid == 0) give_up(1u << 21);
     if (!w.any || !based) {
     } else if (warp >= S::kWarpSoft) {
@@ -641,23 +630,20 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             // One warp with two row tiles: a warp for each would have products of both kinds (Q K^T from
             // shared memory, P V from tensor memory) alternate, and each change costs some 130 cycles
             // (1.53 ms against 1.08 for 4,096 tokens behind 12,288). With one row tile S in one, O in another.
-            const uint32_t one = lane == 0;
+            const uint32_t one = elect_one();
             const int tiles = __shfl_sync(kFull, w.tiles, 0);
             const uint32_t id_s = f16_idesc(128, KT), id_o = f16_idesc(128, D) | (1u << 16);  // V: n along the rows
             // descriptors: the low words hold the address, in 16-byte units, and never carry
             const uint64_t dq0 = sw128_desc(ptx::smem_addr(sq)), dk0 = sw128_desc(ptx::smem_addr(sk));
             const uint64_t dv0 = sw128_desc_n(ptx::smem_addr(sv), KT * 128);
             auto at = [](uint64_t d, uint32_t bytes) { return (d & ~0xFFFFFFFFull) | ((uint32_t)d + (bytes >> 4)); };
-            auto wait = [&](uint64_t* bar, uint32_t ph) {
-                const bool got = __all_sync(kFull, ptx::mbar_wait_bounded(bar, ph, abortp));
-                ptx::tc_fence_after();
-                return got;
-            };
+            auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(kFull, ptx::mbar_wait_bounded(bar, ph, abortp)); };
             auto qk = [&](int mt, int sb, int st) {  // S[sb] = Q[mt] K[st]^T
+                if (one)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const int chunk = k >> 2, in = k & 3;
-                    mma_ss(one, tmem + sb * KT, at(dq0, mt * S::kQBytes + chunk * (128 * 128) + in * 32),
+                    ptx::mma_f16_ss(tmem + sb * KT, at(dq0, mt * S::kQBytes + chunk * (128 * 128) + in * 32),
                            at(dk0, st * S::kTile + chunk * (KT * 128) + in * 32), id_s, k > 0);
                 }
             };
@@ -666,9 +652,11 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!wait(&B.p_full[sb][half], ph)) return false;
+                    ptx::tc_fence_after();  // P was written to tensor memory by other threads
+                    if (one)
 #pragma unroll
                     for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
-                        mma_ts(one, tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, at(dv0, st * S::kTile + k * 2048), id_o,
+                        mma_f16_ts(tmem + S::kColO + mt * D, tmem + sb * KT + 8 * k, at(dv0, st * S::kTile + k * 2048), id_o,
                                j > 0 || k > 0);
                 }
                 return true;
@@ -678,8 +666,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             if (MT == 2 && warp == 0) {
                 auto scores = [&](int mt, int j, int st) {  // S[mt] of tile j
                     qk(mt, mt, st);
-                    commit(one, &B.s_full[mt]);
-                    if (mt == 1 && j + 2 < tiles) commit(one, &B.k_empty[st]);
+                    if (one) ptx::mma_commit(&B.s_full[mt]);
+                    if (one && mt == 1 && j + 2 < tiles) ptx::mma_commit(&B.k_empty[st]);
                 };
                 auto step = [&](int j, int st) {  // tile j, st = j & 1
                     const bool more = j + 1 < tiles;
@@ -690,10 +678,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                         if (!pv(mt, mt, st, j, j & 1)) return false;
                         if (more)
                             scores(mt, j + 1, st ^ 1);
-                        else
-                            commit(one, &B.o_full[mt]);
+                        else if (one)
+                            ptx::mma_commit(&B.o_full[mt]);
                     }
-                    if (j + 2 < tiles) commit(one, &B.v_empty[st]);
+                    if (one && j + 2 < tiles) ptx::mma_commit(&B.v_empty[st]);
                     return true;
                 };
                 ok = ok && wait(&B.q_full, 0) && wait(&B.k_full[0], 0);
@@ -709,8 +697,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                     if (j >= 2 && !wait(&B.s_free[st], ((j >> 1) & 1) ^ 1)) return false;
                     if (!wait(&B.k_full[st], (j >> 1) & 1)) return false;
                     qk(0, st, st);
-                    commit(one, &B.s_full[st]);
-                    if (j + 2 < tiles) commit(one, &B.k_empty[st]);
+                    if (one) ptx::mma_commit(&B.s_full[st]);
+                    if (one && j + 2 < tiles) ptx::mma_commit(&B.k_empty[st]);
                     return true;
                 };
                 ok = ok && wait(&B.q_full, 0);
@@ -722,10 +710,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 auto step = [&](int j, int st) {
                     const uint32_t ph = (j >> 1) & 1;
                     if (!wait(&B.v_full[st], ph) || !pv(0, st, st, j, ph)) return false;
-                    commit(one, &B.o_full[0]);
+                    if (one) ptx::mma_commit(&B.o_full[0]);
                     if (j + 2 < tiles) {
-                        commit(one, &B.v_empty[st]);
-                        commit(one, &B.s_free[st]);
+                        if (one) ptx::mma_commit(&B.v_empty[st]);
+                        if (one) ptx::mma_commit(&B.s_free[st]);
                     }
                     return true;
                 };
@@ -736,7 +724,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             if (!ok && tiles > 0) {
                 if (one) give_up(1u << 19);
-                commit(one, &B.drain[warp]);  // what was issued finishes before tensor memory is given back
+                if (one) ptx::mma_commit(&B.drain[warp]);  // what was issued finishes before tensor memory is given back
                 ptx::mbar_wait_bounded(&B.drain[warp], 0, nullptr);
             }
         }
