@@ -17,7 +17,7 @@ struct Row8;  // eight consecutive elements of a row
 template <>
 struct Row8<__nv_bfloat16> {
     static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -39,7 +39,7 @@ struct Row8<__nv_bfloat16> {
 template <>
 struct Row8<__half> {
     static __device__ __forceinline__ void load(const __half* p, float (&x)[8]) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -62,7 +62,7 @@ struct Row8<__half> {
 template <>
 struct Row8<float> {
     static __device__ __forceinline__ void load(const float* p, float (&x)[8]) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
     static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
@@ -82,9 +82,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Eight elements of a group, one thread of the eight that hold it: the word of
-// their codes, and the group's affine word. Called by whole groups.
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t& affine) {
+// The least and the largest of a group's 64 elements, of which each of eight
+// lanes holds eight; NaN if there is one. 16-bit types work in pairs, the largest
+// negated, so that one exchange a step serves both.
+template <class T>
+__device__ __forceinline__ float2 group_range(const float (&x)[8]);
+
+template <>
+__device__ __forceinline__ float2 group_range<float>(const float (&x)[8]) {
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
@@ -96,41 +101,126 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t& affine) {
         lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m));
         hi = max_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m));
     }
-    // the clamp commutes with min and max; NaN passes through both
-    lo = max_nan(min_nan(lo, kF16Max), -kF16Max);
-    hi = max_nan(min_nan(hi, kF16Max), -kF16Max);
+    return make_float2(lo, hi);
+}
+
+template <class P>
+__device__ __forceinline__ float2 group_range_pairs(P p) {  // p: (least, largest negated) of a lane's eight
+#pragma unroll
+    for (int m = 4; m; m >>= 1) {
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&p), m);
+        p = __hmin2_nan(p, *reinterpret_cast<const P*>(&o));
+    }
+    return make_float2((float)p.x, -(float)p.y);
+}
+
+template <>
+__device__ __forceinline__ float2 group_range<__half>(const float (&x)[8]) {
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+    }
+    return group_range_pairs(__floats2half2_rn(lo, -hi));  // exact: the values are halves
+}
+template <>
+__device__ __forceinline__ float2 group_range<__nv_bfloat16>(const float (&x)[8]) {
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+    }
+    return group_range_pairs(__floats2bfloat162_rn(lo, -hi));
+}
+
+// Eight elements of a group, one lane of the eight that hold it: the word of
+// their codes, and the group's affine word. Called by whole warps.
+// The quotient (x - b) / s is IEEE's: t = d y with y = 1 / s rounded to nearest
+// is within an ulp of it, and t + y (d - s t), the remainder exact in a fused
+// multiply-add, rounds to it (Markstein's theorem; s has 11 bits, so its one exception,
+// a divisor of all ones, cannot come up). Adding 1.5 * 2^23 rounds it to an
+// integer, ties to even, in the low bits.
+template <class T>
+__device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t& affine) {
+    const float2 r = group_range<T>(x);
+    float lo = r.x, hi = r.y;
+    if (lo < -kF16Max || hi > kF16Max) {  // held as +-65504; NaN is left as it is
+        lo = max_nan(min_nan(lo, kF16Max), -kF16Max);
+        hi = max_nan(min_nan(hi, kF16Max), -kF16Max);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaxf(fminf(x[i], kF16Max), -kF16Max);
+    }
     const __half b16 = __float2half_rd(lo);
     const float b = __half2float(b16);
     const __half s16 = __float2half_ru(__fdiv_rn(__fsub_rn(hi, b), 15.0f));
-    const float s = __half2float(s16);
+    const float s = __half2float(s16), y = s > 0.0f ? __frcp_rn(s) : 0.0f;
     affine = (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(b16) << 16);
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float c = fmaxf(fminf(x[i], kF16Max), -kF16Max);
-        const float q = s > 0.0f ? rintf(__fdiv_rn(__fsub_rn(c, b), s)) : 0.0f;
-        // element e = {0,2,4,6,1,3,5,7}[n] in nibble n
-        const int n = (i & 1) * 4 + (i >> 1);
-        word |= (uint32_t)(int)q << (4 * n);
+        const float d = __fsub_rn(x[i], b), t = __fmul_rn(d, y);
+        const float q = __fmaf_rn(__fmaf_rn(-t, s, d), y, t);
+        // element i = {0,2,4,6,1,3,5,7}[n] in nibble n; what the sums carry besides is taken off at the end
+        word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * ((i & 1) * 4 + (i >> 1)));
     }
-    return word;
+    uint32_t carried = 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) carried += 0x4B400000u << (4 * n);
+    return s > 0.0f ? word - carried : 0;
 }
 
-// Thread e of the D/8 threads of a row takes elements 8e .. 8e+7 of K and V.
+// N consecutive words, one store
+template <int N>
+__device__ __forceinline__ void store_words(uint32_t* p, const uint32_t (&w)[N]) {
+    if constexpr (N == 4)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (N == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+        *p = w[0];
+}
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *p;
+    }
+}
+
+// Eight threads a row: thread i takes elements 8i .. 8i+7 of every group of K
+// and V. Their words are neighbours in the record, a group's eight threads
+// read 128 bytes side by side.
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvRows a) {
-    constexpr int kPer = D / 8, NG = D / 64;
+    constexpr int NG = D / 64;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const uint64_t idx = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    const unsigned row = (unsigned)(idx / kPer);
-    const int e = (int)(idx % kPer);
+    const unsigned row = (unsigned)(idx >> 3);
+    const int i = (int)(idx & 7);
     const bool in = row < a.n;
     const unsigned t = a.by_head.div(in ? row : 0), h = (in ? row : 0) - t * a.by_head.d;
-    float k[8], v[8];
-    Row8<T>::load(static_cast<const T*>(a.k_in) + (int64_t)t * a.kt + (int64_t)h * a.kh + e * 8, k);
-    Row8<T>::load(static_cast<const T*>(a.v_in) + (int64_t)t * a.vt + (int64_t)h * a.vh + e * 8, v);
-    const int slot = __ldg(a.slots + t);
-    uint32_t ka, va;
-    const uint32_t kw = quantise8(k, ka), vw = quantise8(v, va);
+    const T* kp = static_cast<const T*>(a.k_in) + (int64_t)t * a.kt + (int64_t)h * a.kh + i * 8;
+    const T* vp = static_cast<const T*>(a.v_in) + (int64_t)t * a.vt + (int64_t)h * a.vh + i * 8;
+    float k[NG][8], v[NG][8];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) Row8<T>::load(kp + g * 64, k[g]);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) Row8<T>::load(vp + g * 64, v[g]);
+    const int slot = a.slots[t];
+    uint32_t ka[NG], va[NG], kw[NG], vw[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        kw[g] = quantise8<T>(k[g], ka[g]);
+        vw[g] = quantise8<T>(v[g], va[g]);
+    }
     if (!in || slot < 0) return;
     if ((unsigned)slot >= a.c.n_slots) {
         *(volatile unsigned*)a.bad = 1u;
@@ -138,14 +228,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     }
     const int page = slot >> a.c.page_shift, place = slot & (a.c.P - 1), r = place & 15;
     uint8_t* rec = a.c.pages + (((size_t)page * a.c.H + h) * (a.c.P >> 4) + (place >> 4)) * kv_record_bytes(D);
-    const int g = e >> 3, i = e & 7;
-    const int word = r * (D / 8) + i * NG + g;
-    reinterpret_cast<uint32_t*>(rec)[word] = kw;
-    reinterpret_cast<uint32_t*>(rec + kv_v_codes(D))[word] = vw;
-    if (i == 0) {
-        reinterpret_cast<uint32_t*>(rec + kv_k_affine(D))[r * NG + g] = ka;
-        reinterpret_cast<uint32_t*>(rec + kv_v_affine(D))[r * NG + g] = va;
-    }
+    store_words<NG>(reinterpret_cast<uint32_t*>(rec) + r * (D / 8) + i * NG, kw);
+    store_words<NG>(reinterpret_cast<uint32_t*>(rec + kv_v_codes(D)) + r * (D / 8) + i * NG, vw);
+    if (i == 0) store_words<NG>(reinterpret_cast<uint32_t*>(rec + kv_k_affine(D)) + r * NG, ka);
+    if (i == 1) store_words<NG>(reinterpret_cast<uint32_t*>(rec + kv_v_affine(D)) + r * NG, va);
 }
 
 __device__ __forceinline__ void dequantise8(uint32_t w, uint32_t affine, float (&x)[8]) {
@@ -160,40 +246,45 @@ __device__ __forceinline__ void dequantise8(uint32_t w, uint32_t affine, float (
 
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvRows a) {
-    constexpr int kPer = D / 8, NG = D / 64;
+    constexpr int NG = D / 64;
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const uint64_t idx = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    const unsigned row = (unsigned)(idx / kPer);
-    const int e = (int)(idx % kPer);
+    const unsigned row = (unsigned)(idx >> 3);
+    const int i = (int)(idx & 7);
     if (row >= a.n) return;
     const unsigned t = a.by_head.div(row), h = row - t * a.by_head.d;
-    const int slot = __ldg(a.slots + t);
-    float k[8] = {}, v[8] = {};
-    if (slot >= 0 && (unsigned)slot < a.c.n_slots) {
+    const int slot = a.slots[t];
+    uint32_t kw[NG] = {}, vw[NG] = {}, ka[NG] = {}, va[NG] = {};  // zeros where there is nothing
+    if ((unsigned)slot < a.c.n_slots) {
         const int page = slot >> a.c.page_shift, place = slot & (a.c.P - 1), r = place & 15;
         const uint8_t* rec =
             a.c.pages + (((size_t)page * a.c.H + h) * (a.c.P >> 4) + (place >> 4)) * kv_record_bytes(D);
-        const int g = e >> 3, i = e & 7;
-        const int word = r * (D / 8) + i * NG + g;
-        const uint32_t kw = reinterpret_cast<const uint32_t*>(rec)[word];
-        const uint32_t vw = reinterpret_cast<const uint32_t*>(rec + kv_v_codes(D))[word];
-        dequantise8(kw, reinterpret_cast<const uint32_t*>(rec + kv_k_affine(D))[r * NG + g], k);
-        dequantise8(vw, reinterpret_cast<const uint32_t*>(rec + kv_v_affine(D))[r * NG + g], v);
+        load_words<NG>(reinterpret_cast<const uint32_t*>(rec) + r * (D / 8) + i * NG, kw);
+        load_words<NG>(reinterpret_cast<const uint32_t*>(rec + kv_v_codes(D)) + r * (D / 8) + i * NG, vw);
+        load_words<NG>(reinterpret_cast<const uint32_t*>(rec + kv_k_affine(D)) + r * NG, ka);
+        load_words<NG>(reinterpret_cast<const uint32_t*>(rec + kv_v_affine(D)) + r * NG, va);
     } else if (slot >= 0) {
         *(volatile unsigned*)a.bad = 1u;
     }
-    Row8<T>::store(static_cast<T*>(a.k_out) + (int64_t)t * a.kt + (int64_t)h * a.kh + e * 8, k);
-    Row8<T>::store(static_cast<T*>(a.v_out) + (int64_t)t * a.vt + (int64_t)h * a.vh + e * 8, v);
+    T* kp = static_cast<T*>(a.k_out) + (int64_t)t * a.kt + (int64_t)h * a.kh + i * 8;
+    T* vp = static_cast<T*>(a.v_out) + (int64_t)t * a.vt + (int64_t)h * a.vh + i * 8;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        float x[8];
+        dequantise8(kw[g], ka[g], x);
+        Row8<T>::store(kp + g * 64, x);
+        dequantise8(vw[g], va[g], x);
+        Row8<T>::store(vp + g * 64, x);
+    }
 }
 
 template <int D, class T>
 cudaError_t launch_rows(const KvRows& a, bool append, cudaStream_t s) {
-    const uint64_t threads = (uint64_t)a.n * (D / 8);
-    const unsigned grid = (unsigned)((threads + kThreads - 1) / kThreads);
-    if (append)
-        kv_append_kernel<D, T><<<grid, kThreads, 0, s>>>(a);
-    else
-        kv_read_kernel<D, T><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const unsigned grid = (unsigned)(((uint64_t)a.n * 8 + kThreads - 1) / kThreads);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(kThreads), 0, s, true, &attr);
+    return append ? cudaLaunchKernelEx(&cfg, kv_append_kernel<D, T>, a) : cudaLaunchKernelEx(&cfg, kv_read_kernel<D, T>, a);
 }
 
 template <int D>
