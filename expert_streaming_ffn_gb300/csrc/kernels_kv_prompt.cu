@@ -159,27 +159,9 @@ __device__ __forceinline__ uint64_t sw128_desc_n(uint32_t saddr, uint32_t n_stri
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Two fp32 operations in one.
-__device__ __forceinline__ uint64_t f2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 f2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
+using ptx::add2;
+using ptx::f2;
+using ptx::fma2;
 
 template <int N>
 __device__ __forceinline__ void more_registers() {

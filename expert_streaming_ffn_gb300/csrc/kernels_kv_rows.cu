@@ -11,19 +11,24 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kF16Max = 65504.0f;
 
+// Eight consecutive elements of a row, as loaded.
 template <class T>
-struct Row8;  // eight consecutive elements of a row
+struct Row8;
+
+template <class T>
+struct Row8Pairs {  // 16-bit types
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const T* p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+};
 
 template <>
-struct Row8<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+struct Row8<__nv_bfloat16> : Row8Pairs<__nv_bfloat16> {
+    using Pair = __nv_bfloat162;
+    __device__ __forceinline__ uint64_t two(int i) const {
+        return ptx::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
         uint32_t w[4];
@@ -37,16 +42,11 @@ struct Row8<__nv_bfloat16> {
 };
 
 template <>
-struct Row8<__half> {
-    static __device__ __forceinline__ void load(const __half* p, float (&x)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+struct Row8<__half> : Row8Pairs<__half> {
+    using Pair = __half2;
+    __device__ __forceinline__ uint64_t two(int i) const {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        return ptx::f2(f.x, f.y);
     }
     static __device__ __forceinline__ void store(__half* p, const float (&x)[8]) {
         uint32_t w[4];
@@ -61,10 +61,12 @@ struct Row8<__half> {
 
 template <>
 struct Row8<float> {
-    static __device__ __forceinline__ void load(const float* p, float (&x)[8]) {
+    float x[8];
+    __device__ __forceinline__ void load(const float* p) {
         const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
+    __device__ __forceinline__ uint64_t two(int i) const { return ptx::f2(x[2 * i], x[2 * i + 1]); }
     static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
         reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
         reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -85,16 +87,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // The least and the largest of a group's 64 elements, of which each of eight
 // lanes holds eight; NaN if there is one. 16-bit types work in pairs, the largest
 // negated, so that one exchange a step serves both.
-template <class T>
-__device__ __forceinline__ float2 group_range(const float (&x)[8]);
-
-template <>
-__device__ __forceinline__ float2 group_range<float>(const float (&x)[8]) {
-    float lo = x[0], hi = x[0];
+__device__ __forceinline__ float2 group_range(const Row8<float>& r) {
+    float lo = r.x[0], hi = r.x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
+        lo = min_nan(lo, r.x[i]);
+        hi = max_nan(hi, r.x[i]);
     }
 #pragma unroll
     for (int m = 4; m; m >>= 1) {
@@ -104,35 +102,19 @@ __device__ __forceinline__ float2 group_range<float>(const float (&x)[8]) {
     return make_float2(lo, hi);
 }
 
-template <class P>
-__device__ __forceinline__ float2 group_range_pairs(P p) {  // p: (least, largest negated) of a lane's eight
+template <class R>
+__device__ __forceinline__ float2 group_range(const R& r) {
+    using P = typename R::Pair;
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const P*>(&w); };
+    auto word = [](P p) { return *reinterpret_cast<const uint32_t*>(&p); };
+    const P lo = __hmin2_nan(__hmin2_nan(pair(r.w[0]), pair(r.w[1])), __hmin2_nan(pair(r.w[2]), pair(r.w[3])));
+    const P hi = __hmax2_nan(__hmax2_nan(pair(r.w[0]), pair(r.w[1])), __hmax2_nan(pair(r.w[2]), pair(r.w[3])));
+    // (least, largest negated) of the even elements, and of the odd ones
+    const uint32_t neg = word(hi) ^ 0x80008000u;
+    P p = __hmin2_nan(pair(__byte_perm(word(lo), neg, 0x5410)), pair(__byte_perm(word(lo), neg, 0x7632)));
 #pragma unroll
-    for (int m = 4; m; m >>= 1) {
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&p), m);
-        p = __hmin2_nan(p, *reinterpret_cast<const P*>(&o));
-    }
+    for (int m = 4; m; m >>= 1) p = __hmin2_nan(p, pair(__shfl_xor_sync(0xFFFFFFFFu, word(p), m)));
     return make_float2((float)p.x, -(float)p.y);
-}
-
-template <>
-__device__ __forceinline__ float2 group_range<__half>(const float (&x)[8]) {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
-    return group_range_pairs(__floats2half2_rn(lo, -hi));  // exact: the values are halves
-}
-template <>
-__device__ __forceinline__ float2 group_range<__nv_bfloat16>(const float (&x)[8]) {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
-    return group_range_pairs(__floats2bfloat162_rn(lo, -hi));
 }
 
 // Eight elements of a group, one lane of the eight that hold it: the word of
@@ -141,29 +123,36 @@ __device__ __forceinline__ float2 group_range<__nv_bfloat16>(const float (&x)[8]
 // is within an ulp of it, and t + y (d - s t), the remainder exact in a fused
 // multiply-add, rounds to it (Markstein's theorem; s has 11 bits, so its one exception,
 // a divisor of all ones, cannot come up). Adding 1.5 * 2^23 rounds it to an
-// integer, ties to even, in the low bits.
-template <class T>
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t& affine) {
-    const float2 r = group_range<T>(x);
+// integer, ties to even, in the low bits. Two elements go through each instruction.
+template <class R>
+__device__ __forceinline__ uint32_t quantise8(const R& row, uint32_t& affine) {
+    const float2 r = group_range(row);
     float lo = r.x, hi = r.y;
+    uint64_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = row.two(i);
     if (lo < -kF16Max || hi > kF16Max) {  // held as +-65504; NaN is left as it is
         lo = max_nan(min_nan(lo, kF16Max), -kF16Max);
         hi = max_nan(min_nan(hi, kF16Max), -kF16Max);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaxf(fminf(x[i], kF16Max), -kF16Max);
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = ptx::f2(x[i]);
+            x[i] = ptx::f2(fmaxf(fminf(v.x, kF16Max), -kF16Max), fmaxf(fminf(v.y, kF16Max), -kF16Max));
+        }
     }
     const __half b16 = __float2half_rd(lo);
     const float b = __half2float(b16);
     const __half s16 = __float2half_ru(__fdiv_rn(__fsub_rn(hi, b), 15.0f));
     const float s = __half2float(s16), y = s > 0.0f ? __frcp_rn(s) : 0.0f;
     affine = (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(b16) << 16);
+    const uint64_t nb = ptx::f2(-b, -b), ns = ptx::f2(-s, -s), yy = ptx::f2(y, y), magic = ptx::f2(12582912.0f, 12582912.0f);
     uint32_t word = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = __fsub_rn(x[i], b), t = __fmul_rn(d, y);
-        const float q = __fmaf_rn(__fmaf_rn(-t, s, d), y, t);
-        // element i = {0,2,4,6,1,3,5,7}[n] in nibble n; what the sums carry besides is taken off at the end
-        word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * ((i & 1) * 4 + (i >> 1)));
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t d = ptx::add2(x[i], nb), t = ptx::mul2(d, yy);
+        const float2 q = ptx::f2(ptx::add2(ptx::fma2(ptx::fma2(t, ns, d), yy, t), magic));
+        // elements 2i, 2i + 1 in nibbles i, i + 4; what the sums carry besides is taken off at the end
+        word += (__float_as_uint(q.x) << (4 * i)) + (__float_as_uint(q.y) << (4 * i + 16));
     }
     uint32_t carried = 0;
 #pragma unroll
@@ -209,17 +198,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const unsigned t = a.by_head.div(in ? row : 0), h = (in ? row : 0) - t * a.by_head.d;
     const T* kp = static_cast<const T*>(a.k_in) + (int64_t)t * a.kt + (int64_t)h * a.kh + i * 8;
     const T* vp = static_cast<const T*>(a.v_in) + (int64_t)t * a.vt + (int64_t)h * a.vh + i * 8;
-    float k[NG][8], v[NG][8];
+    Row8<T> k[NG], v[NG];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) Row8<T>::load(kp + g * 64, k[g]);
+    for (int g = 0; g < NG; ++g) k[g].load(kp + g * 64);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) Row8<T>::load(vp + g * 64, v[g]);
+    for (int g = 0; g < NG; ++g) v[g].load(vp + g * 64);
     const int slot = a.slots[t];
     uint32_t ka[NG], va[NG], kw[NG], vw[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        kw[g] = quantise8<T>(k[g], ka[g]);
-        vw[g] = quantise8<T>(v[g], va[g]);
+        kw[g] = quantise8(k[g], ka[g]);
+        vw[g] = quantise8(v[g], va[g]);
     }
     if (!in || slot < 0) return;
     if ((unsigned)slot >= a.c.n_slots) {
