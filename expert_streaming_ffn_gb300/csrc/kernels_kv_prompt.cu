@@ -538,6 +538,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         // tiles after its last use (the softmax is behind by three at most)
         auto note = [&](int j) {
             if (t == 0) B.hide[(j + 2) & 7] = make_uint4(0, 0, 0, 0);
+            bool any = false;
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) any |= at[it] < 0 && w.k0 + j * KT + it * kPerIt + r0 < w.len;
+            if (!__any_sync(kFull, any)) return;
 #pragma unroll
             for (int it = 0; it < kIts; ++it) {
                 const int r = it * kPerIt + r0;
@@ -545,24 +549,34 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                     atomicOr(reinterpret_cast<unsigned*>(&B.hide[j & 7]) + (r >> 5), 1u << (r & 31));
             }
         };
-        auto put = [&](int j, int side, unsigned char* tile, const uint4 (&cw)[kIts], uint32_t (&aw)[kIts][NG]) {
+        // values that are not finite leave no trace in the tile but are noted (see the epilogue)
+        auto sift = [&](int j, uint32_t (&aw)[kIts][NG]) {
+            unsigned any = 0;
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)  // an exponent of all ones carries into bit 15 or 31
+                    any |= ((aw[it][g] & 0x7C007C00u) + 0x04000400u);
+            if (!__any_sync(kFull, any & 0x80008000u)) return;
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    if (((aw[it][g] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) {
+                        aw[it][g] = 0;
+                        if (piece == 0) {
+                            const int key = w.k0 + j * KT + it * kPerIt + r0, k = atomicAdd(&B.n_poison, 1);
+                            if (k < kPoison) B.poison[k] = key * 4 + g;
+                            atomicMin(&B.poison_lo, key);
+                            atomicMax(&B.poison_hi, key);
+                        }
+                    }
+        };
+        auto put = [&](unsigned char* tile, const uint4 (&cw)[kIts], const uint32_t (&aw)[kIts][NG]) {
             const uint32_t base = ptx::smem_addr(tile);
 #pragma unroll
             for (int it = 0; it < kIts; ++it) {
                 const int r = it * kPerIt + r0;
-                if (side) {
-#pragma unroll
-                    for (int g = 0; g < NG; ++g)
-                        if ((aw[it][g] & 0x7C00u) == 0x7C00u || (aw[it][g] & 0x7C000000u) == 0x7C000000u) {
-                            aw[it][g] = 0;
-                            if (piece == 0) {
-                                const int key = w.k0 + j * KT + r, k = atomicAdd(&B.n_poison, 1);
-                                if (k < kPoison) B.poison[k] = key * 4 + g;
-                                atomicMin(&B.poison_lo, key);
-                                atomicMax(&B.poison_hi, key);
-                            }
-                        }
-                }
                 const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {  // word 4 piece + x: elements 8i .. 8i+7 of group g
@@ -589,7 +603,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.k_empty[st], ph, abortp));
             if (!ok) break;
             note(j);
-            put(j, 0, sk + st * S::kTile, kw, ka);
+            put(sk + st * S::kTile, kw, ka);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.k_full[st]);
             if (more) {
@@ -599,7 +613,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.v_empty[st], ph, abortp));
             if (!ok) break;
-            put(j, 1, sv + st * S::kTile, vw, va);
+            sift(j, va);
+            put(sv + st * S::kTile, vw, va);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.v_full[st]);
             if (more) fetch(j + 1, 1, vw, va);
