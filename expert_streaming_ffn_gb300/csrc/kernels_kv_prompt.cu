@@ -4,7 +4,7 @@
 // A CTA holds 256 query rows (two tiles of 128; one tile for head_dim 256),
 // rows being (new token, query head) pairs of one kv head, so a key tile is
 // dequantised once for all of them. Per key tile of 128 (64 for head_dim 256):
-//   four warps dequantise K, then V, from global memory (the next tile's words
+//   eight warps dequantise K, then V, from global memory (the next tile's words
 //     already in registers) to fp16 in shared memory, 128-byte swizzled; V is used
 //     as it lies, [key][dim], as an operand whose rows run along dim;
 //   two warps issue S = Q K^T into tensor memory and, later, O += P V with P
@@ -44,14 +44,14 @@ struct PShape {
     static constexpr int KT = D <= 128 ? 128 : 64; // keys of a tile
     static constexpr int kRows = 128 * MT;
     static constexpr int kRec = kv_record_bytes(D);
-    // Warps 0 and 1 issue (their warpgroup's other two idle), warps 4 to 7 dequantise, the rest are the
+    // Warps 0 and 1 issue (their warpgroup's other two idle), the next eight dequantise, the rest are the
     // softmax's. The issuing warps come first as the scheduler prefers older warps: as the CTA's last,
     // one warp took 110 ns to issue a product of 38 ns.
-    static constexpr int kWarpMma = 0, kWarpDq = 4, kWarpSoft = 8, kSoftWarps = 4 * MT;
+    static constexpr int kWarpMma = 0, kWarpDq = 4, kDqWarps = 8, kWarpSoft = kWarpDq + kDqWarps, kSoftWarps = 4 * MT;
+    static constexpr int kDqThreads = 32 * kDqWarps;
     static constexpr int kThreads = 32 * (kWarpSoft + kSoftWarps);
-    // With two row tiles the warpgroups share the registers out anew, 56 + 104 + 2 * 176 = 4 * 128;
-    // with one there are 168 for each thread.
-    static constexpr bool kShare = MT == 2;
+    // The warpgroups share the registers out anew: 32 + 2 * 56 + 2 * 168 = 5 * 96, or 56 + 2 * 112 + 184 < 4 * 128
+    static constexpr int kRegMma = MT == 2 ? 32 : 56, kRegDq = MT == 2 ? 56 : 112, kRegSoft = MT == 2 ? 168 : 184;
     static constexpr int kQBytes = 128 * D * 2;  // one row tile
     static constexpr int kTile = KT * D * 2;     // K or V
     static constexpr int kStages = 2;
@@ -61,7 +61,9 @@ struct PShape {
 };
 
 struct Bars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], s_free[2], drain[2];
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], s_free[2], drain[2];
+    uint64_t o_full;     // one row tile: after each product with V but the last
+    uint64_t o_done[2];  // after a row tile's last one
     uint32_t tmem;
     int abort;
     int n_poison, poison_lo, poison_hi;
@@ -252,16 +254,17 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
     if (tid == 0) {
         ptx::mbar_init(&B.q_full, 32 * S::kSoftWarps);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&B.k_full[i], 128);
-            ptx::mbar_init(&B.v_full[i], 128);
+            ptx::mbar_init(&B.k_full[i], S::kDqThreads);
+            ptx::mbar_init(&B.v_full[i], S::kDqThreads);
             ptx::mbar_init(&B.k_empty[i], 1);
             ptx::mbar_init(&B.v_empty[i], 1);
             ptx::mbar_init(&B.s_free[i], 1);
             ptx::mbar_init(&B.drain[i], 1);
             ptx::mbar_init(&B.s_full[i], 1);
             for (int h = 0; h < 2; ++h) ptx::mbar_init(&B.p_full[i][h], 128);
-            ptx::mbar_init(&B.o_full[i], 1);
+            ptx::mbar_init(&B.o_done[i], 1);
         }
+        ptx::mbar_init(&B.o_full, 1);
         B.abort = 0;
         B.n_poison = 0;
         for (int i = 0; i < 8; ++i) B.hide[i] = make_uint4(0, 0, 0, 0);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
     if (!based && tid == 0) give_up(1u << 21);
     if (!w.any || !based) {
     } else if (warp >= S::kWarpSoft) {
-        if constexpr (S::kShare) more_registers<176>();
+        more_registers<S::kRegSoft>();
         // ---------------- a row a thread: queries in, softmax, output ----------------
         const int mt = (warp - S::kWarpSoft) >> 2, r = tid & 127;
         const int row = w.row0 + mt * 128 + r;  // of the kv head's rows of this sequence
@@ -372,8 +375,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 const float mn = over ? fmaxf(m, top * c) : m;
                 const float sc = over && m != kNone ? ex2(m - mn) : 1.0f;
                 if (j > 0 && __any_sync(kFull, sc != 1.0f)) {
-                    if (NS == 2) {  // the last product may still run
-                        ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[0], (j - 1) & 1, abortp));
+                    if (NS == 2) {
+                        // the last product may still run; the one before it does not, as S could not have been
+                        // made, and the next cannot start: so the phase waited for is the current one or the last
+                        ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full, (j - 1) & 1, abortp));
                         if (!ok) {
                             if (lane == 0) give_up(1u << 20);
                             break;
@@ -418,10 +423,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         // ---- output ----
         if (ok && w.tiles > 0) {
-            // o_full: once after the last product of a row tile (MT == 2), or after each (NS == 2; the last S
-            // says no more than that the third to last is done, so the last two phases are waited for in turn)
-            if (NS == 2 && w.tiles > 1) ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[0], w.tiles & 1, abortp));
-            ok = ok && __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_full[mt], NS == 2 ? (w.tiles - 1) & 1 : 0, abortp));
+            ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.o_done[mt], 0, abortp));
             if (!ok && lane == 0) give_up(1u << 17);
             ptx::tc_fence_after();
         }
@@ -478,10 +480,10 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
         }
     } else if (warp >= S::kWarpDq) {
-        if constexpr (S::kShare) fewer_registers<104>();
+        fewer_registers<S::kRegDq>();
         // ---------------- dequantisation ----------------
         // A row's code bytes are kChunks pieces of 16; thread: piece t % kChunks of row t / kChunks, and so on
-        constexpr int kChunks = D / 32, kPerIt = 128 / kChunks, kIts = KT / kPerIt;
+        constexpr int kChunks = D / 32, kPerIt = S::kDqThreads / kChunks, kIts = KT / kPerIt;
         const int t = tid - 32 * S::kWarpDq, piece = t % kChunks, r0 = t / kChunks;
         const int32_t* const table = a.table + (int64_t)w.b * a.table_stride;
         const uint8_t* const head = a.c.pages + (size_t)w.h * (a.c.P >> 4) * kRec;
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         if (!ok && lane == 0) give_up(1u << 18);
     } else {
-        if constexpr (S::kShare) fewer_registers<56>();
+        fewer_registers<S::kRegMma>();
         if (warp < 2) {
             // ---------------- MMA issue ----------------
             // One warp with two row tiles: a warp for each would have products of both kinds (Q K^T from
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                         if (more)
                             scores(mt, j + 1, st ^ 1);
                         else if (one)
-                            ptx::mma_commit(&B.o_full[mt]);
+                            ptx::mma_commit(&B.o_done[mt]);
                     }
                     if (one && j + 2 < tiles) ptx::mma_commit(&B.v_empty[st]);
                     return true;
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 auto step = [&](int j, int st) {
                     const uint32_t ph = (j >> 1) & 1;
                     if (!wait(&B.v_full[st], ph) || !pv(0, st, st, j, ph)) return false;
-                    if (one) ptx::mma_commit(&B.o_full[0]);
+                    if (one) ptx::mma_commit(j + 1 < tiles ? &B.o_full : &B.o_done[0]);
                     if (j + 2 < tiles) {
                         if (one) ptx::mma_commit(&B.v_empty[st]);
                         if (one) ptx::mma_commit(&B.s_free[st]);

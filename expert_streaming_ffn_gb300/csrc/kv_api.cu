@@ -141,8 +141,9 @@ moe_status state_of(moe_ctx* C, KvState** out) {
 }
 
 moe_status expired(KvState* S) {
-    S->bad_host[1] = 0;
-    return set_error(MOE_ETIMEOUT, "a bounded device wait expired in an earlier attention call");
+    const unsigned code = *(volatile unsigned*)(S->bad_host + 1);
+    *(volatile unsigned*)(S->bad_host + 1) = 0;
+    return set_error(MOE_ETIMEOUT, "a bounded device wait expired in an earlier attention call (code %u)", code);
 }
 
 // Counts a launch; with profiling on, times it.
