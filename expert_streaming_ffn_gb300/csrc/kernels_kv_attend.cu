@@ -926,9 +926,14 @@ cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s, int* launc
     return cudaLaunchKernelEx(&jcfg, kv_join_kernel<D, NT, T>, a);
 }
 
+// A tile of 16 columns reads the cache once for what two of 8 read twice, but at an odd number of
+// eights half of the last one is idle. 100,000 keys of 8 heads, one sequence, us for tiles of 8
+// and of 16 at 8, 16, 20 and 32 columns: head_dim 64: 23 31, 34 32, 44 53, 55 52; 128: 36 51,
+// 54 52, 74 89, 94 89; 256 (where two tiles of 8 do not fit an SM): 75 95, 136 97 at 8 and 16.
 template <int D, class T>
 cudaError_t launch_decode_cols(const KvAttend& a, int cols, int sms, cudaStream_t s, int* launched) {
-    return cols <= 8 ? launch_decode<D, 1, T>(a, sms, s, launched) : launch_decode<D, 2, T>(a, sms, s, launched);
+    const bool wide = D == 256 ? cols > 8 : ((cols + 7) / 8 & 1) == 0 && cols > 8;
+    return wide ? launch_decode<D, 2, T>(a, sms, s, launched) : launch_decode<D, 1, T>(a, sms, s, launched);
 }
 
 }  // namespace

@@ -40,8 +40,13 @@ void kv_state_destroy(KvState* st) {
     delete st;
 }
 
-// Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel takes.
-constexpr int kDecodeCols = 16;
+// Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel
+// takes: it reads the cache once a tile of columns, the prompt kernel once for 256 (128 at head_dim
+// 256) whose tiles it fills in any case. us, decode and prompt kernel, one sequence of 16,511 keys, 16
+// of 4,000, 64 of 1,000, 8 heads: head_dim 64: 64 columns 27 36, 75 108, 96 119; 128 columns 41 34, 134 89,
+// 187 102. head_dim 128: 64 columns 38 46, 122 130, 155 144; 128 columns 63 45, 227 111, 300 135. head_dim 256:
+// 16 columns 27 38, 76 107, 84 137; 32 columns 42 43, 129 108, 150 137.
+int decode_cols(int head_dim) { return head_dim == 256 ? 16 : 64; }
 
 constexpr size_t kJoinBytes = 1024 * sizeof(KvJoin);  // for up to 1,024 CTAs
 
@@ -277,7 +282,7 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.min_units = 32;
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
-    const bool prompt = (int64_t)p->max_q * a.G > kDecodeCols;
+    const bool prompt = (int64_t)p->max_q * a.G > decode_cols(cache->head_dim);
     // few short segments are never cut between CTAs: such a call leaves the workspace alone
     const int64_t blocks = (int64_t)p->max_pages * cache->page_tokens / kKvBlock;
     const int64_t segs = ((int64_t)p->n_q * a.G / 8 + p->batch) * cache->n_kv_heads;
