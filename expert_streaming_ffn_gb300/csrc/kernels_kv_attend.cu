@@ -21,11 +21,17 @@
 //     query element is divided by 16), so one AND makes two exact operands.
 //   weights p = 2^(z - m), m a bound that moves only when some z passes it by 8
 //     (so p <= 2^8), the sums then rescaled.
-//   output  o[dim][col] = sum_t code_td * (p f s_tg) + sum_t p f b_tg: the scale
-//     goes into the weights, one fp16 operand per group; f is a power of two, part of the
-//     exponent's bound, that brings the largest scale near 1 so that weights stay within
-//     fp16's range whatever the values' magnitude. Rounding the weights to fp16
-//     (2^-11) is the one rounding beyond fp32 here.
+//   output  o[dim][col] = sum_t code_td w_tg + sum_t p f b_tg, w = p f s_tg: the
+//     scale goes into the weights, one fp16 operand per group; f is a power of two, part of
+//     the exponent's bound, that brings the largest scale near 1 so that weights stay within
+//     fp16's range whatever the values' magnitude. Rounding w to fp16 (2^-11) is the one
+//     rounding beyond fp32. A code being up to 15 times what a value varies by, it shows in
+//     fp16 outputs (5.5e-4 off in all, 2.1e-4 of it their own rounding). For those the codes
+//     count from 8: sum_t (code_td - 8) w_tg + sum_t p f (b_tg + 8 s_tg), the sum of the
+//     rounded weights coming out of one product more a group (3.0e-4; 6 % slower, so not
+//     for bf16, whose own rounding is 1.7e-3).
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "kv_internal.h"
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     kv_decode_kernel(const __grid_constant__ KvAttend a) {
     using S = Shape<D, NT>;
     constexpr int NG = S::NG, W = S::W, SB = S::SB, NC = S::NC, kRec = S::kRec, kStages = S::kStages;
+    constexpr bool kCentre = std::is_same<T, __half>::value;
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* ring = smem;
     float* merge = reinterpret_cast<float*>(smem + S::kRing);
@@ -551,13 +558,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         // The sums hold 2^(cz z - me): me = m - lf, m within kLazy of the largest cz z so far, 2^lf the
         // factor that keeps weight times scale within fp16's range. thr: the z that passes the bound; lim: the largest
         // scale that 2^lf serves.
-        float o[NT][D / 16][4], bacc[NT][NG][2], thr[NT][2], me[NT][2], l[NT][2], lim = 0.0f, lf = 24.0f;
+        float o[NT][D / 16][4], wsum[NT][4], bacc[NT][NG][2], thr[NT][2], me[NT][2], l[NT][2], lim = 0.0f, lf = 24.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wsum[nt][e] = 0.0f;
 #pragma unroll
             for (int j = 0; j < NG; ++j) bacc[nt][j][0] = bacc[nt][j][1] = 0.0f;
 #pragma unroll
@@ -702,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                         thr[nt][e] = mx == kNone ? kNone : (mx + kLazy) / cz[nt][e];
                         me[nt][e] = mx - lf;
                         l[nt][e] *= sc;
+                        if (kCentre) wsum[nt][e] *= sc;
 #pragma unroll
                         for (int j = 0; j < NG; ++j) bacc[nt][j][e] *= sc;
 #pragma unroll
@@ -728,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     }
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    const float2 r0 = affine_of(va[sb][0][j]), r1 = affine_of(va[sb][1][j]);
+                    float2 r0 = affine_of(va[sb][0][j]), r1 = affine_of(va[sb][1][j]);
+                    if (kCentre) r0.y = fmaf(8.0f, r0.x, r0.y), r1.y = fmaf(8.0f, r1.x, r1.y);
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -751,8 +762,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
                     const uint32_t h0 = __byte_perm(vw[0][j], vw[1][j], 0x7632);
                     const uint32_t u1 = __byte_perm(vw[2][j], vw[3][j], 0x5410);
                     const uint32_t h1 = __byte_perm(vw[2][j], vw[3][j], 0x7632);
+                    const uint32_t ones = g == j ? 0x3C003C00u : 0u;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        if (kCentre) mma(wsum[nt], ones, 0u, ones, 0u, pb[nt][0], pb[nt][1]);
                         mma(o[nt][j * 4 + 0], u0 & 0x000F000Fu, h0 & 0x000F000Fu, u1 & 0x000F000Fu, h1 & 0x000F000Fu,
                             pb[nt][0], pb[nt][1]);
                         mma(o[nt][j * 4 + 1], u0 & 0x00F000F0u, h0 & 0x00F000F0u, u1 & 0x00F000F0u, h1 & 0x00F000F0u,
@@ -786,6 +799,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
                     for (int j = 0; j < NG; ++j) bacc[nt][j][e] += __shfl_xor_sync(kFull, bacc[nt][j][e], x);
                 }
+                if (kCentre)
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+                        bacc[nt][j][e] = fmaf(-8.0f, __shfl_sync(kFull, wsum[nt][e], 4 * j + t), bacc[nt][j][e]);
                 if (g == 0) {
                     sm_m[warp * NC + nt * 8 + 2 * t + e] = me[nt][e];
                     sm_l[warp * NC + nt * 8 + 2 * t + e] = l[nt][e];
