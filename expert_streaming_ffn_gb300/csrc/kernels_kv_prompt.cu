@@ -14,8 +14,9 @@
 //     score passes it by 8 (P <= 2^8), and then O is rescaled in tensor memory.
 // With two tiles, one's softmax runs under the other's products; with one tile
 // (head_dim 256, whose O takes half of tensor memory) S has two buffers instead.
-// Few rows: the keys are split over CTAs, fp32 partial results joined by a
-// second kernel.
+// Row tiles that would leave SMs idle, all of a short call's or the last wave of a
+// long one's, have their keys split over CTAs, and a second kernel joins the fp32
+// partial results.
 //
 // Rounding beyond fp32: K and V values, P and Q (scaled by a power of two per row)
 // to fp16.
@@ -180,24 +181,23 @@ struct Work {
     int h, row0;           // kv head, first of its rows
     int k0, tiles;         // first key, and key tiles of this split
     bool any;              // there is such a piece of work
+    bool whole;            // not split
 };
 
+// Row tile `item` (over all sequences and kv heads): its sequence, kv head and rows.
 template <int D>
-__device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
+__device__ __forceinline__ Work find_rows(const KvAttend& a, unsigned item, int lane) {
     using S = PShape<D>;
-    // block: (row tile over all sequences, kv head, split), splits of a tile side by side
-    const unsigned split = blockIdx.x % (unsigned)a.splits, x = blockIdx.x / (unsigned)a.splits;
-    const unsigned h = x % (unsigned)a.c.H;
-    int want = (int)(x / (unsigned)a.c.H);
     Work w{};
-    w.h = (int)h;
+    w.h = (int)(item % (unsigned)a.c.H);
+    int want = (int)(item / (unsigned)a.c.H);
     for (int base = 0; base < a.B; base += 32) {
         const int b = base + lane;
         int first = 0, n = 0, cnt = 0;
         if (b < a.B) {
             if (a.q_start) {
-                first = min(max(*(a.q_start + b), 0), a.n_q);  // within q whatever q_start holds
-                n = min(*(a.q_start + b + 1), a.n_q) - first;
+                first = min(max(a.q_start[b], 0), a.n_q);  // within q whatever q_start holds
+                n = min(a.q_start[b + 1], a.n_q) - first;
             } else {
                 first = b * a.T, n = a.T;
             }
@@ -209,8 +209,7 @@ __device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
             const int y = __shfl_up_sync(kFull, inc, o);
             if (lane >= o) inc += y;
         }
-        const bool mine = want >= inc - cnt && want < inc;
-        const unsigned who = __ballot_sync(kFull, mine);
+        const unsigned who = __ballot_sync(kFull, want >= inc - cnt && want < inc);
         if (who) {
             const int src = __ffs(who) - 1;
             w.b = base + src;
@@ -223,6 +222,18 @@ __device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
         }
         want -= __shfl_sync(kFull, inc, 31);
     }
+    return w;
+}
+
+template <int D>
+__device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
+    using S = PShape<D>;
+    // the first a.full blocks take a row tile each, the others a split of one, a tile's side by side
+    const bool whole = blockIdx.x < (unsigned)a.full;
+    const unsigned y = whole ? 0 : blockIdx.x - (unsigned)a.full, split = y % (unsigned)a.splits;
+    const int splits = whole ? 1 : a.splits;
+    Work w = find_rows<D>(a, whole ? blockIdx.x : (unsigned)a.full + y / (unsigned)a.splits, lane);
+    w.whole = splits == 1;
     if (!w.any) return w;
     w.len = max(0, min(*(a.kv_len + w.b), a.max_pages << a.c.page_shift));
     const int rows = min(S::kRows, w.n * a.G - w.row0);
@@ -231,7 +242,7 @@ __device__ __forceinline__ Work find_work(const KvAttend& a, int lane) {
     const int hi = a.causal ? min(w.len, p1 + 1) : w.len;
     w.k0 = lo & ~15;
     const int tiles = hi > w.k0 ? (hi - w.k0 + S::KT - 1) / S::KT : 0;
-    const int t0 = (int)((int64_t)tiles * split / a.splits), t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    const int t0 = (int)((int64_t)tiles * split / splits), t1 = (int)((int64_t)tiles * (split + 1) / splits);
     w.k0 += t0 * S::KT;
     w.tiles = t1 - t0;
     return w;
@@ -450,9 +461,9 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             if (np > kPoison && B.poison_lo < hi && B.poison_hi >= lo) nan = 15u;
         }
-        float* const slot = a.part + (size_t)blockIdx.x * S::kSlot;
+        float* const slot = a.part + (size_t)(blockIdx.x - (unsigned)a.full) * S::kSlot;
         if (ok) {
-            const bool whole = a.splits == 1;
+            const bool whole = w.whole;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
@@ -757,42 +768,11 @@ __global__ void __launch_bounds__(256) kv_prompt_join_kernel(const __grid_consta
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    // the work of split 0 of this block's tile
-    const unsigned x = blockIdx.x / (S::kRows / 8), r = blockIdx.x % (S::kRows / 8) * 8 + warp;
-    const unsigned h = x % (unsigned)a.c.H;
-    int want = (int)(x / (unsigned)a.c.H), first = 0, row0 = -1, nn = 0;
-    for (int base = 0; base < a.B; base += 32) {
-        const int b = base + lane;
-        int f = 0, n = 0, cnt = 0;
-        if (b < a.B) {
-            if (a.q_start) {
-                f = min(max(*(a.q_start + b), 0), a.n_q);
-                n = min(*(a.q_start + b + 1), a.n_q) - f;
-            } else {
-                f = b * a.T, n = a.T;
-            }
-            if (n > 0) cnt = (int)(((int64_t)n * a.G + S::kRows - 1) / S::kRows);
-        }
-        int inc = cnt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned who = __ballot_sync(kFull, want >= inc - cnt && want < inc);
-        if (who) {
-            const int src = __ffs(who) - 1;
-            first = __shfl_sync(kFull, f, src);
-            nn = __shfl_sync(kFull, n, src);
-            row0 = __shfl_sync(kFull, inc - 1 - want, src) * S::kRows;
-            break;
-        }
-        want -= __shfl_sync(kFull, inc, 31);
-    }
-    if (row0 < 0) return;
-    const int row = row0 + (int)r;
-    if (row >= nn * a.G) return;
-    const int tk = (int)a.by_g.div(row), hq = (int)h * a.G + row - tk * a.G;
+    const unsigned x = blockIdx.x / (S::kRows / 8), r = blockIdx.x % (S::kRows / 8) * 8 + warp;  // of the split tiles
+    const Work w = find_rows<D>(a, (unsigned)a.full + x, lane);
+    const int row = w.row0 + (int)r;
+    if (!w.any || row >= w.n * a.G) return;
+    const int first = w.first, tk = (int)a.by_g.div(row), hq = w.h * a.G + row - tk * a.G;
     const float* p0 = a.part + (size_t)x * a.splits * S::kSlot;
     float M = kNone, L = 0.0f;
     for (int p = lane; p < a.splits; p += 32) M = fmaxf(M, p0[(size_t)p * S::kSlot + (size_t)S::kRows * D + r]);
@@ -818,46 +798,58 @@ __global__ void __launch_bounds__(256) kv_prompt_join_kernel(const __grid_consta
     if (a.lse && lane == 0) a.lse[(int64_t)(first + tk) * a.Hq + hq] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
 }
 
-// Row tiles of a call, at most: the sequences' remainders are known on the device only.
-int64_t row_tiles(const KvAttend& a, int rows) {
-    return a.q_start ? (int64_t)a.n_q * a.G / rows + a.B : (int64_t)a.B * (((int64_t)a.T * a.G + rows - 1) / rows);
-}
-
 template <int D, class T>
-cudaError_t launch_prompt(KvAttend a, int max_len, int sms, cudaStream_t s, int* launched) {
+cudaError_t launch_prompt(const KvAttend& a, int64_t work, cudaStream_t s, int* launched) {
     using S = PShape<D>;
-    const int64_t work = row_tiles(a, S::kRows) * a.c.H;
     auto kernel = kv_prompt_kernel<D, T>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
-    // too few to fill the GPU: the keys are split, four tiles of them to a CTA at least
-    a.splits = 1;
-    if (a.part && work < sms) {
-        const int64_t most = (max_len + 4 * S::KT - 1) / (4 * S::KT);
-        a.splits = (int)std::max<int64_t>(1, std::min(sms / work, most));
-    }
+    const int64_t split = work - a.full;  // row tiles
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(work * a.splits)), dim3(S::kThreads), S::kSmem, s, true, &attr);
+    const cudaLaunchConfig_t cfg =
+        launch_config(dim3((unsigned)(a.full + split * a.splits)), dim3(S::kThreads), S::kSmem, s, true, &attr);
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || a.splits == 1) return e;
     *launched = 2;
-    const cudaLaunchConfig_t jcfg = launch_config(dim3((unsigned)(work * (S::kRows / 8))), dim3(256), 0, s, true, &attr);
+    const cudaLaunchConfig_t jcfg = launch_config(dim3((unsigned)(split * (S::kRows / 8))), dim3(256), 0, s, true, &attr);
     return cudaLaunchKernelEx(&jcfg, kv_prompt_join_kernel<D, T>, a);
+}
+
+template <int D>
+cudaError_t launch_prompt_of(const KvAttend& a, int64_t work, moe_dtype t, cudaStream_t s, int* launched) {
+    return t == MOE_BF16 ? launch_prompt<D, __nv_bfloat16>(a, work, s, launched) : launch_prompt<D, __half>(a, work, s, launched);
 }
 
 }  // namespace
 
-bool kv_prompt_splits(const KvAttend& a, int d, int sms) {
-    return row_tiles(a, d == 256 ? PShape<256>::kRows : PShape<128>::kRows) * a.c.H < sms;
+// Row tiles (at most: the sequences' remainders are known on the device only), and how many of
+// them are split how often: those that do not fill the SMs a last time, if they are at most half as many,
+// four key tiles to a CTA at least. Where whole waves come first, the last wave's tiles are a
+// causal prompt's first rows, and a split has to save more than the second kernel costs: they see 16 key
+// tiles or more. 4,096 new tokens, 512 row tiles on 152 SMs, 56 of them in the fourth wave: behind 12,288
+// keys 800 us whole, 728 with each split in two; alone, where the 56 see up to 448 keys, 139 and 151.
+int64_t kv_prompt_plan(KvAttend& a, int d, int max_q, int max_len, int sms) {
+    const int rows = d == 256 ? PShape<256>::kRows : PShape<128>::kRows, kt = d == 256 ? PShape<256>::KT : PShape<128>::KT;
+    const int64_t tiles =
+        a.q_start ? (int64_t)a.n_q * a.G / rows + a.B : (int64_t)a.B * (((int64_t)a.T * a.G + rows - 1) / rows);
+    const int64_t work = tiles * a.c.H, rest = work % sms, full = work - rest;
+    int64_t keys = max_len;  // that a tile to be split sees
+    if (full && a.causal) keys = std::max<int64_t>(0, (int64_t)max_len - max_q) + (int64_t)max_q * rest / work;
+    if (a.window) keys = std::min<int64_t>(keys, (int64_t)a.window + rows / a.G);
+    const int64_t key_tiles = (keys + kt - 1) / kt;
+    a.splits = 1;
+    a.full = (int)work;
+    if (rest > 0 && (full == 0 || key_tiles >= 16)) {
+        a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / rest, (key_tiles + 3) / 4));
+        if (a.splits > 1) a.full = (int)full;
+    }
+    return work;
 }
 
-cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int max_len, int sms, cudaStream_t s, int* launched) {
-    const bool bf = t == MOE_BF16;
-    if (d == 64)
-        return bf ? launch_prompt<64, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<64, __half>(a, max_len, sms, s, launched);
-    if (d == 128)
-        return bf ? launch_prompt<128, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<128, __half>(a, max_len, sms, s, launched);
-    return bf ? launch_prompt<256, __nv_bfloat16>(a, max_len, sms, s, launched) : launch_prompt<256, __half>(a, max_len, sms, s, launched);
+cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int64_t work, cudaStream_t s, int* launched) {
+    return d == 64    ? launch_prompt_of<64>(a, work, t, s, launched)
+           : d == 128 ? launch_prompt_of<128>(a, work, t, s, launched)
+                      : launch_prompt_of<256>(a, work, t, s, launched);
 }
 
 }  // namespace moe

@@ -286,17 +286,17 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     // few short segments are never cut between CTAs: such a call leaves the workspace alone
     const int64_t blocks = (int64_t)p->max_pages * cache->page_tokens / kKvBlock;
     const int64_t segs = ((int64_t)p->n_q * a.G / 8 + p->batch) * cache->n_kv_heads;
-    const bool shared = prompt ? kv_prompt_splits(a, d, S->sms) : blocks > a.min_units || segs > S->sms;
+    const int cap = p->max_pages * cache->page_tokens;
+    const int64_t work = prompt ? kv_prompt_plan(a, d, p->max_q, p->max_len && p->max_len < cap ? p->max_len : cap, S->sms) : 0;
+    const bool shared = prompt ? a.splits > 1 : blocks > a.min_units || segs > S->sms;
     if (shared) a.join = reinterpret_cast<KvJoin*>(S->ws);
-    if (!shared) a.part = prompt ? nullptr : a.part;
     bool capturing = true;
     if (shared && (st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
     const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
     int launched = 1;
-    const int cap = p->max_pages * cache->page_tokens;
-    CUDA_TRY(prompt ? launch_kv_prompt(a, d, p->dtype, p->max_len ? (p->max_len < cap ? p->max_len : cap) : cap, S->sms, s, &launched)
+    CUDA_TRY(prompt ? launch_kv_prompt(a, d, p->dtype, work, s, &launched)
                     : launch_kv_attend(a, d, p->dtype, p->max_q * a.G, S->sms, s, &launched));
     for (; launched > 1; --launched) ctx_count_launch(C);  // the first is counted already
     return workspace_end(S, s, capturing);

@@ -81,7 +81,8 @@ struct KvAttend {
     // range and ends in another's, and two partial results; null: none can be cut
     KvJoin* join;
     float* part;
-    int splits;     // prompts: CTAs that share a row tile's keys
+    // prompts: row tiles of a CTA each, and how many CTAs share the keys of each other one
+    int full, splits;
     int min_units;  // fewest blocks of 16 tokens that a CTA takes
 };
 
@@ -93,8 +94,9 @@ constexpr size_t kKvPartFloats = 256 * (128 + 2);
 // *launched gets the number of kernels. cols: query columns (new tokens * query heads per kv head) of a sequence, as the caller knows them
 cudaError_t launch_kv_attend(const KvAttend& a, int d, moe_dtype t, int cols, int sms, cudaStream_t s, int* launched);
 
-// The same for many columns a sequence. kv_prompt_splits: whether it may use the workspace.
-bool kv_prompt_splits(const KvAttend& a, int d, int sms);
-cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int max_len, int sms, cudaStream_t s, int* launched);
+// The same for many columns a sequence. The plan sets a.full and a.splits and returns the row
+// tiles; a call with splits > 1 uses the workspace.
+int64_t kv_prompt_plan(KvAttend& a, int d, int max_q, int max_len, int sms);
+cudaError_t launch_kv_prompt(const KvAttend& a, int d, moe_dtype t, int64_t work, cudaStream_t s, int* launched);
 
 }  // namespace moe
