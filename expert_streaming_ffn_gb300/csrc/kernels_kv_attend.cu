@@ -739,7 +739,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     float2 r0 = affine_of(va[sb][0][j]), r1 = affine_of(va[sb][1][j]);
-                    if (kCentre) r0.y = fmaf(8.0f, r0.x, r0.y), r1.y = fmaf(8.0f, r1.x, r1.y);
+                    if (kCentre) {
+                        r0.y = fmaf(8.0f, r0.x, r0.y), r1.y = fmaf(8.0f, r1.x, r1.y);
+                        // a NaN group's bias is NaN too and says so; its weights would reach the other groups' sums
+                        r0.x = fmaxf(r0.x, 0.0f), r1.x = fmaxf(r1.x, 0.0f);
+                    }
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
