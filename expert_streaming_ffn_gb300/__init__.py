@@ -597,18 +597,22 @@ def moe_kv_read(ctx: int, cache: moe_kv_cache, slots, dtype=None, k=None, v=None
     """The rows at slots (CUDA int32 [n]), as (k, v) [n][kv heads][head_dim] of dtype (bf16 unless k and v are
     given); zeros where a slot is negative."""
     n = slots.shape[0]
-    if k is None or v is None:
-        given = k if k is not None else v
-        dtype = given.dtype if given is not None else dtype or _torch.bfloat16
-        shape = (n, cache.heads, cache.dim)
-        k = _torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
-        v = _torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
-    kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
-    vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)
-    if v.dtype != k.dtype:
-        raise ValueError("k and v: expected the same type")
+    if k is None and v is None:
+        dtype = dtype or _torch.bfloat16
+        k = _torch.empty((n, cache.heads, cache.dim), dtype=dtype, device=slots.device)
+        v = _torch.empty_like(k)
+        kt, kh = cache.heads * cache.dim, cache.dim
+        kp, vp, vt, vh = k.data_ptr(), v.data_ptr(), kt, kh
+    else:
+        k = _torch.empty_like(v, memory_format=_torch.contiguous_format) if k is None else k
+        v = _torch.empty_like(k, memory_format=_torch.contiguous_format) if v is None else v
+        dtype = k.dtype
+        kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
+        vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)
+        if v.dtype != dtype:
+            raise ValueError("k and v: expected the same type")
     _check((_lib or load()).moe_kv_read(ctx, cache.ptr, _kv_ints(slots, "slots", (n,), cache), n, kp, kt, kh, vp, vt, vh,
-                                        _kv_type(k.dtype), _kv_stream(stream, cache)), "moe_kv_read")
+                                        _kv_type(dtype), _kv_stream(stream, cache)), "moe_kv_read")
     return k, v
 
 
@@ -623,9 +627,11 @@ def moe_kv_attend(ctx: int, cache: moe_kv_cache, q, page_table, kv_len, q_start=
     qp, qt, qh = _kv_rows(q, "q", n, heads, cache)
     if out is None:
         out = _torch.empty((n, heads, cache.dim), dtype=q.dtype, device=q.device)
+        op, ot, oh = out.data_ptr(), heads * cache.dim, cache.dim
     elif out.dtype != q.dtype:
         raise ValueError("out: expected q's type")
-    op, ot, oh = _kv_rows(out, "out", n, heads, cache)
+    else:
+        op, ot, oh = _kv_rows(out, "out", n, heads, cache)
     lp = 0
     if lse is not None:
         if lse.dtype != _torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous() or \

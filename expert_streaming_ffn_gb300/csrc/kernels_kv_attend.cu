@@ -46,7 +46,11 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kChunkBytes = 4608;
 constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it moves (log2)
 constexpr float kNone = -3e38f;  // the bound before any score
-constexpr int kPieceCost = 24;  // what a piece costs beside its blocks, in blocks
+// What a piece costs beside its blocks (merge, queries, the last chunks' latency), in blocks. 64
+// ragged sequences to 8,192 keys, 100 to 3,000, 256 to 1,000, 8 heads of 128, us at 0, 12, 24, 48, 80:
+// 94 83 76 75 77; 73 61 - 54 56; 89 70 61 62 64. Blocks of head_dim 256 are twice as long (24
+// sequences to 6,000 at 0, 12, 48: 83 63 64).
+constexpr int piece_cost(int d) { return d == 256 ? 20 : 40; }
 
 constexpr int kPlanBytes = 2304;  // of the schedule, at least
 
@@ -162,8 +166,8 @@ __device__ __forceinline__ Seq seq_of(const KvAttend& a, int b, int NC) {
 
 // How the segments' blocks are cut into the CTAs' ranges. Either (pad) a range
 // holds one segment's blocks at most, a segment taking whole ranges; or segments
-// lie end to end, each with kPieceCost units before its blocks for what a piece
-// costs beside them.
+// lie end to end, each with some units before its blocks for what a piece costs beside
+// them (piece_cost).
 struct Cut {
     int64_t quota, total;
     int lead;  // units before a segment's blocks
@@ -204,17 +208,17 @@ struct Plan {
 static_assert(sizeof(Plan) <= kPlanBytes);
 
 // Cuts U blocks in Sg segments of at most `most` blocks into ranges for the grid.
-__device__ __forceinline__ Cut make_cut(const KvAttend& a, int64_t U, int64_t Sg, int most) {
+__device__ __forceinline__ Cut make_cut(const KvAttend& a, int64_t U, int64_t Sg, int most, int lead) {
     Cut c;
     const int grid = gridDim.x;
-    c.lead = kPieceCost;
-    c.total = U + Sg * kPieceCost;
+    c.lead = lead;
+    c.total = U + Sg * lead;
     c.quota = quot(c.total + grid - 1, grid);
     c.pad = false;
     if (Sg <= grid) {  // fewer segments than CTAs: the same number of whole CTAs for each, unless that is too uneven
         const int per = (int)((uint32_t)grid / (uint32_t)max((int)Sg, 1));
         const int each = max(a.min_units, (int)((uint32_t)(most + per - 1) / (uint32_t)per));
-        if (each <= max((int64_t)a.min_units, c.quota + kPieceCost)) c.quota = each, c.lead = 0, c.pad = true;
+        if (each <= max((int64_t)a.min_units, c.quota + lead)) c.quota = each, c.lead = 0, c.pad = true;
     }
     return c;
 }
@@ -232,7 +236,7 @@ __device__ __forceinline__ I warp_inclusive(I x, int lane) {
 // The CTA's range, and the sequence and segment that it starts in. False: the
 // range is empty. Up to 32 sequences, each warp works it out by itself and
 // warp 0 writes it down; the block is not synchronised.
-template <int NC>
+template <int NC, int kLead>
 __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, int warp, int lane) {
     const int H = a.c.H;
     if (a.B <= 32) {
@@ -250,7 +254,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
         } else {
             U = __shfl_sync(kFull, U, 0), Sg = __shfl_sync(kFull, Sg, 0);
         }
-        Cut c = make_cut(a, U, Sg, most);
+        Cut c = make_cut(a, U, Sg, most, kLead);
         const int64_t v = lane < a.B ? c.seg_units(s.per) * segs : 0;
         const int64_t inc = a.B > 1 ? warp_inclusive(v, lane) : v, e = inc - v;
         c.total = __shfl_sync(kFull, inc, a.B > 1 ? 31 : 0);
@@ -287,7 +291,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
     U = 0, Sg = 0, most = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) U += P.scan[i], most = max(most, P.most[i].x), Sg += P.most[i].y;
-    Cut c = make_cut(a, U, Sg, most);
+    Cut c = make_cut(a, U, Sg, most, kLead);
     const int64_t w = c.quota * blockIdx.x;
     int64_t run = 0;
     for (int base = 0; base < a.B; base += kThreads) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     if (tid == 0 && a.join) a.join[blockIdx.x].parts = 0;
-    if (!make_plan<NC>(a, plan, tid, warp, lane)) return;
+    if (!make_plan<NC, piece_cost(D)>(a, plan, tid, warp, lane)) return;
 
     uint32_t use_n = 0;  // chunks used
     uint32_t valid = 0;  // per stage, 4 bits: the blocks that were asked for; bit 16 + stage: in flight
@@ -485,6 +489,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
         return r;
     };
+    // the next piece's queries into the cache while this one's chunks are worked on (held in registers
+    // they would spill)
+    auto touch_q = [&](int i) {
+        const Piece& p = plan.piece[i];
+        constexpr int kLines = (D * 2 + 127) / 128;  // of a row
+        const int c = p.c0 + warp + lane / kLines * 8, tk = (int)a.by_g.div(c), hq = c - tk * a.G;
+        if (lane < NT * kLines && tk < p.n)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt +
+                                                          (int64_t)(p.h * a.G + hq) * a.qh + lane % kLines * 64));
+    };
     // A row is scaled by a power of two to a largest element in [2^10, 2^11), and by the sign
     // of the scale; pairs 1 and 3 of a word are divided by 16 to meet codes times 16.
     auto prepare_q = [&](int i, int par, const RawQ& r) {
@@ -546,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     for (int ip = 0; ip < count; ++ip, parity ^= 1) {
         const Piece& pc = plan.piece[ip];
         const int nb = pc.nb, blk0 = pc.blk;
+        if (ip + 1 < count) touch_q(ip + 1);
         const float* const sx = sm_x + parity * (NG + 1) * NC + 2 * t;
         const uint32_t sq = ptx::smem_addr(sm_q + parity * NT * W * 128 + lane * 4);
         float cz[NT][2];  // scores are cz times the sums below, cz > 0
