@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         const bool in = row < w.n * a.G;
         const int tk = in ? (int)a.by_g.div(row) : 0, hq = w.h * a.G + (in ? row - tk * a.G : 0);
         const int pos = w.len - w.n + tk;
-        const int hi = !in ? 0 : a.causal ? min(w.len, pos + 1) : w.len;
-        const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+        // rows past the last one see everything: they are not stored, and so cost no masking
+        const int hi = !in ? 0x7FFFFFFF : a.causal ? min(w.len, pos + 1) : w.len;
+        const int lo = in && a.window && pos >= a.window ? pos - a.window + 1 : 0;
         float c;  // scores in base 2 are c times S, c > 0
         {
             const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(w.first + tk) * a.qt +
@@ -830,8 +831,8 @@ cudaError_t launch_prompt_of(const KvAttend& a, int64_t work, moe_dtype t, cudaS
 // keys 800 us whole, 728 with each split in two; alone, where the 56 see up to 448 keys, 139 and 151.
 int64_t kv_prompt_plan(KvAttend& a, int d, int max_q, int max_len, int sms) {
     const int rows = d == 256 ? PShape<256>::kRows : PShape<128>::kRows, kt = d == 256 ? PShape<256>::KT : PShape<128>::KT;
-    const int64_t tiles =
-        a.q_start ? (int64_t)a.n_q * a.G / rows + a.B : (int64_t)a.B * (((int64_t)a.T * a.G + rows - 1) / rows);
+    const int64_t tiles = a.q_start ? ((int64_t)a.n_q * a.G + (int64_t)a.B * (rows - 1)) / rows
+                                    : (int64_t)a.B * (((int64_t)a.T * a.G + rows - 1) / rows);
     const int64_t work = tiles * a.c.H, rest = work % sms, full = work - rest;
     int64_t keys = max_len;  // that a tile to be split sees
     if (full && a.causal) keys = std::max<int64_t>(0, (int64_t)max_len - max_q) + (int64_t)max_q * rest / work;
