@@ -388,8 +388,16 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             ptx::tmem_ld_wait();
             if (masked) {
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
-                    if (key0 + i < lo || key0 + i >= hi || (hide[i / 32] >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
+                for (int q = 0; q < KT / 32; ++q) {
+                    // bit i: key key0 + 32 q + i is seen
+                    const int up = hi - key0 - 32 * q, down = lo - key0 - 32 * q;
+                    const uint32_t below = up >= 32 ? ~0u : (1u << max(up, 0)) - 1;
+                    const uint32_t from = down >= 32 ? 0u : ~0u << max(down, 0);
+                    const uint32_t seen = below & from & ~hide[q];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(seen & (1u << i))) s[32 * q + i] = 0xFF800000u;  // -inf
+                }
             }
             float top = kNone;
 #pragma unroll
