@@ -891,12 +891,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 
 // Adds the parts of the segment that starts in the range of CTA blockIdx.x and
 // does not end there, if there is one: block y takes column y, D/4 threads times
-// 1024/D groups of parts. Part 0 lies in that CTA's second slot, part p in the first
+// four groups of parts. Part 0 lies in that CTA's second slot, part p in the first
 // slot of the p-th CTA after it.
 template <int D, int NT, class T>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ KvAttend a) {
+__global__ void __launch_bounds__(D) kv_join_kernel(const __grid_constant__ KvAttend a) {
     using S = Shape<D, NT>;
-    constexpr int NC = S::NC, kLanes = D / 4, kGroups = kThreads / kLanes;
+    constexpr int NC = S::NC, kLanes = D / 4, kGroups = 4, kThreads = D, kWarps = D / 32;
     __shared__ float w[S::kMaxGrid];
     __shared__ float4 sum[kThreads];
     __shared__ float warp_m[kWarps], warp_l[kWarps];
@@ -958,7 +958,7 @@ cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s, int* launc
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || !a.join) return e;
     *launched = 2;
-    const cudaLaunchConfig_t jcfg = launch_config(dim3(grid, S::NC), dim3(kThreads), 0, s, true, &attr);
+    const cudaLaunchConfig_t jcfg = launch_config(dim3(grid, S::NC), dim3(D), 0, s, true, &attr);
     return cudaLaunchKernelEx(&jcfg, kv_join_kernel<D, NT, T>, a);
 }
 
