@@ -207,6 +207,28 @@ struct Plan {
 
 static_assert(sizeof(Plan) <= kPlanBytes);
 
+// The piece of segment seg of sequence s (index b) that starts at block lo of the segment.
+template <int NC, int kRec>
+__device__ __forceinline__ Piece piece_of(const KvAttend& a, const Seq& s, int b, uint32_t seg, int lo, int nb, int rot,
+                                          int parts) {
+    Piece p;
+    p.first = s.first, p.n = s.n, p.len = s.len;
+    p.h = (int)(seg / (uint32_t)s.nct);
+    p.c0 = (int)(seg - (uint32_t)p.h * (uint32_t)s.nct) * NC;
+    p.blk = s.lo_blk + lo;
+    p.nb = nb;
+    p.parts = parts;
+    p.start = lo == 0;
+    p.rot = rot;
+    const int pos0 = s.len - s.n, first = pos0 + (int)a.by_g.div(p.c0);
+    const int last = pos0 + (int)a.by_g.div(min(p.c0 + NC, s.n * a.G) - 1);
+    p.all_hi = a.causal ? min(s.len, first + 1) : s.len;
+    p.table = a.table + (int64_t)b * a.table_stride;
+    p.head = a.c.pages + (size_t)p.h * (a.c.P >> 4) * kRec;
+    p.all_lo = a.window && last >= a.window ? last - a.window + 1 : 0;
+    return p;
+}
+
 // Cuts U blocks in Sg segments of at most `most` blocks into ranges for the grid.
 __device__ __forceinline__ Cut make_cut(const KvAttend& a, int64_t U, int64_t Sg, int most, int lead) {
     Cut c;
@@ -233,11 +255,12 @@ __device__ __forceinline__ I warp_inclusive(I x, int lane) {
     return x;
 }
 
-// The CTA's range, and the sequence and segment that it starts in. False: the
-// range is empty. Up to 32 sequences, each warp works it out by itself and
-// warp 0 writes it down; the block is not synchronised.
-template <int NC, int kLead>
-__device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, int warp, int lane) {
+// The CTA's range, and the sequence and segment that it starts in. 0: the range is
+// empty; 1: its pieces are to be listed; 2: it is a single piece, listed already. Up to 32
+// sequences, each warp works it out by itself and warp 0 writes it down; the block
+// is not synchronised.
+template <int NC, int kLead, int kRec>
+__device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, int warp, int lane) {
     const int H = a.c.H;
     if (a.B <= 32) {
         Seq s{};
@@ -259,8 +282,13 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
         const int64_t inc = a.B > 1 ? warp_inclusive(v, lane) : v, e = inc - v;
         c.total = __shfl_sync(kFull, inc, a.B > 1 ? 31 : 0);
         const int64_t w = c.quota * blockIdx.x;
-        if (w >= c.total) return false;
-        if (warp == 0 && e <= w && w < e + v) {
+        if (w >= c.total) return 0;
+        if (warp == 0 && e <= w && w < e + v && c.pad) {
+            const int units = (int)c.seg_units(s.per), at = (int)(w - e), seg = (int)((uint32_t)at / (uint32_t)units);
+            const int lo = at - seg * units, nb = s.len > 0 ? min((int)c.quota, s.per - lo) : 0;
+            P.piece[0] = piece_of<NC, kRec>(a, s, lane, (uint32_t)seg, lo, nb, 0, (int)((uint32_t)units / (uint32_t)c.quota));
+            P.count = 1, P.more = 0;
+        } else if (warp == 0 && e <= w && w < e + v) {
             P.cut = c;
             P.w = w;
             P.w1 = min(c.total, w + c.quota);
@@ -270,7 +298,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
             P.s = s;
         }
         __syncwarp();
-        return true;
+        return c.pad ? 2 : 1;
     }
     int64_t U = 0, Sg = 0;
     int most = 0;
@@ -316,7 +344,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
             P.s = s;
         }
     }
-    if (w >= run) return false;
+    if (w >= run) return 0;
     if (tid == 0) {
         c.total = run;
         P.cut = c;
@@ -324,7 +352,7 @@ __device__ __forceinline__ bool make_plan(const KvAttend& a, Plan& P, int tid, i
         P.w1 = min(run, w + c.quota);
     }
     __syncthreads();
-    return true;
+    return 1;
 }
 
 // The next list of pieces, by one warp: lane p looks at the p-th segment from the list's first.
@@ -355,24 +383,10 @@ __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane
         const int x = __shfl_up_sync(kFull, rot, o);
         if (lane >= o) rot += x;
     }
-    if (some) {
-        Piece p;
-        p.first = s.first, p.n = s.n, p.len = s.len;
-        p.h = (int)((uint32_t)seg / (uint32_t)s.nct);
-        p.c0 = (int)((uint32_t)seg - (uint32_t)p.h * (uint32_t)s.nct) * NC;
-        p.blk = s.lo_blk + lo;
-        p.nb = nb;
-        p.parts = (int)quot(at + s.per - 1, c.quota) - (int)quot(at, c.quota) + 1;
-        p.start = lo == 0;
-        p.rot = (rot - chunks) & (kWarps - 1);
-        const int pos0 = s.len - s.n, first = pos0 + (int)a.by_g.div(p.c0);
-        const int last = pos0 + (int)a.by_g.div(min(p.c0 + NC, s.n * a.G) - 1);
-        p.all_hi = a.causal ? min(s.len, first + 1) : s.len;
-        p.table = a.table + (int64_t)b * a.table_stride;
-        p.head = a.c.pages + (size_t)p.h * (a.c.P >> 4) * kRec;
-        p.all_lo = a.window && last >= a.window ? last - a.window + 1 : 0;
-        P.piece[__popc(who & ((1u << lane) - 1))] = p;
-    }
+    if (some)
+        P.piece[__popc(who & ((1u << lane) - 1))] = piece_of<NC, kRec>(
+            a, s, b, (uint32_t)seg, lo, nb, (rot - chunks) & (kWarps - 1),
+            (int)quot(at + s.per - 1, c.quota) - (int)quot(at, c.quota) + 1);
     // the next list starts at the segment behind lane 31's
     const bool more = __shfl_sync(kFull, in && at + s.per < P.w1, 31);
     __syncwarp();
@@ -419,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     if (tid == 0 && a.join) a.join[blockIdx.x].parts = 0;
-    if (!make_plan<NC, piece_cost(D)>(a, plan, tid, warp, lane)) return;
+    const int planned = make_plan<NC, piece_cost(D), kRec>(a, plan, tid, warp, lane);
+    if (!planned) return;
 
     uint32_t use_n = 0;  // chunks used
     uint32_t valid = 0;  // per stage, 4 bits: the blocks that were asked for; bit 16 + stage: in flight
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 
 #pragma unroll 1
   for (;;) {  // lists of pieces
-    if (warp == 0) list_pieces<NC, SB, kRec>(a, plan, lane);
+    if (warp == 0 && planned == 1) list_pieces<NC, SB, kRec>(a, plan, lane);
     __syncthreads();
     const int count = plan.count;
 
