@@ -51,7 +51,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMostWarps = 12;  // of a CTA
 constexpr int kChunkBytes = 4608;
 constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it moves (log2)
 constexpr float kNone = -3e38f;  // the bound before any score
@@ -69,8 +69,9 @@ struct Shape {
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int SB = kChunkBytes / kRec;  // blocks of a chunk
     static constexpr int NC = 8 * NT;
+    static constexpr int kWarps = D == 256 && NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
     static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;  // per SM
-    static constexpr int kStages = kCtas == 2 ? 2 : D == 256 && NT == 2 ? 2 : 3;
+    static constexpr int kStages = kCtas == 2 || D == 256 ? 2 : 3;
     static constexpr int kCol = D + 4;  // floats of a column in the merge buffer
     static constexpr int kRing = kWarps * kStages * kChunkBytes;
     static constexpr int kMaxGrid = 160 * kCtas;
@@ -203,15 +204,19 @@ constexpr int kPieces = 32;  // pieces of one list
 
 // What a block knows of the schedule, in shared memory.
 struct Plan {
-    int64_t scan[kWarps];
-    int2 most[kWarps];
     Cut cut;
     int64_t w, w1;     // the CTA's range
     int64_t ex;        // where sequence b's units start
     int b, seg;        // the next piece's sequence, and its segment there
     Seq s;             // that sequence
     int count, more;   // pieces of the list; whether another list follows
-    Piece piece[kPieces];
+    union {
+        Piece piece[kPieces];
+        struct {  // while the range is worked out, before any piece is listed
+            int64_t scan[kMostWarps];
+            int2 most[kMostWarps];
+        };
+    };
 };
 
 static_assert(sizeof(Plan) <= kPlanBytes);
@@ -268,7 +273,7 @@ __device__ __forceinline__ I warp_inclusive(I x, int lane) {
 // empty; 1: its pieces are to be listed; 2: it is a single piece, listed already. Up to 32
 // sequences, each warp works it out by itself and warp 0 writes it down; the block
 // is not synchronised.
-template <int NC, int kLead, int kRec>
+template <int NC, int kLead, int kRec, int kWarps>
 __device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, int warp, int lane) {
     const int H = a.c.H;
     if (a.B <= 32) {
@@ -311,7 +316,7 @@ __device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, in
     }
     int64_t U = 0, Sg = 0;
     int most = 0;
-    for (int b = tid; b < a.B; b += kThreads) {
+    for (int b = tid; b < a.B; b += 32 * kWarps) {
         const Seq s = seq_of(a, b, NC);
         const int64_t segs = (int64_t)H * s.nct;
         U += segs * s.per, Sg += segs;
@@ -331,7 +336,7 @@ __device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, in
     Cut c = make_cut(a, U, Sg, most, kLead);
     const int64_t w = c.quota * blockIdx.x;
     int64_t run = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
+    for (int base = 0; base < a.B; base += 32 * kWarps) {
         const int b = base + tid;
         Seq s{};
         if (b < a.B) s = seq_of(a, b, NC);
@@ -365,7 +370,7 @@ __device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, in
 }
 
 // The next list of pieces, by one warp: lane p looks at the p-th segment from the list's first.
-template <int NC, int SB, int kRec>
+template <int NC, int SB, int kRec, int kWarps>
 __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane) {
     const Cut c = P.cut;
     int b = P.b;
@@ -394,7 +399,7 @@ __device__ __forceinline__ void list_pieces(const KvAttend& a, Plan& P, int lane
     }
     if (some)
         P.piece[__popc(who & ((1u << lane) - 1))] = piece_of<NC, kRec>(
-            a, s, b, (uint32_t)seg, lo, nb, (rot - chunks) & (kWarps - 1),
+            a, s, b, (uint32_t)seg, lo, nb, (int)((unsigned)(rot - chunks) % kWarps),
             (int)quot(at + s.per - 1, c.quota) - (int)quot(at, c.quota) + 1);
     // the next list starts at the segment behind lane 31's
     const bool more = __shfl_sync(kFull, in && at + s.per < P.w1, 31);
@@ -420,10 +425,11 @@ __device__ __forceinline__ void put_out(const KvAttend& a, int first, int h, int
 }
 
 template <int D, int NT, class T>
-__global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
+__global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas))
     kv_decode_kernel(const __grid_constant__ KvAttend a) {
     using S = Shape<D, NT>;
     constexpr int NG = S::NG, W = S::W, SB = S::SB, NC = S::NC, kRec = S::kRec, kStages = S::kStages;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
     constexpr bool kCentre = std::is_same<T, __half>::value;
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* ring = smem;
@@ -442,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     if (tid == 0 && a.join) a.join[blockIdx.x].parts = 0;
-    const int planned = make_plan<NC, piece_cost(D), kRec>(a, plan, tid, warp, lane);
+    const int planned = make_plan<NC, piece_cost(D), kRec, kWarps>(a, plan, tid, warp, lane);
     if (!planned) return;
 
     uint32_t use_n = 0;  // chunks used
@@ -454,15 +460,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
 
 #pragma unroll 1
   for (;;) {  // lists of pieces
-    if (warp == 0 && planned == 1) list_pieces<NC, SB, kRec>(a, plan, lane);
+    if (warp == 0 && planned == 1) list_pieces<NC, SB, kRec, kWarps>(a, plan, lane);
     __syncthreads();
     const int count = plan.count;
 
     // ---- loads: this warp's chunks, kStages ahead, and the page of the one after ----
     int ld_p = -1, ld_c = 1 << 20, ld_page = 0;  // piece, next chunk, this lane's page of it
+    auto first_chunk = [&](int rot) { return warp >= rot ? warp - rot : warp - rot + kWarps; };
     auto find = [&]() {  // moves on to a piece with a chunk for this warp, and fetches its page id
         while ((ld_p < 0 || ld_c * SB >= plan.piece[ld_p].nb) && ++ld_p < count)
-            ld_c = (warp - plan.piece[ld_p].rot) & (kWarps - 1);
+            ld_c = first_chunk(plan.piece[ld_p].rot);
         if (ld_p < count) {
             const Piece& p = plan.piece[ld_p];
             const int i = ld_c * SB + lane;
@@ -502,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     };
     auto fetch_q = [&](int i) {
         const Piece& p = plan.piece[i];
-        RawQ r;
+        RawQ r{};
+        if (kWarps > 8 && warp >= 8) return r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c = p.c0 + nt * 8 + warp, tk = (int)a.by_g.div(c), hq = c - tk * a.G;
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         const Piece& p = plan.piece[i];
         constexpr int kLines = (D * 2 + 127) / 128;  // of a row
         const int c = p.c0 + warp + lane / kLines * 8, tk = (int)a.by_g.div(c), hq = c - tk * a.G;
-        if (lane < NT * kLines && tk < p.n)
+        if ((kWarps == 8 || warp < 8) && lane < NT * kLines && tk < p.n)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const T*>(a.q) + (int64_t)(p.first + tk) * a.qt +
                                                           (int64_t)(p.h * a.G + hq) * a.qh + lane % kLines * 64));
     };
@@ -527,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
     // of the scale; pairs 1 and 3 of a word are divided by 16 to meet codes times 16.
     auto prepare_q = [&](int i, int par, const RawQ& r) {
         const Piece& p = plan.piece[i];
+        if (kWarps > 8 && warp >= 8) return;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int tk = (int)a.by_g.div(p.c0 + nt * 8 + warp);
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kCtas))
         }
 
 #pragma unroll 1
-        for (int c = (warp - pc.rot) & (kWarps - 1); c * SB < nb; c += kWarps) {
+        for (int c = first_chunk(pc.rot); c * SB < nb; c += kWarps) {
             const int st = (int)(use_n % kStages);
             if (!dead && !ptx::mbar_wait_bounded(mybars + st, (use_n / kStages) & 1, nullptr)) {
                 dead = true;
@@ -978,7 +987,7 @@ cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s, int* launc
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const int grid = min(S::kCtas * sms, S::kMaxGrid);
-    const cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(kThreads), S::kSmem, s, true, &attr);
+    const cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(S::kThreads), S::kSmem, s, true, &attr);
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || !a.join) return e;
     *launched = 2;
