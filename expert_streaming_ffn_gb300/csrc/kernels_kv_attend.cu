@@ -126,6 +126,22 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
     }
 }
 
+// The same, of a record of values. Four words: the lanes of a row four to a bank, so each begins with
+// another word and puts them in order.
+template <int N>
+__device__ __forceinline__ void lds_turned(uint32_t a, int t, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint32_t r0 = ptx::lds_u32(a + 4 * t), r1 = ptx::lds_u32(a + 4 * ((t + 1) & 3)),
+                       r2 = ptx::lds_u32(a + 4 * ((t + 2) & 3)), r3 = ptx::lds_u32(a + 4 * ((t + 3) & 3));
+        // ri is word (i + t) mod 4
+        const bool odd = t & 1, two = t & 2;
+        const uint32_t x0 = odd ? r3 : r0, x1 = odd ? r0 : r1, x2 = odd ? r1 : r2, x3 = odd ? r2 : r3;
+        w[0] = two ? x2 : x0, w[1] = two ? x3 : x1, w[2] = two ? x0 : x2, w[3] = two ? x1 : x3;
+    } else {
+        lds_words<N>(a, w);
+    }
+}
+
 template <class T>
 __device__ __forceinline__ float2 unpack2(uint32_t w);
 template <>
@@ -772,10 +788,11 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
                 // tokens pi(2t), pi(2t+1), and the same plus 8: k index 2t, 2t+1, 2t+8, 2t+9 of the product
                 uint32_t vw[4][NG];
                 const int ta = (2 * t) ^ (t & 1), tb = (2 * t + 1) ^ (t & 1);
-                lds_words<NG>(rec + kv_v_codes(D) + ta * (D / 2) + g * NG * 4, vw[0]);
-                lds_words<NG>(rec + kv_v_codes(D) + tb * (D / 2) + g * NG * 4, vw[1]);
-                lds_words<NG>(rec + kv_v_codes(D) + (ta + 8) * (D / 2) + g * NG * 4, vw[2]);
-                lds_words<NG>(rec + kv_v_codes(D) + (tb + 8) * (D / 2) + g * NG * 4, vw[3]);
+                const uint32_t vr = rec + kv_v_codes(D) + g * NG * 4;
+                lds_turned<NG>(vr + ta * (D / 2), t, vw[0]);
+                lds_turned<NG>(vr + tb * (D / 2), t, vw[1]);
+                lds_turned<NG>(vr + (ta + 8) * (D / 2), t, vw[2]);
+                lds_turned<NG>(vr + (tb + 8) * (D / 2), t, vw[3]);
                 float p[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
