@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
 #include <new>
 
 #include "kv_internal.h"
@@ -47,6 +48,15 @@ void kv_state_destroy(KvState* st) {
 // 187 102. head_dim 128: 64 columns 38 46, 122 130, 155 144; 128 columns 63 45, 227 111, 300 135. head_dim 256:
 // 16 columns 27 38, 76 107, 84 137; 32 columns 42 43, 129 108, 150 137.
 int decode_cols(int head_dim) { return head_dim == 256 ? 16 : 64; }
+
+// Blocks of 16 tokens that a CTA of the decode kernel takes at least, as too few leave its warps
+// without a chunk, and the sequence up to which a segment is left to one CTA, which saves the kernel
+// that joins parts. 16 query heads on 8, one sequence, us for 16 and for 32 blocks: head_dim 64, 2,048 tokens:
+// 8.5 8.8, 8,192: 9.3 10.5; 128: 9.0 10.3, 10.8 12.6; 256 (for 12 and 24), 1,500: 10.4 11.5. Cut into
+// such pieces and whole: 64, 1,024 tokens: 8.6 7.4, 1,536: 8.7 9.0; 128, 512: 9.0 7.5, 640: 8.9 8.6, 768: 9.1 8.9,
+// 1,024: 9.0 10.3; 256, 384: 9.8 9.0, 512: 9.7 10.4.
+int decode_piece(int head_dim) { return head_dim == 256 ? 12 : 16; }
+int decode_whole(int head_dim) { return head_dim == 256 ? 24 : head_dim == 128 ? 48 : 64; }
 
 constexpr size_t kJoinBytes = 1024 * sizeof(KvJoin);  // for up to 1,024 CTAs
 
@@ -279,20 +289,20 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     if (*(volatile unsigned*)(S->bad_host + 1)) return expired(S);
     if ((st = ensure_workspace(S, ctx_device(C))) != MOE_OK) return st;
     a.part = reinterpret_cast<float*>(S->ws + kJoinBytes);
-    a.min_units = 32;
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
     const bool prompt = (int64_t)p->max_q * a.G > decode_cols(cache->head_dim);
-    // few short segments are never cut between CTAs: such a call leaves the workspace alone
-    const int64_t blocks = (int64_t)p->max_pages * cache->page_tokens / kKvBlock;
+    const int cap = p->max_pages * cache->page_tokens, most = p->max_len && p->max_len < cap ? p->max_len : cap;
+    // few short segments are never cut between CTAs, however long they turn out: such a call leaves the workspace alone
+    const int64_t seen = a.window ? std::min<int64_t>(most, (int64_t)a.window + p->max_q + kKvBlock) : most;
     const int64_t segs = ((int64_t)p->n_q * a.G / 8 + p->batch) * cache->n_kv_heads;
-    const int cap = p->max_pages * cache->page_tokens;
-    const int64_t work = prompt ? kv_prompt_plan(a, d, p->max_q, p->max_len && p->max_len < cap ? p->max_len : cap, S->sms) : 0;
-    const bool shared = prompt ? a.splits > 1 : blocks > a.min_units || segs > S->sms;
+    const int64_t work = prompt ? kv_prompt_plan(a, d, p->max_q, most, S->sms) : 0;
+    const bool shared = prompt ? a.splits > 1 : seen > (int64_t)decode_whole(d) * kKvBlock || segs > S->sms;
+    a.min_units = shared ? decode_piece(d) : std::max(1, cap / kKvBlock);
     if (shared) a.join = reinterpret_cast<KvJoin*>(S->ws);
     bool capturing = true;
     if (shared && (st = workspace_begin(S, s, &capturing)) != MOE_OK) return st;
-    const double len = p->max_len ? p->max_len : (double)p->max_pages * cache->page_tokens;
+    const double len = most;
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
     int launched = 1;

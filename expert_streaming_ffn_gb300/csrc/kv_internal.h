@@ -83,7 +83,7 @@ struct KvAttend {
     float* part;
     // prompts: row tiles of a CTA each, and how many CTAs share the keys of each other one
     int full, splits;
-    int min_units;  // fewest blocks of 16 tokens that a CTA takes
+    int min_units;  // fewest blocks of 16 tokens that a CTA takes; a whole segment where none is cut
 };
 
 constexpr int kKvMaxCtas = 2;  // resident CTAs per SM of any of the kernels

@@ -131,3 +131,33 @@ def test_nan_values_reach_only_the_rows_that_see_them(ctx, D, hint):
         keep[first:] = False  # later rows read a requantised token
         assert torch.equal(got[keep], clean[keep])
         cache.tensor.copy_(saved)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_segments_about_the_shortest_that_is_cut(ctx, D, dtype):
+    for i, n in enumerate([1, 383, 384, 385, 511, 513, 767, 769, 1023, 1024, 1041]):
+        run(ctx, 7 * D + i, [n], [1], 16, 8, D, 16, dtype, 1, 1)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("hint", [1, 17, 300, 5000, 100000])
+def test_no_result_depends_on_max_len(ctx, D, hint):
+    """Any value for the longest length, too small ones included."""
+    lens = [5000, 77, 1300]
+    cache, table, g = filled(ctx, D + hint, lens, 4, D, 32)
+    q = torch.randn((3, 8, D), generator=g, device="cuda").bfloat16()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = moe.moe_kv_attend(ctx, cache, q, table, ln, max_q=1, max_len=hint)
+    ref = expect(cache, table, lens, np.arange(4), q, np.arange(3), D ** -0.5)
+    lse = torch.zeros((3, 8), device="cuda")
+    again = moe.moe_kv_attend(ctx, cache, q, table, ln, max_q=1, max_len=hint, lse=lse)
+    torch.cuda.synchronize()
+    moe.moe_kv_check(ctx)
+    assert torch.equal(got, again)
+    check(got.double().cpu().numpy(), lse.double().cpu().numpy(), q, ref, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("D,window,lens", [(256, 100, [5000, 300, 90]), (256, 600, [7000] * 5), (128, 512, [9000, 1]), (64, 900, [20000] * 3)])
+def test_windows_of_a_few_keys_behind_a_long_history(ctx, D, window, lens):
+    run(ctx, D + window, lens, [min(3, n) for n in lens], 8, 4, D, 16, torch.float16, 3, 5, window)
