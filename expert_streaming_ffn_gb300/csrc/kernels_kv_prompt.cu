@@ -485,8 +485,31 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         float* const slot = a.part + (size_t)(blockIdx.x - (unsigned)a.full) * S::kSlot;
         if (ok) {
+            // A row a thread would store 16 bytes of 32 lines at a time. The rows go through shared memory,
+            // where this row tile's queries were: a warp's 32 rows of 2 D bytes, chunks of 16 swizzled, whole
+            // rows of output or half rows of fp32 at a time.
             const bool whole = w.whole;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            constexpr int kChunks = D / 8, kRowsAt = 32 / kChunks < 1 ? 1 : 32 / kChunks;  // of a row; rows at a time
+            const uint32_t stage = ptx::smem_addr(sq + mt * S::kQBytes) + (warp & 3) * (32 * D * 2);
+            const unsigned stored = __ballot_sync(kFull, in);
+            auto put = [&](int chunk, uint4 v) { ptx::sts_u4(stage + lane * (D * 2) + ((chunk ^ (lane & 7)) << 4), v); };
+            T* const out = static_cast<T*>(a.out) + (int64_t)(w.first + tk) * a.ot + (int64_t)hq * a.oh;
+            auto pass_on = [&](int half) {
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kRowsAt) {
+                    const int rr = i + lane / kChunks, chunk = lane % kChunks;
+                    const uint4 v = w.tiles > 0 ? ptx::lds_u4(stage + rr * (D * 2) + ((chunk ^ (rr & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                    T* const row_out = reinterpret_cast<T*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(out), rr));
+                    if (!(stored >> rr & 1)) continue;
+                    if (whole)
+                        *reinterpret_cast<uint4*>(row_out + 8 * chunk) = v;
+                    else
+                        __stcg(reinterpret_cast<uint4*>(slot + (size_t)(mt * 128 + (warp & 3) * 32 + rr) * D + half * (D / 2)) + chunk, v);
+                }
+                __syncwarp();
+            };
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
@@ -501,23 +524,23 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                         o[i] = 0;
                     else if (bad)
                         o[i] = 0x7FC00000u;
-                if (in && whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)(w.first + tk) * a.ot +
-                                                          (int64_t)hq * a.oh + 32 * q);
+                if (w.tiles > 0 && whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t u[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             u[e] = pack2<T>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                        dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        put(4 * q + i, make_uint4(u[0], u[1], u[2], u[3]));
                     }
-                } else if (in) {
-                    uint4* dst = reinterpret_cast<uint4*>(slot + (size_t)(mt * 128 + r) * D + 32 * q);
+                } else if (w.tiles > 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) __stcg(dst + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+                    for (int i = 0; i < 8; ++i)
+                        put(8 * (q % (D / 64)) + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
                 }
+                if (!whole && q % (D / 64) == D / 64 - 1) pass_on(q / (D / 64));
             }
+            if (whole) pass_on(0);
             if (in && whole) {
                 if (a.lse) a.lse[(int64_t)(w.first + tk) * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
             } else if (in) {
