@@ -329,25 +329,36 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         const int lo = in && a.window && pos >= a.window ? pos - a.window + 1 : 0;
         float c;  // scores in base 2 are c times S, c > 0
         {
-            const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)(w.first + tk) * a.qt +
-                                                             (int64_t)hq * a.qh);
-            // Up to 16 loads at once, so a row of 128 costs one memory latency (four at a time, and again for the
-            // second look, were 6 us); a row of 256 goes in two parts, loaded twice.
-            constexpr int kPart = D / 8 < 16 ? D / 8 : 16, kParts = D / 8 / kPart;
-            uint4 q[kPart];
-            float top = 0.0f;
+            // A warp's 32 rows as they are, whole rows side by side (a row a thread would touch 32 lines a load), to
+            // where each row belongs; then each thread scales its own there.
+            constexpr int kChunks = D / 8, kRowsAt = 32 / kChunks, kPart = 16 < kChunks ? 16 : kChunks;
+            const T* const mine = static_cast<const T*>(a.q) + (int64_t)(w.first + tk) * a.qt + (int64_t)hq * a.qh;
+            const uint32_t rows = ptx::smem_addr(sq + mt * S::kQBytes);
+            auto place = [&](int r, int i) { return rows + r * 128 + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4); };
+            const unsigned there = __ballot_sync(kFull, in);
 #pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-#pragma unroll
-                for (int i = 0; i < kPart; ++i) q[i] = in ? qp[h * kPart + i] : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 32; h += kPart * kRowsAt) {
+                uint4 q[kPart];
 #pragma unroll
                 for (int i = 0; i < kPart; ++i) {
-                    const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                    const int rr = h + i * kRowsAt + lane / kChunks;
+                    const T* const row = reinterpret_cast<const T*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), rr));
+                    q[i] = there >> rr & 1 ? *reinterpret_cast<const uint4*>(row + lane % kChunks * 8) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<T>(u[e]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
+                for (int i = 0; i < kPart; ++i)
+                    ptx::sts_u4(place((r & 96) + h + i * kRowsAt + lane / kChunks, lane % kChunks), q[i]);
+            }
+            __syncwarp();
+            float top = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < kChunks; ++i) {
+                const uint4 q = ptx::lds_u4(place(r, i));
+                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack2<T>(u[e]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
             }
             int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2 top)
@@ -355,24 +366,17 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             float f = __uint_as_float((uint32_t)(127 + 10 - ex) << 23);
             if (a.scale_log2 <= 0.0f) f = a.scale_log2 < 0.0f ? -f : 0.0f;
             c = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - 10 + ex) << 23);
-            const uint32_t dst = ptx::smem_addr(sq + mt * S::kQBytes) + r * 128;
+#pragma unroll 8
+            for (int i = 0; i < kChunks; ++i) {
+                const uint4 q = ptx::lds_u4(place(r, i));
+                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                uint32_t o[4];
 #pragma unroll
-            for (int h = kParts; h--;) {  // the last part is still there
-                if (h + 1 < kParts)
-#pragma unroll
-                    for (int i = 0; i < kPart; ++i) q[i] = in ? qp[h * kPart + i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int k = 0; k < kPart; ++k) {
-                    const int i = h * kPart + k;
-                    const uint32_t u[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = unpack2<T>(u[e]);
-                        o[e] = pack_h2(x.x * f, x.y * f);
-                    }
-                    ptx::sts_u4(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = unpack2<T>(u[e]);
+                    o[e] = pack_h2(x.x * f, x.y * f);
                 }
+                ptx::sts_u4(place(r, i), make_uint4(o[0], o[1], o[2], o[3]));
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.q_full);
