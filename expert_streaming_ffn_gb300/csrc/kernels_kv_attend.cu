@@ -32,13 +32,13 @@
 //     for bf16, whose own rounding is 1.7e-3).
 //
 // What it measured, 32 query heads on 8 kv heads of 128 but where said, join included:
-//   1 sequence, 131,071 keys, 151 MB of records: 39.3 us, 3.8 TB/s, 0.57 of the copy bandwidth
+//   1 sequence, 131,071 keys, 151 MB of records: 39.3 us, 3.8 TB/s, 0.58 of the copy bandwidth
 //     measured on this GPU, DRAM reads 1.00 of the records. About 7 us are the start (schedule, page
 //     id, first chunk) and the join; in between 5.5 to 6.3 TB/s, 55 % of the cycles issuing.
-//   64 ragged sequences to 8,192 keys, 307 MB: 73.8 us, 4.2 TB/s, 0.63; CTAs end 44 to 72 us in.
-//   head_dim 256, windows of 1,024, 35 MB: 21 us, 0.25: one CTA of 8 warps an SM, waiting on
-//     shared memory (the words of V lie four to a bank).
-//   1 sequence, 16 query heads, 333 keys: 7.3 us, the start alone; 512 keys 7.4, 8,192 12.8, 65,536 25.6.
+//   64 ragged sequences to 8,192 keys, 307 MB: 73.4 us, 4.2 TB/s, 0.63; CTAs end 63 us in on average, the last 70.
+//   head_dim 256, 16 query heads, 16 sequences, windows of 1,024, 35 MB: 19.6 us, 0.28: six rounds of
+//     chunks for the 12 warps of a CTA. 100,000 keys, 8 columns: 59 us, 0.59.
+//   1 sequence, 16 query heads, 333 keys: 7.3 us, the start alone; 512 keys 7.6, 8,192 10.9, 65,536 25.4.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -57,9 +57,10 @@ constexpr float kLazy = 8.0f;   // how far a score may pass the bound before it 
 constexpr float kNone = -3e38f;  // the bound before any score
 // What a piece costs beside its blocks (merge, queries, the last chunks' latency), in blocks. 64
 // ragged sequences to 8,192 keys, 100 to 3,000, 256 to 1,000, 8 heads of 128, us at 0, 12, 24, 48, 80:
-// 94 83 76 75 77; 73 61 - 54 56; 89 70 61 62 64. Blocks of head_dim 256 are twice as long (24
-// sequences to 6,000 at 0, 12, 48: 83 63 64).
-constexpr int piece_cost(int d) { return d == 256 ? 20 : 40; }
+// 94 83 76 75 77; 73 61 - 54 56; 89 70 61 62 64. Blocks of head_dim 256 are twice as
+// long: at 0, 10, 20, 30, 40, 24 sequences to 6,000 keys, 100 to 3,000 and 64 to 1,000: 76 63 50 50 51; 128 116
+// 104 101 103; 76 49 41 40 41.
+constexpr int piece_cost(int d) { return d == 256 ? 30 : 40; }
 
 constexpr int kPlanBytes = 2304;  // of the schedule, at least
 
@@ -69,6 +70,8 @@ struct Shape {
     static constexpr int kRec = kv_record_bytes(D);
     static constexpr int SB = kChunkBytes / kRec;  // blocks of a chunk
     static constexpr int NC = 8 * NT;
+    // Eight warps, two CTAs an SM. At head_dim 256 one CTA fills an SM's registers, and more at 12 warps of 168 than
+    // at 8 of 208: 100,000 keys of 8 heads 61 us against 75.
     static constexpr int kWarps = D == 256 && NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
     static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;  // per SM
     static constexpr int kStages = kCtas == 2 || D == 256 ? 2 : 3;
@@ -1015,7 +1018,7 @@ cudaError_t launch_decode(const KvAttend& a, int sms, cudaStream_t s, int* launc
 // A tile of 16 columns reads the cache once for what two of 8 read twice, but at an odd number of
 // eights half of the last one is idle. 100,000 keys of 8 heads, one sequence, us for tiles of 8
 // and of 16 at 8, 16, 20 and 32 columns: head_dim 64: 23 31, 34 32, 44 53, 55 52; 128: 36 51,
-// 54 52, 74 89, 94 89; 256 (where two tiles of 8 do not fit an SM): 75 95, 136 97 at 8 and 16.
+// 54 52, 74 89, 94 89; 256: 59 91 at 8, 104 90 at 12, 104 91 at 16.
 template <int D, class T>
 cudaError_t launch_decode_cols(const KvAttend& a, int cols, int sms, cudaStream_t s, int* launched) {
     const bool wide = D == 256 ? cols > 8 : ((cols + 7) / 8 & 1) == 0 && cols > 8;

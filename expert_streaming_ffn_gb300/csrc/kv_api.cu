@@ -46,7 +46,7 @@ void kv_state_destroy(KvState* st) {
 // 256) whose tiles it fills in any case. us, decode and prompt kernel, one sequence of 16,511 keys, 16
 // of 4,000, 64 of 1,000, 8 heads: head_dim 64: 64 columns 27 36, 75 108, 96 119; 128 columns 41 34, 134 89,
 // 187 102. head_dim 128: 64 columns 38 46, 122 130, 155 144; 128 columns 63 45, 227 111, 300 135. head_dim 256:
-// 16 columns 27 38, 76 107, 84 137; 32 columns 42 43, 129 108, 150 137.
+// 16 columns 27 37, 71 94, 82 117; 32 columns 40 42, 123 95, 146 122.
 int decode_cols(int head_dim) { return head_dim == 256 ? 16 : 64; }
 
 // Blocks of 16 tokens that a CTA of the decode kernel takes at least, as too few leave its warps
