@@ -43,11 +43,11 @@ void kv_state_destroy(KvState* st) {
 
 // Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel
 // takes: it reads the cache once a tile of columns, the prompt kernel once for 256 (128 at head_dim
-// 256) whose tiles it fills in any case. us, decode and prompt kernel, one sequence of 16,511 keys, 16
-// of 4,000, 64 of 1,000, 8 heads: head_dim 64: 64 columns 27 36, 75 108, 96 119; 128 columns 41 34, 134 89,
-// 187 102. head_dim 128: 64 columns 38 46, 122 130, 155 144; 128 columns 63 45, 227 111, 300 135. head_dim 256:
-// 16 columns 27 37, 71 94, 82 117; 32 columns 40 42, 123 95, 146 122.
-int decode_cols(int head_dim) { return head_dim == 256 ? 16 : 64; }
+// 256) whose tiles it fills in any case. us, decode and prompt kernel, one sequence of 16,511 keys and of
+// 100,000, 16 of 4,000, 64 of 1,000, 8 heads: head_dim 64: 32 columns 17 22, 53 68, 42 49, 54 64; 48 columns 20 22,
+// 72 68, 57 49, 74 64. head_dim 128: 32 columns 25 29, 90 91, 66 64, 83 86; 48 columns 30 29, 126 93, 92 64, 119 86.
+// head_dim 256: 16 columns 26 33, 91 131, 72 94, 82 117; 20 columns 35 34, 149 132, 110 94, 137 119.
+int decode_cols(int head_dim) { return head_dim == 256 ? 16 : 32; }
 
 // Blocks of 16 tokens that a CTA of the decode kernel takes at least, as too few leave its warps
 // without a chunk, and the sequence up to which a segment is left to one CTA, which saves the kernel
