@@ -317,8 +317,9 @@ __device__ __forceinline__ int make_plan(const KvAttend& a, Plan& P, int tid, in
         const int64_t w = c.quota * blockIdx.x;
         if (w >= c.total) return 0;
         if (warp == 0 && e <= w && w < e + v && c.pad) {
-            const int units = (int)c.seg_units(s.per), at = (int)(w - e), seg = (int)((uint32_t)at / (uint32_t)units);
-            const int lo = at - seg * units, nb = s.len > 0 ? min((int)c.quota, s.per - lo) : 0;
+            // a range can be as long as the page table is wide, so that offsets of ranges pass 32 bits
+            const int units = (int)c.seg_units(s.per), seg = (int)quot(w - e, units);
+            const int lo = (int)(w - e - (int64_t)seg * units), nb = s.len > 0 ? min((int)c.quota, s.per - lo) : 0;
             P.piece[0] = piece_of<NC, kRec>(a, s, lane, (uint32_t)seg, lo, nb, 0, (int)((uint32_t)units / (uint32_t)c.quota));
             P.count = 1, P.more = 0;
         } else if (warp == 0 && e <= w && w < e + v) {

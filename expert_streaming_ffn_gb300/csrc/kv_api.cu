@@ -250,9 +250,10 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     if (p->n_heads < 1 || p->n_heads % cache->n_kv_heads)
         return set_error(MOE_EINVAL, "%s: n_heads = %d must be a multiple of n_kv_heads = %d", who, p->n_heads,
                          cache->n_kv_heads);
-    if ((int64_t)p->max_pages * cache->page_tokens >= (int64_t)1 << 31 ||
+    // kernels count the keys of tiles past a sequence's end in 32 bits
+    if ((int64_t)p->max_pages * cache->page_tokens >= ((int64_t)1 << 31) - 1024 ||
         (int64_t)p->n_q * p->n_heads >= (int64_t)1 << 31)
-        return set_error(MOE_EINVAL, "%s: max_pages * page_tokens and n_q * n_heads must be below 2^31", who);
+        return set_error(MOE_EINVAL, "%s: max_pages * page_tokens must be below 2^31 - 1024, n_q * n_heads below 2^31", who);
     if (p->n_q == 0) return MOE_OK;
     if (p->batch == 0) return set_error(MOE_EINVAL, "%s: n_q = %d rows of no sequence", who, p->n_q);
     if (!p->q_start && p->n_q % p->batch)

@@ -561,7 +561,7 @@ typedef struct {
     int64_t page_table_stride;
     const int32_t* kv_len;      /* device [batch]; a length past max_pages * page_tokens counts as that */
     const int32_t* q_start;     /* device [batch + 1], or NULL */
-    int32_t batch, n_q, n_heads, max_pages;
+    int32_t batch, n_q, n_heads, max_pages; /* n_q * n_heads < 2^31, max_pages * page_tokens < 2^31 - 1024 */
     int32_t max_q;   /* largest n_b, as the caller knows it on the host: it chooses the kernel, and so
                         the rounding; results are right whatever it is */
     int32_t max_len; /* likewise the largest kv_len, or 0 for max_pages * page_tokens */
