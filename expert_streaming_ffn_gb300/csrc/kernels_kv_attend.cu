@@ -23,9 +23,10 @@
 //     (so p <= 2^8), the sums then rescaled.
 //   output  o[dim][col] = sum_t code_td w_tg + sum_t p f b_tg, w = p f s_tg: the
 //     scale goes into the weights, one fp16 operand per group; f is a power of two, part of
-//     the exponent's bound, that brings the largest scale near 1 so that weights stay within
-//     fp16's range whatever the values' magnitude. Rounding w to fp16 (2^-11) is the one
-//     rounding beyond fp32. A code being up to 15 times what a value varies by, it shows in
+//     the exponent's bound, that brings the largest scale to [2^5, 2^7) so that weights use
+//     fp16's range whatever the values' magnitude. Rounding w to fp16 is the one
+//     rounding beyond fp32: 2^-11, or where w is below fp16's normal range (2^-14) 2^-25, which is
+//     2^-30 to 2^-32 of the warp's largest. A code being up to 15 times what a value varies by, it shows in
 //     fp16 outputs (5.5e-4 off in all, 2.1e-4 of it their own rounding). For those the codes
 //     count from 8: sum_t (code_td - 8) w_tg + sum_t p f (b_tg + 8 s_tg), the sum of the
 //     rounded weights coming out of one product more a group (3.0e-4; 6 % slower, so not
@@ -761,8 +762,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
                 if (top > lim) {  // the same in every lane
                     const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -24), 15);
-                    lf = (float)-ex;
-                    lim = __uint_as_float((uint32_t)(127 + 4 + ex) << 23);
+                    lf = (float)(5 - ex);  // the weights stay below 2^(kLazy + 5 + 2)
+                    lim = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)

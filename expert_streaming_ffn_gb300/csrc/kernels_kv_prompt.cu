@@ -9,9 +9,9 @@
 //     as it lies, [key][dim], as an operand whose rows run along dim;
 //   two warps issue S = Q K^T into tensor memory and, later, O += P V with P
 //     from tensor memory, where it takes the place of S;
-//   four warps per tile, a row a thread, turn S into P = 2^(c s - m), fp16, in two
+//   four warps per tile, a row a thread, turn S into P = 2^(c s - m + 7), fp16, in two
 //     halves, so that O += P V starts on the first. The bound m moves only when a
-//     score passes it by 8 (P <= 2^8), and then O is rescaled in tensor memory.
+//     score passes it by 8 (P <= 2^15), and then O is rescaled in tensor memory.
 // With two tiles, one's softmax runs under the other's products; with one tile
 // (head_dim 256, whose O takes half of tensor memory) S has two buffers instead.
 // Row tiles that would leave SMs idle, all of a short call's or the last wave of a
@@ -19,7 +19,9 @@
 // partial results.
 //
 // Rounding beyond fp32: K and V values, P and Q (scaled by a power of two per row)
-// to fp16 (2^-11 each; fp16 outputs 4.4e-4 to 6e-4 off in all, 2.1e-4 of it their own rounding).
+// to fp16 (2^-11 each; fp16 outputs 4.4e-4 to 6e-4 off in all, 2.1e-4 of it their own rounding). A weight 2^21
+// below the row's largest is below fp16's normal range and off by 2^-32 of the largest instead: the 2^7 in P is the
+// range that the bound leaves.
 //
 // What it measured, 32 query heads on 8 kv heads of 128 but where said:
 //   4,096 new tokens behind 12,288 keys: 717 us, 1,341 TFLOP/s, 0.70 of the bf16 rate measured on this
@@ -48,6 +50,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -3e38f;
+constexpr float kHead = 7.0f;  // log2 of what P is scaled by: P <= 2^(kLazy + kHead)
 constexpr int kPoison = 64;  // NaN values noted exactly; more are taken as a range
 
 template <int D>
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 if (over) thr = fmaxf((mn + kLazy) / c, top);
             }
             uint64_t sum = f2(0.0f, 0.0f);
-            const uint64_t cc = f2(c, c), mm = f2(-m, -m);
+            const uint64_t cc = f2(c, c), mm = f2(kHead - m, kHead - m);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {  // in halves, so that the product with V starts on the first
 #pragma unroll
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             if (whole) pass_on(0);
             if (in && whole) {
-                if (a.lse) a.lse[(int64_t)(w.first + tk) * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+                if (a.lse) a.lse[(int64_t)(w.first + tk) * a.Hq + hq] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m - kHead + log2f(l));
             } else if (in) {
                 __stcg(slot + (size_t)S::kRows * D + mt * 128 + r, m);
                 __stcg(slot + (size_t)S::kRows * (D + 1) + mt * 128 + r, l);
@@ -844,7 +847,7 @@ __global__ void __launch_bounds__(256) kv_prompt_join_kernel(const __grid_consta
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + (int64_t)(first + tk) * a.ot + (int64_t)hq * a.oh + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(y[e] * inv, y[e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[(int64_t)(first + tk) * a.Hq + hq] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
+    if (a.lse && lane == 0) a.lse[(int64_t)(first + tk) * a.Hq + hq] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M - kHead + log2f(L));
 }
 
 template <int D, class T>

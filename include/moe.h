@@ -547,9 +547,11 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const int32_t* s
  *   lse[i][h] = ln sum_j exp(scale * q_ih . K_j)
  * A token that sees nothing (an empty sequence, a position below 0) gets
  * out = 0, lse = -inf. Softmax statistics and sums are fp32. Keys, values and
- * probabilities enter the tensor cores in fp16 or exact integer codes, queries
- * as fp16 scaled by a power of two per row (exact for all but elements under
- * 2^-14 of the row's largest). Repeating a call on the same data gives the same bits. */
+ * probabilities enter the tensor cores in fp16 or exact integer codes (a
+ * probability under 2^-19 of a row's largest is off by up to 2^-30 of that
+ * instead of a relative 2^-11), queries as fp16 scaled by a power of two per
+ * row (exact for all but elements under 2^-14 of the row's largest).
+ * Repeating a call on the same data gives the same bits. */
 typedef struct {
     const void* q; /* device, [n_q][n_heads][head_dim] of dtype (MOE_F16 or MOE_BF16), head_dim contiguous,
                       rows on 16-byte boundaries; strides in elements */

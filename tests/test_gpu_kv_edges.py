@@ -1,4 +1,10 @@
-"""Attention over the 4-bit cache at the edges of its arguments and of what its records hold."""
+"""Attention over the 4-bit cache at the edges of its arguments and of what its records hold.
+
+Bounds are those of test_gpu_kv.py (U = 2^-11 a rounding to fp16, u the output's own) with two terms written
+out. Weights are rounded together with their scale where codes are multiplied, so the error is one U of what the
+group's codes span, at most twice its largest value, whatever the element: 2 U times the largest mag of the group. And a weight below
+fp16's range is off by 2^-25 of the largest scale, whose codes span at most twice the largest value: seen * 2^-24 * top.
+"""
 import numpy as np
 import pytest
 
@@ -10,6 +16,7 @@ pytestmark = [pytest.mark.gpu,
 
 import expert_streaming_ffn_gb300 as moe  # noqa: E402
 
+U = 2.0 ** -11
 HINTS = [1, 4096]  # max_q, which chooses the kernel: decode, prompt
 
 
@@ -19,6 +26,39 @@ def ctx():
     c = moe.moe_ctx_create(0)
     yield c
     moe.moe_ctx_destroy(c)
+
+
+def unit(dtype):
+    return 2.0 ** -8 if dtype == torch.bfloat16 else U
+
+
+def bound(e, dtype, more=0):
+    """Of an output, from what the oracle says of it; `more` roundings of keys and values besides."""
+    delta = (3 + more) * U * e["dot"][..., None]
+    mag = e["mag"]
+    group = np.repeat(mag.reshape(mag.shape[:-1] + (-1, 64)).max(-1), 64, -1)
+    return (2 * delta * np.exp(2 * delta) + (3 + more) * U + unit(dtype)) * mag + 2 * U * group + e["seen"][..., None] * 2.0 ** -24 * e["top"][..., None]
+
+
+def in_order(pages, P):
+    """A cache of one sequence whose pages lie in order, and its table."""
+    n_pages, H, _, per = pages.shape
+    cache = moe.moe_kv_make_cache(torch.from_numpy(pages).cuda(), H, per // 18, P)
+    return cache, torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+
+
+def attend(ctx, cache, table, n, q, hint, **kw):
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = moe.moe_kv_attend(ctx, cache, q, table, ln, max_q=hint, **kw)
+    torch.cuda.synchronize()
+    moe.moe_kv_check(ctx)
+    return got
+
+
+def exact(pages, P, q, n, **kw):
+    table = np.arange(pages.shape[0])[None]
+    scale = kw.pop("scale", q.shape[2] ** -0.5)
+    return kv.attend(pages, P, q.double().cpu().numpy(), table, [n], [0, q.shape[0]], scale, **kw)
 
 
 @pytest.mark.parametrize("B,H,hint", [(2, 64, 1), (2, 64, 4096), (16, 8, 1), (40, 4, 1)])
@@ -42,3 +82,43 @@ def test_page_tables_near_the_widest(ctx, B, H, hint):
     with pytest.raises(moe.MoeError, match="max_pages") as e:
         moe.moe_kv_attend(ctx, cache, q, wide.expand(B, per + 1), ln, max_q=hint, max_len=n)
     assert e.value.status == moe.MOE_EINVAL
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("bits", [12.3, 20.6, 24.6])
+@pytest.mark.parametrize("D,dtype,n", [(64, torch.bfloat16, 333), (128, torch.float16, 333), (128, torch.bfloat16, 2000), (256, torch.float16, 200)])
+def test_small_weights_beside_a_key_that_takes_nearly_all(ctx, D, dtype, n, bits, hint):
+    """One key takes nearly all of the softmax and its value is zero, so the output is made of weights `bits` binary
+    orders below it. Keys, values and queries are exact in fp16 (codes times a power of two) and the values positive, so
+    what is left is: the weights' rounding, U of normal ones and, below fp16's normal range, half its step, 2^-30 of the
+    largest weight as that is stored as at least 2^5; the output's u, or 2^-25 where fp16 has no normal number;
+    logits of up to 30 off by 30 * 2^-22; and fp32 sums, n 2^-24 of what the codes span, one for these values."""
+    H, P, T = 1, 32, 2
+    rng = np.random.default_rng(n + D)
+    code = lambda lo, hi: rng.integers(lo, hi, (n, H, D)).astype(np.float32)  # noqa: E731
+    k, v = code(0, 3), code(8, 16)
+    sink = n // 2
+    k[sink, :, :16] = 15
+    v[sink] = 0
+    for x in (k, v):  # every group spans 0 to 15, so that its scale is a power of two
+        live = np.arange(n) != sink if x is v else np.arange(n) >= 0
+        x[live, :, 62::64], x[live, :, 63::64] = 0, 15
+    pages = kv.empty_pages(-(-n // P), H, D, P)
+    kv.append(pages, P, k / 8, v / 16, np.arange(n))
+    K, V = kv.read(pages, P, np.arange(n))
+    assert (K == k / 8).all() and (V == v / 16).all()
+    q = torch.zeros((T, 4, D), dtype=dtype, device="cuda")
+    q[:, :, :16] = 1
+    scale = bits * np.log(2) / 28
+    cache, table = in_order(pages, P)
+    lse = torch.zeros((T, 4), device="cuda")
+    got = attend(ctx, cache, table, n, q, hint, scale=scale, causal=False, lse=lse).double().cpu().numpy()
+    out, rl, _ = exact(pages, P, q, n, scale=float(np.float32(scale)), causal=False)
+    z = scale * K[:, 0, :16].sum(-1)
+    p = np.exp(z - z.max())
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0  # of an output below fp16's normal range
+    live = np.arange(n) != sink
+    low = ((p < 2.0 ** -14)[:, None] * V[:, 0]).sum(0) * 2.0 ** -30 / p.sum()
+    tol = (U + unit(dtype) + 2 * 30 * 2.0 ** -22) * out + n * 2.0 ** -24 * p[live].sum() / p.sum() + low + tiny
+    assert (np.abs(got - out) <= tol).all(), (np.abs(got - out) / tol).max()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= 1e-4).all()
