@@ -119,6 +119,11 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A pair of fp16 values, infinities as +-65,504; NaN stays.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+    return as_u32(__hmax2_nan(__hmin2_nan(as_h2(x), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
+}
+
 #define R8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 #define W8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
 
@@ -612,6 +617,17 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                 }
             }
         };
+        // Whether some value of these groups could lie past fp16's range: a bias of 2^15 or more or a scale of 2^11 or
+        // more (below both, 15 scales and the bias stay under 65,504), infinities and NaN among them. Adding to the exponents
+        // carries into bits 15 and 31.
+        auto past = [&](const uint32_t (&aw)[kIts][NG]) {
+            __half2 top = as_h2(0);
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) top = __hmax2_nan(top, __habs2(as_h2(aw[it][g])));
+            return (((as_u32(top) & 0x7C007C00u) + 0x08001800u) & 0x80008000u) != 0;
+        };
         // keys of tile j that are not there, for the softmax to leave out; and room for tile j + 2's, eight
         // tiles after its last use (the softmax is behind by three at most)
         auto note = [&](int j) {
@@ -627,42 +643,50 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
                     atomicOr(reinterpret_cast<unsigned*>(&B.hide[j & 7]) + (r >> 5), 1u << (r & 31));
             }
         };
-        // values that are not finite leave no trace in the tile but are noted (see the epilogue)
-        auto sift = [&](int j, uint32_t (&aw)[kIts][NG]) {
-            unsigned any = 0;
+        auto at_word = [&](uint32_t base, int it, int x) {  // word 4 piece + x of row it: elements 8i .. 8i+7 of group g
+            const int r = it * kPerIt + r0, g = (4 * piece + x) % NG, i = (4 * piece + x) / NG;
+            return base + g * (KT * 128) + r * 128 + ((i ^ (r & 7)) << 4);
+        };
+        auto affine_at = [](const uint32_t (&a)[NG], int x) { return a[x % NG]; };
+        auto put = [&](unsigned char* tile, const uint4 (&cw)[kIts], const uint32_t (&aw)[kIts][NG]) {
+            const uint32_t base = ptx::smem_addr(tile);
 #pragma unroll
-            for (int it = 0; it < kIts; ++it)
+            for (int it = 0; it < kIts; ++it) {
+                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
 #pragma unroll
-                for (int g = 0; g < NG; ++g)  // an exponent of all ones carries into bit 15 or 31
-                    any |= ((aw[it][g] & 0x7C007C00u) + 0x04000400u);
-            if (!__any_sync(kFull, any & 0x80008000u)) return;
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t af = affine_at(aw[it], x);
+                    const __half2 s2 = __half2half2(__ushort_as_half((unsigned short)(af & 0xFFFFu)));
+                    const __half2 b2 = __half2half2(__ushort_as_half((unsigned short)(af >> 16)));
+                    ptx::sts_u4(at_word(base, it, x), dequant8(words[x], s2, b2));
+                }
+            }
+        };
+        // A second pass over the few tiles that may hold a value past fp16's range. Finite ones (a scale rounded up
+        // takes a group's largest to 65,624 at most) become its largest number: an infinity would make NaN of the products
+        // with the weights of zero of rows that do not see it. Value groups that are not finite leave no trace in the tile but
+        // are noted (see the epilogue).
+        auto mend = [&](unsigned char* tile, const uint32_t (&aw)[kIts][NG], bool values, int j) {
+            const uint32_t base = ptx::smem_addr(tile);
+            auto finite = [](uint32_t af) { return !(((af & 0x7C007C00u) + 0x04000400u) & 0x80008000u); };
 #pragma unroll
-            for (int it = 0; it < kIts; ++it)
+            for (int it = 0; it < kIts; ++it) {
+                if (values && piece == 0)
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    if (((aw[it][g] & 0x7C007C00u) + 0x04000400u) & 0x80008000u) {
-                        aw[it][g] = 0;
-                        if (piece == 0) {
+                    for (int g = 0; g < NG; ++g)
+                        if (!finite(aw[it][g])) {
                             const int key = w.k0 + j * KT + it * kPerIt + r0, k = atomicAdd(&B.n_poison, 1);
                             if (k < kPoison) B.poison[k] = key * 4 + g;
                             atomicMin(&B.poison_lo, key);
                             atomicMax(&B.poison_hi, key);
                         }
-                    }
-        };
-        auto put = [&](unsigned char* tile, const uint4 (&cw)[kIts], const uint32_t (&aw)[kIts][NG]) {
-            const uint32_t base = ptx::smem_addr(tile);
 #pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-                const int r = it * kPerIt + r0;
-                const uint32_t words[4] = {cw[it].x, cw[it].y, cw[it].z, cw[it].w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {  // word 4 piece + x: elements 8i .. 8i+7 of group g
-                    const int g = (4 * piece + x) % NG, i = (4 * piece + x) / NG;
-                    const uint32_t af = NG == 1 ? aw[it][0] : NG == 4 ? aw[it][x] : aw[it][x & 1];
-                    const __half2 s2 = __half2half2(__ushort_as_half((unsigned short)(af & 0xFFFFu)));
-                    const __half2 b2 = __half2half2(__ushort_as_half((unsigned short)(af >> 16)));
-                    ptx::sts_u4(base + g * (KT * 128) + r * 128 + ((i ^ (r & 7)) << 4), dequant8(words[x], s2, b2));
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t p = at_word(base, it, x);
+                    uint4 v = ptx::lds_u4(p);
+                    v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                    if (values && !finite(affine_at(aw[it], x))) v = make_uint4(0, 0, 0, 0);
+                    ptx::sts_u4(p, v);
                 }
             }
         };
@@ -682,6 +706,7 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             if (!ok) break;
             note(j);
             put(sk + st * S::kTile, kw, ka);
+            if (__any_sync(kFull, past(ka))) mend(sk + st * S::kTile, ka, false, j);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.k_full[st]);
             if (more) {
@@ -691,8 +716,8 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             }
             ok = __all_sync(kFull, ptx::mbar_wait_bounded(&B.v_empty[st], ph, abortp));
             if (!ok) break;
-            sift(j, va);
             put(sv + st * S::kTile, vw, va);
+            if (__any_sync(kFull, past(va))) mend(sv + st * S::kTile, va, true, j);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&B.v_full[st]);
             if (more) fetch(j + 1, 1, vw, va);

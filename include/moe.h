@@ -492,6 +492,8 @@ moe_status moe_layer_prefetch(moe_layer* layer, int32_t n, int32_t* queued);
  * With NG = head_dim/64 groups, 32-bit word i * NG + j of a token's codes holds
  * elements 8i .. 8i+7 of group j, nibble n (bits 4n..4n+3) element
  * {0, 2, 4, 6, 1, 3, 5, 7}[n] of them. An element's value is scale * code + bias.
+ * Rounding the scale up takes a group's largest value above its largest
+ * element by up to 15 roundings, so past fp16's 65,504 for elements near that (65,624 at most).
  * Token t of a sequence lies in page page_table[t / page_tokens], at place
  * t % page_tokens. New pages need no initialisation: places past a sequence's
  * length are never used, whatever bytes they hold. Several caches (one per
@@ -549,8 +551,9 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const int32_t* s
  * out = 0, lse = -inf. Softmax statistics and sums are fp32. Keys, values and
  * probabilities enter the tensor cores in fp16 or exact integer codes (a
  * probability under 2^-19 of a row's largest is off by up to 2^-30 of that
- * instead of a relative 2^-11), queries as fp16 scaled by a power of two per
- * row (exact for all but elements under 2^-14 of the row's largest).
+ * instead of a relative 2^-11; keys and values past fp16's range may be taken
+ * as +-65,504), queries as fp16 scaled by a power of two per row (exact for
+ * all but elements under 2^-14 of the row's largest).
  * Repeating a call on the same data gives the same bits. */
 typedef struct {
     const void* q; /* device, [n_q][n_heads][head_dim] of dtype (MOE_F16 or MOE_BF16), head_dim contiguous,

@@ -122,3 +122,44 @@ def test_small_weights_beside_a_key_that_takes_nearly_all(ctx, D, dtype, n, bits
     tol = (U + unit(dtype) + 2 * 30 * 2.0 ** -22) * out + n * 2.0 ** -24 * p[live].sum() / p.sum() + low + tiny
     assert (np.abs(got - out) <= tol).all(), (np.abs(got - out) / tol).max()
     assert (np.abs(lse.double().cpu().numpy() - rl) <= 1e-4).all()
+
+
+# (least, largest) element of a group, the others small: held as up to 65,520, 65,540, 65,536 and 65,592
+PAST = [(0.0, 65472.0), (-100.0, 1e30), (-np.inf, np.inf), (-57400.0, 65504.0)]
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16), (256, torch.float16)])
+def test_values_past_the_largest_fp16(ctx, D, dtype, side, hint):
+    """A group's largest value lies above its largest element by up to 15 roundings of its scale, past fp16's
+    65,504. Rows that do not see it are as they were (in the prompt kernel to the bit; in the decode
+    kernel the power of two that weights are scaled by may be another, and the bound below holds). The others are within
+    the bound, to which the prompt kernel adds 65,624 taken as 65,504, less than 4 U of the value. Queries are
+    small where a key is that large, so that its logits are of ordinary size."""
+    H, P, n, T = 2, 32, 200, 150
+    rng = np.random.default_rng(D)
+    k, v = (rng.standard_normal((n, H, D)).astype(np.float32) for _ in range(2))
+    q = rng.standard_normal((T, 2 * H, D))
+    at = D - 64 + 5  # the element that is large, in the last group
+    q[:, :, D - 64:] *= 2.0 ** -14
+    q = torch.from_numpy(q.astype(np.float32)).to(dtype).cuda()
+    pages = kv.empty_pages(-(-n // P), H, D, P)
+    kv.append(pages, P, k, v, np.arange(n))
+    cache, table = in_order(pages, P)
+    clean = attend(ctx, cache, table, n, q, hint)
+    for j, (lo, hi) in zip((60, 90, 120, 170), PAST):
+        x = (k if side == "k" else v)[j:j + 1].copy()
+        x[0, 1, D - 64:] *= 0.01
+        x[0, 1, at], x[0, 1, at + 1] = hi, lo
+        changed = pages.copy()
+        kv.append(changed, P, x if side == "k" else k[j:j + 1], v[j:j + 1] if side == "k" else x, [j])
+        held = kv.read(changed, P, [j])[side == "v"]
+        assert held.max() > 65504
+        cache, table = in_order(changed, P)
+        got = attend(ctx, cache, table, n, q, hint)
+        first = j - (n - T)
+        assert hint == 1 or torch.equal(got[:first], clean[:first])
+        out, _, e = exact(changed, P, q, n)
+        diff = np.abs(got.double().cpu().numpy() - out)
+        assert (diff <= bound(e, dtype, 4)).all(), (lo, hi, np.argwhere(~(diff <= bound(e, dtype, 4)))[:4])
