@@ -51,7 +51,6 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -3e38f;
 constexpr float kHead = 7.0f;  // log2 of what P is scaled by: P <= 2^(kLazy + kHead)
-constexpr int kPoison = 64;  // NaN values noted exactly; more are taken as a range
 
 template <int D>
 struct PShape {
@@ -83,8 +82,7 @@ struct Bars {
     uint64_t o_done[2];  // after a row tile's last one
     uint32_t tmem;
     int abort;
-    int n_poison, poison_lo, poison_hi;
-    int poison[kPoison];  // key * 4 + group
+    int nan_lo, nan_hi;   // first and last key with a value group that is not finite
     uint4 hide[8];        // of tiles j mod 8: keys (bits) whose page is outside the cache
 };
 
@@ -123,6 +121,9 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
 __device__ __forceinline__ uint32_t finite2(uint32_t x) {
     return as_u32(__hmax2_nan(__hmin2_nan(as_h2(x), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
 }
+
+// Whether scale and bias are finite: an exponent of all ones carries into bit 15 or 31.
+__device__ __forceinline__ bool finite_affine(uint32_t af) { return !(((af & 0x7C007C00u) + 0x04000400u) & 0x80008000u); }
 
 #define R8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 #define W8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -298,10 +299,9 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         }
         ptx::mbar_init(&B.o_full, 1);
         B.abort = 0;
-        B.n_poison = 0;
         for (int i = 0; i < 8; ++i) B.hide[i] = make_uint4(0, 0, 0, 0);
-        B.poison_lo = 0x7FFFFFFF;
-        B.poison_hi = -1;
+        B.nan_lo = 0x7FFFFFFF;
+        B.nan_hi = -1;
     }
     ptx::fence_mbar_init();
     if (warp == S::kWarpMma) {
@@ -485,15 +485,30 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
             if (!ok && lane == 0) give_up(1u << 17);
             ptx::tc_fence_after();
         }
-        // NaN values are kept out of the products, where a weight of zero would spread them:
-        // the rows that see one are NaN in its group
+        // NaN values are kept out of the products, where a weight of zero would spread them: the rows that see one
+        // are NaN in its group. Which do is worked out from the records once more, 32 keys at a time (a microsecond or two),
+        // between the first and the last such key that the CTA met.
         unsigned nan = 0;
-        if (const int np = *(volatile int*)&B.n_poison) {
-            for (int i = 0; i < min(np, kPoison); ++i) {
-                const int e = B.poison[i], k = e >> 2;
-                if (k >= lo && k < hi) nan |= 1u << (e & 3);
+        if (const int last = *(volatile int*)&B.nan_hi; last >= 0) {
+            const int from = max((int)__reduce_min_sync(kFull, (unsigned)(in ? lo : 0x7FFFFFFF)), *(volatile int*)&B.nan_lo);
+            const int to = min((int)__reduce_max_sync(kFull, (unsigned)(in ? max(hi, 0) : 0)), last + 1);
+            const int32_t* const table = a.table + (int64_t)w.b * a.table_stride;
+            for (int base = from; base < to; base += 32) {
+                const int key = base + lane;
+                const int page = key < to ? table[key >> a.c.page_shift] : -1;
+                unsigned mine = 0;
+                if ((unsigned)page < (unsigned)a.c.n_pages) {
+                    const uint8_t* rec = a.c.pages + (((size_t)page * a.c.H + w.h) * (a.c.P >> 4) + ((key & (a.c.P - 1)) >> 4)) * kRec;
+                    const uint32_t* ap = reinterpret_cast<const uint32_t*>(rec + kv_v_affine(D)) + (key & 15) * NG;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) mine |= (unsigned)!finite_affine(ap[g]) << g;
+                }
+                const int up = hi - base, down = lo - base;
+                const uint32_t seen = (up >= 32 ? ~0u : (1u << max(up, 0)) - 1) & (down >= 32 ? 0u : ~0u << max(down, 0));
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    if (__ballot_sync(kFull, mine >> g & 1) & seen) nan |= 1u << g;
             }
-            if (np > kPoison && B.poison_lo < hi && B.poison_hi >= lo) nan = 15u;
         }
         float* const slot = a.part + (size_t)(blockIdx.x - (unsigned)a.full) * S::kSlot;
         if (ok) {
@@ -668,24 +683,21 @@ __global__ void __launch_bounds__(PShape<D>::kThreads, 1) kv_prompt_kernel(const
         // are noted (see the epilogue).
         auto mend = [&](unsigned char* tile, const uint32_t (&aw)[kIts][NG], bool values, int j) {
             const uint32_t base = ptx::smem_addr(tile);
-            auto finite = [](uint32_t af) { return !(((af & 0x7C007C00u) + 0x04000400u) & 0x80008000u); };
 #pragma unroll
             for (int it = 0; it < kIts; ++it) {
                 if (values && piece == 0)
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
-                        if (!finite(aw[it][g])) {
-                            const int key = w.k0 + j * KT + it * kPerIt + r0, k = atomicAdd(&B.n_poison, 1);
-                            if (k < kPoison) B.poison[k] = key * 4 + g;
-                            atomicMin(&B.poison_lo, key);
-                            atomicMax(&B.poison_hi, key);
+                        if (!finite_affine(aw[it][g])) {
+                            atomicMin(&B.nan_lo, w.k0 + j * KT + it * kPerIt + r0);
+                            atomicMax(&B.nan_hi, w.k0 + j * KT + it * kPerIt + r0);
                         }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint32_t p = at_word(base, it, x);
                     uint4 v = ptx::lds_u4(p);
                     v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-                    if (values && !finite(affine_at(aw[it], x))) v = make_uint4(0, 0, 0, 0);
+                    if (values && !finite_affine(affine_at(aw[it], x))) v = make_uint4(0, 0, 0, 0);
                     ptx::sts_u4(p, v);
                 }
             }

@@ -163,3 +163,39 @@ def test_values_past_the_largest_fp16(ctx, D, dtype, side, hint):
         out, _, e = exact(changed, P, q, n)
         diff = np.abs(got.double().cpu().numpy() - out)
         assert (diff <= bound(e, dtype, 4)).all(), (lo, hi, np.argwhere(~(diff <= bound(e, dtype, 4)))[:4])
+
+
+def affine(pages):
+    """Writable views of the records' K and V affine words: fp16 [pages][H][blocks][16][NG][scale, bias] each."""
+    d = pages.shape[-1] // 18
+    return [pages[..., (16 + side) * d:(17 + side) * d].view(np.float16).reshape(pages.shape[:-1] + (16, d // 64, 2)) for side in (0, 1)]
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_nan_values(ctx, D, window, hint):
+    """Ninety tokens whose values are NaN in one group, at two places: NaN is that group of the rows that see
+    one of them, and nothing else; a windowed row between the places sees none."""
+    H, P, n, T = 2, 32, 420, 400
+    rng = np.random.default_rng(D)
+    pages = kv.empty_pages(-(-n // P), H, D, P)
+    kv.append(pages, P, *(rng.standard_normal((n, H, D)).astype(np.float32) for _ in range(2)), np.arange(n))
+    q = torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).half().cuda()
+    cache, table = in_order(pages, P)
+    clean = attend(ctx, cache, table, n, q, hint, window=window)
+    bad = np.r_[150:195, 225:270]
+    group = D // 64 - 1
+    affine(pages)[1][bad // P, 1, bad % P // 16, bad % 16, group, 0] = np.nan  # kv head 1
+    cache, table = in_order(pages, P)
+    got = attend(ctx, cache, table, n, q, hint, window=window)
+    pos = n - T + np.arange(T)[:, None]
+    see = (bad <= pos) & ((bad > pos - window) if window else True)
+    want = np.zeros((T, H, D), bool)
+    want[see.any(1), 1, 64 * group:64 * group + 64] = True
+    nan = got.isnan().cpu().numpy()
+    assert (nan == want).all(), np.argwhere(nan != want)[:4]
+    # the rest is what it was, but for other powers of two that the weights are scaled by: both within 3 U + u of
+    # mag, at most the largest value, which is below 5
+    diff = np.abs(got.double().cpu().numpy() - clean.double().cpu().numpy())[~want]
+    assert diff.max() <= 2 * 4 * U * 5
