@@ -626,7 +626,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
 
         // The sums hold 2^(cz z - me): me = m - lf, m within kLazy of the largest cz z so far, 2^lf the
         // factor that keeps weight times scale within fp16's range. thr: the z that passes the bound; lim: the largest
-        // scale that 2^lf serves.
+        // scale (by magnitude) that 2^lf serves.
         float o[NT][D / 16][4], wsum[NT][4], bacc[NT][NG][2], thr[NT][2], me[NT][2], l[NT][2], lim = 0.0f, lf = 24.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
-                        sm = __hmax2(sm, *reinterpret_cast<const __half2*>(&va[sb][r][j]));
+                        sm = __hmax2(sm, __habs2(*reinterpret_cast<const __half2*>(&va[sb][r][j])));
             const float smax = __low2float(sm);
             over |= smax > lim;
             if (__any_sync(kFull, over)) {
@@ -811,8 +811,9 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
                     float2 r0 = affine_of(va[sb][0][j]), r1 = affine_of(va[sb][1][j]);
                     if (kCentre) {
                         r0.y = fmaf(8.0f, r0.x, r0.y), r1.y = fmaf(8.0f, r1.x, r1.y);
-                        // a NaN group's bias is NaN too and says so; its weights would reach the other groups' sums
-                        r0.x = fmaxf(r0.x, 0.0f), r1.x = fmaxf(r1.x, 0.0f);
+                        // a group that is not finite: this bias says so, and its weights would reach the other groups' sums
+                        if (!(fabsf(r0.x) <= 65504.0f)) r0.x = 0.0f;
+                        if (!(fabsf(r1.x) <= 65504.0f)) r1.x = 0.0f;
                     }
                     uint32_t pb[NT][2];
 #pragma unroll

@@ -491,7 +491,8 @@ moe_status moe_layer_prefetch(moe_layer* layer, int32_t n, int32_t* queued);
  *   V affine: likewise.
  * With NG = head_dim/64 groups, 32-bit word i * NG + j of a token's codes holds
  * elements 8i .. 8i+7 of group j, nibble n (bits 4n..4n+3) element
- * {0, 2, 4, 6, 1, 3, 5, 7}[n] of them. An element's value is scale * code + bias.
+ * {0, 2, 4, 6, 1, 3, 5, 7}[n] of them. An element's value is scale * code + bias,
+ * the scale of either sign (moe_kv_append writes none below zero).
  * Rounding the scale up takes a group's largest value above its largest
  * element by up to 15 roundings, so past fp16's 65,504 for elements near that (65,624 at most).
  * Token t of a sequence lies in page page_table[t / page_tokens], at place

@@ -199,3 +199,25 @@ def test_many_nan_values(ctx, D, window, hint):
     # mag, at most the largest value, which is below 5
     diff = np.abs(got.double().cpu().numpy() - clean.double().cpu().numpy())[~want]
     assert diff.max() <= 2 * 4 * U * 5
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("share", [1.0, 0.5])
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (64, torch.bfloat16), (128, torch.float16), (128, torch.bfloat16),
+                                     (256, torch.float16), (256, torch.bfloat16)])
+def test_negative_scales(ctx, D, dtype, share, hint):
+    """Records of the caller's own whose scales are negative, all of them or half: value = scale * code + bias
+    all the same. A group's values are mirrored (code c for 15 - c), so they are of ordinary size."""
+    H, P, n, T = 2, 32, 333, 3
+    rng = np.random.default_rng(D + int(10 * share))
+    pages = kv.empty_pages(-(-n // P), H, D, P)
+    kv.append(pages, P, *(rng.standard_normal((n, H, D)).astype(np.float32) for _ in range(2)), np.arange(n))
+    for a in affine(pages):
+        turn = rng.random(a.shape[:-1]) < share
+        a[..., 1] = np.where(turn, a[..., 1] + 15 * a[..., 0], a[..., 1])
+        a[..., 0] = np.where(turn, -a[..., 0], a[..., 0])
+    q = torch.from_numpy(rng.standard_normal((T, 4 * H, D)).astype(np.float32)).to(dtype).cuda()
+    cache, table = in_order(pages, P)
+    got = attend(ctx, cache, table, n, q, hint).double().cpu().numpy()
+    out, _, e = exact(pages, P, q, n)
+    assert (np.abs(got - out) <= bound(e, dtype)).all(), np.abs(got - out).max()
