@@ -189,6 +189,23 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _new(shape, dtype, device, stream):
+    """An output that the caller did not give, allocated on the stream that the call runs on: torch hands memory out and
+    takes it back in stream order, so memory of another stream may be in use by what is pending there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = getattr(stream, "cuda_stream", stream)
+        if raw == 2:  # cudaStreamPerThread: another stream in every thread
+            raise ValueError("the per-thread default stream has no memory of its own: give the outputs")
+        # 0 and 1 (cudaStreamLegacy) are the legacy default stream
+        stream = torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 # ---------------------------------------------------------------------------
 # context and layer
 
@@ -259,9 +276,9 @@ def moe_route(layer: int, x, top_k: int, zbias=None, ids=None, gates=None, strea
 
     T = x.shape[0]
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        ids = _new((T, top_k), torch.int32, x.device, stream)
     if gates is None:
-        gates = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        gates = _new((T, top_k), torch.float32, x.device, stream)
     _check(load().moe_route(layer, _dptr(x), T, _dptr(zbias), _dptr(ids), _dptr(gates), _stream(stream)),
            "moe_route")
     return ids, gates
@@ -325,7 +342,7 @@ def moe_forward(layer: int, x, zbias=None, y=None, ids_out=None, gates_out=None,
 
     T, d = x.shape
     if y is None:
-        y = torch.empty((T, d), dtype=torch.float32, device=x.device)
+        y = _new((T, d), torch.float32, x.device, stream)
     _check(load().moe_forward(layer, _dptr(x), T, _dptr(zbias), _dptr(y), _dptr(ids_out), _dptr(gates_out),
                               _stream(stream)), "moe_forward")
     return y
@@ -338,7 +355,7 @@ def moe_forward_prompt(layer: int, x, zbias=None, y=None, ids_out=None, gates_ou
 
     T, d = x.shape
     if y is None:
-        y = torch.empty((T, d), dtype=torch.float32, device=x.device)
+        y = _new((T, d), torch.float32, x.device, stream)
     _check(load().moe_forward_prompt(layer, _dptr(x), T, _dptr(zbias), _dptr(y), _dptr(ids_out), _dptr(gates_out),
                                      _stream(stream)), "moe_forward_prompt")
     return y
@@ -599,13 +616,13 @@ def moe_kv_read(ctx: int, cache: moe_kv_cache, slots, dtype=None, k=None, v=None
     n = slots.shape[0]
     if k is None and v is None:
         dtype = dtype or _torch.bfloat16
-        k = _torch.empty((n, cache.heads, cache.dim), dtype=dtype, device=slots.device)
-        v = _torch.empty_like(k)
+        k = _new((n, cache.heads, cache.dim), dtype, slots.device, stream)
+        v = _new(k.shape, dtype, slots.device, stream)
         kt, kh = cache.heads * cache.dim, cache.dim
         kp, vp, vt, vh = k.data_ptr(), v.data_ptr(), kt, kh
     else:
-        k = _torch.empty_like(v, memory_format=_torch.contiguous_format) if k is None else k
-        v = _torch.empty_like(k, memory_format=_torch.contiguous_format) if v is None else v
+        k = _new(v.shape, v.dtype, v.device, stream) if k is None else k
+        v = _new(k.shape, k.dtype, k.device, stream) if v is None else v
         dtype = k.dtype
         kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
         vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)
@@ -626,7 +643,7 @@ def moe_kv_attend(ctx: int, cache: moe_kv_cache, q, page_table, kv_len, q_start=
     B, (n, heads) = kv_len.shape[0], q.shape[:2]
     qp, qt, qh = _kv_rows(q, "q", n, heads, cache)
     if out is None:
-        out = _torch.empty((n, heads, cache.dim), dtype=q.dtype, device=q.device)
+        out = _new((n, heads, cache.dim), q.dtype, q.device, stream)
         op, ot, oh = out.data_ptr(), heads * cache.dim, cache.dim
     elif out.dtype != q.dtype:
         raise ValueError("out: expected q's type")
