@@ -211,7 +211,7 @@ struct moe_ctx {
     unsigned* err_host = nullptr;   // mapped pinned word that kernels report expired waits into
     unsigned* err_dev = nullptr;
     uint32_t err_generation = 0;  // bumped whenever a kernel reported an expired wait
-    KvState* kv = nullptr;        // the cache calls' workspace and error word, made by the first of them
+    KvState* kv = nullptr;        // the cache calls' error words and workspace
     std::mutex kv_mu;
     long fail_copy_at = -1;  // test hook: the n-th miss copy from now reports failure
     long copies_issued = 0;
@@ -491,7 +491,7 @@ void moe::ctx_launch_end(void* rec) { delete static_cast<Prof*>(rec); }
 bool moe::ctx_profiling(const moe_ctx* C) { return C->profiling; }
 void moe::ctx_count_launch(moe_ctx* C) { ++C->launches; }
 int moe::ctx_device(const moe_ctx* C) { return C->device; }
-KvState*& moe::ctx_kv(moe_ctx* C) { return C->kv; }
+KvState* moe::ctx_kv(moe_ctx* C) { return C->kv; }
 std::mutex& moe::ctx_kv_mutex(moe_ctx* C) { return C->kv_mu; }
 
 namespace {
@@ -1393,7 +1393,7 @@ extern "C" moe_status moe_ctx_create(int device, moe_ctx** out) {
     if (cudaStreamCreateWithFlags(&C->copy_stream, cudaStreamNonBlocking) != cudaSuccess ||
         cudaEventCreateWithFlags(&C->staging_free, cudaEventDisableTiming) != cudaSuccess ||
         cudaHostAlloc(&C->err_host, sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
-        cudaHostGetDevicePointer(&C->err_dev, C->err_host, 0) != cudaSuccess) {
+        cudaHostGetDevicePointer(&C->err_dev, C->err_host, 0) != cudaSuccess || !(C->kv = kv_state_create())) {
         cudaGetLastError();
         delete C;
         return set_error(MOE_ECUDA, "stream/event creation failed");

@@ -33,6 +33,19 @@ struct KvState {
     bool ws_used = false;
 };
 
+KvState* kv_state_create() {
+    KvState* n = new (std::nothrow) KvState();
+    if (!n) return nullptr;
+    if (cudaHostAlloc(&n->bad_host, 2 * sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
+        cudaHostGetDevicePointer(&n->bad_dev, n->bad_host, 0) != cudaSuccess) {
+        cudaGetLastError();
+        kv_state_destroy(n);
+        return nullptr;
+    }
+    n->bad_host[0] = n->bad_host[1] = 0;
+    return n;
+}
+
 void kv_state_destroy(KvState* st) {
     if (!st) return;
     cudaFreeHost(st->bad_host);
@@ -60,9 +73,13 @@ int decode_whole(int head_dim) { return head_dim == 256 ? 24 : head_dim == 128 ?
 
 constexpr size_t kJoinBytes = 1024 * sizeof(KvJoin);  // for up to 1,024 CTAs
 
-// The workspace of an attention call, made by the first of them.
-moe_status ensure_workspace(KvState* S, int device) {
+// The workspace of an attention call on s, made by the first of them.
+moe_status ensure_workspace(KvState* S, int device, cudaStream_t s) {
     if (S->ws) return MOE_OK;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    CUDA_TRY(cudaStreamIsCapturing(s, &cs));
+    if (cs != cudaStreamCaptureStatusNone)  // an allocation would end the capture
+        return set_error(MOE_ESTATE, "moe_kv_attend: a context's first attention call cannot be captured (it allocates)");
     int sms = 0;
     CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
     if ((size_t)sms * kKvMaxCtas * sizeof(KvJoin) > kJoinBytes)
@@ -136,25 +153,6 @@ bool rows_ok(const void* p, int64_t ts, int64_t hs, moe_dtype t) {
     return !(reinterpret_cast<uintptr_t>(p) & 15) && ts % per == 0 && hs % per == 0;
 }
 
-// The context's cache state, made by its first cache call. Held under the context's mutex.
-moe_status state_of(moe_ctx* C, KvState** out) {
-    KvState*& st = ctx_kv(C);
-    if (!st) {
-        KvState* n = new (std::nothrow) KvState();
-        if (!n) return set_error(MOE_ENOMEM, "out of host memory");
-        if (cudaHostAlloc(&n->bad_host, 2 * sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
-            cudaHostGetDevicePointer(&n->bad_dev, n->bad_host, 0) != cudaSuccess) {
-            cudaGetLastError();
-            kv_state_destroy(n);
-            return set_error(MOE_ENOMEM, "cache state allocation failed");
-        }
-        n->bad_host[0] = n->bad_host[1] = 0;
-        st = n;
-    }
-    *out = st;
-    return MOE_OK;
-}
-
 moe_status expired(KvState* S) {
     const unsigned code = *(volatile unsigned*)(S->bad_host + 1);
     *(volatile unsigned*)(S->bad_host + 1) = 0;
@@ -192,8 +190,7 @@ moe_status rows_call(const char* who, moe_ctx* C, const moe_kv_cache* cache, con
         return set_error(MOE_EINVAL, "%s: rows of k and v must start on 16-byte boundaries", who);
     CUDA_TRY(cudaSetDevice(ctx_device(C)));
     std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
-    KvState* S;
-    if ((st = state_of(C, &S)) != MOE_OK) return st;
+    KvState* const S = ctx_kv(C);
     KvRows a{};
     a.c = view(cache);
     a.slots = slots;
@@ -266,8 +263,7 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
         return set_error(MOE_EINVAL, "%s: rows of q and out must start on 16-byte boundaries", who);
     CUDA_TRY(cudaSetDevice(ctx_device(C)));
     std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
-    KvState* S;
-    if ((st = state_of(C, &S)) != MOE_OK) return st;
+    KvState* const S = ctx_kv(C);
     KvAttend a{};
     a.c = view(cache);
     a.q = p->q;
@@ -288,7 +284,7 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     a.bad = S->bad_dev;
     a.err = S->bad_dev + 1;
     if (*(volatile unsigned*)(S->bad_host + 1)) return expired(S);
-    if ((st = ensure_workspace(S, ctx_device(C))) != MOE_OK) return st;
+    if ((st = ensure_workspace(S, ctx_device(C), (cudaStream_t)stream)) != MOE_OK) return st;
     a.part = reinterpret_cast<float*>(S->ws + kJoinBytes);
     const int d = cache->head_dim;
     cudaStream_t s = (cudaStream_t)stream;
@@ -316,9 +312,9 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
 extern "C" moe_status moe_kv_check(moe_ctx* C) {
     if (!C) return set_error(MOE_EINVAL, "moe_kv_check: ctx is NULL");
     std::lock_guard<std::mutex> lock(ctx_kv_mutex(C));
-    KvState* S = ctx_kv(C);
-    if (S && *(volatile unsigned*)(S->bad_host + 1)) return expired(S);
-    if (S && *(volatile unsigned*)S->bad_host) {
+    KvState* const S = ctx_kv(C);
+    if (*(volatile unsigned*)(S->bad_host + 1)) return expired(S);
+    if (*(volatile unsigned*)S->bad_host) {
         *(volatile unsigned*)S->bad_host = 0;
         return set_error(MOE_EINVAL, "an earlier cache call met a slot or page id outside its cache");
     }

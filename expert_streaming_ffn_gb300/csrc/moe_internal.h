@@ -352,10 +352,11 @@ cudaError_t launch_pf_gemm(const PfArgs& a, int phase, const void* b0, const voi
 enum KvKind { K_KV_APPEND = 7, K_KV_READ = 8, K_KV_ATTEND = 9 };  // kernel kinds, after those of api.cu
 
 struct KvState;  // kv_api.cu
+KvState* kv_state_create();  // null if the allocation failed
 void kv_state_destroy(KvState* st);
 
 int ctx_device(const moe_ctx* C);
-KvState*& ctx_kv(moe_ctx* C);
+KvState* ctx_kv(moe_ctx* C);
 std::mutex& ctx_kv_mutex(moe_ctx* C);  // held by a cache call while it enqueues
 bool ctx_profiling(const moe_ctx* C);
 void ctx_count_launch(moe_ctx* C);

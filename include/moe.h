@@ -578,14 +578,14 @@ typedef struct {
 } moe_kv_attend_args;
 
 /* Asynchronous on `stream`, no synchronisation. The context owns a workspace
- * for partial results: its first call on a context allocates it (make it
- * before any stream capture), and calls on several streams of one context are
+ * for partial results: its first call on a context allocates it (and gives
+ * MOE_ESTATE under stream capture), and calls on several streams of one context are
  * ordered after one another on the device where they use it. Replays of a
  * captured call must not run at the same time as other attention calls of the
  * context. Several host threads may call. A page id outside the cache hides
  * that page's keys and is noted (moe_kv_check).
- * Errors: MOE_EINVAL, MOE_ENOMEM (workspace), MOE_ECUDA, MOE_ETIMEOUT (a
- * bounded device wait expired in an earlier call). */
+ * Errors: MOE_EINVAL, MOE_ENOMEM (workspace), MOE_ESTATE, MOE_ECUDA,
+ * MOE_ETIMEOUT (a bounded device wait expired in an earlier call). */
 moe_status moe_kv_attend(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_attend_args* args, void* stream);
 
 /* MOE_EINVAL if a finished moe_kv_* call of the context met a slot or page id

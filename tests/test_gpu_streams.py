@@ -1,4 +1,8 @@
-"""Outputs that a call makes itself, on a stream other than the current one."""
+"""Outputs that a call makes itself, on a stream other than the current one; and first calls under stream capture."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -71,3 +75,48 @@ def test_the_default_streams(calls):
     for name in ("attend", "read", "route"):
         with pytest.raises(ValueError, match="per-thread"):
             calls[name](2)
+
+
+FIRST_CALLS = """
+import torch
+import expert_streaming_ffn_gb300 as moe
+ctx = moe.moe_ctx_create(0)
+cache = moe.moe_kv_new_cache(4, 2, 64, 16)
+k = torch.randn((40, 2, 64), device="cuda").bfloat16()
+v = torch.randn_like(k)
+slots = torch.arange(40, dtype=torch.int32, device="cuda")
+q, out = torch.randn((1, 4, 64), device="cuda").bfloat16(), torch.empty((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+table, ln = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.tensor([40], dtype=torch.int32, device="cuda")
+rows = [torch.empty_like(k), torch.empty_like(v)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.moe_kv_append(ctx, cache, k, v, slots)
+    moe.moe_kv_read(ctx, cache, slots, k=rows[0], v=rows[1])
+    try:
+        moe.moe_kv_attend(ctx, cache, q, table, ln, out=out)
+        raise SystemExit("the first attention call was captured")
+    except moe.MoeError as e:
+        assert e.status == moe.MOE_ESTATE, e
+graph.replay()
+got = moe.moe_kv_read(ctx, cache, slots)
+torch.cuda.synchronize()
+assert torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1])
+assert (rows[0] - k).abs().max() < 0.5 and (rows[1] - v).abs().max() < 0.5  # steps of a fifteenth of a span of 6 or so
+want = moe.moe_kv_attend(ctx, cache, q, table, ln)
+with torch.cuda.graph(graph := torch.cuda.CUDAGraph()):
+    moe.moe_kv_attend(ctx, cache, q, table, ln, out=out)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, want)
+moe.moe_ctx_destroy(ctx)
+print("first calls ok")
+"""
+
+
+def test_first_calls_of_a_context_under_capture():
+    """Append and read allocate nothing, so they can be a context's first calls and captured ones; the first attention call
+    says that it cannot, and the capture goes on. In a process of its own, where no kernel has run before."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first calls ok" in r.stdout, r.stdout + r.stderr
