@@ -200,14 +200,16 @@ struct moe_ctx {
     uint8_t* staging = nullptr;  // transient arena for bypassed experts
     size_t staging_bytes = 0;
     cudaEvent_t staging_free = nullptr;  // after the last kernels that read staging
-    bool profiling = false;
+    // counted and timed by the context's layers and cache calls, from any thread
+    std::atomic<bool> profiling{false};
+    std::atomic<uint64_t> launches{0};  // kernels launched
+    std::mutex prof_mu;                 // of prof, acc, timing_pool and the trace
     std::vector<ProfRec> prof;
     struct Acc {
         uint64_t n = 0;
         double ms = 0, bytes = 0, flops = 0;
     } acc[kKinds];
     std::vector<cudaEvent_t> timing_pool;
-    uint64_t launches = 0;          // kernels launched by this context's layers
     unsigned* err_host = nullptr;   // mapped pinned word that kernels report expired waits into
     unsigned* err_dev = nullptr;
     uint32_t err_generation = 0;  // bumped whenever a kernel reported an expired wait
@@ -222,24 +224,36 @@ struct moe_ctx {
     std::vector<TraceHost> trace_host;
 
     unsigned long long* trace_span(int kind, int layer, uint32_t seq) {
-        if (!trace_spans || (int)trace_launches.size() >= kTraceSpans) return nullptr;
+        if (!trace_spans) return nullptr;
+        std::lock_guard<std::mutex> lock(prof_mu);
+        if ((int)trace_launches.size() >= kTraceSpans) return nullptr;
         const int slot = (int)trace_launches.size();
         trace_launches.push_back(TraceLaunch{kind, layer, seq, slot, realtime_ns()});
         return trace_spans + 2 * slot;
     }
     void trace_mark(const char* what, int layer, uint32_t seq) {
-        if (trace_spans) trace_host.push_back(TraceHost{what, layer, seq, realtime_ns()});
+        if (!trace_spans) return;
+        std::lock_guard<std::mutex> lock(prof_mu);
+        trace_host.push_back(TraceHost{what, layer, seq, realtime_ns()});
     }
 
     cudaEvent_t timing_event() {
-        if (!timing_pool.empty()) {
-            cudaEvent_t e = timing_pool.back();
-            timing_pool.pop_back();
-            return e;
+        {
+            std::lock_guard<std::mutex> lock(prof_mu);
+            if (!timing_pool.empty()) {
+                cudaEvent_t e = timing_pool.back();
+                timing_pool.pop_back();
+                return e;
+            }
         }
         cudaEvent_t e = nullptr;
         cudaEventCreate(&e);
         return e;
+    }
+    void give_back(cudaEvent_t a, cudaEvent_t b) {
+        std::lock_guard<std::mutex> lock(prof_mu);
+        timing_pool.push_back(a);
+        timing_pool.push_back(b);
     }
 };
 
@@ -465,9 +479,10 @@ struct Prof {
     moe_ctx* C;
     cudaStream_t s;
     ProfRec r{};
-    Prof(moe_ctx* c, cudaStream_t st, int kind, double bytes, double flops) : C(c), s(st) {
+    const bool on;
+    Prof(moe_ctx* c, cudaStream_t st, int kind, double bytes, double flops) : C(c), s(st), on(c->profiling) {
         ++C->launches;
-        if (!C->profiling) return;
+        if (!on) return;
         r.kind = kind;
         r.bytes = bytes;
         r.flops = flops;
@@ -476,8 +491,9 @@ struct Prof {
         cudaEventRecord(r.a, s);
     }
     ~Prof() {
-        if (!C->profiling) return;
+        if (!on) return;
         cudaEventRecord(r.b, s);
+        std::lock_guard<std::mutex> lock(C->prof_mu);
         C->prof.push_back(r);
     }
 };
@@ -496,19 +512,27 @@ std::mutex& moe::ctx_kv_mutex(moe_ctx* C) { return C->kv_mu; }
 
 namespace {
 
+// Waits for the records so far and adds them to the sums. The wait is without the lock: a
+// kernel may wait for copies that another thread has yet to issue.
 void drain_prof(moe_ctx* C) {
-    for (ProfRec& r : C->prof) {
+    std::vector<ProfRec> recs;
+    {
+        std::lock_guard<std::mutex> lock(C->prof_mu);
+        recs.swap(C->prof);
+    }
+    for (const ProfRec& r : recs) {
         cudaEventSynchronize(r.b);
         float ms = 0;
         cudaEventElapsedTime(&ms, r.a, r.b);
-        C->acc[r.kind].n += 1;
-        C->acc[r.kind].ms += ms;
-        C->acc[r.kind].bytes += r.bytes;
-        C->acc[r.kind].flops += r.flops;
-        C->timing_pool.push_back(r.a);
-        C->timing_pool.push_back(r.b);
+        {
+            std::lock_guard<std::mutex> lock(C->prof_mu);
+            C->acc[r.kind].n += 1;
+            C->acc[r.kind].ms += ms;
+            C->acc[r.kind].bytes += r.bytes;
+            C->acc[r.kind].flops += r.flops;
+        }
+        C->give_back(r.a, r.b);
     }
-    C->prof.clear();
 }
 
 // Exposed copy time: how long the routed-expert kernel had misses still
@@ -521,8 +545,7 @@ void drain_waits(moe_layer* L) {
         if (cudaEventElapsedTime(&ms, w.ffn_start, w.copies_done) == cudaSuccess && ms > 0)
             L->stats.exposed_copy_us += 1000.0 * ms;
         cudaGetLastError();
-        L->ctx->timing_pool.push_back(w.ffn_start);
-        L->ctx->timing_pool.push_back(w.copies_done);
+        L->ctx->give_back(w.ffn_start, w.copies_done);
     }
     L->waits.clear();
 }
@@ -959,10 +982,10 @@ moe_status route_into(moe_layer* L, const uint16_t* x, int T, const float* zbias
 // the router, before the host has read the routing: the shared expert, and
 // each routed pair whose expert the device slot table shows resident (the
 // kernel looks the experts up itself once the router has finished). Misses
-// are skipped there and launched after the cache step. *prof_index is the
-// launch's timing record (profiling), whose bytes the caller corrects once
-// the misses are known.
-moe_status run_resident_on_device(moe_layer* L, const uint16_t* x, float* y, cudaStream_t s, long* prof_index) {
+// are skipped there and launched after the cache step. *timed: the launch is
+// timed (profiling), as if every pair were resident; the caller takes the misses'
+// bytes off once it knows them.
+moe_status run_resident_on_device(moe_layer* L, const uint16_t* x, float* y, cudaStream_t s, bool* timed) {
     std::vector<Item> items;
     items.push_back(Item{L->d_shared, 0, 1, nullptr, -1, -1, 0});
     for (int p = 0; p < L->sh.top_k; ++p) items.push_back(Item{nullptr, p, p + 1, nullptr, -1, -1, 1});
@@ -971,7 +994,7 @@ moe_status run_resident_on_device(moe_layer* L, const uint16_t* x, float* y, cud
     a.slot_of = L->d_slot_of;
     a.slots = L->d_slots;
     a.ebytes = L->ebytes;
-    *prof_index = L->ctx->profiling ? (long)L->ctx->prof.size() : -1;
+    *timed = L->ctx->profiling;
     L->record_resident = true;
     const moe_status st = launch_items_any(L, items, a, K_FFN, s);
     L->record_resident = false;
@@ -1285,9 +1308,9 @@ moe_status forward_chunk(moe_layer* L, const uint16_t* x, int T, const float* zb
     const bool device_routed = T == 1 && 1 + sh.top_k <= (int)(sizeof(FfnSmall::item) / sizeof(FfnItem));
     moe_status st = route_into(L, x, T, zbias, L->d_ids, L->d_gates, true, s, decode ? y : nullptr);
     if (st != MOE_OK) return st;
-    long r_prof = -1;
+    bool timed = false;
     if (device_routed) {
-        st = run_resident_on_device(L, x, y, s, &r_prof);
+        st = run_resident_on_device(L, x, y, s, &timed);
         if (st != MOE_OK) return st;
     } else if (decode) {
         st = run_shared(L, x, T, y, s);
@@ -1312,9 +1335,10 @@ moe_status forward_chunk(moe_layer* L, const uint16_t* x, int T, const float* zb
         const size_t n_miss = L->step.miss_experts.size();
         const double mb = (double)n_miss * L->ebytes;
         L->stats.bytes_resident -= (uint64_t)mb;
-        if (r_prof >= 0 && r_prof < (long)C->prof.size()) {
-            C->prof[r_prof].bytes -= mb;
-            C->prof[r_prof].flops -= 6.0 * n_miss * sh.d_model * sh.d_ff;
+        if (timed && n_miss) {
+            std::lock_guard<std::mutex> lock(C->prof_mu);
+            C->acc[K_FFN].bytes -= mb;
+            C->acc[K_FFN].flops -= 6.0 * n_miss * sh.d_model * sh.d_ff;
         }
     }
     L->stats.steps += 1;
@@ -1800,6 +1824,7 @@ extern "C" moe_status moe_ctx_kernel_times(moe_ctx* C, int32_t kind, uint64_t* l
     if (!C || kind < 0 || kind >= kKinds) return set_error(MOE_EINVAL, "moe_ctx_kernel_times: bad arguments");
     cudaSetDevice(C->device);
     drain_prof(C);
+    std::lock_guard<std::mutex> lock(C->prof_mu);
     if (launches) *launches = C->acc[kind].n;
     if (total_ms) *total_ms = C->acc[kind].ms;
     if (bytes) *bytes = C->acc[kind].bytes;
@@ -1811,6 +1836,7 @@ extern "C" moe_status moe_ctx_reset_kernel_times(moe_ctx* C) {
     if (!C) return set_error(MOE_EINVAL, "ctx is NULL");
     cudaSetDevice(C->device);
     drain_prof(C);
+    std::lock_guard<std::mutex> lock(C->prof_mu);
     for (auto& a : C->acc) a = moe_ctx::Acc{};
     return MOE_OK;
 }
