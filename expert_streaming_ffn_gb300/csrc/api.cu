@@ -281,7 +281,7 @@ struct moe_layer {
     cudaEvent_t ev_done = nullptr;     // end of the layer's last call
     cudaEvent_t ev_pending = nullptr;  // copies issued by moe_cache_step
     bool pending = false;              // ev_pending recorded since the last forward
-    cudaStream_t last_stream = nullptr;  // stream of the last call that recorded ev_done
+    unsigned long long last_stream = 0;  // id of the stream of the last call that recorded ev_done (handles come back)
     bool have_last_stream = false;
     bool loaded = false;
     // scratch, sized for cap_T tokens per call
@@ -1286,7 +1286,9 @@ moe_status forward_chunk(moe_layer* L, const uint16_t* x, int T, const float* zb
     C->trace_mark("call", L->id, L->seq + 1);
     // the layer's previous call and any copies moe_cache_step issued come first;
     // a call on the stream that recorded ev_done is already ordered after it
-    if (!L->have_last_stream || L->last_stream != s) CUDA_TRY(cudaStreamWaitEvent(s, L->ev_done, 0));
+    unsigned long long stream_id = 0;
+    CUDA_TRY(cudaStreamGetId(s, &stream_id));
+    if (!L->have_last_stream || L->last_stream != stream_id) CUDA_TRY(cudaStreamWaitEvent(s, L->ev_done, 0));
     if (L->pending) {
         CUDA_TRY(cudaStreamWaitEvent(s, L->ev_pending, 0));
         L->pending = false;
@@ -1373,7 +1375,7 @@ moe_status forward_chunk(moe_layer* L, const uint16_t* x, int T, const float* zb
     if (gates_out)
         CUDA_TRY(cudaMemcpyAsync(gates_out, L->d_gates, sizeof(float) * npairs, cudaMemcpyDeviceToDevice, s));
     CUDA_TRY(cudaEventRecord(L->ev_done, s));
-    L->last_stream = s;
+    L->last_stream = stream_id;
     L->have_last_stream = true;
     if (L->step.bypass > 0) CUDA_TRY(cudaEventRecord(C->staging_free, s));
     L->stats.host_issue_us += us_since(t0);
@@ -1704,7 +1706,7 @@ extern "C" moe_status moe_route(moe_layer* L, const void* x, int32_t T, const fl
                         ids + (size_t)t0 * L->sh.top_k, gates + (size_t)t0 * L->sh.top_k, false, s);
         if (st != MOE_OK) return st;
         CUDA_TRY(cudaEventRecord(L->ev_done, s));
-        L->last_stream = s;
+        CUDA_TRY(cudaStreamGetId(s, &L->last_stream));
         L->have_last_stream = true;
     }
     return MOE_OK;

@@ -29,7 +29,7 @@ struct KvState {
     int sms = 0;
     unsigned char* ws = nullptr;
     cudaEvent_t ws_done = nullptr;
-    cudaStream_t ws_stream = nullptr;
+    unsigned long long ws_stream = 0;  // its id
     bool ws_used = false;
 };
 
@@ -97,19 +97,24 @@ moe_status ensure_workspace(KvState* S, int device, cudaStream_t s) {
 }
 
 // Orders a call on s behind the last call that used the workspace on another
-// stream. A call being captured records no event outside its graph.
+// stream. A call being captured records no event outside its graph. Streams are told apart by
+// their ids: a handle can come back after its stream was destroyed, whose work may
+// still run, and the per-thread default stream's is the same in every thread.
 moe_status workspace_begin(KvState* S, cudaStream_t s, bool* capturing) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     CUDA_TRY(cudaStreamIsCapturing(s, &cs));
     *capturing = cs != cudaStreamCaptureStatusNone;
-    if (!*capturing && S->ws_used && S->ws_stream != s) CUDA_TRY(cudaStreamWaitEvent(s, S->ws_done, 0));
+    if (*capturing) return MOE_OK;
+    unsigned long long id = 0;
+    CUDA_TRY(cudaStreamGetId(s, &id));
+    if (S->ws_used && S->ws_stream != id) CUDA_TRY(cudaStreamWaitEvent(s, S->ws_done, 0));
+    S->ws_stream = id;
     return MOE_OK;
 }
 
 moe_status workspace_end(KvState* S, cudaStream_t s, bool capturing) {
     if (capturing) return MOE_OK;
     CUDA_TRY(cudaEventRecord(S->ws_done, s));
-    S->ws_stream = s;
     S->ws_used = true;
     return MOE_OK;
 }
@@ -303,10 +308,12 @@ extern "C" moe_status moe_kv_attend(moe_ctx* C, const moe_kv_cache* cache, const
     Launch l(C, K_KV_ATTEND, len * p->batch * cache->n_kv_heads * d * 1.125 + 4.0 * p->n_q * p->n_heads * d,
              4.0 * p->n_q * len * p->n_heads * d, s);
     int launched = 1;
-    CUDA_TRY(prompt ? launch_kv_prompt(a, d, p->dtype, work, s, &launched)
-                    : launch_kv_attend(a, d, p->dtype, p->max_q * a.G, S->sms, s, &launched));
+    const cudaError_t launch = prompt ? launch_kv_prompt(a, d, p->dtype, work, s, &launched)
+                                      : launch_kv_attend(a, d, p->dtype, p->max_q * a.G, S->sms, s, &launched);
     for (; launched > 1; --launched) ctx_count_launch(C);  // the first is counted already
-    return workspace_end(S, s, capturing);
+    st = workspace_end(S, s, capturing);  // the first of two launches may have gone out before an error
+    CUDA_TRY(launch);
+    return st;
 }
 
 extern "C" moe_status moe_kv_check(moe_ctx* C) {

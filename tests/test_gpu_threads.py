@@ -1,4 +1,5 @@
 """Cache calls, layer calls and readings of the kernel times of one context from several host threads."""
+import ctypes
 import threading
 
 import numpy as np
@@ -33,9 +34,9 @@ def together(*bodies):
         raise errors[0]
 
 
-def cache_calls(ctx, seed, n, stream):
-    """A cache of its own, filled; then calls on it: append, read and attention, whose results are compared with the
-    first ones'."""
+def attention(ctx, seed, n):
+    """A cache of its own, filled: the attention call on it (of an output and a stream), its result, the cache, its slots and
+    the rows in them."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     H, D, P = 2, 128, 32
     cache = moe.moe_kv_new_cache(-(-n // P), H, D, P)
@@ -44,7 +45,16 @@ def cache_calls(ctx, seed, n, stream):
     moe.moe_kv_append(ctx, cache, k, v, slots)
     q = torch.randn((1, 8, D), generator=g, device="cuda").bfloat16()
     table, ln = torch.arange(-(-n // P), dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda")
-    want = moe.moe_kv_attend(ctx, cache, q, table, ln)
+
+    def call(out, stream):
+        moe.moe_kv_attend(ctx, cache, q, table, ln, out=out, stream=stream)
+
+    return call, moe.moe_kv_attend(ctx, cache, q, table, ln), cache, slots, k, v
+
+
+def cache_calls(ctx, seed, n, stream):
+    """Calls on a cache: append, read and attention, whose results are compared with the first ones'."""
+    call, want, cache, slots, k, v = attention(ctx, seed, n)
     rows = moe.moe_kv_read(ctx, cache, slots)
     outs = [torch.zeros_like(want) for _ in range(8)]
     back = [torch.empty_like(k), torch.empty_like(v)]
@@ -53,7 +63,7 @@ def cache_calls(ctx, seed, n, stream):
     def body():
         for i in range(ROUNDS):
             moe.moe_kv_append(ctx, cache, k, v, slots, stream=stream)
-            moe.moe_kv_attend(ctx, cache, q, table, ln, out=outs[i % 8], stream=stream)
+            call(outs[i % 8], stream)
             if i % 8 == 7:
                 moe.moe_kv_read(ctx, cache, slots, k=back[0], v=back[1], stream=stream)
         torch.cuda.synchronize()
@@ -108,4 +118,34 @@ def test_cache_and_layer_calls_and_kernel_times():
     timed = sum(v[0] for v in t.values())
     assert moe.moe_ctx_launches(ctx) - n0 == timed + ROUNDS
     moe.moe_layer_destroy(layer)
+    moe.moe_ctx_destroy(ctx)
+
+
+def test_the_per_thread_default_stream_is_a_stream_of_each_thread():
+    """Its handle (2) is the same in every thread, the streams behind it are not: calls that share the context's workspace
+    are ordered after one another all the same."""
+    moe.load()
+    ctx = moe.moe_ctx_create(0)
+    together(*(cache_calls(ctx, seed, n, 2) for seed, n in ((1, 5000), (2, 7000), (3, 20000))))
+    moe.moe_ctx_destroy(ctx)
+
+
+def test_streams_that_are_made_anew():
+    """A new stream may get the handle of one that was destroyed with work pending on it."""
+    moe.load()
+    ctx = moe.moe_ctx_create(0)
+    rt = torch.cuda.cudart()
+    calls = [attention(ctx, i, n)[:2] for i, n in enumerate((20000, 31000))]
+    outs = [torch.zeros_like(calls[i % 2][1]) for i in range(40)]
+    torch.cuda.synchronize()
+    handles = []
+    for i, out in enumerate(outs):
+        h = ctypes.c_void_p()
+        rt.cudaStreamCreate(ctypes.addressof(h))
+        handles.append(h.value)
+        calls[i % 2][0](out, h.value)
+        rt.cudaStreamDestroy(h.value)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, calls[i % 2][1]), (i, len(set(handles)))
     moe.moe_ctx_destroy(ctx)
