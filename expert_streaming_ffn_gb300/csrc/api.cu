@@ -1472,7 +1472,7 @@ void write_trace(moe_ctx* C) {
 extern "C" void moe_ctx_destroy(moe_ctx* C) {
     if (!C) return;
     cudaSetDevice(C->device);
-    cudaStreamSynchronize(C->copy_stream);
+    cudaDeviceSynchronize();  // kernels of cache calls may still use the workspace and write the error words
     drain_prof(C);
     if (C->trace_spans) {
         write_trace(C);

@@ -127,7 +127,7 @@ typedef struct {
  * "host <step> <layer> <call> <host ns>".
  * Errors: MOE_EINVAL (no such device), MOE_ECUDA. */
 moe_status moe_ctx_create(int device, moe_ctx** out);
-void moe_ctx_destroy(moe_ctx* ctx); /* after all its layers are destroyed */
+void moe_ctx_destroy(moe_ctx* ctx); /* after all its layers are destroyed; waits for the device */
 
 /* ---- layer -------------------------------------------------------------- */
 

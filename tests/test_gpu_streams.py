@@ -120,3 +120,24 @@ def test_first_calls_of_a_context_under_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "first calls ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_a_context_destroyed_with_calls_pending():
+    """Destroying waits for them: a call that cuts segments uses the context's workspace, one with a bad slot its error words."""
+    moe.load()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = 30000
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    k = torch.randn((n, 2, 128), generator=g, device="cuda").bfloat16()
+    q = torch.randn((1, 8, 128), generator=g, device="cuda").bfloat16()
+    table, ln = torch.arange(-(-n // 64), dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda")
+    outs = []
+    for _ in range(3):
+        ctx = moe.moe_ctx_create(0)
+        cache = moe.moe_kv_new_cache(table.shape[1], 2, 128, 64)
+        moe.moe_kv_append(ctx, cache, k, k, slots)
+        outs.append(moe.moe_kv_attend(ctx, cache, q, table, ln))
+        moe.moe_kv_append(ctx, cache, k[:2], k[:2], slots[:2] + 2 ** 30)  # past the end
+        moe.moe_ctx_destroy(ctx)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and outs[0].abs().max() > 0
