@@ -541,7 +541,7 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const int32_t* s
                        int64_t v_head_stride, moe_dtype dtype, void* stream);
 
 /* Attention of new tokens over the cache. Sequence b has n_b new tokens, rows
- * q_start[b] .. q_start[b+1] of q (ascending from 0; NULL: n_q / batch rows each), the last of
+ * q_start[b] .. q_start[b+1] of q (ascending from 0 to n_q; NULL: n_q / batch rows each), the last of
  * the kv_len[b] tokens that the cache holds of it (append them first): new
  * token i sits at position p = kv_len[b] - n_b + i and sees the keys j with
  * 0 <= j < kv_len[b], j <= p if causal, and j > p - window if window > 0.
@@ -554,7 +554,8 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const int32_t* s
  * probability under 2^-19 of a row's largest is off by up to 2^-30 of that
  * instead of a relative 2^-11; keys and values past fp16's range may be taken
  * as +-65,504), queries as fp16 scaled by a power of two per row (exact for
- * all but elements under 2^-14 of the row's largest).
+ * all but elements under 2^-14 of the row's largest). Logits scale * q . K are to
+ * stay within +-4e6: beyond, fp32 does not hold their differences.
  * Repeating a call on the same data gives the same bits. */
 typedef struct {
     const void* q; /* device, [n_q][n_heads][head_dim] of dtype (MOE_F16 or MOE_BF16), head_dim contiguous,

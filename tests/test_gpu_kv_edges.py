@@ -221,3 +221,30 @@ def test_negative_scales(ctx, D, dtype, share, hint):
     got = attend(ctx, cache, table, n, q, hint).double().cpu().numpy()
     out, _, e = exact(pages, P, q, n)
     assert (np.abs(got - out) <= bound(e, dtype)).all(), np.abs(got - out).max()
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("bits", [1e3, 1e5, 4e6])
+@pytest.mark.parametrize("D,dtype,n", [(64, torch.float16, 333), (128, torch.bfloat16, 2000), (256, torch.float16, 200)])
+def test_large_scores(ctx, D, dtype, n, bits, hint):
+    """Scores far apart, to four million binary orders: two keys tie for the largest and all others vanish, so the output
+    is the mean of the two values, exact (codes times a power of two) but for its own rounding and one U of the codes' span for
+    the weights'. lse has the relative precision of fp32: a few roundings of 2^-24, 2^-21 in all."""
+    H, P, T = 1, 32, 3
+    rng = np.random.default_rng(n + D)
+    k, v = (rng.integers(0, 9, (n, H, D)).astype(np.float32) for _ in range(2))
+    pair = [n // 3, n - 2]
+    k[pair, :, :16] = 15
+    for x in (k, v):
+        x[:, :, 62::64], x[:, :, 63::64] = 0, 15
+    pages = kv.empty_pages(-(-n // P), H, D, P)
+    kv.append(pages, P, k / 8, v / 16, np.arange(n))
+    q = torch.zeros((T, 4, D), dtype=dtype, device="cuda")
+    q[:, :, :16] = 1
+    scale = float(np.float32(bits * np.log(2) / 30))
+    cache, table = in_order(pages, P)
+    lse = torch.zeros((T, 4), device="cuda")
+    got = attend(ctx, cache, table, n, q, hint, scale=scale, causal=False, lse=lse).double().cpu().numpy()
+    want = (v[pair] / 16).astype(np.float64).mean((0, 1))
+    assert (np.abs(got - want) <= unit(dtype) * want + U).all()
+    assert (np.abs(lse.double().cpu().numpy() - (30 * scale + np.log(2))) <= 30 * scale * 2.0 ** -21).all()
