@@ -623,6 +623,8 @@ def moe_kv_read(ctx: int, cache: moe_kv_cache, slots, dtype=None, k=None, v=None
     else:
         k = _new(v.shape, v.dtype, v.device, stream) if k is None else k
         v = _new(k.shape, k.dtype, k.device, stream) if v is None else v
+        if dtype not in (None, k.dtype):
+            raise ValueError(f"k and v: expected {dtype}, got {k.dtype}")
         dtype = k.dtype
         kp, kt, kh = _kv_rows(k, "k", n, cache.heads, cache)
         vp, vt, vh = _kv_rows(v, "v", n, cache.heads, cache)

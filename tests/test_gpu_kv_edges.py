@@ -248,3 +248,13 @@ def test_large_scores(ctx, D, dtype, n, bits, hint):
     want = (v[pair] / 16).astype(np.float64).mean((0, 1))
     assert (np.abs(got - want) <= unit(dtype) * want + U).all()
     assert (np.abs(lse.double().cpu().numpy() - (30 * scale + np.log(2))) <= 30 * scale * 2.0 ** -21).all()
+
+
+def test_read_refuses_a_type_that_its_outputs_do_not_have(ctx):
+    cache = moe.moe_kv_new_cache(1, 2, 64, 16)
+    s = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = (torch.empty((1, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for given in (dict(k=k, v=v), dict(k=k), dict(v=v)):
+        with pytest.raises(ValueError, match="float32"):
+            moe.moe_kv_read(ctx, cache, s, dtype=torch.float32, **given)
+        assert moe.moe_kv_read(ctx, cache, s, dtype=torch.bfloat16, **given)[0].dtype == torch.bfloat16
