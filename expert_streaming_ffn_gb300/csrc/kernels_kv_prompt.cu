@@ -19,22 +19,22 @@
 // partial results.
 //
 // Rounding beyond fp32: K and V values, P and Q (scaled by a power of two per row)
-// to fp16 (2^-11 each; fp16 outputs 4.4e-4 to 6e-4 off in all, 2.1e-4 of it their own rounding). A weight 2^21
-// below the row's largest is below fp16's normal range and off by 2^-32 of the largest instead: the 2^7 in P is the
-// range that the bound leaves.
+// to fp16 (2^-11 each; fp16 outputs 4.3e-4 to 6e-4 off in all, 2.1e-4 of it their own rounding; keys and values
+// past fp16's range are its largest number). A weight 2^21 below the row's largest is below fp16's normal
+// range and off by 2^-32 of the largest instead: the 2^7 in P is the range that the bound leaves.
 //
 // What it measured, 32 query heads on 8 kv heads of 128 but where said:
-//   4,096 new tokens behind 12,288 keys: 717 us, 1,341 TFLOP/s, 0.70 of the bf16 rate measured on this
-//     GPU for a library product. Its cycle is 1.65 us for 256 rows by 128 keys, the time in which one
+//   4,096 new tokens behind 12,288 keys: 710 us, 1,355 TFLOP/s, 0.71 of the bf16 rate measured on this
+//     GPU for a library product (the first calls after a pause 820 to 850, under the power cap). Its cycle is 1.65 us for 256 rows by 128 keys, the time in which one
 //     warp gets 2 x 2 products through, those with P from tensor memory and those from shared memory in
 //     turn: the products alone, without softmax or dequantisation, took 733 us at the cut that was then
 //     in use, the whole kernel 809.
 //   4,096 alone: 130 us, 1,060 TFLOP/s: row tiles see 1 to 32 key tiles, and 512 of them make 3.4 waves
 //     on 152 SMs (tensor pipe busy 46 % of the time, 51 % of the cycles issuing).
 //   128 behind 16,383: 43 us, 802 TFLOP/s, 16 row tiles, each one's keys split over 9 CTAs.
-//   As the first, head_dim 256, 16 heads: 1,070 TFLOP/s; head_dim 64: 882, its products of 64 columns bound by their
-//     issue. Four prompts to 1,024 tokens, 16 heads of 64: 17.5 us, of which the start and the end of a CTA
-//     are most.
+//   As the first, head_dim 256, 16 heads: 1,070 TFLOP/s; head_dim 64: 877. Of neither is a single unit busy (4,096
+//     alone: tensor pipe 36 % and 31 %, half of the cycles issuing). Four prompts to 1,024 tokens, 16 heads of
+//     64: 17.7 us, of which the start and the end of a CTA are most.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -570,7 +570,8 @@ typedef struct {
     const int32_t* q_start;     /* device [batch + 1], or NULL */
     int32_t batch, n_q, n_heads, max_pages; /* n_q * n_heads < 2^31, max_pages * page_tokens < 2^31 - 1024 */
     int32_t max_q;   /* largest n_b, as the caller knows it on the host: it chooses the kernel, and so
-                        the rounding; results are right whatever it is */
+                        the rounding; results are right whatever it is (1 keeps codes exact: fp16 outputs are
+                        3e-4 off in place of 4.4e-4, and prompts slower) */
     int32_t max_len; /* likewise the largest kv_len, or 0 for max_pages * page_tokens */
     int32_t causal;  /* 0 or 1 */
     int32_t window;  /* 0: none */
