@@ -250,10 +250,14 @@ struct moe_ctx {
         cudaEventCreate(&e);
         return e;
     }
-    void give_back(cudaEvent_t a, cudaEvent_t b) {
-        std::lock_guard<std::mutex> lock(prof_mu);
-        timing_pool.push_back(a);
-        timing_pool.push_back(b);
+    void give_back(cudaEvent_t a, cudaEvent_t b) noexcept {
+        try {
+            std::lock_guard<std::mutex> lock(prof_mu);
+            timing_pool.insert(timing_pool.end(), {a, b});
+        } catch (...) {  // no host memory for the pool: the events go instead of the process
+            cudaEventDestroy(a);
+            cudaEventDestroy(b);
+        }
     }
 };
 
@@ -493,8 +497,12 @@ struct Prof {
     ~Prof() {
         if (!on) return;
         cudaEventRecord(r.b, s);
-        std::lock_guard<std::mutex> lock(C->prof_mu);
-        C->prof.push_back(r);
+        try {
+            std::lock_guard<std::mutex> lock(C->prof_mu);
+            C->prof.push_back(r);
+        } catch (...) {  // no host memory: the launch stays untimed
+            C->give_back(r.a, r.b);
+        }
     }
 };
 
