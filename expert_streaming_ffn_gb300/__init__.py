@@ -27,7 +27,7 @@ LFU, LRU = 0, 1
 GELU_TANH, SILU = 0, 1
 MOE_F32, MOE_F16, MOE_BF16 = 0, 1, 2
 KERNEL_KINDS = ("router", "expert_ffn", "combine", "gemm_gateup", "gemm_down", "pf_gather", "expert_ffn_miss",
-                "kv_append", "kv_read", "kv_attend")
+                "kv_append", "kv_read", "kv_attend", "rms_norm", "f8_quant", "f8_matmul")
 
 
 class MoeError(RuntimeError):
@@ -86,6 +86,26 @@ class moe_kv_attend_args(ctypes.Structure):
                [("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
+class moe_norm_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_token_stride", ctypes.c_int64),
+                ("residual_head_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("sum", ctypes.c_void_p),
+                ("sum_token_stride", ctypes.c_int64), ("sum_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("code_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int)]
+
+
+class moe_f8_matmul_args(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("a_stride", ctypes.c_int64), ("a_scales", ctypes.c_void_p),
+                ("a_scale_stride", ctypes.c_int64), ("w", ctypes.c_void_p), ("w_stride", ctypes.c_int64),
+                ("w_scales", ctypes.c_void_p), ("w_scale_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int)]
+
+
 # (name, restype, argtypes) of every exported symbol in include/moe.h
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _P = ctypes.POINTER
@@ -141,6 +161,10 @@ SIGNATURES = [
     ("moe_kv_read", _i32, [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _vp]),
     ("moe_kv_attend", _i32, [_vp, _vp, _vp, _vp]),
     ("moe_kv_check", _i32, [_vp]),
+    ("moe_rms_norm", _i32, [_vp, _vp, _vp]),
+    ("moe_f8_quant_rows", _i32, [_vp, _vp, _i64, ctypes.c_int, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    ("moe_f8_quant_weight", _i32, [_vp, _vp, _i64, ctypes.c_int, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    ("moe_f8_matmul", _i32, [_vp, _vp, _vp]),
 ]
 
 
@@ -673,6 +697,156 @@ def moe_kv_attend(ctx: int, cache: moe_kv_cache, q, page_table, kv_len, q_start=
 def moe_kv_check(ctx: int) -> None:
     """Raises if a finished cache call met a slot or page id outside its cache since the last check."""
     _check(load().moe_kv_check(ctx), "moe_kv_check")
+
+
+# ---------------------------------------------------------------------------
+# norm, 8-bit rows and weights, and their matrix product
+
+_norm_pack = struct.Struct("@PqqPqqPPqqPqqPqPqiiif4i").pack  # the fields of moe_norm_args, in order
+_f8_matmul_pack = struct.Struct("@PqPqPqPqPqiiii").pack  # and of moe_f8_matmul_args
+_SAME = object()
+
+
+def _rows3(t, what: str, shape, device: int):
+    """(pointer, token stride, head stride) of a CUDA tensor of that shape, [n][d] or [n][heads][d]."""
+    if t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{what}: expected a tensor {list(shape)} on CUDA device {device}, got {list(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if len(shape) > 2 and shape[1] > 1 else 0
+
+
+def _codes(t, what: str, shape, device: int):
+    """(pointer, stride) of e4m3 codes [n][k]."""
+    if t.dtype != _torch.float8_e4m3fn or t.shape != shape or t.get_device() != device or t.stride(1) != 1:
+        raise ValueError(f"{what}: expected float8_e4m3fn {list(shape)} on CUDA device {device}, the last dimension contiguous, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
+
+
+def _scales(t, what: str, shape, device: int):
+    """(pointer, stride) of fp32 scales of that shape."""
+    if t.dtype != _torch.float32 or t.shape != shape or t.get_device() != device or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected float32 {list(shape)} on CUDA device {device}, the last dimension contiguous, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _dense_stream(stream, device: int):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _cuda(t, what: str) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
+    return device
+
+
+def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dtype=_SAME, f8: bool = False, out=None,
+                 sum=None, codes=None, scales=None, stream=None):
+    """Root-mean-square norm of the rows of h = x + residual (CUDA [n][d] or [n][heads][d], f32, f16 or bf16, any
+    strides in front of the last dimension), times weight [d]. Returns (out, sum, codes, scales): out of dtype (x's unless
+    given; None: no such output), sum = h of the residual's type (None without one), and with f8 the e4m3 codes
+    [n][d] and f32 scales [ceil(d / 128)][n] of the same rows (None, None without). Outputs given are filled."""
+    torch = _torch or _kv_torch()
+    device, shape = _cuda(x, "x"), x.shape
+    if x.dim() not in (2, 3):
+        raise ValueError("x: expected [n][d] or [n][heads][d]")
+    n, d, heads = shape[0], shape[-1], shape[1] if x.dim() == 3 else 1
+    xp, xt, xh = _rows3(x, "x", shape, device)
+    rp = rt = rh = rd = sp = st = sh = wp = wd = op = ot = oh = od = cp = ct = lp = lt = 0
+    if weight is not None:
+        if weight.shape != (d,) or weight.get_device() != device or (d > 1 and weight.stride(0) != 1):
+            raise ValueError(f"weight: expected [{d}], contiguous, on CUDA device {device}")
+        wp, wd = weight.data_ptr(), _kv_type(weight.dtype)
+    if residual is not None:
+        rp, rt, rh = _rows3(residual, "residual", shape, device)
+        rd = _kv_type(residual.dtype)
+        if sum is None:
+            sum = _new(shape, residual.dtype, x.device, stream)
+        elif sum.dtype != residual.dtype:
+            raise ValueError("sum: expected the residual's type")
+        sp, st, sh = _rows3(sum, "sum", shape, device)
+    elif sum is not None:
+        raise ValueError("sum: there is no residual")
+    if out is None:
+        if dtype is _SAME:
+            dtype = x.dtype
+        if dtype is not None:
+            out = _new(shape, dtype, x.device, stream)
+    elif dtype is not _SAME and dtype != out.dtype:
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+    if out is not None:
+        op, ot, oh = _rows3(out, "out", shape, device)
+        od = _kv_type(out.dtype)
+    if f8 or codes is not None or scales is not None:
+        if heads != 1:
+            raise ValueError("an 8-bit output takes rows of one head")
+        if codes is None:
+            codes = _new((n, d), torch.float8_e4m3fn, x.device, stream)
+        if scales is None:
+            scales = _new((-(-d // 128), n), torch.float32, x.device, stream)
+        cp, ct = _codes(codes, "codes", (n, d), device)
+        lp, lt = _scales(scales, "scales", (-(-d // 128), n), device)
+    args = _norm_pack(xp, xt, xh, rp, rt, rh, wp, sp, st, sh, op, ot, oh, cp, ct, lp, lt, n, heads, d, eps,
+                      _kv_type(x.dtype), rd, wd, od)
+    _check((_lib or load()).moe_rms_norm(ctx, args, _dense_stream(stream, device)), "moe_rms_norm")
+    return out, sum, codes, scales
+
+
+def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
+    torch = _torch or _kv_torch()
+    device = _cuda(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: expected [n][k]")
+    n, k = x.shape
+    xp, xt, _ = _rows3(x, "x", x.shape, device)
+    shape = (-(-n // 128), -(-k // 128)) if weight else (-(-k // 128), n)
+    if codes is None:
+        codes = _new((n, k), torch.float8_e4m3fn, x.device, stream)
+    if scales is None:
+        scales = _new(shape, torch.float32, x.device, stream)
+    cp, ct = _codes(codes, "codes", (n, k), device)
+    lp, lt = _scales(scales, "scales", shape, device)
+    _check(getattr(_lib or load(), fn)(ctx, xp, xt, _kv_type(x.dtype), n, k, cp, ct, lp, lt, _dense_stream(stream, device)), fn)
+    return codes, scales
+
+
+def moe_f8_quant_rows(ctx: int, x, codes=None, scales=None, stream=None):
+    """Rows x (CUDA [n][k], f32, f16 or bf16) as (codes e4m3 [n][k], scales f32 [ceil(k / 128)][n])."""
+    return _f8_quant("moe_f8_quant_rows", ctx, x, False, codes, scales, stream)
+
+
+def moe_f8_quant_weight(ctx: int, w, codes=None, scales=None, stream=None):
+    """Weights w (CUDA [n][k], f32, f16 or bf16) as (codes e4m3 [n][k], scales f32 [ceil(n / 128)][ceil(k / 128)])."""
+    return _f8_quant("moe_f8_quant_weight", ctx, w, True, codes, scales, stream)
+
+
+def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stream=None):
+    """The product of 8-bit rows a [m][k] and weights w [n][k], each as moe_f8_quant_rows and moe_f8_quant_weight
+    give them: out [m][n] of dtype (bf16 unless given)."""
+    torch = _torch or _kv_torch()
+    device = _cuda(a, "a")
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a and w: expected [m][k] and [n][k]")
+    (m, k), n = a.shape, w.shape[0]
+    ap, at = _codes(a, "a", (m, k), device)
+    wp, wt = _codes(w, "w", (n, k), device)
+    kb = -(-k // 128)
+    asp, ast = _scales(a_scales, "a_scales", (kb, m), device)
+    wsp, wst = _scales(w_scales, "w_scales", (-(-n // 128), kb), device)
+    if out is None:
+        out = _new((m, n), dtype or torch.bfloat16, a.device, stream)
+    elif dtype not in (None, out.dtype):
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+    op, ot, _ = _rows3(out, "out", (m, n), device)
+    args = _f8_matmul_pack(ap, at, asp, ast, wp, wt, wsp, wst, op, ot, m, n, k, _kv_type(out.dtype))
+    _check((_lib or load()).moe_f8_matmul(ctx, args, _dense_stream(stream, device)), "moe_f8_matmul")
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -141,7 +141,7 @@ using namespace moe;
 
 namespace {
 
-constexpr int kKinds = 10;
+constexpr int kKinds = 13;
 enum Kind { K_ROUTER = 0, K_FFN = 1, K_COMBINE = 2, K_GEMM_GU = 3, K_GEMM_DN = 4, K_GATHER = 5, K_FFN_MISS = 6 };  // and KvKind
 constexpr double kHostWaitLimitS = 10.0;  // longest the host waits for the routing of one call
 // Rounds of ready-word source values kept in pinned memory. A round's entry is
@@ -195,7 +195,7 @@ __global__ void read_globaltimer(unsigned long long* out) {
 }  // namespace
 
 struct moe_ctx {
-    int device = 0;
+    int device = 0, sms = 0;
     cudaStream_t copy_stream = nullptr;
     uint8_t* staging = nullptr;  // transient arena for bypassed experts
     size_t staging_bytes = 0;
@@ -515,6 +515,7 @@ void moe::ctx_launch_end(void* rec) { delete static_cast<Prof*>(rec); }
 bool moe::ctx_profiling(const moe_ctx* C) { return C->profiling; }
 void moe::ctx_count_launch(moe_ctx* C) { ++C->launches; }
 int moe::ctx_device(const moe_ctx* C) { return C->device; }
+int moe::ctx_sms(const moe_ctx* C) { return C->sms; }
 KvState* moe::ctx_kv(moe_ctx* C) { return C->kv; }
 std::mutex& moe::ctx_kv_mutex(moe_ctx* C) { return C->kv_mu; }
 
@@ -1424,7 +1425,8 @@ extern "C" moe_status moe_ctx_create(int device, moe_ctx** out) {
     moe_ctx* C = new (std::nothrow) moe_ctx();
     if (!C) return set_error(MOE_ENOMEM, "out of host memory");
     C->device = device;
-    if (cudaStreamCreateWithFlags(&C->copy_stream, cudaStreamNonBlocking) != cudaSuccess ||
+    if (cudaDeviceGetAttribute(&C->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        cudaStreamCreateWithFlags(&C->copy_stream, cudaStreamNonBlocking) != cudaSuccess ||
         cudaEventCreateWithFlags(&C->staging_free, cudaEventDisableTiming) != cudaSuccess ||
         cudaHostAlloc(&C->err_host, sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
         cudaHostGetDevicePointer(&C->err_dev, C->err_host, 0) != cudaSuccess || !(C->kv = kv_state_create())) {

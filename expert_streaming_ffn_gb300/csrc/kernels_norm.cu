@@ -1,0 +1,347 @@
+// Root-mean-square norm of rows, with the residual's addition and an 8-bit output, and quantisation to 8 bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "dense_internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kLeast = 448.0f * 1.17549435e-38f;  // a block's largest magnitude counts as at least this: no scale is subnormal
+
+// Eight consecutive elements of B bytes each, as loaded.
+template <int B>
+struct Raw {
+    uint32_t w[2 * B];
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * B);
+#pragma unroll
+        for (int i = 0; i < B / 2; ++i) {
+            const uint4 v = p[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 2 * B; ++i) w[i] = 0;
+    }
+    // the values; `bf` tells the 16-bit types apart
+    __device__ __forceinline__ void get(float (&f)[8], bool bf) const {
+        if constexpr (B == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+        } else if (bf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
+    }
+};
+template <>
+struct Raw<0> {
+    __device__ __forceinline__ void load(const void*, int64_t) {}
+    __device__ __forceinline__ void zero() {}
+};
+
+// Eight values to memory, rounded once to the type.
+__device__ __forceinline__ void store8(void* base, int64_t at, const float (&f)[8], moe_dtype t) {
+    if (t == MOE_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (t == MOE_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float largest8(const float (&f)[8]) {
+    float m = fabsf(f[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+    return m;
+}
+
+// The scale of a block by its largest magnitude, and 1 / scale. An infinity or a NaN makes the whole block NaN.
+__device__ __forceinline__ float block_scale(float largest, float& inv) {
+    float s = __fdiv_rn(fmaxf(largest, kLeast), kE4m3Max);
+    if (!(largest < __int_as_float(0x7F800000))) s = __int_as_float(0x7FC00000);
+    inv = __frcp_rn(s);
+    return s;
+}
+
+// Eight values to codes, the nearest to f / s. The quotient is IEEE's but for rare divisors (all ones): t = f y with
+// y = 1 / s rounded to nearest is within an ulp of it, and t + y (f - s t), the remainder exact in a fused multiply-add,
+// rounds to it (Markstein's theorem). A plain product f y would move quotients that are ties, and 16-bit inputs have many.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv) {
+    uint32_t h[4];
+    const uint64_t yy = ptx::f2(inv, inv), ns = ptx::f2(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x = ptx::f2(f[2 * i], f[2 * i + 1]), t = ptx::mul2(x, yy);
+        const float2 q = ptx::f2(ptx::fma2(ptx::fma2(t, ns, x), yy, t));
+        uint16_t c;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(q.y), "f"(q.x));
+        h[i] = c;
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// One row: a thread holds V vectors of eight elements, vector i + v * G of the row for thread i of the row's G.
+// kCta: the row's threads are the CTA's; else G = 8, 16 or 32 lanes of a warp, `group` of them.
+template <int XB, int RB, int V, bool kCta>
+__global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a, const int group) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int G = kCta ? (int)blockDim.x : group;
+    const unsigned per = kCta ? 1 : blockDim.x / (unsigned)group;
+    const int i = kCta ? (int)threadIdx.x : (int)threadIdx.x & (G - 1);
+    const unsigned want = kCta ? blockIdx.x : blockIdx.x * per + threadIdx.x / (unsigned)G;
+    const bool live = want < a.rows;
+    const unsigned row = live ? want : 0;
+    const unsigned t = a.by_head.div(row), h = row - t * a.by_head.d;
+    const int nv = a.dim >> 3;
+    Raw<XB> x[V];
+    Raw<RB> r[V];
+    const int64_t xo = (int64_t)t * a.xt + (int64_t)h * a.xh, ro = (int64_t)t * a.rt + (int64_t)h * a.rh;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int j = i + v * G;
+        if (live && j < nv) {
+            x[v].load(a.x, xo + 8 * j);
+            r[v].load(a.res, ro + 8 * j);
+        } else {
+            x[v].zero();
+            r[v].zero();
+        }
+    }
+    float f[V][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v].get(f[v], a.x_type == MOE_BF16);
+        if constexpr (RB != 0) {
+            float g[8];
+            r[v].get(g, a.res_type == MOE_BF16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[v][e] += g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
+    }
+    for (int m = (kCta ? 32 : G) >> 1; m; m >>= 1) ss += __shfl_xor_sync(kFull, ss, m);
+    if constexpr (kCta) {
+        __shared__ float part[32];
+        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) part[threadIdx.x >> 5] = ss;
+        __syncthreads();
+        ss = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+        for (int m = 16; m; m >>= 1) ss += __shfl_xor_sync(kFull, ss, m);
+    }
+    const float k = rsqrtf(ss / (float)a.dim + a.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int j = i + v * G;
+        const bool in = live && j < nv;
+        if constexpr (RB != 0)
+            if (a.sum && in) store8(a.sum, (int64_t)t * a.st + (int64_t)h * a.sh + 8 * j, f[v], a.res_type);
+        float w[8];
+        if (a.weight && in) {
+            if (a.weight_type == MOE_F32) {
+                Raw<4> q;
+                q.load(a.weight, 8 * j);
+                q.get(w, false);
+            } else {
+                Raw<2> q;
+                q.load(a.weight, 8 * j);
+                q.get(w, a.weight_type == MOE_BF16);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[v][e] *= k * w[e];
+        if (a.out && in) store8(a.out, (int64_t)t * a.ot + (int64_t)h * a.oh + 8 * j, f[v], a.out_type);
+        if (a.codes) {  // a block is 16 neighbouring vectors, so 16 lanes of a warp (8 where a row has no more)
+            float top = largest8(f[v]);
+            for (int m = min(16, G) >> 1; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
+            float inv;
+            const float s = block_scale(top, inv);
+            if (in) {
+                *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.ct + 8 * j) = codes8(f[v], s, inv);
+                if ((j & 15) == 0) a.scales[(int64_t)(j >> 4) * a.scale_stride + t] = s;
+            }
+        }
+    }
+}
+
+template <int XB, int RB, int V>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+    const int nv = a.dim >> 3;
+    cudaLaunchAttribute attr;
+    if (nv <= 32 * V && V == 1) {
+        const int G = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+        const unsigned threads = 256, per = threads / G;
+        const cudaLaunchConfig_t cfg = launch_config(dim3((a.rows + per - 1) / per), dim3(threads), 0, s, true, &attr);
+        return cudaLaunchKernelEx(&cfg, norm_kernel<XB, RB, 1, false>, a, G);
+    }
+    const unsigned threads = (unsigned)((nv + V - 1) / V + 31) / 32 * 32;
+    const cudaLaunchConfig_t cfg = launch_config(dim3(a.rows), dim3(threads), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, norm_kernel<XB, RB, V, true>, a, 0);
+}
+
+template <int XB, int RB>
+cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t s) {
+    const int nv = a.dim >> 3;
+    return nv <= 512 ? launch_norm<XB, RB, 1>(a, s) : nv <= 1024 ? launch_norm<XB, RB, 2>(a, s) : launch_norm<XB, RB, 4>(a, s);
+}
+
+template <int XB>
+cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t s) {
+    return !a.res ? launch_norm_of<XB, 0>(a, s) : a.res_type == MOE_F32 ? launch_norm_of<XB, 4>(a, s) : launch_norm_of<XB, 2>(a, s);
+}
+
+// Rows to codes: 16 lanes a block, eight elements each. V vectors a thread, a CTA's threads apart.
+template <int B, int V>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const uint64_t first = (uint64_t)blockIdx.x * (256 * V) + threadIdx.x;
+    const unsigned per = a.by_row.d;
+    Raw<B> x[V];
+    int row[V], vec[V];
+    bool in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint64_t at = first + 256 * v;
+        row[v] = (int)a.by_row.div((uint32_t)(at >> 4));
+        vec[v] = (int)((at >> 4) - (uint64_t)row[v] * per) * 16 + (int)(at & 15);
+        in[v] = row[v] < a.n && 8 * vec[v] < a.dim;
+        if (in[v])
+            x[v].load(a.x, (int64_t)row[v] * a.x_stride + 8 * vec[v]);
+        else
+            x[v].zero();
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float f[8];
+        x[v].get(f, a.type == MOE_BF16);
+        float top = largest8(f);
+#pragma unroll
+        for (int m = 8; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
+        float inv;
+        const float s = block_scale(top, inv);
+        if (!in[v]) continue;
+        *reinterpret_cast<uint2*>(a.codes + (int64_t)row[v] * a.code_stride + 8 * vec[v]) = codes8(f, s, inv);
+        if ((vec[v] & 15) == 0) a.scales[(int64_t)(vec[v] >> 4) * a.scale_stride + row[v]] = s;
+    }
+}
+
+// A block of 128 x 128 weights a CTA, in registers between the pass for its largest magnitude and the pass for its codes.
+template <int B>
+__global__ void __launch_bounds__(256) quant_weight_kernel(const __grid_constant__ QuantArgs a) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int nb = (int)a.by_row.div(blockIdx.x), kb = (int)(blockIdx.x - (unsigned)nb * a.by_row.d);
+    const int i = threadIdx.x & 15, r0 = nb * kF8Block + (threadIdx.x >> 4), col = kb * kF8Block + 8 * i;
+    Raw<B> x[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        if (r0 + 16 * v < a.n && col < a.dim)
+            x[v].load(a.x, (int64_t)(r0 + 16 * v) * a.x_stride + col);
+        else
+            x[v].zero();
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        float f[8];
+        x[v].get(f, a.type == MOE_BF16);
+        top = max_nan(top, largest8(f));
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
+    __shared__ float part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = max_nan(top, part[w]);
+    float inv;
+    const float s = block_scale(top, inv);
+    if (threadIdx.x == 0) a.scales[(int64_t)nb * a.scale_stride + kb] = s;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        if (r0 + 16 * v >= a.n || col >= a.dim) continue;
+        float f[8];
+        x[v].get(f, a.type == MOE_BF16);
+        *reinterpret_cast<uint2*>(a.codes + (int64_t)(r0 + 16 * v) * a.code_stride + col) = codes8(f, s, inv);
+    }
+}
+
+template <int B, int V>
+cudaError_t launch_quant_rows(const QuantArgs& a, uint64_t vecs, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg =
+        launch_config(dim3((unsigned)((vecs + 256 * V - 1) / (256 * V))), dim3(256), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, quant_rows_kernel<B, V>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
+    return a.x_type == MOE_F32 ? launch_norm_of<4>(a, s) : launch_norm_of<2>(a, s);
+}
+
+cudaError_t launch_f8_quant_rows(const QuantArgs& a0, int sms, cudaStream_t s) {
+    QuantArgs a = a0;
+    a.by_row = FastDiv((uint32_t)((a.dim + kF8Block - 1) / kF8Block));
+    const uint64_t vecs = (uint64_t)a.n * a.by_row.d * 16;
+    const bool many = vecs >= (uint64_t)sms * 2048 * 4;
+    if (a.type == MOE_F32) return many ? launch_quant_rows<4, 2>(a, vecs, s) : launch_quant_rows<4, 1>(a, vecs, s);
+    return many ? launch_quant_rows<2, 4>(a, vecs, s) : launch_quant_rows<2, 1>(a, vecs, s);
+}
+
+cudaError_t launch_f8_quant_weight(const QuantArgs& a0, cudaStream_t s) {
+    QuantArgs a = a0;
+    a.by_row = FastDiv((uint32_t)((a.dim + kF8Block - 1) / kF8Block));
+    cudaLaunchAttribute attr;
+    const dim3 grid(a.by_row.d * (unsigned)((a.n + kF8Block - 1) / kF8Block));
+    const cudaLaunchConfig_t cfg = launch_config(grid, dim3(256), 0, s, true, &attr);
+    return a.type == MOE_F32 ? cudaLaunchKernelEx(&cfg, quant_weight_kernel<4>, a)
+                             : cudaLaunchKernelEx(&cfg, quant_weight_kernel<2>, a);
+}
+
+}  // namespace moe

@@ -20,7 +20,7 @@ using namespace moe;
 namespace moe {
 
 // What the cache calls of a context keep: mapped words in which kernels note
-// bad slots and page ids [0] and expired waits [1], and the attention's
+// bad slots and page ids [0], expired waits [1] and those of matrix products [2], and the attention's
 // workspace, with the stream of the last call that uses it and an event behind
 // that call.
 struct KvState {
@@ -36,13 +36,13 @@ struct KvState {
 KvState* kv_state_create() {
     KvState* n = new (std::nothrow) KvState();
     if (!n) return nullptr;
-    if (cudaHostAlloc(&n->bad_host, 2 * sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
+    if (cudaHostAlloc(&n->bad_host, 3 * sizeof(unsigned), cudaHostAllocMapped) != cudaSuccess ||
         cudaHostGetDevicePointer(&n->bad_dev, n->bad_host, 0) != cudaSuccess) {
         cudaGetLastError();
         kv_state_destroy(n);
         return nullptr;
     }
-    n->bad_host[0] = n->bad_host[1] = 0;
+    n->bad_host[0] = n->bad_host[1] = n->bad_host[2] = 0;
     return n;
 }
 
@@ -53,6 +53,9 @@ void kv_state_destroy(KvState* st) {
     if (st->ws_done) cudaEventDestroy(st->ws_done);
     delete st;
 }
+
+unsigned* ctx_f8_err(moe_ctx* C) { return ctx_kv(C)->bad_dev + 2; }
+unsigned ctx_f8_expired(moe_ctx* C) { return __atomic_exchange_n(ctx_kv(C)->bad_host + 2, 0u, __ATOMIC_RELAXED); }
 
 // Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel
 // takes: it reads the cache once a tile of columns, the prompt kernel once for 256 (128 at head_dim

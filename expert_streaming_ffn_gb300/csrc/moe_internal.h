@@ -349,7 +349,7 @@ cudaError_t launch_pf_gemm(const PfArgs& a, int phase, const void* b0, const voi
 
 // ---- what the cache calls (kv_api.cu) use of a context --------------------------
 
-enum KvKind { K_KV_APPEND = 7, K_KV_READ = 8, K_KV_ATTEND = 9 };  // kernel kinds, after those of api.cu
+enum KvKind { K_KV_APPEND = 7, K_KV_READ = 8, K_KV_ATTEND = 9, K_RMS_NORM = 10, K_F8_QUANT = 11, K_F8_MATMUL = 12 };  // kernel kinds, after those of api.cu
 
 struct KvState;  // kv_api.cu
 KvState* kv_state_create();  // null if the allocation failed
@@ -357,6 +357,9 @@ void kv_state_destroy(KvState* st);
 
 int ctx_device(const moe_ctx* C);
 KvState* ctx_kv(moe_ctx* C);
+int ctx_sms(const moe_ctx* C);
+unsigned* ctx_f8_err(moe_ctx* C);     // device address of the word that notes an expired wait of a matrix product
+unsigned ctx_f8_expired(moe_ctx* C);  // its value, which it takes back
 std::mutex& ctx_kv_mutex(moe_ctx* C);  // held by a cache call while it enqueues
 bool ctx_profiling(const moe_ctx* C);
 void ctx_count_launch(moe_ctx* C);

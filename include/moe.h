@@ -596,6 +596,89 @@ moe_status moe_kv_attend(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_a
  * first for an answer on the calls enqueued so far. */
 moe_status moe_kv_check(moe_ctx* ctx);
 
+/* ---- norm, 8-bit rows and weights, and their matrix product ------------------ */
+
+/* What stands between attention and the experts in a decoder layer: the norms in
+ * front of either, and the projections, whose operands are 8-bit floating point
+ * (e4m3) with an fp32 scale for each block of 128:
+ *   rows [n][k]:    a block is 128 elements of one row, the scale of row i's block
+ *                   b is scales[b * scale_stride + i] (neighbouring rows' scales lie
+ *                   side by side);
+ *   weights [n][k]: a block is 128 rows by 128 elements, scales[(i / 128) *
+ *                   scale_stride + j / 128] that of element (i, j).
+ * The last blocks may be smaller. An element's value is scale * code. Quantising:
+ *   scale = max(largest magnitude of the block, 448 * 2^-126) / 448 in fp32,
+ *   code = value / scale rounded to the nearest e4m3, ties to even,
+ * so codes span +-448, and a value is off by at most 2^-4 of itself or 2^-10 of the
+ * scale. An infinity or a NaN makes its whole block NaN, scale and codes.
+ * Every tensor is in the memory of the context's device; rows of 16- and
+ * 32-bit elements and of codes start on 16-byte boundaries (base pointers and
+ * strides), and strides count elements. The calls are asynchronous on `stream`; they
+ * synchronise nothing, allocate nothing and share no workspace, so they may be
+ * captured, and run at the same time on several streams and threads. Repeating a
+ * call on the same data gives the same bits. They serve inference: none has a
+ * backward pass. */
+typedef struct {
+    const void* x; /* [n_tokens][n_heads][dim] of x_dtype; a row is dim contiguous elements */
+    int64_t x_token_stride, x_head_stride;
+    const void* residual; /* the same shape, of residual_dtype, or NULL */
+    int64_t residual_token_stride, residual_head_stride;
+    const void* weight; /* [dim] of weight_dtype, 16-byte aligned, or NULL: ones */
+    void* sum;          /* of residual_dtype, or NULL */
+    int64_t sum_token_stride, sum_head_stride;
+    void* out; /* of out_dtype, or NULL */
+    int64_t out_token_stride, out_head_stride;
+    void* codes; /* e4m3 [n_tokens][dim], or NULL; needs n_heads = 1 */
+    int64_t code_stride;
+    float* scales; /* with codes */
+    int64_t scale_stride;
+    int32_t n_tokens, n_heads; /* n_tokens * n_heads < 2^31 */
+    int32_t dim;               /* a multiple of 16, at most 32,768 */
+    float eps;                 /* finite, >= 0 */
+    moe_dtype x_dtype, residual_dtype, weight_dtype, out_dtype; /* those of absent tensors are not looked at */
+} moe_norm_args;
+
+/* Root-mean-square norm of each row:
+ *   h = x + residual (x alone without one);  sum = h
+ *   y = h / sqrt(mean(h^2) + eps) * weight;  out = y;  codes, scales = y quantised as rows
+ * All arithmetic is fp32 (|h| below 2^55, so that its squares' sum stays finite), y comes from the
+ * unrounded h, and sum, out and codes are each rounded once. At least one of sum, out and codes is given. sum and out
+ * may be x or residual themselves (the same pointer, type and strides); other overlaps are not allowed.
+ * moe_forward's y (f32) is an x; its own x wants bf16 out with dim = d_model.
+ * Errors: MOE_EINVAL, MOE_ECUDA. */
+moe_status moe_rms_norm(moe_ctx* ctx, const moe_norm_args* args, void* stream);
+
+/* Quantise rows x [n][k] (k a multiple of 16), for what no norm makes: attention's
+ * output before its projection, say. code_stride is a multiple of 16.
+ * Errors: MOE_EINVAL, MOE_ECUDA. */
+moe_status moe_f8_quant_rows(moe_ctx* ctx, const void* x, int64_t x_stride, moe_dtype dtype, int32_t n, int32_t k,
+                             void* codes, int64_t code_stride, float* scales, int64_t scale_stride, void* stream);
+
+/* The same for weights w [n][k], when a model is loaded. */
+moe_status moe_f8_quant_weight(moe_ctx* ctx, const void* w, int64_t w_stride, moe_dtype dtype, int32_t n, int32_t k,
+                               void* codes, int64_t code_stride, float* scales, int64_t scale_stride, void* stream);
+
+typedef struct {
+    const void* a; /* e4m3 rows [m][k], with their scales */
+    int64_t a_stride;
+    const float* a_scales;
+    int64_t a_scale_stride;
+    const void* w; /* e4m3 weights [n][k], with their scales */
+    int64_t w_stride;
+    const float* w_scales;
+    int64_t w_scale_stride;
+    void* out; /* [m][n] of out_dtype, rows out_stride apart; any alignment and stride of elements */
+    int64_t out_stride;
+    int32_t m, n, k; /* n >= 1; k a multiple of 16; any m >= 0 */
+    moe_dtype out_dtype;
+} moe_f8_matmul_args;
+
+/* out[i][j] = sum over blocks b of 128 of k: a_scales[b][i] * w_scales[j / 128][b] * sum of a[i][l] * w[j][l] in b,
+ * products exact, all sums in fp32, rounded once to out_dtype (past fp16's range to infinity). The product of two
+ * scales is to be within fp32's range. out overlaps no input.
+ * Errors: MOE_EINVAL, MOE_ECUDA, MOE_ETIMEOUT (a bounded device wait expired in an earlier product). */
+moe_status moe_f8_matmul(moe_ctx* ctx, const moe_f8_matmul_args* args, void* stream);
+
 /* ---- diagnostics -------------------------------------------------------- */
 
 const char* moe_status_str(moe_status s);
@@ -608,7 +691,8 @@ const char* moe_last_error(void);
  * hit), 2 combine, 3 prefill grouped GEMM gate/up, 4 prefill grouped GEMM
  * down, 5 prefill token-row conversion to fp16, 6 decode expert FFN over the
  * experts copied in by the call (its duration includes the wait for the
- * copies), 7 moe_kv_append, 8 moe_kv_read, 9 moe_kv_attend. Returns launches, total
+ * copies), 7 moe_kv_append, 8 moe_kv_read, 9 moe_kv_attend,
+ * 10 moe_rms_norm, 11 moe_f8_quant_rows and moe_f8_quant_weight, 12 moe_f8_matmul. Returns launches, total
  * milliseconds and the algorithmic bytes and flops of those launches. Waits
  * for the events. */
 moe_status moe_ctx_set_profiling(moe_ctx* ctx, int32_t on);
@@ -616,7 +700,7 @@ moe_status moe_ctx_kernel_times(moe_ctx* ctx, int32_t kind, uint64_t* launches, 
                                 double* bytes, double* flops);
 moe_status moe_ctx_reset_kernel_times(moe_ctx* ctx);
 
-/* Number of kernels the context's layers and cache calls have launched since its creation
+/* Number of kernels the context's layers and other calls have launched since its creation
  * (every launch is counted, profiling or not). */
 moe_status moe_ctx_launches(moe_ctx* ctx, uint64_t* out);
 
