@@ -35,24 +35,29 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kLanes = 128;
 constexpr int kLaneBytes = kLanes * 128;  // of a K-block: 128 rows of 128 codes
 
-template <int C_, bool kRows_>
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Weights form, up to C rows a tile.
+template <int C_>
 struct Form {
     static constexpr int C = C_;
-    static constexpr bool kRows = kRows_;  // lanes are rows
-    static constexpr int kEpi = kRows ? 8 : 4;
+    static constexpr int kEpi = 4;
     static constexpr int kThreads = 32 * (kEpi + 2);
-    static constexpr int kPer = kRows ? C / 2 : C;  // columns of an epilogue thread
     static constexpr int kStageBytes = kLaneBytes + C * 128;
-    static constexpr int kStages = kRows ? 4 : C == 16 ? 6 : C == 32 ? 5 : C == 64 ? 4 : 6;
-    static constexpr int kBufs = kRows ? 2 : 4;
+    static constexpr int kStages = C == 16 ? 6 : C == 32 ? 5 : C == 64 ? 4 : 6;
+    static constexpr int kBufs = 4;
     static constexpr int kTmem = kBufs * C;
-    static constexpr int kChunk = C == 128 ? 8 : 16;  // weights form: K-blocks of row scales held at a time, twice
-    static constexpr int kScaleBytes = kRows ? 0 : 2 * kChunk * C * 4;
+    static constexpr int kChunk = C == 128 ? 8 : 16;  // K-blocks of row scales held at a time, twice
+    static constexpr int kScaleBytes = 2 * kChunk * C * 4;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + 256;
-    static constexpr int kCtas = !kRows && C <= 64 ? 2 : 1;  // resident on an SM
+    static constexpr int kCtas = C <= 64 ? 2 : 1;  // resident on an SM
     static_assert(kTmem >= 32 && kTmem * kCtas <= 512 && (kTmem & (kTmem - 1)) == 0, "tensor memory");
     static_assert(kSmem * kCtas <= 232448 - 1024 * (kCtas - 1), "shared memory");
-    static_assert(kRows || kStages * kStageBytes >= C * kLanes * 4, "partial sums of a split lie in the ring");
+    static_assert(kStages * kStageBytes >= C * kLanes * 4, "partial sums of a split lie in the ring");
 };
 
 struct Tiles {
@@ -79,6 +84,28 @@ __device__ __forceinline__ uint32_t f8_idesc(int M, int N) {
 // 32 lanes x 16 columns, as eight register pairs
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
     ptx::tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
+}
+
+// 32 lanes x 32 columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool in) {
@@ -162,7 +189,7 @@ template <class F>
 __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     f8_matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ Tiles T,
                      const __grid_constant__ CUtensorMap map_lanes, const __grid_constant__ CUtensorMap map_cols) {
-    constexpr int C = F::C, kStages = F::kStages, kBufs = F::kBufs, kPer = F::kPer, kChunk = F::kChunk;
+    constexpr int C = F::C, kStages = F::kStages, kBufs = F::kBufs, kChunk = F::kChunk;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -175,7 +202,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     __shared__ int abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(full + i, 1);
@@ -217,8 +244,8 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         lt = 16 * g + (r - ct * deep);
     };
 
-    if (warp == F::kEpi) {
-        if (lane == 0) {
+    if (warp >= F::kEpi) {
+        if (warp == F::kEpi && lane == 0) {
             // ---------------- loads ----------------
             int st = 0, issued = 0;
             uint32_t ph = 0;
@@ -249,9 +276,10 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                 ptx::mbar_wait_bounded(full + sl, st - 1 - i < 0 ? ph ^ 1 : ph, nullptr);
             }
         }
-    } else if (warp == F::kEpi + 1) {
-        if (lane == 0) {
+        if (warp == F::kEpi + 1) {
             // ---------------- MMA issue ----------------
+            // the whole warp goes round, so that descriptors stay in uniform registers, and one lane issues
+            const bool leader = elect_one();
             const uint32_t idesc = f8_idesc(kLanes, C);
             const uint64_t d0 = sw128_desc(ptx::smem_addr(ring));
             int st = 0, buf = 0;
@@ -259,19 +287,22 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
             bool ok = true;
             for (int t = first; t < T.total && ok; t += step) {
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!ptx::mbar_wait_bounded(full + st, ph, abortp) ||
-                        !ptx::mbar_wait_bounded(acc_empty + buf, bph ^ 1, abortp)) {
-                        fail(2u);
+                    if (!__all_sync(kFull, ptx::mbar_wait_sleep(full + st, ph, abortp) &&
+                                               ptx::mbar_wait_sleep(acc_empty + buf, bph ^ 1, abortp))) {
+                        if (leader) fail(2u);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     const uint64_t ad = d0 + (uint64_t)((st * F::kStageBytes) >> 4), bd = ad + (kLaneBytes >> 4);
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // K = 32 an MMA: 32 bytes on in the swizzled rows
-                        mma_f8_ss(tmem + buf * C, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-                    ptx::mma_commit(empty + st);
-                    ptx::mma_commit(acc_full + buf);
+                        for (int k = 0; k < 4; ++k)  // K = 32 an MMA: 32 bytes on in the swizzled rows
+                            mma_f8_ss(tmem + buf * C, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                        ptx::mma_commit(empty + st);
+                        ptx::mma_commit(acc_full + buf);
+                    }
+                    __syncwarp();
                     if (++st == kStages) {
                         st = 0;
                         ph ^= 1;
@@ -282,81 +313,24 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                     }
                 }
             }
-            ptx::mma_commit(drain);
+            if (leader) ptx::mma_commit(drain);
+            __syncwarp();
             ptx::mbar_wait_bounded(drain, 0, nullptr);
         }
     } else {
         // ---------------- epilogue ----------------
-        const int q = warp & 3, half = warp >> 2;  // rows form: warps 4-7 take the second half of the columns
-        const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + half * kPer;
+        const uint32_t taddr = tmem + ((uint32_t)(32 * warp) << 16);
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
-        const bool wide = !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % (a.type == MOE_F32 ? 4 : 8) == 0;
         for (int t = first; t < T.total; t += step) {
             int lt, ct;
             place(t, lt, ct);
-            uint64_t acc[kPer / 2];
+            uint64_t acc[C / 2];
 #pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) acc[i] = 0;
-            const int lrow = lt * kLanes + 32 * q + lane;  // this thread's lane: a row, or a weight
-            if constexpr (F::kRows) {
-                const bool in = lrow < a.m;
-                const int nb = ct * (C / kF8Block) + half;
-                const bool nin = nb * kF8Block < a.n;
-                const float* sa = a.sa + (in ? lrow : 0);
-                const float* sw = a.sw + (nin ? (int64_t)nb * a.sw_stride : 0);
-                float s_next[4], w_lane = 0.0f;
-                auto fetch = [&](int kb) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s_next[i] = in && kb + i < kb1 ? sa[(int64_t)(kb + i) * a.sa_stride] : 0.0f;
-                };
-                fetch(kb0);
-                for (int kb = kb0; kb < kb1 && ok; kb += 4) {
-                    if (((kb - kb0) & 31) == 0) w_lane = nin && kb + lane < kb1 ? sw[kb + lane] : 0.0f;
-                    float s_now[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s_now[i] = s_next[i];
-                    fetch(kb + 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (kb + i >= kb1) break;
-                        const float sc = s_now[i] * __shfl_sync(kFull, w_lane, (kb + i - kb0) & 31);
-                        if (!__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + buf, bph, abortp))) {
-                            if (lane == 0) fail(4u);
-                            ok = false;
-                            break;
-                        }
-                        ptx::tc_fence_after();
-                        const uint64_t s2 = ptx::f2(sc, sc);
-                        const uint32_t at = taddr + buf * C;
-                        uint32_t d[2][16];
-                        tmem_ld16(at, d[0]);
-#pragma unroll
-                        for (int c = 0; c < kPer / 16; ++c) {
-                            ptx::tmem_ld_wait();
-                            if (c + 1 < kPer / 16) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                acc[8 * c + e] = ptx::fma2(
-                                    ptx::f2(__uint_as_float(d[c & 1][2 * e]), __uint_as_float(d[c & 1][2 * e + 1])), s2,
-                                    acc[8 * c + e]);
-                        }
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acc_empty + buf);
-                        if (++buf == kBufs) {
-                            buf = 0;
-                            bph ^= 1;
-                        }
-                    }
-                }
-                if (ok && in) {
-                    const int n0 = ct * C + half * kPer;
-                    if (n0 < a.n) store_row<kPer>(a.out, (int64_t)lrow * a.out_stride + n0, acc, a.n - n0, wide, a.type);
-                }
-            } else {
+            for (int i = 0; i < C / 2; ++i) acc[i] = 0;
+            const int lrow = lt * kLanes + 32 * warp + lane;  // this thread's lane: a weight
+            {
                 const bool nin = lt * kLanes < a.n;
                 const float* sw = a.sw + (nin ? (int64_t)lt * a.sw_stride : 0);
                 const int m0 = ct * C;
@@ -397,9 +371,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                         uint32_t d[2][16];
                         tmem_ld16(at, d[0]);
 #pragma unroll
-                        for (int c = 0; c < kPer / 16; ++c) {
+                        for (int c = 0; c < C / 16; ++c) {
                             ptx::tmem_ld_wait();
-                            if (c + 1 < kPer / 16) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
+                            if (c + 1 < C / 16) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float4 s4 = ptx::lds_f4(sp + 64 * c + 16 * e);
@@ -434,7 +408,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                     ptx::named_sync(1, 32 * F::kEpi);  // this tile's scales are read before the next tile's come
                 } else if (ok) {
                     // the ring is done with: the last accumulator's MMAs have read it
-                    float* part = reinterpret_cast<float*>(ring) + 32 * q + lane;
+                    float* part = reinterpret_cast<float*>(ring) + 32 * warp + lane;
 #pragma unroll
                     for (int c = 0; c < C / 2; ++c) {
                         const float2 v = ptx::f2(acc[c]);
@@ -445,7 +419,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
             }
         }
     }
-    if constexpr (!F::kRows) {
+    {
         if (T.splits > 1) {  // one tile a cluster
             __syncwarp();
             cluster_sync();
@@ -471,6 +445,487 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == F::kEpi) ptx::tmem_dealloc(tmem, F::kTmem);
+}
+
+// ---- rows form ------------------------------------------------------------------
+//
+// Two CTAs of a cluster share a tile of 256 rows by 256 weights (cta_group::2): each brings its 128 rows and half of
+// the weights, 32 KB a K-block, and holds the sums of its rows. An SM then moves two thirds of the bytes into shared
+// memory that a tile of 128 x 256 of its own would take, and one thread issues for two SMs. Tensor memory holds two
+// K-blocks' sums. Their buffers go back and forth by halves of 128 weights, which the MMAs take one after the other: from
+// the end of a half until its buffer is needed again there are three halves, 768 cycles of tensor work, for the way to the
+// epilogue, its loads (eight warps a half, 64 columns each) and the way back.
+
+struct Pair {
+    static constexpr int C = 256, kCtaRows = 128, kEpi = 16, kScaleWarps = 2;
+    static constexpr int kWarpLoad = kEpi, kWarpMma = kEpi + 1, kWarpScale = kEpi + 2;
+    static constexpr int kThreads = 32 * (kEpi + 4);
+    static constexpr int kStageBytes = 2 * kLaneBytes;
+    static constexpr int kStages = 6, kSlots = 4;  // a slot: the sums of a K-block and half of the weights
+    static constexpr int kScaleBytes = kSlots * kCtaRows * 4;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + 256;
+    // 640 threads x 96 registers at launch = 512 x 112 + 128 x 32
+    static constexpr int kRegsEpi = 112, kRegsOther = 32;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_addr(p)), "r"(rank));
+    return at;
+}
+// One lane's arrival at a barrier of the cluster and at one of this CTA.
+// (No release at cluster scope: it would wait for all memory operations of the thread, and what is handed over here is
+// tensor memory, which tcgen05's fences order.)
+__device__ __forceinline__ void arrive_both(bool one, uint32_t cluster_addr, uint32_t own_addr) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+        "@p mbarrier.arrive.shared::cluster.b64 _, [%1];\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%2];\n\t}" ::"r"((uint32_t)one),
+        "r"(cluster_addr), "r"(own_addr)
+        : "memory");
+}
+// A box into this CTA's shared memory, its bytes counted at a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load_pair(void* dst, const void* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(ptx::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at the barrier of this offset in both CTAs when every MMA issued before is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(Pair::kThreads, 1)
+    f8_rows_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ Tiles T,
+                   const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w) {
+    using F = Pair;
+    constexpr int kStages = F::kStages, kSlots = F::kSlots, C = F::C;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* ring =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float* scales = reinterpret_cast<float*>(ring + kStages * F::kStageBytes);  // [kSlots][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * F::kStageBytes + F::kScaleBytes);  // first CTA's: both loaded
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;        // sums and scales are there
+    uint64_t* acc_empty = acc_full + kSlots;     // first CTA's: both have read their sums
+    uint64_t* scale_empty = acc_empty + kSlots;  // this CTA has
+    uint64_t* drain = scale_empty + kSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    __shared__ int abort_flag;
+
+    const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(acc_full + i, 2);
+            ptx::mbar_init(acc_empty + i, F::kEpi);  // half of either CTA's warps
+            ptx::mbar_init(scale_empty + i, F::kEpi / 2);
+        }
+        ptx::mbar_init(drain, 1);
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&map_a);
+        ptx::prefetch_tensormap(&map_w);
+    }
+    if (warp == F::kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(tmem_slot)),
+                     "r"(kSlots * C / 2)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // barriers are there before the other CTA uses them
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int* abortp = &abort_flag;
+    auto fail = [&](unsigned bit) {
+        if (!*abortp) *(volatile unsigned*)a.err = bit;
+        abort_flag = 1;
+    };
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+
+    const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1, kblocks = T.kblocks;
+    // neighbouring tiles go along the rows, 8 deep, so that tiles of one time share both operands in L2
+    auto place = [&](int t, int& lt, int& ct) {
+        const int group = 8 * T.cols, g = t / group, deep = min(8, T.lanes - 8 * g), r = t - g * group;
+        ct = r / deep;
+        lt = 8 * g + (r - ct * deep);
+    };
+
+    if (warp >= F::kEpi) {
+        fewer_registers<F::kRegsOther>();
+        if (warp == F::kWarpLoad) {
+            // ---------------- loads ----------------
+            const bool leader = elect_one();
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t full0 = peer_addr(full, 0);
+            for (int t = first; t < T.total && ok; t += step) {
+                int lt, ct;
+                place(t, lt, ct);
+                const int ya = lt * 256 + (int)rank * 128, yw = ct * C + (int)rank * 64;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!__all_sync(kFull, ptx::mbar_wait_sleep(empty + st, ph ^ 1, abortp))) {
+                        if (leader) fail(1u);
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        unsigned char* p = ring + st * F::kStageBytes;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, 2 * F::kStageBytes);
+                        tma_load_pair(p, &map_a, kb * 128, ya, full0 + 8 * st);
+                        tma_load_pair(p + kLaneBytes, &map_w, kb * 128, yw, full0 + 8 * st);
+                        tma_load_pair(p + kLaneBytes + kLaneBytes / 2, &map_w, kb * 128, yw + 128, full0 + 8 * st);
+                    }
+                    __syncwarp();
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+        } else if (warp == F::kWarpMma && rank == 0) {
+            // ---------------- MMA issue ----------------
+            // the whole warp goes round, so that descriptors stay in uniform registers, and one lane issues
+            const bool leader = elect_one();
+            const uint32_t idesc = f8_idesc(256, C / 2);
+            const uint64_t d0 = sw128_desc(ptx::smem_addr(ring));
+            int st = 0, slot = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int t = first; t < T.total && ok; t += step) {
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    const uint64_t ad = d0 + (uint64_t)((st * F::kStageBytes) >> 4), bd = ad + (kLaneBytes >> 4);
+                    ok = __all_sync(kFull, ptx::mbar_wait_sleep(full + st, ph, abortp));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && __all_sync(kFull, ptx::mbar_wait_sleep(acc_empty + slot, bph ^ 1, abortp));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // K = 32 an MMA: 32 bytes on in the swizzled rows
+                                mma_f8_pair(tmem + slot * (C / 2), ad + 2 * k, bd + 512 * h + 2 * k, idesc, k > 0);
+                            commit_pair(acc_full + slot);
+                            if (h == 1) commit_pair(empty + st);
+                        }
+                        __syncwarp();
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            bph ^= 1;
+                        }
+                    }
+                    if (!ok) {
+                        if (leader) fail(2u);
+                        break;
+                    }
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (leader) commit_pair(drain);
+            __syncwarp();
+            ptx::mbar_wait_sleep(drain, 0, nullptr);
+        } else if (warp == F::kWarpMma) {
+            ptx::mbar_wait_sleep(drain, 0, nullptr);  // the commits' arrivals here are the other CTA's last writes
+        } else if (warp >= F::kWarpScale) {
+            // ---------------- scales: rows' times weights' ----------------
+            // a warp a half of the weights, a lane four rows, two K-blocks ahead; the weight block's scales 32 K-blocks
+            // a register
+            const int h = warp - F::kWarpScale;
+            int slot = h;
+            uint32_t bph = 0;
+            bool ok = true;
+            for (int t = first; t < T.total && ok; t += step) {
+                int lt, ct;
+                place(t, lt, ct);
+                const int m = lt * 256 + (int)rank * 128 + lane, left = a.m - m, nb = ct * 2 + h;
+                const float* sa = a.sa + (left > 0 ? m : 0);
+                const bool nin = nb * kF8Block < a.n;
+                const float* sw = a.sw + (nin ? (int64_t)nb * a.sw_stride : 0);
+                float q[2][4], w = 0.0f;
+                auto fetch = [&](float (&v)[4], int kb) {
+                    const float* p = sa + (int64_t)kb * a.sa_stride;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = kb < kblocks && 32 * r < left ? p[32 * r] : 0.0f;
+                };
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fetch(q[i], i);
+                for (int k2 = 0; k2 < kblocks && ok; k2 += 2) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int kb = k2 + i;
+                        if (kb >= kblocks) break;
+                        if ((kb & 31) == 0) w = nin && kb + lane < kblocks ? sw[kb + lane] : 0.0f;
+                        if (!__all_sync(kFull, ptx::mbar_wait_sleep(scale_empty + slot, bph ^ 1, abortp))) {
+                            if (lane == 0) fail(8u);
+                            ok = false;
+                            break;
+                        }
+                        const float x = __shfl_sync(kFull, w, kb & 31);
+                        float* to = scales + slot * 128 + lane;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) to[32 * r] = q[i][r] * x;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(acc_full + slot);
+                        fetch(q[i], kb + 2);
+                        slot += 2;
+                        if (slot >= kSlots) {
+                            slot = h;
+                            bph ^= 1;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        more_registers<F::kRegsEpi>();
+        // ---------------- epilogue ----------------
+        // TMEM lanes 32 q on; of the slots of half h, columns 64 part on of 128
+        const int q = warp & 3, part = (warp >> 2) & 1, h = warp >> 3;
+        const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + part * 64;
+        const uint32_t free0 = peer_addr(acc_empty, 0), mine0 = ptx::smem_addr(scale_empty), sp = ptx::smem_addr(scales) + 4 * (32 * q + lane);
+        int slot = h;
+        uint32_t bph = 0;
+        bool ok = true;
+        for (int t = first; t < T.total && ok; t += step) {
+            uint64_t acc[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = 0;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + slot, bph, abortp))) {
+                    if (lane == 0) fail(4u);
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                uint32_t d[32];
+                tmem_ld32(taddr + slot * (C / 2), d);
+                const float sc = ptx::lds_f32(sp + slot * 512);
+                const uint64_t s2 = ptx::f2(sc, sc);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[e] = ptx::fma2(ptx::f2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), s2, acc[e]);
+                tmem_ld32(taddr + slot * (C / 2) + 32, d);
+                ptx::tmem_ld_wait();
+                ptx::tc_fence_before();
+                arrive_both(lane == 0, free0 + 8 * slot, mine0 + 8 * slot);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[16 + e] = ptx::fma2(ptx::f2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), s2, acc[16 + e]);
+                slot += 2;
+                if (slot >= kSlots) {
+                    slot = h;
+                    bph ^= 1;
+                }
+            }
+            if (ok) {
+                int lt, ct;
+                place(t, lt, ct);
+                const int m = lt * 256 + (int)rank * 128 + 32 * q + lane, n = ct * C + h * 128 + part * 64;
+                const bool wide =
+                    !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % (a.type == MOE_F32 ? 4 : 8) == 0;
+                if (m < a.m && n < a.n) store_row<64>(a.out, (int64_t)m * a.out_stride + n, acc, a.n - n, wide, a.type);
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (*abortp) {
+        // Where a wait expired, a copy may be on its way that no barrier of this CTA counts: they take microseconds, so
+        // a millisecond is given to them.
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    cluster_sync();  // nothing of the pair's is under way in either CTA
+    ptx::tc_fence_after();
+    if (warp == F::kWarpMma)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSlots * C / 2) : "memory");
+}
+
+// ---- a few rows ------------------------------------------------------------------
+//
+// Up to 16 rows are bound by the weights' way from memory, and short calls by latency. So there are no roles and no
+// tensor memory: a CTA takes 16 weights at a time, its warps take their K-blocks in turn, and the product is
+// mma.sync's (m16n8k32, e4m3, the weights as the 16). The order of K within a block is free as long as both operands
+// share it, so a lane takes 16 consecutive bytes of a row, four words of which pairs feed two MMAs. A lane copies
+// exactly the weights that it will use itself (cp.async), so its shared memory is a queue of its own: nothing to
+// synchronise, no bank conflict, and kFewDeep K-blocks a warp in flight at no cost in registers.
+
+constexpr int kFewWarps = 8, kFewDeep = 4, kFewLanes = 16;
+constexpr int kFewSmem = kFewWarps * kFewDeep * 4 * 512;
+constexpr int few_ctas(int NT) { return NT == 1 ? 3 : 2; }  // resident on an SM
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(  // in order with the copies that overwrite its operands' places
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// What a K-block needs besides its weights: NT tiles of eight rows, a lane's 16 bytes of each half, and scales.
+template <int NT>
+struct FewRows {
+    uint4 x[NT][2];
+    float s[NT][2], w;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
+    f8_few_kernel(const __grid_constant__ MatmulArgs a, const int kblocks, const int groups) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ float part[2][kFewWarps][8 * NT][kFewLanes + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t queue = ptx::smem_addr(smem_raw) + warp * (kFewDeep * 4 * 512) + lane * 16;
+    {
+        // the weights may be what the kernel before writes, so they are only brought into L2 before the wait
+        const int64_t n = (int64_t)blockIdx.x * kFewLanes + threadIdx.x;
+        if (threadIdx.x < kFewLanes && n < a.n)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.w + n * a.w_stride), "r"(min(a.k, 16384)) : "memory");
+    }
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const uint8_t* ap[NT];
+    bool ain[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        ain[i] = 8 * i + g < a.m;
+        ap[i] = a.a + (ain[i] ? (8 * i + g) * a.a_stride : 0) + 16 * t;
+    }
+    // the next K-block to copy: of group pg, block pk
+    int pg = blockIdx.x, pk = warp, ps = 0;
+    auto copy = [&] {
+        if (pg < groups && pk < kblocks) {
+            const int k = pk * kF8Block + 16 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = (int64_t)pg * kFewLanes + g + 8 * h;
+                const uint8_t* p = a.w + (n < a.n ? n * a.w_stride : 0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool in = n < a.n && k + 64 * c < a.k;
+                    cp_async16(queue + ps * 2048 + (2 * h + c) * 512, p + (in ? k + 64 * c : 0), in);
+                }
+            }
+        }
+        cp_async_commit();
+        ps = ps + 1 == kFewDeep ? 0 : ps + 1;
+        pk += kFewWarps;
+        if (pk >= kblocks) {
+            pk = warp;
+            pg += gridDim.x;
+        }
+    };
+    auto rows = [&](FewRows<NT>& r, int group, int kb) {
+        const bool in = group < groups && kb < kblocks;
+        const int k = kb * kF8Block;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                r.x[i][c] = in && ain[i] && k + 64 * c + 16 * t < a.k ? *reinterpret_cast<const uint4*>(ap[i] + k + 64 * c)
+                                                                      : make_uint4(0, 0, 0, 0);
+                const int m = 8 * i + 2 * t + c;
+                r.s[i][c] = in && m < a.m ? a.sa[(int64_t)kb * a.sa_stride + m] : 0.0f;
+            }
+        r.w = in ? a.sw[(int64_t)(group / (kF8Block / kFewLanes)) * a.sw_stride + kb] : 0.0f;
+    };
+#pragma unroll
+    for (int d = 0; d < kFewDeep; ++d) copy();
+    FewRows<NT> next;
+    rows(next, blockIdx.x, warp);
+    int cs = 0, turn = 0;
+    for (int group = blockIdx.x; group < groups; group += gridDim.x, turn ^= 1) {
+        float acc[NT][4] = {};
+        for (int kb = warp; kb < kblocks; kb += kFewWarps) {
+            const FewRows<NT> r = next;
+            const bool last = kb + kFewWarps >= kblocks;
+            rows(next, last ? group + (int)gridDim.x : group, last ? warp : kb + kFewWarps);
+            cp_async_wait<kFewDeep - 1>();
+            uint4 w[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) w[h][c] = ptx::lds_u4(queue + cs * 2048 + (2 * h + c) * 512);
+            cs = cs + 1 == kFewDeep ? 0 : cs + 1;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float s[4] = {};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 u = w[0][c], v = w[1][c], b = r.x[i][c];
+                    mma_e4m3(s, u.x, v.x, u.y, v.y, b.x, b.y);
+                    mma_e4m3(s, u.z, v.z, u.w, v.w, b.z, b.w);
+                }
+                // lanes hold rows 2t, 2t + 1 of weights g and g + 8
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float sc = r.s[i][c] * r.w;
+                    acc[i][c] = fmaf(s[c], sc, acc[i][c]);
+                    acc[i][2 + c] = fmaf(s[2 + c], sc, acc[i][2 + c]);
+                }
+            }
+            copy();  // into the place just read
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[turn][warp][8 * i + 2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[i][e];
+        __syncthreads();
+        // (the other half of `part` is written meanwhile, and this one only after the next barrier)
+        if (threadIdx.x < 8 * NT * kFewLanes) {
+            const int r = threadIdx.x / kFewLanes, c = threadIdx.x % kFewLanes;
+            const int64_t n = (int64_t)group * kFewLanes + c;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) v += part[turn][w][r][c];
+            if (r < a.m && n < a.n) store1(a.out, r * a.out_stride + n, v, a.type);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+template <int NT>
+cudaError_t launch_few(const MatmulArgs& a, int sms, cudaStream_t s) {
+    static_assert(8 * NT * kFewLanes <= 32 * kFewWarps, "a thread an output");
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(f8_few_kernel<NT>), kFewSmem);
+    if (e != cudaSuccess) return e;
+    const int groups = (a.n + kFewLanes - 1) / kFewLanes;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)std::min(groups, few_ctas(NT) * sms)), dim3(32 * kFewWarps), kFewSmem, s,
+                                                 true, &attr);
+    return cudaLaunchKernelEx(&cfg, f8_few_kernel<NT>, a, (a.k + kF8Block - 1) / kF8Block, groups);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -507,45 +962,65 @@ cudaError_t encode_codes(CUtensorMap* m, const uint8_t* base, int rows, int k, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+Tiles tiles_of(int lanes, int cols, int lane_tile, int col_tile, int k) {
+    Tiles T;
+    T.lanes = (lanes + lane_tile - 1) / lane_tile;
+    T.cols = (cols + col_tile - 1) / col_tile;
+    T.total = T.lanes * T.cols;
+    T.kblocks = (k + kF8Block - 1) / kF8Block;
+    T.splits = 1;
+    return T;
+}
+
+// Programmatic dependent launch of clusters of `cluster` CTAs (attr must outlive the launch).
+cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, cudaStream_t s, unsigned cluster,
+                                  cudaLaunchAttribute (&attr)[2]) {
+    cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(threads), smem, s, true, attr);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
 template <class F>
 cudaError_t launch_form(const MatmulArgs& a, int sms, cudaStream_t s) {
-    Tiles T;
-    const int ln = F::kRows ? a.m : a.n, cn = F::kRows ? a.n : a.m;
-    T.lanes = (ln + kLanes - 1) / kLanes;
-    T.cols = (cn + F::C - 1) / F::C;
-    T.total = T.lanes * T.cols;
-    T.kblocks = (a.k + kF8Block - 1) / kF8Block;
-    T.splits = 1;
+    Tiles T = tiles_of(a.n, a.m, kLanes, F::C, a.k);
     const int room = sms * F::kCtas;
-    if (!F::kRows && T.total < room) T.splits = std::max(1, std::min({8, room / T.total, T.kblocks / 2}));
-    CUtensorMap ml, mc;
-    cudaError_t e = F::kRows ? encode_codes(&ml, a.a, a.m, a.k, a.a_stride, kLanes)
-                             : encode_codes(&ml, a.w, a.n, a.k, a.w_stride, kLanes);
-    if (e != cudaSuccess) return e;
-    e = F::kRows ? encode_codes(&mc, a.w, a.n, a.k, a.w_stride, F::C) : encode_codes(&mc, a.a, a.m, a.k, a.a_stride, F::C);
-    if (e != cudaSuccess) return e;
-    e = ensure_smem_attr(reinterpret_cast<const void*>(f8_matmul_kernel<F>), F::kSmem);
+    if (T.total < room) T.splits = std::max(1, std::min({8, room / T.total, T.kblocks / 2}));
+    CUtensorMap mw, ma;
+    cudaError_t e = encode_codes(&mw, a.w, a.n, a.k, a.w_stride, kLanes);
+    if (e == cudaSuccess) e = encode_codes(&ma, a.a, a.m, a.k, a.a_stride, F::C);
+    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_matmul_kernel<F>), F::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     const unsigned grid = T.splits > 1 ? (unsigned)(T.total * T.splits) : (unsigned)std::min(T.total, room);
-    cudaLaunchConfig_t cfg = launch_config(dim3(grid), dim3(F::kThreads), F::kSmem, s, true, attr);
-    if (T.splits > 1) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = (unsigned)T.splits;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-    }
-    return cudaLaunchKernelEx(&cfg, f8_matmul_kernel<F>, a, T, ml, mc);
+    const cudaLaunchConfig_t cfg = cluster_config(grid, F::kThreads, F::kSmem, s, (unsigned)T.splits, attr);
+    return cudaLaunchKernelEx(&cfg, f8_matmul_kernel<F>, a, T, mw, ma);
+}
+
+cudaError_t launch_rows(const MatmulArgs& a, int sms, cudaStream_t s) {
+    const Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
+    CUtensorMap ma, mw;
+    cudaError_t e = encode_codes(&ma, a.a, a.m, a.k, a.a_stride, Pair::kCtaRows);
+    if (e == cudaSuccess) e = encode_codes(&mw, a.w, a.n, a.k, a.w_stride, Pair::C / 4);
+    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_rows_kernel), Pair::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        cluster_config(2u * (unsigned)std::min(T.total, sms / 2), Pair::kThreads, Pair::kSmem, s, 2, attr);
+    return cudaLaunchKernelEx(&cfg, f8_rows_kernel, a, T, ma, mw);
 }
 
 }  // namespace
 
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
-    if (a.m <= 16) return launch_form<Form<16, false>>(a, sms, s);
-    if (a.m <= 32) return launch_form<Form<32, false>>(a, sms, s);
-    if (a.m <= 64) return launch_form<Form<64, false>>(a, sms, s);
-    if (a.m <= 256) return launch_form<Form<128, false>>(a, sms, s);
-    return launch_form<Form<256, true>>(a, sms, s);
+    if (a.m <= 8) return launch_few<1>(a, sms, s);
+    if (a.m <= 16) return launch_few<2>(a, sms, s);
+    if (a.m <= 32) return launch_form<Form<32>>(a, sms, s);
+    if (a.m <= 64) return launch_form<Form<64>>(a, sms, s);
+    if (a.m <= 256) return launch_form<Form<128>>(a, sms, s);
+    return launch_rows(a, sms, s);
 }
 
 }  // namespace moe
