@@ -707,6 +707,12 @@ _f8_matmul_pack = struct.Struct("@PqPqPqPqPqiiii").pack  # and of moe_f8_matmul_
 _SAME = object()
 
 
+def _dense_new(shape, dtype, device: int, stream):
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    return _new(shape, dtype, _torch.device("cuda", device), stream)
+
+
 def _rows3(t, what: str, shape, device: int):
     """(pointer, token stride, head stride) of a CUDA tensor of that shape, [n][d] or [n][heads][d]."""
     if t.shape != shape or t.get_device() != device:
@@ -719,18 +725,20 @@ def _rows3(t, what: str, shape, device: int):
 
 def _codes(t, what: str, shape, device: int):
     """(pointer, stride) of e4m3 codes [n][k]."""
-    if t.dtype != _torch.float8_e4m3fn or t.shape != shape or t.get_device() != device or t.stride(1) != 1:
+    st = t.stride()
+    if t.dtype != _torch.float8_e4m3fn or t.shape != shape or t.get_device() != device or st[1] != 1:
         raise ValueError(f"{what}: expected float8_e4m3fn {list(shape)} on CUDA device {device}, the last dimension contiguous, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else -(-shape[1] // 16) * 16
+    return t.data_ptr(), st[0] if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
 def _scales(t, what: str, shape, device: int):
     """(pointer, stride) of fp32 scales of that shape."""
-    if t.dtype != _torch.float32 or t.shape != shape or t.get_device() != device or (shape[1] > 1 and t.stride(1) != 1):
+    st = t.stride()
+    if t.dtype != _torch.float32 or t.shape != shape or t.get_device() != device or (st[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what}: expected float32 {list(shape)} on CUDA device {device}, the last dimension contiguous, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1]
 
 
 def _dense_stream(stream, device: int):
@@ -753,45 +761,59 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
     given; None: no such output), sum = h of the residual's type (None without one), and with f8 the e4m3 codes
     [n][d] and f32 scales [ceil(d / 128)][n] of the same rows (None, None without). Outputs given are filled."""
     torch = _torch or _kv_torch()
-    device, shape = _cuda(x, "x"), x.shape
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    device = _cuda(x, "x")
+    if len(shape) == 3:
+        n, heads, d = shape
+        ht, tt = d, heads * d  # strides of a new tensor
+    elif len(shape) == 2:
+        n, d = shape
+        heads, ht, tt = 1, 0, d
+    else:
         raise ValueError("x: expected [n][d] or [n][heads][d]")
-    n, d, heads = shape[0], shape[-1], shape[1] if x.dim() == 3 else 1
     xp, xt, xh = _rows3(x, "x", shape, device)
     rp = rt = rh = rd = sp = st = sh = wp = wd = op = ot = oh = od = cp = ct = lp = lt = 0
     if weight is not None:
-        if weight.shape != (d,) or weight.get_device() != device or (d > 1 and weight.stride(0) != 1):
+        if weight.shape != shape[-1:] or weight.get_device() != device or (d > 1 and weight.stride(0) != 1):
             raise ValueError(f"weight: expected [{d}], contiguous, on CUDA device {device}")
         wp, wd = weight.data_ptr(), _kv_type(weight.dtype)
     if residual is not None:
         rp, rt, rh = _rows3(residual, "residual", shape, device)
         rd = _kv_type(residual.dtype)
         if sum is None:
-            sum = _new(shape, residual.dtype, x.device, stream)
-        elif sum.dtype != residual.dtype:
-            raise ValueError("sum: expected the residual's type")
-        sp, st, sh = _rows3(sum, "sum", shape, device)
+            sum = _dense_new(shape, residual.dtype, device, stream)
+            sp, st, sh = sum.data_ptr(), tt, ht
+        else:
+            if sum.dtype != residual.dtype:
+                raise ValueError("sum: expected the residual's type")
+            sp, st, sh = _rows3(sum, "sum", shape, device)
     elif sum is not None:
         raise ValueError("sum: there is no residual")
-    if out is None:
-        if dtype is _SAME:
-            dtype = x.dtype
-        if dtype is not None:
-            out = _new(shape, dtype, x.device, stream)
-    elif dtype is not _SAME and dtype != out.dtype:
-        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
     if out is not None:
+        if dtype is not _SAME and dtype != out.dtype:
+            raise ValueError(f"out: expected {dtype}, got {out.dtype}")
         op, ot, oh = _rows3(out, "out", shape, device)
         od = _kv_type(out.dtype)
+    elif dtype is not None:
+        if dtype is _SAME:
+            dtype = x.dtype
+        od = _kv_type(dtype)
+        out = _dense_new(shape, dtype, device, stream)
+        op, ot, oh = out.data_ptr(), tt, ht
     if f8 or codes is not None or scales is not None:
         if heads != 1:
             raise ValueError("an 8-bit output takes rows of one head")
+        blocks = (d + 127) // 128
         if codes is None:
-            codes = _new((n, d), torch.float8_e4m3fn, x.device, stream)
+            codes = _dense_new((n, d), torch.float8_e4m3fn, device, stream)
+            cp, ct = codes.data_ptr(), d
+        else:
+            cp, ct = _codes(codes, "codes", (n, d), device)
         if scales is None:
-            scales = _new((-(-d // 128), n), torch.float32, x.device, stream)
-        cp, ct = _codes(codes, "codes", (n, d), device)
-        lp, lt = _scales(scales, "scales", (-(-d // 128), n), device)
+            scales = _dense_new((blocks, n), torch.float32, device, stream)
+            lp, lt = scales.data_ptr(), n
+        else:
+            lp, lt = _scales(scales, "scales", (blocks, n), device)
     args = _norm_pack(xp, xt, xh, rp, rt, rh, wp, sp, st, sh, op, ot, oh, cp, ct, lp, lt, n, heads, d, eps,
                       _kv_type(x.dtype), rd, wd, od)
     _check((_lib or load()).moe_rms_norm(ctx, args, _dense_stream(stream, device)), "moe_rms_norm")
@@ -801,17 +823,22 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
 def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
     torch = _torch or _kv_torch()
     device = _cuda(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x: expected [n][k]")
-    n, k = x.shape
-    xp, xt, _ = _rows3(x, "x", x.shape, device)
-    shape = (-(-n // 128), -(-k // 128)) if weight else (-(-k // 128), n)
+    n, k = shape
+    xp, xt, _ = _rows3(x, "x", shape, device)
+    of_scales = ((n + 127) // 128 if weight else (k + 127) // 128, (k + 127) // 128 if weight else n)
     if codes is None:
-        codes = _new((n, k), torch.float8_e4m3fn, x.device, stream)
+        codes = _dense_new((n, k), torch.float8_e4m3fn, device, stream)
+        cp, ct = codes.data_ptr(), k
+    else:
+        cp, ct = _codes(codes, "codes", (n, k), device)
     if scales is None:
-        scales = _new(shape, torch.float32, x.device, stream)
-    cp, ct = _codes(codes, "codes", (n, k), device)
-    lp, lt = _scales(scales, "scales", shape, device)
+        scales = _dense_new(of_scales, torch.float32, device, stream)
+        lp, lt = scales.data_ptr(), of_scales[1]
+    else:
+        lp, lt = _scales(scales, "scales", of_scales, device)
     _check(getattr(_lib or load(), fn)(ctx, xp, xt, _kv_type(x.dtype), n, k, cp, ct, lp, lt, _dense_stream(stream, device)), fn)
     return codes, scales
 
@@ -833,18 +860,23 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
     device = _cuda(a, "a")
     if a.dim() != 2 or w.dim() != 2:
         raise ValueError("a and w: expected [m][k] and [n][k]")
-    (m, k), n = a.shape, w.shape[0]
+    m, k = a.shape
+    n, kb = w.shape[0], (k + 127) // 128
     ap, at = _codes(a, "a", (m, k), device)
     wp, wt = _codes(w, "w", (n, k), device)
-    kb = -(-k // 128)
     asp, ast = _scales(a_scales, "a_scales", (kb, m), device)
-    wsp, wst = _scales(w_scales, "w_scales", (-(-n // 128), kb), device)
+    wsp, wst = _scales(w_scales, "w_scales", ((n + 127) // 128, kb), device)
     if out is None:
-        out = _new((m, n), dtype or torch.bfloat16, a.device, stream)
-    elif dtype not in (None, out.dtype):
-        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
-    op, ot, _ = _rows3(out, "out", (m, n), device)
-    args = _f8_matmul_pack(ap, at, asp, ast, wp, wt, wsp, wst, op, ot, m, n, k, _kv_type(out.dtype))
+        dtype = dtype or torch.bfloat16
+        od = _kv_type(dtype)
+        out = _dense_new((m, n), dtype, device, stream)
+        op, ot = out.data_ptr(), n
+    else:
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+        od = _kv_type(out.dtype)
+        op, ot, _ = _rows3(out, "out", (m, n), device)
+    args = _f8_matmul_pack(ap, at, asp, ast, wp, wt, wsp, wst, op, ot, m, n, k, od)
     _check((_lib or load()).moe_f8_matmul(ctx, args, _dense_stream(stream, device)), "moe_f8_matmul")
     return out
 

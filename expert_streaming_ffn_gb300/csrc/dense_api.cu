@@ -119,7 +119,7 @@ extern "C" moe_status moe_rms_norm(moe_ctx* C, const moe_norm_args* p, void* str
     if (p->codes) per += 1.0 + 4.0 / kF8Block;
     cudaStream_t s = (cudaStream_t)stream;
     Launch l(C, K_RMS_NORM, per * a.rows * a.dim, 0, s);
-    CUDA_TRY(launch_rms_norm(a, s));
+    CUDA_TRY(launch_rms_norm(a, ctx_sms(C), s));
     return MOE_OK;
 }
 

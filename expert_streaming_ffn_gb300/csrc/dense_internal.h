@@ -25,7 +25,7 @@ struct NormArgs {
     FastDiv by_head{1};
     moe_dtype x_type, res_type, weight_type, out_type;  // sum has res_type
 };
-cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_rms_norm(const NormArgs& a, int sms, cudaStream_t s);
 
 struct QuantArgs {
     const void* x;

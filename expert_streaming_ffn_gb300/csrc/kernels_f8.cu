@@ -8,7 +8,7 @@
 //
 // A CTA's tile has 128 lanes (the MMA's M) and C columns (its N). Two forms:
 //   rows form (many rows): lanes are rows, columns 256 weights. A lane's scale is its row's times the weights' block's.
-//   weights form (few rows): lanes are 128 weights, which share a scale, columns up to C rows (16, 32, 64 or 128), so
+//   weights form (few rows): lanes are 128 weights, which share a scale, columns up to C rows (16, 32 or 64), so
 //     that no tensor work or memory goes to rows that are not there. K is split over the CTAs of a cluster where tiles
 //     are few, and each of them adds a share of the columns through distributed shared memory, in a fixed order.
 //
@@ -48,13 +48,13 @@ struct Form {
     static constexpr int kEpi = 4;
     static constexpr int kThreads = 32 * (kEpi + 2);
     static constexpr int kStageBytes = kLaneBytes + C * 128;
-    static constexpr int kStages = C == 16 ? 6 : C == 32 ? 5 : C == 64 ? 4 : 6;
+    static constexpr int kStages = C == 16 ? 6 : C == 32 ? 5 : 4;
     static constexpr int kBufs = 4;
     static constexpr int kTmem = kBufs * C;
-    static constexpr int kChunk = C == 128 ? 8 : 16;  // K-blocks of row scales held at a time, twice
+    static constexpr int kChunk = 16;  // K-blocks of row scales held at a time, twice
     static constexpr int kScaleBytes = 2 * kChunk * C * 4;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + 256;
-    static constexpr int kCtas = C <= 64 ? 2 : 1;  // resident on an SM
+    static constexpr int kCtas = 2;  // resident on an SM
     static_assert(kTmem >= 32 && kTmem * kCtas <= 512 && (kTmem & (kTmem - 1)) == 0, "tensor memory");
     static_assert(kSmem * kCtas <= 232448 - 1024 * (kCtas - 1), "shared memory");
     static_assert(kStages * kStageBytes >= C * kLanes * 4, "partial sums of a split lie in the ring");
@@ -108,6 +108,13 @@ __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A box of a tensor map into L2.
+__device__ __forceinline__ void prefetch_box(const void* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
@@ -125,11 +132,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
-    float v;
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
+    float4 v;
     uint32_t at;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
@@ -151,37 +161,73 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, moe_dtype t) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// N consecutive elements of a row from fp32 pairs, the first `n` of them; `wide`: on 16-byte boundaries.
-template <int N>
-__device__ __forceinline__ void store_row(void* out, int64_t at, const uint64_t (&v)[N / 2], int n, bool wide, moe_dtype t) {
-    if (n >= N && wide) {
-        if (t == MOE_F32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const float2 x = ptx::f2(v[2 * i]), y = ptx::f2(v[2 * i + 1]);
-                p[i] = make_float4(x.x, x.y, y.x, y.y);
-            }
-        } else {
-            uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-#pragma unroll
-            for (int i = 0; i < N / 8; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = ptx::f2(v[4 * i + j]);
-                    w[j] = pack2(x.x, x.y, t);
-                }
-                p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+// Four consecutive elements of a row, the first `n` of them.
+__device__ __forceinline__ void store4(const MatmulArgs& a, int64_t at, const float4& x, int n) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.out) + at * (a.type == MOE_F32 ? 4 : 2);
+    if (n >= 4 && !(p & (a.type == MOE_F32 ? 15 : 7))) {
+        if (a.type == MOE_F32)
+            *reinterpret_cast<float4*>(p) = x;
+        else
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x.x, x.y, a.type), pack2(x.z, x.w, a.type));
         return;
     }
+    if (n > 0) store1(a.out, at, x.x, a.type);
+    if (n > 1) store1(a.out, at + 1, x.y, a.type);
+    if (n > 2) store1(a.out, at + 2, x.z, a.type);
+    if (n > 3) store1(a.out, at + 3, x.w, a.type);
+}
+
+// A warp's 32 rows from m0 on by 64 columns from n0 on, a lane a row, to memory by way of `stage` (32 rows x 16 columns in
+// shared memory, groups of four swizzled so that neither way has bank conflicts), so that lanes that store side by side
+// write a row's neighbouring elements.
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, float* stage, int m0, int n0, const uint64_t (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    const bool wide = !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % (a.type == MOE_F32 ? 4 : 8) == 0 && n0 + 64 <= a.n;
+    const int rows = min(32, a.m - m0);
+    float4* const mine = reinterpret_cast<float4*>(stage) + 4 * lane;
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const float2 x = ptx::f2(v[i]);
-        if (2 * i < n) store1(out, at + 2 * i, x.x, t);
-        if (2 * i + 1 < n) store1(out, at + 2 * i + 1, x.y, t);
+    for (int c = 0; c < 4; ++c) {
+        if (n0 + 16 * c >= a.n) break;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float2 x = ptx::f2(v[8 * c + 2 * g]), y = ptx::f2(v[8 * c + 2 * g + 1]);
+            mine[g ^ ((lane >> 1) & 3)] = make_float4(x.x, x.y, y.x, y.y);
+        }
+        __syncwarp();
+        if (wide) {
+#pragma unroll 1
+            for (int r = lane >> 2; r < rows; r += 8) {
+                const int g = lane & 3;
+                store4(a, (int64_t)(m0 + r) * a.out_stride + n0 + 16 * c + 4 * g,
+                       reinterpret_cast<const float4*>(stage)[4 * r + (g ^ ((r >> 1) & 3))], 4);
+            }
+        } else {
+            const int e = lane & 15, n = n0 + 16 * c + e;
+#pragma unroll 1
+            for (int r = lane >> 4; r < rows; r += 2)
+                if (n < a.n)
+                    store1(a.out, (int64_t)(m0 + r) * a.out_stride + n, stage[16 * r + 4 * ((e >> 2) ^ ((r >> 1) & 3)) + (e & 3)], a.type);
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// Element n of `cols` rows from m0 on, from pairs. (Short code per element: a call of one tile runs it once, from memory.)
+template <class T, int N>
+__device__ __forceinline__ void store_columns(const MatmulArgs& a, int m0, int n, int cols, const uint64_t (&v)[N]) {
+    T* p = static_cast<T*>(a.out) + (int64_t)m0 * a.out_stride + n;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        if (2 * c >= cols) break;
+        const float2 x = ptx::f2(v[c]);
+        put(p, x.x);
+        p += a.out_stride;
+        if (2 * c + 1 < cols) put(p, x.y);
+        p += a.out_stride;
     }
 }
 
@@ -231,9 +277,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         if (!*abortp) *(volatile unsigned*)a.err = bit;
         abort_flag = 1;
     };
-    ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
-
     const int rank = T.splits > 1 ? (int)cluster_rank() : 0;
     const int kb0 = (int)((int64_t)T.kblocks * rank / T.splits), kb1 = (int)((int64_t)T.kblocks * (rank + 1) / T.splits);
     const int first = (int)blockIdx.x / T.splits, step = (int)gridDim.x / T.splits;
@@ -243,6 +286,15 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         ct = r / deep;
         lt = 16 * g + (r - ct * deep);
     };
+
+    // the weights may be what the kernel before writes, so before the wait they are only brought into L2
+    if (warp == F::kEpi && lane == 0 && first < T.total) {
+        int lt, ct;
+        place(first, lt, ct);
+        for (int kb = kb0; kb < min(kb1, kb0 + 2 * kStages); ++kb) prefetch_box(&map_lanes, kb * 128, lt * kLanes);
+    }
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
 
     if (warp >= F::kEpi) {
         if (warp == F::kEpi && lane == 0) {
@@ -395,15 +447,15 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                     }
                 }
                 cp_async_wait<0>();
+                const int cols = min(C, a.m - m0);
                 if (T.splits == 1) {
                     if (ok && lrow < a.n) {
-#pragma unroll
-                        for (int c = 0; c < C / 2; ++c) {
-                            const float2 v = ptx::f2(acc[c]);
-                            if (m0 + 2 * c < a.m) store1(a.out, (int64_t)(m0 + 2 * c) * a.out_stride + lrow, v.x, a.type);
-                            if (m0 + 2 * c + 1 < a.m)
-                                store1(a.out, (int64_t)(m0 + 2 * c + 1) * a.out_stride + lrow, v.y, a.type);
-                        }
+                        if (a.type == MOE_F32)
+                            store_columns<float>(a, m0, lrow, cols, acc);
+                        else if (a.type == MOE_BF16)
+                            store_columns<__nv_bfloat16>(a, m0, lrow, cols, acc);
+                        else
+                            store_columns<__half>(a, m0, lrow, cols, acc);
                     }
                     ptx::named_sync(1, 32 * F::kEpi);  // this tile's scales are read before the next tile's come
                 } else if (ok) {
@@ -411,6 +463,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                     float* part = reinterpret_cast<float*>(ring) + 32 * warp + lane;
 #pragma unroll
                     for (int c = 0; c < C / 2; ++c) {
+                        if (2 * c >= cols) break;
                         const float2 v = ptx::f2(acc[c]);
                         part[(2 * c) * kLanes] = v.x;
                         part[(2 * c + 1) * kLanes] = v.y;
@@ -426,15 +479,27 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
             int lt, ct;
             place(first, lt, ct);
             if (warp < F::kEpi && !*abortp) {
-                const int n = lt * kLanes + 32 * warp + lane, cols = min(C, a.m - ct * C);
-                const uint32_t at = ptx::smem_addr(ring) + 4 * (32 * warp + lane);
-                for (int c = rank; c < cols; c += T.splits) {
-                    float v[8];
+                // a warp a column, a lane four weights; the loads of two columns before the first sum, as a peer's memory is far
+                const int n = lt * kLanes + 4 * lane, cols = min(C, a.m - ct * C);
+                const uint32_t at = ptx::smem_addr(ring) + 16 * lane;
+                for (int j = warp; rank + T.splits * j < cols; j += 2 * F::kEpi) {
+                    float4 v[2][8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] = r < T.splits ? ld_peer(at + c * (kLanes * 4), r) : 0.0f;
+                    for (int d = 0; d < 2; ++d) {
+                        const int c = rank + T.splits * (j + F::kEpi * d);
 #pragma unroll
-                    for (int r = 1; r < 8; ++r) v[0] += v[r];
-                    if (n < a.n) store1(a.out, (int64_t)(ct * C + c) * a.out_stride + n, v[0], a.type);
+                        for (int r = 0; r < 8; ++r)
+                            v[d][r] = r < T.splits && c < cols ? ld_peer4(at + c * (kLanes * 4), r) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        const int c = rank + T.splits * (j + F::kEpi * d);
+                        if (c >= cols) break;
+                        float4 x = v[d][0];
+#pragma unroll
+                        for (int r = 1; r < 8; ++r) x.x += v[d][r].x, x.y += v[d][r].y, x.z += v[d][r].z, x.w += v[d][r].w;
+                        store4(a, (int64_t)(ct * C + c) * a.out_stride + n, x, a.n - n);
+                    }
                 }
             }
             __syncwarp();
@@ -461,9 +526,10 @@ struct Pair {
     static constexpr int kWarpLoad = kEpi, kWarpMma = kEpi + 1, kWarpScale = kEpi + 2;
     static constexpr int kThreads = 32 * (kEpi + 4);
     static constexpr int kStageBytes = 2 * kLaneBytes;
-    static constexpr int kStages = 6, kSlots = 4;  // a slot: the sums of a K-block and half of the weights
+    static constexpr int kStages = 5, kSlots = 4;  // a slot: the sums of a K-block and half of the weights
     static constexpr int kScaleBytes = kSlots * kCtaRows * 4;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + 256;
+    static constexpr int kOutBytes = kEpi * 2048;  // a warp's 32 rows x 16 sums, on their way to memory
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + kOutBytes + 256;
     // 640 threads x 96 registers at launch = 512 x 112 + 128 x 32
     static constexpr int kRegsEpi = 112, kRegsOther = 32;
     static_assert(kSmem <= 232448, "shared memory");
@@ -519,7 +585,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     unsigned char* ring =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     float* scales = reinterpret_cast<float*>(ring + kStages * F::kStageBytes);  // [kSlots][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * F::kStageBytes + F::kScaleBytes);  // first CTA's: both loaded
+    float* outs = reinterpret_cast<float*>(ring + kStages * F::kStageBytes + F::kScaleBytes);  // [kEpi][32][16]
+    uint64_t* full =
+        reinterpret_cast<uint64_t*>(ring + kStages * F::kStageBytes + F::kScaleBytes + F::kOutBytes);  // first CTA's: both loaded
     uint64_t* empty = full + kStages;
     uint64_t* acc_full = empty + kStages;        // sums and scales are there
     uint64_t* acc_empty = acc_full + kSlots;     // first CTA's: both have read their sums
@@ -747,10 +815,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
             if (ok) {
                 int lt, ct;
                 place(t, lt, ct);
-                const int m = lt * 256 + (int)rank * 128 + 32 * q + lane, n = ct * C + h * 128 + part * 64;
-                const bool wide =
-                    !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % (a.type == MOE_F32 ? 4 : 8) == 0;
-                if (m < a.m && n < a.n) store_row<64>(a.out, (int64_t)m * a.out_stride + n, acc, a.n - n, wide, a.type);
+                store_tile(a, outs + warp * 512, lt * 256 + (int)rank * 128 + 32 * q, ct * C + h * 128 + part * 64, acc);
             }
         }
     }
@@ -983,18 +1048,54 @@ cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, 
     return cfg;
 }
 
+// How many clusters of n CTAs of the weights form are resident at once (n = 1 .. 8). A cluster lies within a GPC, so
+// large ones leave SMs idle: of 304 places, clusters of 8 fill 288, of 7 266, of 6 276, of 5 290, of 4 296.
+template <class F>
+int resident_clusters(int n, int sms) {
+    static std::mutex mu;
+    static int device = -1, held[9];
+    std::lock_guard<std::mutex> lock(mu);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev != device) {
+        held[1] = sms * F::kCtas;
+        for (int i = 2; i <= 8; ++i) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg = cluster_config(8u * i, F::kThreads, F::kSmem, nullptr, (unsigned)i, attr);
+            if (cudaOccupancyMaxActiveClusters(&held[i], f8_matmul_kernel<F>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                held[i] = 0;
+            }
+        }
+        device = dev;
+    }
+    return held[n];
+}
+
+// CTAs that share a tile's K-blocks: as many as find room at once, at least two K-blocks each. Only where tiles leave
+// more than half of the SMs without one and there are some K-blocks to share, as joining the parts takes about 1 us. us for
+// 1, 2, 4 and (where they fit) 5, 6 or 8 CTAs: 32 rows, 22 tiles of 32 K-blocks 9.9 7.7 6.1 5.7; 48 tiles of 22: 8.4 8.1
+// 7.5 7.3 (6: 11.3, a second wave); 64 tiles of 64: 19.2 15.7 14.0; 128 tiles of 16: 9.0 9.4; 22 tiles of 6: 3.9 4.5.
+template <class F>
+int splits_of(const Tiles& T, int sms) {
+    if (2 * T.total > sms || T.kblocks < 8) return 1;
+    int s = std::min(8, T.kblocks / 2);
+    while (s > 1 && resident_clusters<F>(s, sms) < T.total) --s;
+    return s;
+}
+
 template <class F>
 cudaError_t launch_form(const MatmulArgs& a, int sms, cudaStream_t s) {
+    const cudaError_t e0 = ensure_smem_attr(reinterpret_cast<const void*>(f8_matmul_kernel<F>), F::kSmem);
+    if (e0 != cudaSuccess) return e0;
     Tiles T = tiles_of(a.n, a.m, kLanes, F::C, a.k);
-    const int room = sms * F::kCtas;
-    if (T.total < room) T.splits = std::max(1, std::min({8, room / T.total, T.kblocks / 2}));
+    T.splits = splits_of<F>(T, sms);
     CUtensorMap mw, ma;
     cudaError_t e = encode_codes(&mw, a.w, a.n, a.k, a.w_stride, kLanes);
     if (e == cudaSuccess) e = encode_codes(&ma, a.a, a.m, a.k, a.a_stride, F::C);
-    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_matmul_kernel<F>), F::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    const unsigned grid = T.splits > 1 ? (unsigned)(T.total * T.splits) : (unsigned)std::min(T.total, room);
+    const unsigned grid = T.splits > 1 ? (unsigned)(T.total * T.splits) : (unsigned)std::min(T.total, sms * F::kCtas);
     const cudaLaunchConfig_t cfg = cluster_config(grid, F::kThreads, F::kSmem, s, (unsigned)T.splits, attr);
     return cudaLaunchKernelEx(&cfg, f8_matmul_kernel<F>, a, T, mw, ma);
 }
@@ -1014,12 +1115,35 @@ cudaError_t launch_rows(const MatmulArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
+// us of a call in the weights form of 64 rows and in the rows form, by what they measured: a fixed part, and a time per
+// K-block of a tile (for two tiles on an SM at a time, which share its bandwidth, or one), for as many tiles as an SM gets.
+namespace {
+double weights_form_us(const MatmulArgs& a, int sms) {
+    using F = Form<64>;
+    const Tiles T = tiles_of(a.n, a.m, kLanes, F::C, a.k);
+    const int s = splits_of<F>(T, sms), each = (T.total + sms - 1) / sms;
+    if (s > 1) return 5.5 + 0.28 * ((T.kblocks + s - 1) / s);
+    return each == 1 ? 3.9 + 0.28 * T.kblocks : 3.5 + 0.46 * T.kblocks * ((each + 1) / 2);
+}
+double rows_form_us(const MatmulArgs& a, int sms) {
+    const Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
+    return 5.0 + 0.40 * T.kblocks * ((T.total + sms / 2 - 1) / (sms / 2));
+}
+}  // namespace
+
+// Measured, us (columns: mma.sync, weights form of 16 / 32 / 64 rows, rows form):
+//   8 rows:   6,144 x 2,816: 5.6 7.7; 2,816 x 704: 2.2 3.4; 20,000 x 512: 4.7 3.6; 16,384 x 2,048: 9.2 8.8; 640 x 8,192: 6.5 5.1
+//   16 rows:  1,024 x 1,024: 2.0 3.6; 2,816 x 704: 2.7 3.4; 2,816 x 4,096: 6.3 5.2; 6,144 x 2,816: 8.5 7.7
+//   64 rows (of 32, of 64, rows): 2,816 x 4,096: 7.6 6.9 15.5; 8,192 x 8,192: 19.2 18.4 25.5; 6,144 x 2,816: 8.4 9.6 12.6
+//   128 rows (of 64, rows): 6,144 x 2,816: 10.0 14.4; 512 of them: 23.4 15.1; 192 of 16,384 x 2,048: 18.5 13.6
+// mma.sync pays where each CTA's share is short: one round of CTAs, weights of up to 18 (9 to 16 rows: 6) million elements.
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
-    if (a.m <= 8) return launch_few<1>(a, sms, s);
-    if (a.m <= 16) return launch_few<2>(a, sms, s);
+    const int64_t weights = (int64_t)a.n * a.k, groups = (a.n + kFewLanes - 1) / kFewLanes;
+    if (a.m <= 8 && weights <= 18000000 && a.k <= 4096 && groups <= few_ctas(1) * sms) return launch_few<1>(a, sms, s);
+    if (a.m <= 16 && weights <= 6000000 && a.k <= 2048 && groups <= few_ctas(2) * sms) return launch_few<2>(a, sms, s);
+    if (a.m <= 16) return launch_form<Form<16>>(a, sms, s);
     if (a.m <= 32) return launch_form<Form<32>>(a, sms, s);
-    if (a.m <= 64) return launch_form<Form<64>>(a, sms, s);
-    if (a.m <= 256) return launch_form<Form<128>>(a, sms, s);
+    if (a.m <= 64 || weights_form_us(a, sms) <= rows_form_us(a, sms)) return launch_form<Form<64>>(a, sms, s);
     return launch_rows(a, sms, s);
 }
 

@@ -93,9 +93,29 @@ __device__ __forceinline__ float largest8(const float (&f)[8]) {
     return m;
 }
 
+// The largest magnitude of eight raw elements; 16-bit types by pairs.
+__device__ __forceinline__ float largest8(const Raw<4>& v, bool) {
+    float f[8];
+    v.get(f, false);
+    return largest8(f);
+}
+__device__ __forceinline__ float largest8(const Raw<2>& v, bool bf) {
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = v.w[i] & 0x7FFF7FFFu;
+    // (as magnitudes, halves compare like unsigned integers, and NaN above all)
+    const uint32_t p = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+    const uint32_t top = max(p & 0xFFFFu, p >> 16);
+    return bf ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+}
+
 // The scale of a block by its largest magnitude, and 1 / scale. An infinity or a NaN makes the whole block NaN.
+// The division by 448 is IEEE's: the product with 1 / 448 rounded to nearest is within an ulp of the quotient, and one
+// step with the remainder, exact in a fused multiply-add, rounds to it (Markstein's theorem).
 __device__ __forceinline__ float block_scale(float largest, float& inv) {
-    float s = __fdiv_rn(fmaxf(largest, kLeast), kE4m3Max);
+    constexpr float r = 1.0f / kE4m3Max;
+    const float top = fmaxf(largest, kLeast), t = top * r;
+    float s = fmaf(fmaf(t, -kE4m3Max, top), r, t);
     if (!(largest < __int_as_float(0x7F800000))) s = __int_as_float(0x7FC00000);
     inv = __frcp_rn(s);
     return s;
@@ -118,67 +138,79 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv)
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// One row: a thread holds V vectors of eight elements, vector i + v * G of the row for thread i of the row's G.
-// kCta: the row's threads are the CTA's; else G = 8, 16 or 32 lanes of a warp, `group` of them.
-template <int XB, int RB, int V, bool kCta>
+// Rows by groups of G threads, U rows a group, all loaded before the first is used: a thread holds V vectors of eight
+// elements of each, vector i + v * G for thread i. kCta: the group is the CTA; else G = 8, 16 or 32 lanes of a warp.
+template <int XB, int RB, int V, int U, bool kCta>
 __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a, const int group) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int G = kCta ? (int)blockDim.x : group;
     const unsigned per = kCta ? 1 : blockDim.x / (unsigned)group;
     const int i = kCta ? (int)threadIdx.x : (int)threadIdx.x & (G - 1);
-    const unsigned want = kCta ? blockIdx.x : blockIdx.x * per + threadIdx.x / (unsigned)G;
-    const bool live = want < a.rows;
-    const unsigned row = live ? want : 0;
-    const unsigned t = a.by_head.div(row), h = row - t * a.by_head.d;
+    const unsigned first = kCta ? blockIdx.x * U : blockIdx.x * (per * U) + threadIdx.x / (unsigned)G;
     const int nv = a.dim >> 3;
-    Raw<XB> x[V];
-    Raw<RB> r[V];
-    const int64_t xo = (int64_t)t * a.xt + (int64_t)h * a.xh, ro = (int64_t)t * a.rt + (int64_t)h * a.rh;
+    unsigned t[U], h[U];
+    bool live[U];
+    Raw<XB> x[U][V];
+    Raw<RB> r[U][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int j = i + v * G;
-        if (live && j < nv) {
-            x[v].load(a.x, xo + 8 * j);
-            r[v].load(a.res, ro + 8 * j);
-        } else {
-            x[v].zero();
-            r[v].zero();
+    for (int u = 0; u < U; ++u) {
+        const unsigned row = first + u * per;
+        live[u] = row < a.rows;
+        t[u] = a.by_head.div(live[u] ? row : 0);
+        h[u] = (live[u] ? row : 0) - t[u] * a.by_head.d;
+        const int64_t xo = (int64_t)t[u] * a.xt + (int64_t)h[u] * a.xh, ro = (int64_t)t[u] * a.rt + (int64_t)h[u] * a.rh;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int j = i + v * G;
+            if (live[u] && j < nv) {
+                x[u][v].load(a.x, xo + 8 * j);
+                r[u][v].load(a.res, ro + 8 * j);
+            } else {
+                x[u][v].zero();
+                r[u][v].zero();
+            }
         }
     }
-    float f[V][8];
-    float ss = 0.0f;
+    float f[U][V][8], ss[U];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        x[v].get(f[v], a.x_type == MOE_BF16);
-        if constexpr (RB != 0) {
-            float g[8];
-            r[v].get(g, a.res_type == MOE_BF16);
+    for (int u = 0; u < U; ++u) {
+        ss[u] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[v][e] += g[e];
+        for (int v = 0; v < V; ++v) {
+            x[u][v].get(f[u][v], a.x_type == MOE_BF16);
+            if constexpr (RB != 0) {
+                float g[8];
+                r[u][v].get(g, a.res_type == MOE_BF16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[u][v][e] += g[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss[u] = fmaf(f[u][v][e], f[u][v][e], ss[u]);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[v][e], f[v][e], ss);
     }
-    for (int m = (kCta ? 32 : G) >> 1; m; m >>= 1) ss += __shfl_xor_sync(kFull, ss, m);
+    for (int m = (kCta ? 32 : G) >> 1; m; m >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(kFull, ss[u], m);
     if constexpr (kCta) {
-        __shared__ float part[32];
+        __shared__ float part[U][32];
         const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        ss = lane < warps ? part[lane] : 0.0f;
+        if (lane == 0)
 #pragma unroll
-        for (int m = 16; m; m >>= 1) ss += __shfl_xor_sync(kFull, ss, m);
+            for (int u = 0; u < U; ++u) part[u][threadIdx.x >> 5] = ss[u];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ss[u] = lane < warps ? part[u][lane] : 0.0f;
+#pragma unroll
+            for (int m = 16; m; m >>= 1) ss[u] += __shfl_xor_sync(kFull, ss[u], m);
+        }
     }
-    const float k = rsqrtf(ss / (float)a.dim + a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int j = i + v * G;
-        const bool in = live && j < nv;
-        if constexpr (RB != 0)
-            if (a.sum && in) store8(a.sum, (int64_t)t * a.st + (int64_t)h * a.sh + 8 * j, f[v], a.res_type);
         float w[8];
-        if (a.weight && in) {
+        if (a.weight && j < nv) {
             if (a.weight_type == MOE_F32) {
                 Raw<4> q;
                 q.load(a.weight, 8 * j);
@@ -193,45 +225,57 @@ __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel
             for (int e = 0; e < 8; ++e) w[e] = 1.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[v][e] *= k * w[e];
-        if (a.out && in) store8(a.out, (int64_t)t * a.ot + (int64_t)h * a.oh + 8 * j, f[v], a.out_type);
-        if (a.codes) {  // a block is 16 neighbouring vectors, so 16 lanes of a warp (8 where a row has no more)
-            float top = largest8(f[v]);
-            for (int m = min(16, G) >> 1; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
-            float inv;
-            const float s = block_scale(top, inv);
-            if (in) {
-                *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.ct + 8 * j) = codes8(f[v], s, inv);
-                if ((j & 15) == 0) a.scales[(int64_t)(j >> 4) * a.scale_stride + t] = s;
+        for (int u = 0; u < U; ++u) {
+            const bool in = live[u] && j < nv;
+            float(&y)[8] = f[u][v];
+            if constexpr (RB != 0)
+                if (a.sum && in) store8(a.sum, (int64_t)t[u] * a.st + (int64_t)h[u] * a.sh + 8 * j, y, a.res_type);
+            const float k = rsqrtf(ss[u] / (float)a.dim + a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= k * w[e];
+            if (a.out && in) store8(a.out, (int64_t)t[u] * a.ot + (int64_t)h[u] * a.oh + 8 * j, y, a.out_type);
+            if (a.codes) {  // a block is 16 neighbouring vectors, so 16 lanes of a warp (8 where a row has no more)
+                float top = largest8(y);
+                for (int m = min(16, G) >> 1; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
+                float inv;
+                const float s = block_scale(top, inv);
+                if (in) {
+                    *reinterpret_cast<uint2*>(a.codes + (int64_t)t[u] * a.ct + 8 * j) = codes8(y, s, inv);
+                    if ((j & 15) == 0) a.scales[(int64_t)(j >> 4) * a.scale_stride + t[u]] = s;
+                }
             }
         }
     }
 }
 
-template <int XB, int RB, int V>
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
-    const int nv = a.dim >> 3;
+template <int XB, int RB, int V, int U, bool kCta>
+cudaError_t launch_norm(const NormArgs& a, unsigned threads, int group, cudaStream_t s) {
+    const unsigned per = (kCta ? 1 : threads / group) * U;
     cudaLaunchAttribute attr;
-    if (nv <= 32 * V && V == 1) {
-        const int G = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
-        const unsigned threads = 256, per = threads / G;
-        const cudaLaunchConfig_t cfg = launch_config(dim3((a.rows + per - 1) / per), dim3(threads), 0, s, true, &attr);
-        return cudaLaunchKernelEx(&cfg, norm_kernel<XB, RB, 1, false>, a, G);
-    }
-    const unsigned threads = (unsigned)((nv + V - 1) / V + 31) / 32 * 32;
-    const cudaLaunchConfig_t cfg = launch_config(dim3(a.rows), dim3(threads), 0, s, true, &attr);
-    return cudaLaunchKernelEx(&cfg, norm_kernel<XB, RB, V, true>, a, 0);
+    const cudaLaunchConfig_t cfg = launch_config(dim3((a.rows + per - 1) / per), dim3(threads), 0, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, norm_kernel<XB, RB, V, U, kCta>, a, group);
 }
 
 template <int XB, int RB>
-cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_norm_of(const NormArgs& a, int sms, cudaStream_t s) {
     const int nv = a.dim >> 3;
-    return nv <= 512 ? launch_norm<XB, RB, 1>(a, s) : nv <= 1024 ? launch_norm<XB, RB, 2>(a, s) : launch_norm<XB, RB, 4>(a, s);
+    // several rows a group once there are enough of them to fill every SM's threads all the same
+    const bool many = (uint64_t)a.rows * nv >= (uint64_t)sms * 2048 * 2;
+    if (nv <= 32) {
+        const int G = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+        return many ? launch_norm<XB, RB, 1, 2, false>(a, 256, G, s) : launch_norm<XB, RB, 1, 1, false>(a, 256, G, s);
+    }
+    if (nv <= 64) return many ? launch_norm<XB, RB, 2, 2, false>(a, 256, 32, s) : launch_norm<XB, RB, 2, 1, false>(a, 256, 32, s);
+    if (nv <= 128 && many) return launch_norm<XB, RB, 4, 1, false>(a, 256, 32, s);
+    const unsigned v = nv <= 512 ? 1 : nv <= 1024 ? 2 : 4, threads = (unsigned)((nv + v - 1) / v + 31) / 32 * 32;
+    if (v == 1) return many ? launch_norm<XB, RB, 1, 2, true>(a, threads, 0, s) : launch_norm<XB, RB, 1, 1, true>(a, threads, 0, s);
+    return v == 2 ? launch_norm<XB, RB, 2, 1, true>(a, threads, 0, s) : launch_norm<XB, RB, 4, 1, true>(a, threads, 0, s);
 }
 
 template <int XB>
-cudaError_t launch_norm_of(const NormArgs& a, cudaStream_t s) {
-    return !a.res ? launch_norm_of<XB, 0>(a, s) : a.res_type == MOE_F32 ? launch_norm_of<XB, 4>(a, s) : launch_norm_of<XB, 2>(a, s);
+cudaError_t launch_norm_of(const NormArgs& a, int sms, cudaStream_t s) {
+    return !a.res ? launch_norm_of<XB, 0>(a, sms, s)
+                  : a.res_type == MOE_F32 ? launch_norm_of<XB, 4>(a, sms, s) : launch_norm_of<XB, 2>(a, sms, s);
 }
 
 // Rows to codes: 16 lanes a block, eight elements each. V vectors a thread, a CTA's threads apart.
@@ -257,14 +301,14 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float f[8];
-        x[v].get(f, a.type == MOE_BF16);
-        float top = largest8(f);
+        float top = largest8(x[v], a.type == MOE_BF16);
 #pragma unroll
         for (int m = 8; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
         float inv;
         const float s = block_scale(top, inv);
         if (!in[v]) continue;
+        float f[8];
+        x[v].get(f, a.type == MOE_BF16);
         *reinterpret_cast<uint2*>(a.codes + (int64_t)row[v] * a.code_stride + 8 * vec[v]) = codes8(f, s, inv);
         if ((vec[v] & 15) == 0) a.scales[(int64_t)(vec[v] >> 4) * a.scale_stride + row[v]] = s;
     }
@@ -287,11 +331,7 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const __grid_constant
     }
     float top = 0.0f;
 #pragma unroll
-    for (int v = 0; v < 8; ++v) {
-        float f[8];
-        x[v].get(f, a.type == MOE_BF16);
-        top = max_nan(top, largest8(f));
-    }
+    for (int v = 0; v < 8; ++v) top = max_nan(top, largest8(x[v], a.type == MOE_BF16));
 #pragma unroll
     for (int m = 16; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
     __shared__ float part[8];
@@ -321,8 +361,8 @@ cudaError_t launch_quant_rows(const QuantArgs& a, uint64_t vecs, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
-    return a.x_type == MOE_F32 ? launch_norm_of<4>(a, s) : launch_norm_of<2>(a, s);
+cudaError_t launch_rms_norm(const NormArgs& a, int sms, cudaStream_t s) {
+    return a.x_type == MOE_F32 ? launch_norm_of<4>(a, sms, s) : launch_norm_of<2>(a, sms, s);
 }
 
 cudaError_t launch_f8_quant_rows(const QuantArgs& a0, int sms, cudaStream_t s) {
