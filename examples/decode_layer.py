@@ -1,9 +1,10 @@
 """One decoder layer over a 4-bit key/value cache: a prompt, then decode steps.
 
 Attention (query, key and value projections, the cache, the output projection) runs
-beside the MoE layer: moe_kv_append puts the new tokens' keys and values into the
-cache, moe_kv_attend attends over it, moe_forward_prompt / moe_forward run the experts. Weights and
-tokens are random, from a seed; the projections are plain matrix products.
+beside the MoE layer: moe_rms_norm adds what came before to the residual and norms the sum, into
+8 bits for the projections (moe_f8_matmul) or bf16 for the experts; moe_kv_append puts the new tokens' keys and
+values into the cache, moe_kv_attend attends over it, moe_f8_quant_rows takes its output to the output projection, and
+moe_forward_prompt / moe_forward run the experts. Weights and tokens are random, from a seed.
 
     python examples/decode_layer.py [--prompt 300] [--steps 16] [--sequences 2]
 
@@ -34,8 +35,8 @@ class Attention:
         self.heads = d_model // head_dim
         self.kv_heads = max(1, self.heads // group)
         rows = (self.heads + 2 * self.kv_heads) * head_dim
-        self.w_in = (torch.randn((d_model, rows), generator=g, device="cuda") * d_model ** -0.5).bfloat16()
-        self.w_out = (torch.randn((self.heads * head_dim, d_model), generator=g, device="cuda") * d_model ** -0.5).bfloat16()
+        self.w_in, self.w_out = (moe.moe_f8_quant_weight(ctx, torch.randn(shape, generator=g, device="cuda") * d_model ** -0.5)
+                                 for shape in ((rows, d_model), (d_model, self.heads * head_dim)))
         per = -(-max_tokens // PAGE)
         self.cache = moe.moe_kv_new_cache(sequences * per, self.kv_heads, head_dim, PAGE)
         # pages as an allocator might deal them out
@@ -43,10 +44,11 @@ class Attention:
         self.length = torch.zeros(sequences, dtype=torch.int32, device="cuda")
         self.worst = 0.0
 
-    def __call__(self, x, check=False):
-        """x [sequences][new tokens][d_model] bf16: the block's output, added to nothing."""
-        B, T, _ = x.shape
-        qkv = (x.flatten(0, 1) @ self.w_in).unflatten(1, (-1, self.dim))
+    def __call__(self, codes, scales, check=False):
+        """The normed rows [sequences * new tokens][d_model] in 8 bits: the block's output, fp32, added to nothing."""
+        B = self.table.shape[0]
+        T = codes.shape[0] // B
+        qkv = moe.moe_f8_matmul(self.ctx, codes, scales, *self.w_in).unflatten(1, (-1, self.dim))
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), 1)
         pos = (self.length[:, None] + torch.arange(T, device="cuda")).long()
         slots = torch.gather(self.table, 1, pos // PAGE) * PAGE + pos % PAGE
@@ -55,7 +57,7 @@ class Attention:
         out = moe.moe_kv_attend(self.ctx, self.cache, q, self.table, self.length)
         if check:
             self.worst = max(self.worst, self.difference(q.unflatten(0, (B, T)), out.unflatten(0, (B, T))))
-        return (out.flatten(1) @ self.w_out).view(B, T, -1)
+        return moe.moe_f8_matmul(self.ctx, *moe.moe_f8_quant_rows(self.ctx, out.flatten(1)), *self.w_out, dtype=torch.float32)
 
     def difference(self, q, out):
         """Largest difference from fp32 attention over the values read back."""
@@ -70,10 +72,6 @@ class Attention:
             want = torch.einsum("hij,jhd->ihd", s.softmax(-1), v)
             worst = max(worst, (out[b].float() - want).abs().max().item())
         return worst
-
-
-def norm(x):
-    return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True))).bfloat16()
 
 
 def main(argv=None):
@@ -91,18 +89,21 @@ def main(argv=None):
         def run(prompt, steps, check):
             attention = Attention(ctx, s.d_model, a.sequences, prompt + steps, seed=0)
             g = torch.Generator(device="cuda").manual_seed(1)
-            x = torch.randn((a.sequences, prompt, s.d_model), generator=g, device="cuda").bfloat16()
+            x = torch.randn((a.sequences * prompt, s.d_model), generator=g, device="cuda").bfloat16()
+            weights = [1 + 0.1 * torch.randn((s.d_model,), generator=g, device="cuda") for _ in range(2)]
+            _, _, codes, scales = moe.moe_rms_norm(ctx, x, weights[0], dtype=None, f8=True)
             times = []
             for step in range(steps + 1):
                 torch.cuda.synchronize()
                 t = time.perf_counter()
-                x = x + attention(norm(x), check and step in (0, steps))
-                y = norm(x).flatten(0, 1).contiguous()
-                ffn = moe.moe_forward_prompt if y.shape[0] > 64 else moe.moe_forward
-                x = x + ffn(layer, y).view(x.shape).bfloat16()
+                o = attention(codes, scales, check and step in (0, steps))
+                y, x, _, _ = moe.moe_rms_norm(ctx, o, weights[1], residual=x, dtype=torch.bfloat16)
+                ffn = (moe.moe_forward_prompt if y.shape[0] > 64 else moe.moe_forward)(layer, y)
+                # the next tokens: what the last ones became
+                last = slice(x.shape[0] // a.sequences - 1, None, x.shape[0] // a.sequences)
+                _, x, codes, scales = moe.moe_rms_norm(ctx, ffn[last], weights[0], residual=x[last], dtype=None, f8=True)
                 torch.cuda.synchronize()
                 times.append(time.perf_counter() - t)
-                x = x[:, -1:]  # the next token: what the last one became
             return attention, x, times
 
         run(a.prompt, min(2, a.steps), False)  # libraries load, workspaces grow

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         for (int kb = kb0; kb < min(kb1, kb0 + 2 * kStages); ++kb) prefetch_box(&map_lanes, kb * 128, lt * kLanes);
     }
     ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
+    if (a.early) ptx::pdl_launch_dependents();
 
     if (warp >= F::kEpi) {
         if (warp == F::kEpi && lane == 0) {
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         abort_flag = 1;
     };
     ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
+    if (a.early) ptx::pdl_launch_dependents();
 
     const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1, kblocks = T.kblocks;
     // neighbouring tiles go along the rows, 8 deep, so that tiles of one time share both operands in L2
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.w + n * a.w_stride), "r"(min(a.k, 16384)) : "memory");
     }
     ptx::pdl_wait();
-    ptx::pdl_launch_dependents();
+    if (a.early) ptx::pdl_launch_dependents();
     const uint8_t* ap[NT];
     bool ain[NT];
 #pragma unroll

@@ -414,3 +414,46 @@ def test_profiling_counts_the_calls(ctx):
         assert t["f8_matmul"][3] == 2 * 4 * 4 * 256
     finally:
         moe.moe_ctx_set_profiling(ctx, False)
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 100])
+@pytest.mark.parametrize("source", ["out", "sum", "product"])
+def test_rows_go_straight_into_the_experts(ctx, tokens, source):
+    """moe_forward right behind the call that writes its x, nothing in between: it reads these rows, not the ones before."""
+    import synth
+
+    s = synth.SHAPES_TINY
+    layer = moe.moe_layer_create(ctx, s, 4, moe.LFU)
+    try:
+        moe.moe_layer_set_weights(layer, synth.layer_weights(s, 0))
+        moe.moe_layer_set_deterministic(layer, True)
+        g = rng(tokens)
+        x = torch.zeros((tokens, s.d_model), dtype=torch.bfloat16, device="cuda")
+        w = moe.moe_f8_quant_weight(ctx, randn(g, s.d_model, 4096) * 4096 ** -0.5)
+        rows = [randn(g, tokens, s.d_model) for _ in range(24)]
+        zero = torch.zeros_like(x)
+        wide_rows = [moe.moe_f8_quant_rows(ctx, randn(g, tokens, 4096)) for _ in range(24)]
+        noise = torch.empty((1 << 22,), device="cuda")
+
+        def write(i):
+            if source == "out":
+                moe.moe_rms_norm(ctx, rows[i], out=x)
+            elif source == "sum":
+                moe.moe_rms_norm(ctx, rows[i], residual=zero, sum=x, dtype=None, f8=True)
+            else:
+                moe.moe_f8_matmul(ctx, *wide_rows[i], *w, out=x)
+
+        want, got = [], []
+        for i in range(24):
+            write(i)
+            torch.cuda.synchronize()
+            want.append(moe.moe_forward(layer, x).clone())
+            torch.cuda.synchronize()
+        for i in range(24):
+            noise.normal_()  # the device is behind the host, so that the calls queue up
+            write(i)
+            got.append(moe.moe_forward(layer, x))
+        torch.cuda.synchronize()
+        assert all((a == b).all() for a, b in zip(want, got))
+    finally:
+        moe.moe_layer_destroy(layer)
