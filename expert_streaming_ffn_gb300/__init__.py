@@ -761,20 +761,24 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
     given; None: no such output), sum = h of the residual's type (None without one), and with f8 the e4m3 codes
     [n][d] and f32 scales [ceil(d / 128)][n] of the same rows (None, None without). Outputs given are filled."""
     torch = _torch or _kv_torch()
-    shape = x.shape
+    shape, st = x.shape, x.stride()
     device = _cuda(x, "x")
-    if len(shape) == 3:
+    if len(st) == 3:
         n, heads, d = shape
         ht, tt = d, heads * d  # strides of a new tensor
-    elif len(shape) == 2:
+        xt, xh = st[0] if n > 1 else 0, st[1] if heads > 1 else 0
+    elif len(st) == 2:
         n, d = shape
         heads, ht, tt = 1, 0, d
+        xt, xh = st[0] if n > 1 else 0, 0
     else:
         raise ValueError("x: expected [n][d] or [n][heads][d]")
-    xp, xt, xh = _rows3(x, "x", shape, device)
+    if st[-1] != 1:
+        raise ValueError("x: the last dimension must be contiguous")
+    xp = x.data_ptr()
     rp = rt = rh = rd = sp = st = sh = wp = wd = op = ot = oh = od = cp = ct = lp = lt = 0
     if weight is not None:
-        if weight.shape != shape[-1:] or weight.get_device() != device or (d > 1 and weight.stride(0) != 1):
+        if weight.numel() != d or weight.dim() != 1 or weight.get_device() != device or (d > 1 and weight.stride(0) != 1):
             raise ValueError(f"weight: expected [{d}], contiguous, on CUDA device {device}")
         wp, wd = weight.data_ptr(), _kv_type(weight.dtype)
     if residual is not None:
@@ -827,7 +831,12 @@ def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
     if len(shape) != 2:
         raise ValueError("x: expected [n][k]")
     n, k = shape
-    xp, xt, _ = _rows3(x, "x", shape, device)
+    xt, xe = x.stride()
+    if xe != 1:
+        raise ValueError("x: the last dimension must be contiguous")
+    if n < 2:
+        xt = 0
+    xp = x.data_ptr()
     of_scales = ((n + 127) // 128 if weight else (k + 127) // 128, (k + 127) // 128 if weight else n)
     if codes is None:
         codes = _dense_new((n, k), torch.float8_e4m3fn, device, stream)
@@ -858,10 +867,11 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
     give them: out [m][n] of dtype (bf16 unless given)."""
     torch = _torch or _kv_torch()
     device = _cuda(a, "a")
-    if a.dim() != 2 or w.dim() != 2:
+    of_a, of_w = a.shape, w.shape
+    if len(of_a) != 2 or len(of_w) != 2:
         raise ValueError("a and w: expected [m][k] and [n][k]")
-    m, k = a.shape
-    n, kb = w.shape[0], (k + 127) // 128
+    m, k = of_a
+    n, kb = of_w[0], (k + 127) // 128
     ap, at = _codes(a, "a", (m, k), device)
     wp, wt = _codes(w, "w", (n, k), device)
     asp, ast = _scales(a_scales, "a_scales", (kb, m), device)

@@ -144,7 +144,7 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
     if (p->m < 0 || p->n < 1 || p->k < 16 || p->k % 16 || p->k > 1 << 30)
         return set_error(MOE_EINVAL, "%s: m = %d, n = %d, k = %d (k a multiple of 16, 16 to 2^30)", who, p->m, p->n, p->k);
     if (p->m == 0) return MOE_OK;
-    if ((int64_t)blocks(p->m) * blocks(p->n) >= (int64_t)1 << 30)
+    if ((int64_t)blocks(p->m) * blocks(p->n) >= (int64_t)1 << 29)
         return set_error(MOE_EINVAL, "%s: m = %d by n = %d is too large", who, p->m, p->n);
     if (!p->a || !p->a_scales || !p->w || !p->w_scales || !p->out) return set_error(MOE_EINVAL, "%s: NULL argument", who);
     if (!at16(p->a) || p->a_stride % 16 || !at16(p->w) || p->w_stride % 16)

@@ -429,10 +429,11 @@ def test_rows_go_straight_into_the_experts(ctx, tokens, source):
         moe.moe_layer_set_deterministic(layer, True)
         g = rng(tokens)
         x = torch.zeros((tokens, s.d_model), dtype=torch.bfloat16, device="cuda")
-        w = moe.moe_f8_quant_weight(ctx, randn(g, s.d_model, 4096) * 4096 ** -0.5)
+        k = 65536  # a product that takes its time
+        w = moe.moe_f8_quant_weight(ctx, randn(g, s.d_model, k) * k ** -0.5)
         rows = [randn(g, tokens, s.d_model) for _ in range(24)]
         zero = torch.zeros_like(x)
-        wide_rows = [moe.moe_f8_quant_rows(ctx, randn(g, tokens, 4096)) for _ in range(24)]
+        wide_rows = [moe.moe_f8_quant_rows(ctx, randn(g, tokens, k)) for _ in range(24)]
         noise = torch.empty((1 << 22,), device="cuda")
 
         def write(i):
@@ -457,3 +458,93 @@ def test_rows_go_straight_into_the_experts(ctx, tokens, source):
         assert all((a == b).all() for a, b in zip(want, got))
     finally:
         moe.moe_layer_destroy(layer)
+
+
+FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import expert_streaming_ffn_gb300 as moe
+ctx = moe.moe_ctx_create(0)
+a = torch.randn(({m}, 1024), device="cuda")
+w = torch.randn((700, 1024), device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    _, _, c, s = moe.moe_rms_norm(ctx, a, dtype=None, f8=True)
+    q = moe.moe_f8_quant_weight(ctx, w)
+    out = moe.moe_f8_matmul(ctx, c, s, *q, dtype=torch.float32)
+graph.replay()
+torch.cuda.synchronize()
+n = torch.nn.functional.rms_norm(a, (1024,), eps=1e-6) @ w.t()
+print(((out - n).norm() / n.norm()).item())
+"""
+
+
+@pytest.mark.parametrize("m", [4, 24, 700])
+def test_first_calls_of_a_process_can_be_captured(m):
+    """The first call of each kind looks a few things up and allocates nothing, so it may be part of a graph. 8 bits a side: each
+    operand within 2^-4 of itself, so the product's relative error in the 2-norm is below 2 * 2^-4."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, m=m)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert float(r.stdout.split()[-1]) < 2 * 2.0 ** -4
+
+
+def test_calls_from_several_threads(ctx):
+    """Host threads with a stream each, the same context: the same bits as one after the other."""
+    import threading
+
+    p = params(ctx, 512, 1024, 3)
+    shapes = [1, 20, 50, 90, 300]
+    x = [randn(rng(i), n, 512) for i, n in enumerate(shapes)]
+    res = [randn(rng(30 + i), n, 512).bfloat16() for i, n in enumerate(shapes)]
+    want = []
+    for i in range(len(shapes)):
+        r = res[i].clone()
+        want.append(layer(ctx, p, x[i], r)[-1])
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in shapes], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    r = res[i].clone()
+                    got[i].append(layer(ctx, p, x[i], r)[-1])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert all((y == want[i]).all() for i in range(len(shapes)) for y in got[i])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_offsets_past_32_bits(ctx, dtype):
+    """Rows whose elements lie beyond 2^31 of each other: norm, quantisation and product by strides."""
+    stride = (1 << 31) // 2 + 4096 if dtype == "f32" else (1 << 31) + 4096
+    n, d = 3, 256
+    if (n - 1) * stride * (4 if dtype == "f32" else 2) > 40 << 30:
+        pytest.skip("no room")
+    x = torch.empty(((n - 1) * stride + d,), dtype=T[dtype], device="cuda").as_strided((n, d), (stride, 1))
+    x.copy_(randn(rng(8), n, d))
+    small = x.contiguous()
+    out, _, c, s = moe.moe_rms_norm(ctx, x, out=x, f8=True)
+    want, _, cw, sw = moe.moe_rms_norm(ctx, small, f8=True)
+    assert (x == want).all() and (c.float() == cw.float()).all() and (s == sw).all()
+    c1, s1 = moe.moe_f8_quant_rows(ctx, x)
+    c2, s2 = moe.moe_f8_quant_rows(ctx, want)
+    assert (c1.float() == c2.float()).all() and (s1 == s2).all()
+    w = moe.moe_f8_quant_weight(ctx, randn(rng(9), 500, d))
+    y = torch.empty(((n - 1) * stride + 500,), dtype=T[dtype], device="cuda").as_strided((n, 500), (stride, 1))
+    moe.moe_f8_matmul(ctx, c1, s1, *w, out=y)
+    assert (y == moe.moe_f8_matmul(ctx, c1, s1, *w, dtype=T[dtype])).all()
