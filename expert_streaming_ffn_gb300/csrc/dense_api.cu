@@ -110,6 +110,7 @@ extern "C" moe_status moe_rms_norm(moe_ctx* C, const moe_norm_args* p, void* str
     a.rows = (unsigned)p->n_tokens * (unsigned)p->n_heads;
     a.dim = p->dim;
     a.eps = p->eps;
+    a.inv_dim = 1.0f / (float)p->dim;
     a.by_head = FastDiv((uint32_t)p->n_heads);
     a.x_type = p->x_dtype, a.res_type = p->residual_dtype, a.weight_type = p->weight_dtype, a.out_type = p->out_dtype;
     a.early = may_release_early(p->sum != nullptr, p->residual_dtype) && may_release_early(p->out != nullptr, p->out_dtype);

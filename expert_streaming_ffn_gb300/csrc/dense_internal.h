@@ -26,7 +26,7 @@ struct NormArgs {
     int64_t ct, scale_stride;
     unsigned rows;  // tokens * heads
     int dim;
-    float eps;
+    float eps, inv_dim;
     FastDiv by_head{1};
     moe_dtype x_type, res_type, weight_type, out_type;  // sum has res_type
     bool early;  // may_release_early()

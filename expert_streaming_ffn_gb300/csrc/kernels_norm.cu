@@ -31,23 +31,17 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < 2 * B; ++i) w[i] = 0;
     }
-    // the values; `bf` tells the 16-bit types apart
-    __device__ __forceinline__ void get(float (&f)[8], bool bf) const {
-        if constexpr (B == 4) {
+    // the values, by pairs; `bf` tells the 16-bit types apart
+    __device__ __forceinline__ void get(uint64_t (&f)[4], bool bf) const {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-        } else if (bf) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (B == 4) {
+                f[i] = ptx::f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            } else if (bf) {
+                f[i] = ptx::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            } else {
                 const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                f[2 * i] = v.x;
-                f[2 * i + 1] = v.y;
+                f[i] = ptx::f2(v.x, v.y);
             }
         }
     }
@@ -59,21 +53,22 @@ struct Raw<0> {
 };
 
 // Eight values to memory, rounded once to the type.
-__device__ __forceinline__ void store8(void* base, int64_t at, const float (&f)[8], moe_dtype t) {
+__device__ __forceinline__ void store8(void* base, int64_t at, const uint64_t (&f)[4], moe_dtype t) {
     if (t == MOE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        ulonglong2* p = reinterpret_cast<ulonglong2*>(static_cast<float*>(base) + at);
+        p[0] = make_ulonglong2(f[0], f[1]);
+        p[1] = make_ulonglong2(f[2], f[3]);
         return;
     }
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const float2 v = ptx::f2(f[i]);
         if (t == MOE_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            const __half2 h = __floats2half2_rn(v.x, v.y);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
@@ -86,16 +81,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ float largest8(const float (&f)[8]) {
-    float m = fabsf(f[0]);
+__device__ __forceinline__ float largest8(const uint64_t (&f)[4]) {
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = ptx::f2(f[i]);
+        m = max_nan(m, max_nan(fabsf(v.x), fabsf(v.y)));
+    }
     return m;
 }
-
-// The largest magnitude of eight raw elements; 16-bit types by pairs.
+// Of raw elements; 16-bit types by pairs.
 __device__ __forceinline__ float largest8(const Raw<4>& v, bool) {
-    float f[8];
+    uint64_t f[4];
     v.get(f, false);
     return largest8(f);
 }
@@ -111,26 +108,30 @@ __device__ __forceinline__ float largest8(const Raw<2>& v, bool bf) {
 
 // The scale of a block by its largest magnitude, and 1 / scale. An infinity or a NaN makes the whole block NaN.
 // The division by 448 is IEEE's: the product with 1 / 448 rounded to nearest is within an ulp of the quotient, and one
-// step with the remainder, exact in a fused multiply-add, rounds to it (Markstein's theorem).
+// step with the remainder, exact in a fused multiply-add, rounds to it (Markstein's theorem). 1 / scale is the
+// approximation's after a Newton step, within an ulp.
 __device__ __forceinline__ float block_scale(float largest, float& inv) {
     constexpr float r = 1.0f / kE4m3Max;
     const float top = fmaxf(largest, kLeast), t = top * r;
     float s = fmaf(fmaf(t, -kE4m3Max, top), r, t);
     if (!(largest < __int_as_float(0x7F800000))) s = __int_as_float(0x7FC00000);
-    inv = __frcp_rn(s);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    inv = fmaf(fmaf(-s, y, 1.0f), y, y);
     return s;
 }
 
-// Eight values to codes, the nearest to f / s. The quotient is IEEE's but for rare divisors (all ones): t = f y with
-// y = 1 / s rounded to nearest is within an ulp of it, and t + y (f - s t), the remainder exact in a fused multiply-add,
-// rounds to it (Markstein's theorem). A plain product f y would move quotients that are ties, and 16-bit inputs have many.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv) {
+// Eight values to codes, the nearest to f / s. t = f y with y = 1 / s is within two ulps of the quotient, and in
+// t + y (f - s t) the remainder is exact in a fused multiply-add, so that the sum before its rounding is within 2^-21 ulp of
+// the quotient: ties between codes, which are short numbers, come out as such. A plain product f y would move them, and
+// 16-bit inputs have many.
+__device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], float s, float inv) {
     uint32_t h[4];
     const uint64_t yy = ptx::f2(inv, inv), ns = ptx::f2(-s, -s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t x = ptx::f2(f[2 * i], f[2 * i + 1]), t = ptx::mul2(x, yy);
-        const float2 q = ptx::f2(ptx::fma2(ptx::fma2(t, ns, x), yy, t));
+        const uint64_t t = ptx::mul2(f[i], yy);
+        const float2 q = ptx::f2(ptx::fma2(ptx::fma2(t, ns, f[i]), yy, t));
         uint16_t c;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(q.y), "f"(q.x));
         h[i] = c;
@@ -172,22 +173,25 @@ __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel
             }
         }
     }
-    float f[U][V][8], ss[U];
+    uint64_t f[U][V][4];
+    float ss[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        ss[u] = 0.0f;
+        uint64_t sum = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             x[u][v].get(f[u][v], a.x_type == MOE_BF16);
             if constexpr (RB != 0) {
-                float g[8];
+                uint64_t g[4];
                 r[u][v].get(g, a.res_type == MOE_BF16);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[u][v][e] += g[e];
+                for (int e = 0; e < 4; ++e) f[u][v][e] = ptx::add2(f[u][v][e], g[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss[u] = fmaf(f[u][v][e], f[u][v][e], ss[u]);
+            for (int e = 0; e < 4; ++e) sum = ptx::fma2(f[u][v][e], f[u][v][e], sum);
         }
+        const float2 two = ptx::f2(sum);
+        ss[u] = two.x + two.y;
     }
     for (int m = (kCta ? 32 : G) >> 1; m; m >>= 1)
 #pragma unroll
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int j = i + v * G;
-        float w[8];
+        uint64_t w[4] = {};
         if (a.weight && j < nv) {
             if (a.weight_type == MOE_F32) {
                 Raw<4> q;
@@ -220,19 +224,19 @@ __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel
                 q.load(a.weight, 8 * j);
                 q.get(w, a.weight_type == MOE_BF16);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = live[u] && j < nv;
-            float(&y)[8] = f[u][v];
+            uint64_t(&y)[4] = f[u][v];
             if constexpr (RB != 0)
                 if (a.sum && in) store8(a.sum, (int64_t)t[u] * a.st + (int64_t)h[u] * a.sh + 8 * j, y, a.res_type);
-            const float k = rsqrtf(ss[u] / (float)a.dim + a.eps);
+            const float k = rsqrtf(fmaf(ss[u], a.inv_dim, a.eps));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= k * w[e];
+            for (int e = 0; e < 4; ++e) y[e] = ptx::mul2(y[e], ptx::f2(k, k));
+            if (a.weight)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = ptx::mul2(y[e], w[e]);
             if (a.out && in) store8(a.out, (int64_t)t[u] * a.ot + (int64_t)h[u] * a.oh + 8 * j, y, a.out_type);
             if (a.codes) {  // a block is 16 neighbouring vectors, so 16 lanes of a warp (8 where a row has no more)
                 float top = largest8(y);
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
         float inv;
         const float s = block_scale(top, inv);
         if (!in[v]) continue;
-        float f[8];
+        uint64_t f[4];
         x[v].get(f, a.type == MOE_BF16);
         *reinterpret_cast<uint2*>(a.codes + (int64_t)row[v] * a.code_stride + 8 * vec[v]) = codes8(f, s, inv);
         if ((vec[v] & 15) == 0) a.scales[(int64_t)(vec[v] >> 4) * a.scale_stride + row[v]] = s;
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const __grid_constant
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
         if (r0 + 16 * v >= a.n || col >= a.dim) continue;
-        float f[8];
+        uint64_t f[4];
         x[v].get(f, a.type == MOE_BF16);
         *reinterpret_cast<uint2*>(a.codes + (int64_t)(r0 + 16 * v) * a.code_stride + col) = codes8(f, s, inv);
     }
