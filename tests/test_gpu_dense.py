@@ -2,8 +2,9 @@
 
 Bounds (u = 2^-24, half a step of fp32):
 * norm: h = x + r is off by u of itself; the sum of dim squares is in order within a thread (at most 32 of them) and in a
-  tree across threads (at most 10 steps), so off by 43 u of itself, its root by 22 u; rsqrtf by 4 u (2 ulp), the division,
-  the addition of eps and the two products by u each: 32 u of |y| in all, and half a step of the output's type.
+  tree across threads (at most 10 steps), so off by 43 u of itself, its root by 22 u; rsqrtf by 4 u (2 ulp), the factor
+  1 / dim, its product and the addition of eps by u each under the root, and two products: 32 u of |y| in all, and half
+  a step of the output's type.
 * quantised y: half a step of e4m3, 2^-4 of the value or, among subnormal codes, 2^-10 of the scale, besides the error of y.
 * matrix product: a K-block's 128 products are exact and summed in fp32 in any order, whichever way a step rounds (2 u each):
   256 u of the sum of their magnitudes; its two scales' product and the addition to the K-blocks before, u each.
@@ -102,6 +103,20 @@ def test_norm(ctx, n, heads, dim, xt, rt, wt, ot):
     check_norm(x, w, 1e-5, r, got)
 
 
+@pytest.mark.parametrize("n,heads,dim", [(81000, 1, 64), (2601, 16, 128), (20001, 1, 256), (19000, 1, 272), (10007, 1, 512), (5003, 1, 1008),
+                                         (5000, 1, 1024), (3001, 1, 2816), (1301, 1, 4096), (1000, 1, 5008), (700, 1, 8192), (400, 1, 16400)])
+@pytest.mark.parametrize("xt,rt,wt,ot", [("f32", "bf16", "bf16", "bf16"), ("f16", None, "f32", "f32"), ("bf16", "f32", None, None)])
+def test_norm_of_many_rows(ctx, n, heads, dim, xt, rt, wt, ot):
+    """Rows enough that each thread takes several vectors, or rows, at a time."""
+    g = rng(n)
+    x = (randn(g, n, heads, dim) * torch.exp(randn(g, dim))).to(T[xt])
+    r = randn(g, n, heads, dim).to(T[rt]) if rt else None
+    w = (1 + 0.3 * randn(g, dim)).to(T[wt]) if wt else None
+    if ot is None and heads > 1:
+        ot = "f16"
+    check_norm(x, w, 1e-5, r, moe.moe_rms_norm(ctx, x, w, 1e-5, residual=r, dtype=T.get(ot), f8=heads == 1))
+
+
 def test_norm_rows_of_wider_tensors_in_place(ctx):
     """Heads of a fused projection, normed where they lie; the residual's sum over the residual; what lies beside stays."""
     g = rng(1)
@@ -178,7 +193,7 @@ def quant_ref(x, weight):
 
 @pytest.mark.parametrize("weight", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("n,k", [(1, 16), (1, 128), (3, 4096), (129, 144), (64, 2816), (257, 704), (1000, 272)])
+@pytest.mark.parametrize("n,k", [(1, 16), (1, 128), (3, 4096), (129, 144), (64, 2816), (257, 704), (1000, 272), (2501, 4096), (5003, 2064)])
 def test_quant_is_exact(ctx, n, k, dtype, weight):
     g = rng(n + k)
     x = (randn(g, n, k) * torch.exp(2 * randn(g, 1, k))).to(T[dtype])
