@@ -132,6 +132,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same from branches that the cluster's warps come to apart.
+__device__ __forceinline__ void cluster_sync_apart() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
     float4 v;
     uint32_t at;
@@ -203,10 +207,12 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, float* stage, in
             }
         } else {
             const int e = lane & 15, n = n0 + 16 * c + e;
-#pragma unroll 1
-            for (int r = lane >> 4; r < rows; r += 2)
-                if (n < a.n)
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                if (r < rows && n < a.n)
                     store1(a.out, (int64_t)(m0 + r) * a.out_stride + n, stage[16 * r + 4 * ((e >> 2) ^ ((r >> 1) & 3)) + (e & 3)], a.type);
+            }
         }
         __syncwarp();
     }
@@ -532,7 +538,9 @@ struct Pair {
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes + kOutBytes + 256;
     // 640 threads x 96 registers at launch = 512 x 112 + 128 x 32
     static constexpr int kRegsEpi = 112, kRegsOther = 32;
+    static constexpr int kPartStride = C + 4;  // floats of a row of partial sums: rows begin on different banks
     static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kCtaRows * kPartStride * 4 <= kStages * kStageBytes, "partial sums of a split lie in the ring");
 };
 
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -567,15 +575,42 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives at the barrier of this offset in both CTAs when every MMA issued before is done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// Arrives at the barrier of this offset in both CTAs of the pair (a mask of ranks) when every MMA issued before is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t pair) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             ptx::smem_addr(bar)),
-        "h"((uint16_t)3)
+        "h"(pair)
         : "memory");
 }
 
+// This CTA's share of the columns of its rows, summed over the S pairs of its cluster in their order.
+template <int S>
+__device__ __forceinline__ void join_pairs(const MatmulArgs& a, uint32_t sums, uint32_t rank, int share, int m0, int n0) {
+    constexpr int kVecs = Pair::C / S / 4, kRowsAtOnce = 32 * Pair::kEpi / kVecs, kDeep = 8 / S;
+    const int c = share * (Pair::C / S) + 4 * ((int)threadIdx.x % kVecs), n = n0 + c;
+    const int rows = min(Pair::kCtaRows, a.m - m0);
+    for (int r0 = (int)threadIdx.x / kVecs; r0 < rows; r0 += kRowsAtOnce * kDeep) {
+        float4 v[kDeep][S];  // the loads of several rows before the first sum, as a peer's memory is far
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+            for (int p = 0; p < S; ++p)
+                v[d][p] = ld_peer4(sums + 4 * (min(r0 + d * kRowsAtOnce, Pair::kCtaRows - 1) * Pair::kPartStride + c), 2 * p + rank);
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int r = r0 + d * kRowsAtOnce;
+            if (r >= rows) break;
+            float4 x = v[d][0];
+#pragma unroll
+            for (int p = 1; p < S; ++p) x.x += v[d][p].x, x.y += v[d][p].y, x.z += v[d][p].z, x.w += v[d][p].w;
+            store4(a, (int64_t)(m0 + r) * a.out_stride + n, x, a.n - n);
+        }
+    }
+}
+
+// kSplit: clusters of 2 * T.splits CTAs share a tile's K-blocks, and have one tile each.
+template <bool kSplit>
 __global__ void __launch_bounds__(Pair::kThreads, 1)
     f8_rows_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ Tiles T,
                    const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w) {
@@ -597,7 +632,10 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     __shared__ int abort_flag;
 
     const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    // the cluster's pairs take a part of the K-blocks each
+    const uint32_t crank = cluster_rank(), rank = crank & 1, lead = kSplit ? crank & ~1u : 0;
+    const uint16_t both = (uint16_t)(3u << lead);
+    const int splits = kSplit ? T.splits : 1, share = kSplit ? (int)(crank >> 1) : 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(full + i, 1);
@@ -633,7 +671,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     ptx::pdl_wait();
     if (a.early) ptx::pdl_launch_dependents();
 
-    const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1, kblocks = T.kblocks;
+    const int first = (int)blockIdx.x / (2 * splits), step = (int)gridDim.x / (2 * splits);
+    const int kb0 = (int)((int64_t)T.kblocks * share / splits);
+    const int kblocks = (int)((int64_t)T.kblocks * (share + 1) / splits) - kb0;
     // neighbouring tiles go along the rows, 8 deep, so that tiles of one time share both operands in L2
     auto place = [&](int t, int& lt, int& ct) {
         const int group = 8 * T.cols, g = t / group, deep = min(8, T.lanes - 8 * g), r = t - g * group;
@@ -649,7 +689,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
             int st = 0;
             uint32_t ph = 0;
             bool ok = true;
-            const uint32_t full0 = peer_addr(full, 0);
+            const uint32_t full0 = peer_addr(full, lead);
             for (int t = first; t < T.total && ok; t += step) {
                 int lt, ct;
                 place(t, lt, ct);
@@ -663,9 +703,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                     if (leader) {
                         unsigned char* p = ring + st * F::kStageBytes;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, 2 * F::kStageBytes);
-                        tma_load_pair(p, &map_a, kb * 128, ya, full0 + 8 * st);
-                        tma_load_pair(p + kLaneBytes, &map_w, kb * 128, yw, full0 + 8 * st);
-                        tma_load_pair(p + kLaneBytes + kLaneBytes / 2, &map_w, kb * 128, yw + 128, full0 + 8 * st);
+                        tma_load_pair(p, &map_a, (kb0 + kb) * 128, ya, full0 + 8 * st);
+                        tma_load_pair(p + kLaneBytes, &map_w, (kb0 + kb) * 128, yw, full0 + 8 * st);
+                        tma_load_pair(p + kLaneBytes + kLaneBytes / 2, &map_w, (kb0 + kb) * 128, yw + 128, full0 + 8 * st);
                     }
                     __syncwarp();
                     if (++st == kStages) {
@@ -696,8 +736,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)  // K = 32 an MMA: 32 bytes on in the swizzled rows
                                 mma_f8_pair(tmem + slot * (C / 2), ad + 2 * k, bd + 512 * h + 2 * k, idesc, k > 0);
-                            commit_pair(acc_full + slot);
-                            if (h == 1) commit_pair(empty + st);
+                            commit_pair(acc_full + slot, both);
+                            if (h == 1) commit_pair(empty + st, both);
                         }
                         __syncwarp();
                         if (++slot == kSlots) {
@@ -715,7 +755,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                     }
                 }
             }
-            if (leader) commit_pair(drain);
+            if (leader) commit_pair(drain, both);
             __syncwarp();
             ptx::mbar_wait_sleep(drain, 0, nullptr);
         } else if (warp == F::kWarpMma) {
@@ -732,9 +772,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                 int lt, ct;
                 place(t, lt, ct);
                 const int m = lt * 256 + (int)rank * 128 + lane, left = a.m - m, nb = ct * 2 + h;
-                const float* sa = a.sa + (left > 0 ? m : 0);
+                const float* sa = a.sa + (int64_t)kb0 * a.sa_stride + (left > 0 ? m : 0);
                 const bool nin = nb * kF8Block < a.n;
-                const float* sw = a.sw + (nin ? (int64_t)nb * a.sw_stride : 0);
+                const float* sw = a.sw + (nin ? (int64_t)nb * a.sw_stride : 0) + kb0;
                 float q[2][4], w = 0.0f;
                 auto fetch = [&](float (&v)[4], int kb) {
                     const float* p = sa + (int64_t)kb * a.sa_stride;
@@ -770,13 +810,17 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                 }
             }
         }
+        if constexpr (kSplit) {  // where the epilogue's warps wait for the other pairs' sums
+            __syncwarp();
+            cluster_sync_apart();
+        }
     } else {
         more_registers<F::kRegsEpi>();
         // ---------------- epilogue ----------------
         // TMEM lanes 32 q on; of the slots of half h, columns 64 part on of 128
         const int q = warp & 3, part = (warp >> 2) & 1, h = warp >> 3;
         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + part * 64;
-        const uint32_t free0 = peer_addr(acc_empty, 0), mine0 = ptx::smem_addr(scale_empty), sp = ptx::smem_addr(scales) + 4 * (32 * q + lane);
+        const uint32_t free0 = peer_addr(acc_empty, lead), mine0 = ptx::smem_addr(scale_empty), sp = ptx::smem_addr(scales) + 4 * (32 * q + lane);
         int slot = h;
         uint32_t bph = 0;
         bool ok = true;
@@ -812,10 +856,30 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                     bph ^= 1;
                 }
             }
-            if (ok) {
-                int lt, ct;
-                place(t, lt, ct);
-                store_tile(a, outs + warp * 512, lt * 256 + (int)rank * 128 + 32 * q, ct * C + h * 128 + part * 64, acc);
+            int lt, ct;
+            place(t, lt, ct);
+            const int m0 = lt * 256 + (int)rank * 128;
+            if constexpr (!kSplit) {
+                if (ok) store_tile(a, outs + warp * 512, m0 + 32 * q, ct * C + h * 128 + part * 64, acc);
+            } else {
+                // One tile a cluster: its pairs' sums go through the ring, which is done with once the second half's warps
+                // have seen the last K-block's sums.
+                ptx::named_sync(1, 32 * F::kEpi);
+                if (ok) {
+                    float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + (32 * q + lane) * F::kPartStride + h * 128 + part * 64);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = ptx::f2(acc[2 * i]), y = ptx::f2(acc[2 * i + 1]);
+                        to[i] = make_float4(x.x, x.y, y.x, y.y);
+                    }
+                }
+                cluster_sync_apart();
+                if (!*abortp) {
+                    if (splits == 2)
+                        join_pairs<2>(a, ptx::smem_addr(ring), rank, share, m0, ct * C);
+                    else
+                        join_pairs<4>(a, ptx::smem_addr(ring), rank, share, m0, ct * C);
+                }
             }
         }
     }
@@ -1048,21 +1112,21 @@ cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, 
     return cfg;
 }
 
-// How many clusters of n CTAs of the weights form are resident at once (n = 1 .. 8). A cluster lies within a GPC, so
-// large ones leave SMs idle: of 304 places, clusters of 8 fill 288, of 7 266, of 6 276, of 5 290, of 4 296.
-template <class F>
-int resident_clusters(int n, int sms) {
+// How many clusters of n (1 .. 8) CTAs of the kernel are resident at once. A cluster lies within a GPC, so large ones leave
+// SMs idle: of 304 places for the weights form, clusters of 8 fill 288, of 7 266, of 6 276, of 5 290, of 4 296; of 152 for
+// the rows form, clusters of 4 fill 144, of 8 120.
+template <class F, class K>
+int resident_clusters(K* kernel, int n) {
     static std::mutex mu;
     static int device = -1, held[9];
-    std::lock_guard<std::mutex> lock(mu);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
     if (dev != device) {
-        held[1] = sms * F::kCtas;
-        for (int i = 2; i <= 8; ++i) {
+        for (int i = 1; i <= 8; ++i) {
             cudaLaunchAttribute attr[2];
             const cudaLaunchConfig_t cfg = cluster_config(8u * i, F::kThreads, F::kSmem, nullptr, (unsigned)i, attr);
-            if (cudaOccupancyMaxActiveClusters(&held[i], f8_matmul_kernel<F>, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
                 cudaGetLastError();
                 held[i] = 0;
             }
@@ -1080,7 +1144,7 @@ template <class F>
 int splits_of(const Tiles& T, int sms) {
     if (2 * T.total > sms || T.kblocks < 8) return 1;
     int s = std::min(8, T.kblocks / 2);
-    while (s > 1 && resident_clusters<F>(s, sms) < T.total) --s;
+    while (s > 1 && resident_clusters<F>(f8_matmul_kernel<F>, s) < T.total) --s;
     return s;
 }
 
@@ -1100,23 +1164,25 @@ cudaError_t launch_form(const MatmulArgs& a, int sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, f8_matmul_kernel<F>, a, T, mw, ma);
 }
 
-cudaError_t launch_rows(const MatmulArgs& a, int sms, cudaStream_t s) {
-    const Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
+cudaError_t launch_rows(const MatmulArgs& a, int splits, int sms, cudaStream_t s) {
+    Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
+    T.splits = splits;
     CUtensorMap ma, mw;
     cudaError_t e = encode_codes(&ma, a.a, a.m, a.k, a.a_stride, Pair::kCtaRows);
     if (e == cudaSuccess) e = encode_codes(&mw, a.w, a.n, a.k, a.w_stride, Pair::C / 4);
-    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_rows_kernel), Pair::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg =
-        cluster_config(2u * (unsigned)std::min(T.total, sms / 2), Pair::kThreads, Pair::kSmem, s, 2, attr);
-    return cudaLaunchKernelEx(&cfg, f8_rows_kernel, a, T, ma, mw);
+    const unsigned grid = 2u * (unsigned)(splits > 1 ? T.total * splits : std::min(T.total, sms / 2));
+    const cudaLaunchConfig_t cfg = cluster_config(grid, Pair::kThreads, Pair::kSmem, s, 2u * (unsigned)splits, attr);
+    return splits > 1 ? cudaLaunchKernelEx(&cfg, f8_rows_kernel<true>, a, T, ma, mw)
+                      : cudaLaunchKernelEx(&cfg, f8_rows_kernel<false>, a, T, ma, mw);
 }
 
 }  // namespace
 
-// us of a call in the weights form of 64 rows and in the rows form, by what they measured: a fixed part, and a time per
-// K-block of a tile (for two tiles on an SM at a time, which share its bandwidth, or one), for as many tiles as an SM gets.
+// us of a call in the weights form of 64 rows and in the rows form, by what they measured: a fixed part (more where K is
+// shared and parts are joined), and a time per K-block of a tile (for two tiles on an SM at a time, which share its
+// bandwidth, or one), for as many tiles as an SM gets.
 namespace {
 double weights_form_us(const MatmulArgs& a, int sms) {
     using F = Form<64>;
@@ -1125,9 +1191,20 @@ double weights_form_us(const MatmulArgs& a, int sms) {
     if (s > 1) return 5.5 + 0.28 * ((T.kblocks + s - 1) / s);
     return each == 1 ? 3.9 + 0.28 * T.kblocks : 3.5 + 0.46 * T.kblocks * ((each + 1) / 2);
 }
-double rows_form_us(const MatmulArgs& a, int sms) {
+
+// *splits: pairs of CTAs a tile. us for 1, 2 and 4: 1,052 rows of 7,536 by 1,154 weights (25 tiles) 31.7 20.6 30.9; 300 of
+// 16,384 by 300 (4 tiles) 51.8 29.3 20.2; 700 of 2,048 by 2,048 (24 tiles) 13.2 11.7 22.3.
+double rows_form_us(const MatmulArgs& a, int sms, int* splits) {
     const Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
-    return 5.0 + 0.40 * T.kblocks * ((T.total + sms / 2 - 1) / (sms / 2));
+    *splits = 1;
+    // (a tile's stores: rows of an odd stride, or not on 16-byte boundaries, go out an element at a time)
+    const bool wide = !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % (a.type == MOE_F32 ? 4 : 8) == 0 && a.n % 64 == 0;
+    double best = 3.5 + (0.40 * T.kblocks + (wide ? 1.7 : 4.5)) * ((T.total + sms / 2 - 1) / (sms / 2));
+    for (int s = 2; s <= 4 && T.kblocks >= 4 * s; s *= 2) {
+        const double us = (s == 2 ? 8.0 : 9.5) + 0.40 * ((T.kblocks + s - 1) / s);
+        if (us < best && T.total <= resident_clusters<Pair>(f8_rows_kernel<true>, 2 * s)) best = us, *splits = s;
+    }
+    return best;
 }
 }  // namespace
 
@@ -1143,8 +1220,14 @@ cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
     if (a.m <= 16 && weights <= 6000000 && a.k <= 2048 && groups <= few_ctas(2) * sms) return launch_few<2>(a, sms, s);
     if (a.m <= 16) return launch_form<Form<16>>(a, sms, s);
     if (a.m <= 32) return launch_form<Form<32>>(a, sms, s);
-    if (a.m <= 64 || weights_form_us(a, sms) <= rows_form_us(a, sms)) return launch_form<Form<64>>(a, sms, s);
-    return launch_rows(a, sms, s);
+    if (a.m <= 64) return launch_form<Form<64>>(a, sms, s);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(f8_matmul_kernel<Form<64>>), Form<64>::kSmem);
+    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_rows_kernel<false>), Pair::kSmem);
+    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(f8_rows_kernel<true>), Pair::kSmem);
+    if (e != cudaSuccess) return e;
+    int splits;
+    const double rows = rows_form_us(a, sms, &splits);
+    return weights_form_us(a, sms) <= rows ? launch_form<Form<64>>(a, sms, s) : launch_rows(a, splits, sms, s);
 }
 
 }  // namespace moe

@@ -264,7 +264,8 @@ def check_matmul(a, sa, w, sw, out):
 @pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 6144, 2816), (1, 128, 128), (2, 2816, 4096), (5, 999, 2048), (16, 130, 144), (17, 257, 2832),
                                    (32, 704, 2816), (33, 64, 512), (64, 8192, 640), (65, 100, 2048), (77, 2816, 4096), (128, 6144, 256),
                                    (129, 385, 1040), (143, 1000, 2816), (200, 128, 16384), (257, 300, 704), (300, 2816, 2048), (1000, 515, 1296),
-                                   (2049, 1030, 400), (40, 40000, 272), (513, 6144, 2816)])
+                                   (2049, 1030, 400), (40, 40000, 272), (513, 6144, 2816),
+                                   (1052, 1154, 7536), (2200, 631, 4096), (600, 330, 16384), (700, 2047, 2064)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "f16"])
 def test_matmul(ctx, m, n, k, dtype):
     ops = operands(rng(m + n + k), m, n, k)
@@ -326,7 +327,7 @@ def test_matmul_of_no_rows(ctx):
 
 def test_matmul_of_zero_accumulates_nothing_left_over(ctx):
     """Repeated calls of several shapes give the same bits, whatever ran before on the SMs' tensor memory."""
-    shapes = [(1, 500, 512), (20, 1000, 2816), (60, 300, 1024), (100, 2816, 704), (600, 900, 1024)]
+    shapes = [(1, 500, 512), (20, 1000, 2816), (60, 300, 1024), (100, 2816, 704), (600, 900, 1024), (1052, 1154, 7536), (2000, 400, 8192)]
     ops = [operands(rng(i), *s) for i, s in enumerate(shapes)]
     first = [moe.moe_f8_matmul(ctx, *o, dtype=torch.float32) for o in ops]
     for _ in range(5):
