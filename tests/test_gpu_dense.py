@@ -272,6 +272,18 @@ def test_matmul(ctx, m, n, k, dtype):
     check_matmul(*ops, moe.moe_f8_matmul(ctx, *ops, dtype=T[dtype]))
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 2000, 2816), (13, 2000, 4096), (40, 2000, 4096), (300, 2000, 4096), (1000, 1000, 4096)])
+def test_matmul_keeps_fp32(ctx, m, n, k):
+    """Sums are held in fp32 throughout. Of 32 K-blocks each addition rounds by u of the sum so far at most, whose rms is at most
+    the result's: sqrt(33) u if they are independent, and 2 u for the scales: 8 u of the result's norm."""
+    g = rng(m)
+    a, sa = moe.moe_f8_quant_rows(ctx, randn(g, m, k))
+    w, sw = moe.moe_f8_quant_weight(ctx, randn(g, n, k) * k ** -0.5)
+    out = moe.moe_f8_matmul(ctx, a, sa, w, sw, dtype=torch.float32).double()
+    want = value(a, sa)[0] @ value(w, sw, True)[0].t()
+    assert (out - want).norm() <= 8 * U * want.norm()
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 200, 400), (40, 333, 1024), (100, 300, 272), (700, 777, 528)])
 @pytest.mark.parametrize("pad", [1, 8])
 def test_matmul_strided(ctx, m, n, k, pad):
