@@ -771,8 +771,6 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
             if (leader) commit_pair(drain, both);
             __syncwarp();
             ptx::mbar_wait_sleep(drain, 0, nullptr);
-        } else if (warp == F::kWarpMma) {
-            ptx::mbar_wait_sleep(drain, 0, nullptr);  // the commits' arrivals here are the other CTA's last writes
         } else if (warp >= F::kWarpScale) {
             // ---------------- scales: rows' times weights' ----------------
             // a warp a half of the weights, a lane four rows, two K-blocks ahead; the weight block's scales 32 K-blocks
@@ -904,6 +902,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         // a millisecond is given to them.
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
+    // the commits' arrivals are the other CTA's last writes here
+    if (warp == F::kWarpMma && rank == 1) ptx::mbar_wait_sleep(drain, 0, nullptr);
+    __syncwarp();
     cluster_sync();  // nothing of the pair's is under way in either CTA
     ptx::tc_fence_after();
     if (warp == F::kWarpMma)
