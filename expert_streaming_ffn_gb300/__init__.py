@@ -707,10 +707,11 @@ _f8_matmul_pack = struct.Struct("@PqPqPqPqPqiiii").pack  # and of moe_f8_matmul_
 _SAME = object()
 
 
-def _dense_new(shape, dtype, device: int, stream):
+def _dense_new(shape, dtype, where, stream):
+    """A new output; `where` a torch.device (an index takes torch a microsecond longer)."""
     if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    return _new(shape, dtype, _torch.device("cuda", device), stream)
+        return _torch.empty(shape, dtype=dtype, device=where)
+    return _new(shape, dtype, where, stream)
 
 
 def _rows3(t, what: str, shape, device: int):
@@ -723,22 +724,22 @@ def _rows3(t, what: str, shape, device: int):
     return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if len(shape) > 2 and shape[1] > 1 else 0
 
 
-def _codes(t, what: str, shape, device: int):
+def _codes(t, what: str, n: int, k: int, device: int):
     """(pointer, stride) of e4m3 codes [n][k]."""
     st = t.stride()
-    if t.dtype != _torch.float8_e4m3fn or t.shape != shape or t.get_device() != device or st[1] != 1:
-        raise ValueError(f"{what}: expected float8_e4m3fn {list(shape)} on CUDA device {device}, the last dimension contiguous, "
+    if t.shape != (n, k) or t.dtype != _torch.float8_e4m3fn or t.get_device() != device or st[1] != 1:
+        raise ValueError(f"{what}: expected float8_e4m3fn {[n, k]} on CUDA device {device}, the last dimension contiguous, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr(), st[0] if shape[0] > 1 else -(-shape[1] // 16) * 16
+    return t.data_ptr(), st[0] if n > 1 else -(-k // 16) * 16
 
 
-def _scales(t, what: str, shape, device: int):
-    """(pointer, stride) of fp32 scales of that shape."""
+def _scales(t, what: str, n: int, k: int, device: int):
+    """(pointer, stride) of fp32 scales [n][k]."""
     st = t.stride()
-    if t.dtype != _torch.float32 or t.shape != shape or t.get_device() != device or (st[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{what}: expected float32 {list(shape)} on CUDA device {device}, the last dimension contiguous, "
+    if t.shape != (n, k) or t.dtype != _torch.float32 or t.get_device() != device or (st[1] != 1 and k > 1):
+        raise ValueError(f"{what}: expected float32 {[n, k]} on CUDA device {device}, the last dimension contiguous, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1]
+    return t.data_ptr(), st[0] if n > 1 else k
 
 
 def _dense_stream(stream, device: int):
@@ -762,13 +763,13 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
     [n][d] and f32 scales [ceil(d / 128)][n] of the same rows (None, None without). Outputs given are filled."""
     torch = _torch or _kv_torch()
     shape, st = x.shape, x.stride()
-    device = _cuda(x, "x")
+    device, where = _cuda(x, "x"), x.device
     if len(st) == 3:
-        n, heads, d = shape
+        shape = n, heads, d = tuple(shape)
         ht, tt = d, heads * d  # strides of a new tensor
         xt, xh = st[0] if n > 1 else 0, st[1] if heads > 1 else 0
     elif len(st) == 2:
-        n, d = shape
+        shape = n, d = tuple(shape)
         heads, ht, tt = 1, 0, d
         xt, xh = st[0] if n > 1 else 0, 0
     else:
@@ -785,7 +786,7 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
         rp, rt, rh = _rows3(residual, "residual", shape, device)
         rd = _kv_type(residual.dtype)
         if sum is None:
-            sum = _dense_new(shape, residual.dtype, device, stream)
+            sum = _dense_new(shape, residual.dtype, where, stream)
             sp, st, sh = sum.data_ptr(), tt, ht
         else:
             if sum.dtype != residual.dtype:
@@ -802,31 +803,33 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
         if dtype is _SAME:
             dtype = x.dtype
         od = _kv_type(dtype)
-        out = _dense_new(shape, dtype, device, stream)
+        out = _dense_new(shape, dtype, where, stream)
         op, ot, oh = out.data_ptr(), tt, ht
     if f8 or codes is not None or scales is not None:
         if heads != 1:
             raise ValueError("an 8-bit output takes rows of one head")
         blocks = (d + 127) // 128
         if codes is None:
-            codes = _dense_new((n, d), torch.float8_e4m3fn, device, stream)
+            codes = _dense_new((n, d), torch.float8_e4m3fn, where, stream)
             cp, ct = codes.data_ptr(), d
         else:
-            cp, ct = _codes(codes, "codes", (n, d), device)
+            cp, ct = _codes(codes, "codes", n, d, device)
         if scales is None:
-            scales = _dense_new((blocks, n), torch.float32, device, stream)
+            scales = _dense_new((blocks, n), torch.float32, where, stream)
             lp, lt = scales.data_ptr(), n
         else:
-            lp, lt = _scales(scales, "scales", (blocks, n), device)
+            lp, lt = _scales(scales, "scales", blocks, n, device)
     args = _norm_pack(xp, xt, xh, rp, rt, rh, wp, sp, st, sh, op, ot, oh, cp, ct, lp, lt, n, heads, d, eps,
                       _kv_type(x.dtype), rd, wd, od)
-    _check((_lib or load()).moe_rms_norm(ctx, args, _dense_stream(stream, device)), "moe_rms_norm")
+    status = (_lib or load()).moe_rms_norm(ctx, args, _dense_stream(stream, device))
+    if status:
+        _check(status, "moe_rms_norm")
     return out, sum, codes, scales
 
 
 def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
     torch = _torch or _kv_torch()
-    device = _cuda(x, "x")
+    device, where = _cuda(x, "x"), x.device
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x: expected [n][k]")
@@ -839,15 +842,15 @@ def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
     xp = x.data_ptr()
     of_scales = ((n + 127) // 128 if weight else (k + 127) // 128, (k + 127) // 128 if weight else n)
     if codes is None:
-        codes = _dense_new((n, k), torch.float8_e4m3fn, device, stream)
+        codes = _dense_new((n, k), torch.float8_e4m3fn, where, stream)
         cp, ct = codes.data_ptr(), k
     else:
-        cp, ct = _codes(codes, "codes", (n, k), device)
+        cp, ct = _codes(codes, "codes", n, k, device)
     if scales is None:
-        scales = _dense_new(of_scales, torch.float32, device, stream)
+        scales = _dense_new(of_scales, torch.float32, where, stream)
         lp, lt = scales.data_ptr(), of_scales[1]
     else:
-        lp, lt = _scales(scales, "scales", of_scales, device)
+        lp, lt = _scales(scales, "scales", *of_scales, device)
     _check(getattr(_lib or load(), fn)(ctx, xp, xt, _kv_type(x.dtype), n, k, cp, ct, lp, lt, _dense_stream(stream, device)), fn)
     return codes, scales
 
@@ -872,14 +875,14 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
         raise ValueError("a and w: expected [m][k] and [n][k]")
     m, k = of_a
     n, kb = of_w[0], (k + 127) // 128
-    ap, at = _codes(a, "a", (m, k), device)
-    wp, wt = _codes(w, "w", (n, k), device)
-    asp, ast = _scales(a_scales, "a_scales", (kb, m), device)
-    wsp, wst = _scales(w_scales, "w_scales", ((n + 127) // 128, kb), device)
+    ap, at = _codes(a, "a", m, k, device)
+    wp, wt = _codes(w, "w", n, k, device)
+    asp, ast = _scales(a_scales, "a_scales", kb, m, device)
+    wsp, wst = _scales(w_scales, "w_scales", (n + 127) // 128, kb, device)
     if out is None:
         dtype = dtype or torch.bfloat16
         od = _kv_type(dtype)
-        out = _dense_new((m, n), dtype, device, stream)
+        out = _dense_new((m, n), dtype, a.device, stream)
         op, ot = out.data_ptr(), n
     else:
         if dtype not in (None, out.dtype):
@@ -887,7 +890,9 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
         od = _kv_type(out.dtype)
         op, ot, _ = _rows3(out, "out", (m, n), device)
     args = _f8_matmul_pack(ap, at, asp, ast, wp, wt, wsp, wst, op, ot, m, n, k, od)
-    _check((_lib or load()).moe_f8_matmul(ctx, args, _dense_stream(stream, device)), "moe_f8_matmul")
+    status = (_lib or load()).moe_f8_matmul(ctx, args, _dense_stream(stream, device))
+    if status:
+        _check(status, "moe_f8_matmul")
     return out
 
 

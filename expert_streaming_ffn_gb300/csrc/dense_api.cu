@@ -154,6 +154,8 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
         return set_error(MOE_EINVAL, "%s: strides of a and w must be at least k = %d, below 2^40", who, p->k);
     if (!at4(p->a_scales) || !at4(p->w_scales) || (reinterpret_cast<uintptr_t>(p->out) & (type_size(p->out_dtype) - 1)))
         return set_error(MOE_EINVAL, "%s: scales and out must be aligned to their elements", who);
+    if ((p->a_scale_stride < p->m && blocks(p->k) > 1) || (p->w_scale_stride < blocks(p->k) && blocks(p->n) > 1))
+        return set_error(MOE_EINVAL, "%s: rows of scales overlap", who);
     if (p->out_stride < p->n && p->m > 1) return set_error(MOE_EINVAL, "%s: rows of out overlap", who);
     CUDA_TRY(cudaSetDevice(ctx_device(C)));
     if (unsigned code = ctx_f8_expired(C))

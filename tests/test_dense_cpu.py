@@ -49,7 +49,7 @@ NORM = [dict(x=None), dict(x=P + 8), dict(x_token_stride=252), dict(x_head_strid
 MATMUL = [dict(a=None), dict(w=None), dict(out=None), dict(a_scales=None), dict(w_scales=None), dict(m=-1), dict(n=0), dict(k=0),
           dict(k=250), dict(a=P + 8), dict(w=P + 1), dict(a_stride=264), dict(w_stride=264), dict(a_stride=240), dict(w_stride=0),
           dict(a_stride=1 << 41), dict(a_scales=P + 1), dict(w_scales=P + 2), dict(out=P + 1), dict(out=P + 2, out_dtype=0),
-          dict(out_stride=99), dict(out_dtype=3), dict(m=(1 << 31) - 1, n=(1 << 31) - 1, out_stride=1 << 31), dict(k=(1 << 30) + 16)]
+          dict(out_stride=99), dict(out_dtype=3), dict(a_scale_stride=3), dict(w_scale_stride=1, n=200, out_stride=200), dict(w_scale_stride=-2, n=200, out_stride=200), dict(m=(1 << 31) - 1, n=(1 << 31) - 1, out_stride=1 << 31), dict(k=(1 << 30) + 16)]
 
 
 @pytest.mark.parametrize("bad", NORM)
