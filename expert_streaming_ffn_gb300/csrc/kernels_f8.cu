@@ -12,12 +12,13 @@
 // ones, while epilogue warps add scale * sum. Where tiles are few the CTAs of a cluster share K and join their sums through
 // distributed shared memory, in a fixed order; so the same call gives the same bits.
 //
-// Weights form, warps: four epilogue warps (warp q reads TMEM lanes 32 q on), one that loads both operands by TMA into a
-// ring of K-blocks (128 bytes a row, 128-byte swizzle), one that issues the MMAs.
+// Weights form, warps: four or eight epilogue warps (warp w reads TMEM lanes 32 (w mod 4) on), one that loads both operands
+// by TMA into a ring of K-blocks (128 bytes a row, 128-byte swizzle), one that issues the MMAs.
 //   100,003 weights of 2,048 by 5 rows: 33.3 us, 6.2 TB/s, 0.92 of the copy bandwidth measured on this GPU, bound by HBM.
-//   2,816 of 4,096 by 77 rows 8.7 us (floor 1.8), 6,144 of 2,816 by 143 10 us (2.9): about 4 to 5 us of start, first loads
-//   and last stores, then 0.28 us a K-block for one CTA on an SM (0.46 for two), which is the way from a K-block's last MMA
-//   through its sums to the next use of their buffer.
+//   2,816 of 4,096 by 77 rows 9 us (floor 1.8), 6,144 of 2,816 by 143 9.8 us (2.9): about 4 us of start, first loads
+//   and last stores, then 0.27 us a K-block for one CTA on an SM (0.41 for two): an epilogue warp's chain of barrier (120
+//   cycles when it is there), load from tensor memory (100), scales and sums. Deeper rings (one CTA on an SM) and sixteen
+//   epilogue warps of 16 columns were no faster.
 // Every wait is bounded; when one expires the kernel sets an error word, every other wait gives up, its own copies and
 // MMAs in flight are waited for and its tensor memory is freed.
 #include <cuda.h>
@@ -49,7 +50,8 @@ __device__ __forceinline__ bool elect_one() {
 template <int C_>
 struct Form {
     static constexpr int C = C_;
-    static constexpr int kEpi = 4;
+    static constexpr int kEpi = C == 16 ? 4 : 8;
+    static constexpr int kPer = 4 * C / kEpi;  // columns of an epilogue warp
     static constexpr int kThreads = 32 * (kEpi + 2);
     static constexpr int kStageBytes = kLaneBytes + C * 128;
     static constexpr int kStages = C == 16 ? 6 : C == 32 ? 5 : 4;
@@ -85,11 +87,6 @@ __device__ __forceinline__ uint32_t f8_idesc(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 lanes x 16 columns, as eight register pairs
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
-    ptx::tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
-}
-
 // 32 lanes x 32 columns
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -100,6 +97,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr)
+        : "memory");
+}
+
+// One lane's arrival at a barrier of this CTA.
+__device__ __forceinline__ void arrive_one(bool one, uint32_t addr) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"((uint32_t)one),
+        "r"(addr)
         : "memory");
 }
 
@@ -245,7 +250,7 @@ template <class F>
 __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     f8_matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ Tiles T,
                      const __grid_constant__ CUtensorMap map_lanes, const __grid_constant__ CUtensorMap map_cols) {
-    constexpr int C = F::C, kStages = F::kStages, kBufs = F::kBufs, kChunk = F::kChunk;
+    constexpr int C = F::C, kPer = F::kPer, kStages = F::kStages, kBufs = F::kBufs, kChunk = F::kChunk;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -307,8 +312,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
     if (a.early) ptx::pdl_launch_dependents();
 
     if (warp >= F::kEpi) {
-        if (warp == F::kEpi && lane == 0) {
+        if (warp == F::kEpi) {
             // ---------------- loads ----------------
+            const bool leader = elect_one();
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -316,15 +322,18 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                 int lt, ct;
                 place(t, lt, ct);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!ptx::mbar_wait_sleep(empty + st, ph ^ 1, abortp)) {
-                        fail(1u);
+                    if (!__all_sync(kFull, ptx::mbar_wait_sleep(empty + st, ph ^ 1, abortp))) {
+                        if (leader) fail(1u);
                         ok = false;
                         break;
                     }
-                    unsigned char* p = ring + st * F::kStageBytes;
-                    ptx::mbar_arrive_expect_tx(full + st, F::kStageBytes);
-                    ptx::tma_load_2d(p, &map_lanes, kb * 128, lt * kLanes, full + st);
-                    ptx::tma_load_2d(p + kLaneBytes, &map_cols, kb * 128, ct * C, full + st);
+                    if (leader) {
+                        unsigned char* p = ring + st * F::kStageBytes;
+                        ptx::mbar_arrive_expect_tx(full + st, F::kStageBytes);
+                        ptx::tma_load_2d(p, &map_lanes, kb * 128, lt * kLanes, full + st);
+                        ptx::tma_load_2d(p + kLaneBytes, &map_cols, kb * 128, ct * C, full + st);
+                    }
+                    __syncwarp();
                     ++issued;
                     if (++st == kStages) {
                         st = 0;
@@ -381,75 +390,75 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         }
     } else {
         // ---------------- epilogue ----------------
-        const uint32_t taddr = tmem + ((uint32_t)(32 * warp) << 16);
+        const int q = warp & 3, col0 = (warp >> 2) * kPer;  // TMEM lanes 32 q on, columns col0 on
+        const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + col0;
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
         for (int t = first; t < T.total; t += step) {
             int lt, ct;
             place(t, lt, ct);
-            uint64_t acc[C / 2];
+            uint64_t acc[kPer / 2];
 #pragma unroll
-            for (int i = 0; i < C / 2; ++i) acc[i] = 0;
-            const int lrow = lt * kLanes + 32 * warp + lane;  // this thread's lane: a weight
+            for (int i = 0; i < kPer / 2; ++i) acc[i] = 0;
+            const int lrow = lt * kLanes + 32 * q + lane;  // this thread's lane: a weight
             {
-                const bool nin = lt * kLanes < a.n;
-                const float* sw = a.sw + (nin ? (int64_t)lt * a.sw_stride : 0);
+                const float* sw = a.sw + (int64_t)lt * a.sw_stride;
                 const int m0 = ct * C;
-                // row scales, kChunk K-blocks at a time, a chunk ahead
+                // Scales, rows' times weights', kChunk K-blocks at a time and a chunk ahead: a thread copies rows' scales to
+                // shared memory, and multiplies them by the weights' once they are there.
+                constexpr int kMine = kChunk * C / (32 * F::kEpi);
+                float w_next[kMine], w_now[kMine];
                 auto fetch = [&](int kb, int half_of) {
-                    for (int i = threadIdx.x; i < kChunk * C; i += 32 * F::kEpi) {
-                        const int b = kb + i / C, r = m0 + i % C;
+#pragma unroll
+                    for (int j = 0; j < kMine; ++j) {
+                        const int i = threadIdx.x + j * 32 * F::kEpi, b = kb + i / C, r = m0 + i % C;
                         const bool in = b < kb1 && r < a.m;
                         cp_async4(ptx::smem_addr(scales + half_of * kChunk * C + i),
                                   a.sa + (in ? (int64_t)b * a.sa_stride + r : 0), in);
+                        w_next[j] = b < kb1 ? sw[b] : 0.0f;
                     }
                     cp_async_commit();
                 };
                 fetch(kb0, 0);
-                float w_lane = 0.0f;
                 int turn = 0;
-                for (int kb = kb0; kb < kb1; ++kb) {  // to the end even after a failed wait: the warps meet at barriers
-                    const int i = (kb - kb0) % kChunk;
-                    if (i == 0) {
-                        // the last chunk's readers are done before its place is written again
-                        if (kb > kb0) turn ^= 1;
-                        ptx::named_sync(1, 32 * F::kEpi);
-                        fetch(kb + kChunk, turn ^ 1);
-                        cp_async_wait<1>();
-                        ptx::named_sync(1, 32 * F::kEpi);
-                    }
-                    if (((kb - kb0) & 31) == 0) w_lane = kb + lane < kb1 ? sw[kb + lane] : 0.0f;
-                    const float ws = __shfl_sync(kFull, w_lane, (kb - kb0) & 31);
-                    const uint64_t w2 = ptx::f2(ws, ws);
-                    if (ok && !__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + buf, bph, abortp))) {
-                        if (lane == 0) fail(4u);
-                        ok = false;
-                    }
-                    if (ok) {
-                        ptx::tc_fence_after();
-                        const uint32_t at = taddr + buf * C;
-                        const uint32_t sp = ptx::smem_addr(scales + (turn * kChunk + i) * C);
-                        uint32_t d[2][16];
-                        tmem_ld16(at, d[0]);
+                for (int kc = kb0; kc < kb1; kc += kChunk, turn ^= 1) {  // to the end even after a failed wait: the warps meet at barriers
+                    ptx::named_sync(1, 32 * F::kEpi);  // the other half's readers are done with it
 #pragma unroll
-                        for (int c = 0; c < C / 16; ++c) {
-                            ptx::tmem_ld_wait();
-                            if (c + 1 < C / 16) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
+                    for (int j = 0; j < kMine; ++j) w_now[j] = w_next[j];
+                    fetch(kc + kChunk, turn ^ 1);
+                    cp_async_wait<1>();
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 s4 = ptx::lds_f4(sp + 64 * c + 16 * e);
-                                acc[8 * c + 2 * e] = ptx::fma2(
-                                    ptx::f2(__uint_as_float(d[c & 1][4 * e]), __uint_as_float(d[c & 1][4 * e + 1])),
-                                    ptx::mul2(ptx::f2(s4.x, s4.y), w2), acc[8 * c + 2 * e]);
-                                acc[8 * c + 2 * e + 1] = ptx::fma2(
-                                    ptx::f2(__uint_as_float(d[c & 1][4 * e + 2]), __uint_as_float(d[c & 1][4 * e + 3])),
-                                    ptx::mul2(ptx::f2(s4.z, s4.w), w2), acc[8 * c + 2 * e + 1]);
-                            }
+                    for (int j = 0; j < kMine; ++j) scales[turn * kChunk * C + threadIdx.x + j * 32 * F::kEpi] *= w_now[j];
+                    ptx::named_sync(1, 32 * F::kEpi);
+                    uint32_t sp = ptx::smem_addr(scales + turn * kChunk * C + col0);
+                    const int n = min(kChunk, kb1 - kc);
+                    for (int i = 0; i < n; ++i, sp += 4 * C) {
+                        if (ok && !__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + buf, bph, abortp))) {
+                            if (lane == 0) fail(4u);
+                            ok = false;
                         }
+                        if (!ok) continue;
+                        ptx::tc_fence_after();
+                        uint32_t d[kPer];
+                        if constexpr (kPer == 32)
+                            tmem_ld32(taddr + buf * C, d);
+                        else
+                            ptx::tmem_ld16(taddr + buf * C, d);
+                        float4 s4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s4[e] = ptx::lds_f4(sp + 16 * e);
+                        ptx::tmem_ld_wait();
                         ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acc_empty + buf);
+                        arrive_one(lane == 0, ptx::smem_addr(acc_empty + buf));
+#pragma unroll
+                        for (int e = 0; e < kPer / 4; ++e) {
+                            const float4 x = e < 4 ? s4[e & 3] : ptx::lds_f4(sp + 16 * e);
+                            acc[2 * e] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])),
+                                                   ptx::f2(x.x, x.y), acc[2 * e]);
+                            acc[2 * e + 1] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e + 2]), __uint_as_float(d[4 * e + 3])),
+                                                       ptx::f2(x.z, x.w), acc[2 * e + 1]);
+                        }
                         if (++buf == kBufs) {
                             buf = 0;
                             bph ^= 1;
@@ -457,22 +466,22 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
                     }
                 }
                 cp_async_wait<0>();
-                const int cols = min(C, a.m - m0);
+                const int cols = min(kPer, a.m - m0 - col0);
                 if (T.splits == 1) {
                     if (ok && lrow < a.n) {
                         if (a.type == MOE_F32)
-                            store_columns<float>(a, m0, lrow, cols, acc);
+                            store_columns<float>(a, m0 + col0, lrow, cols, acc);
                         else if (a.type == MOE_BF16)
-                            store_columns<__nv_bfloat16>(a, m0, lrow, cols, acc);
+                            store_columns<__nv_bfloat16>(a, m0 + col0, lrow, cols, acc);
                         else
-                            store_columns<__half>(a, m0, lrow, cols, acc);
+                            store_columns<__half>(a, m0 + col0, lrow, cols, acc);
                     }
                     ptx::named_sync(1, 32 * F::kEpi);  // this tile's scales are read before the next tile's come
                 } else if (ok) {
                     // the ring is done with: the last accumulator's MMAs have read it
-                    float* part = reinterpret_cast<float*>(ring) + 32 * warp + lane;
+                    float* part = reinterpret_cast<float*>(ring) + col0 * kLanes + 32 * q + lane;
 #pragma unroll
-                    for (int c = 0; c < C / 2; ++c) {
+                    for (int c = 0; c < kPer / 2; ++c) {
                         if (2 * c >= cols) break;
                         const float2 v = ptx::f2(acc[c]);
                         part[(2 * c) * kLanes] = v.x;
@@ -1205,7 +1214,7 @@ double weights_form_us(const MatmulArgs& a, int sms) {
     const Tiles T = tiles_of(a.n, a.m, kLanes, F::C, a.k);
     const int s = splits_of<F>(T, sms), each = (T.total + sms - 1) / sms;
     if (s > 1) return 5.5 + 0.28 * ((T.kblocks + s - 1) / s);
-    return each == 1 ? 3.9 + 0.28 * T.kblocks : 3.5 + 0.46 * T.kblocks * ((each + 1) / 2);
+    return each == 1 ? 3.9 + 0.28 * T.kblocks : 3.5 + 0.41 * T.kblocks * ((each + 1) / 2);
 }
 
 // *splits: pairs of CTAs a tile. us for 1, 2 and 4: 1,052 rows of 7,536 by 1,154 weights (25 tiles) 31.7 20.6 30.9; 300 of
@@ -1227,8 +1236,8 @@ double rows_form_us(const MatmulArgs& a, int sms, int* splits) {
 // Measured, us (columns: mma.sync, weights form of 16 / 32 / 64 rows, rows form):
 //   8 rows:   6,144 x 2,816: 5.6 7.7; 2,816 x 704: 2.2 3.4; 20,000 x 512: 4.7 3.6; 16,384 x 2,048: 9.2 8.8; 640 x 8,192: 6.5 5.1
 //   16 rows:  1,024 x 1,024: 2.0 3.6; 2,816 x 704: 2.7 3.4; 2,816 x 4,096: 6.3 5.2; 6,144 x 2,816: 8.5 7.7
-//   64 rows (of 32, of 64, rows): 2,816 x 4,096: 7.6 6.9 15.5; 8,192 x 8,192: 19.2 18.4 25.5; 6,144 x 2,816: 8.4 9.6 12.6
-//   128 rows (of 64, rows): 6,144 x 2,816: 10.0 14.4; 512 of them: 23.4 15.1; 192 of 16,384 x 2,048: 18.5 13.6
+//   64 rows (of 32, of 64, rows): 2,816 x 4,096: 8.3 8.4 15.5; 8,192 x 8,192: 19.0 17.4 25.5; 6,144 x 2,816: 8.5 9.4 12.6
+//   128 rows (of 64, rows): 6,144 x 2,816: 9.7 14.9; 512 of them: 19.9 15.4; 192 of 16,384 x 2,048: 16.0 14.4
 // mma.sync pays where each CTA's share is short: one round of CTAs, weights of up to 18 (9 to 16 rows: 6) million elements.
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
     const int64_t weights = (int64_t)a.n * a.k, groups = (a.n + kFewLanes - 1) / kFewLanes;
