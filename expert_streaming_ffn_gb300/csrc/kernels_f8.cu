@@ -402,128 +402,124 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 #pragma unroll
             for (int i = 0; i < kPer / 2; ++i) acc[i] = 0;
             const int lrow = lt * kLanes + 32 * q + lane;  // this thread's lane: a weight
-            {
-                const float* sw = a.sw + (int64_t)lt * a.sw_stride;
-                const int m0 = ct * C;
-                // Scales, rows' times weights', kChunk K-blocks at a time and a chunk ahead: a thread copies rows' scales to
-                // shared memory, and multiplies them by the weights' once they are there.
-                constexpr int kMine = kChunk * C / (32 * F::kEpi);
-                float w_next[kMine], w_now[kMine];
-                auto fetch = [&](int kb, int half_of) {
+            const float* sw = a.sw + (int64_t)lt * a.sw_stride;
+            const int m0 = ct * C;
+            // Scales, rows' times weights', kChunk K-blocks at a time and a chunk ahead: a thread copies rows' scales to
+            // shared memory, and multiplies them by the weights' once they are there.
+            constexpr int kMine = kChunk * C / (32 * F::kEpi);
+            float w_next[kMine], w_now[kMine];
+            auto fetch = [&](int kb, int half_of) {
 #pragma unroll
-                    for (int j = 0; j < kMine; ++j) {
-                        const int i = threadIdx.x + j * 32 * F::kEpi, b = kb + i / C, r = m0 + i % C;
-                        const bool in = b < kb1 && r < a.m;
-                        cp_async4(ptx::smem_addr(scales + half_of * kChunk * C + i),
-                                  a.sa + (in ? (int64_t)b * a.sa_stride + r : 0), in);
-                        w_next[j] = b < kb1 ? sw[b] : 0.0f;
+                for (int j = 0; j < kMine; ++j) {
+                    const int i = threadIdx.x + j * 32 * F::kEpi, b = kb + i / C, r = m0 + i % C;
+                    const bool in = b < kb1 && r < a.m;
+                    cp_async4(ptx::smem_addr(scales + half_of * kChunk * C + i),
+                              a.sa + (in ? (int64_t)b * a.sa_stride + r : 0), in);
+                    w_next[j] = b < kb1 ? sw[b] : 0.0f;
+                }
+                cp_async_commit();
+            };
+            fetch(kb0, 0);
+            int turn = 0;
+            for (int kc = kb0; kc < kb1; kc += kChunk, turn ^= 1) {  // to the end even after a failed wait: the warps meet at barriers
+                ptx::named_sync(1, 32 * F::kEpi);  // the other half's readers are done with it
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) w_now[j] = w_next[j];
+                fetch(kc + kChunk, turn ^ 1);
+                cp_async_wait<1>();
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) scales[turn * kChunk * C + threadIdx.x + j * 32 * F::kEpi] *= w_now[j];
+                ptx::named_sync(1, 32 * F::kEpi);
+                uint32_t sp = ptx::smem_addr(scales + turn * kChunk * C + col0);
+                const int n = min(kChunk, kb1 - kc);
+                for (int i = 0; i < n; ++i, sp += 4 * C) {
+                    if (ok && !__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + buf, bph, abortp))) {
+                        if (lane == 0) fail(4u);
+                        ok = false;
                     }
-                    cp_async_commit();
-                };
-                fetch(kb0, 0);
-                int turn = 0;
-                for (int kc = kb0; kc < kb1; kc += kChunk, turn ^= 1) {  // to the end even after a failed wait: the warps meet at barriers
-                    ptx::named_sync(1, 32 * F::kEpi);  // the other half's readers are done with it
+                    if (!ok) continue;
+                    ptx::tc_fence_after();
+                    uint32_t d[kPer];
+                    if constexpr (kPer == 32)
+                        tmem_ld32(taddr + buf * C, d);
+                    else
+                        ptx::tmem_ld16(taddr + buf * C, d);
+                    float4 s4[4];
 #pragma unroll
-                    for (int j = 0; j < kMine; ++j) w_now[j] = w_next[j];
-                    fetch(kc + kChunk, turn ^ 1);
-                    cp_async_wait<1>();
+                    for (int e = 0; e < 4; ++e) s4[e] = ptx::lds_f4(sp + 16 * e);
+                    ptx::tmem_ld_wait();
+                    ptx::tc_fence_before();
+                    arrive_one(lane == 0, ptx::smem_addr(acc_empty + buf));
 #pragma unroll
-                    for (int j = 0; j < kMine; ++j) scales[turn * kChunk * C + threadIdx.x + j * 32 * F::kEpi] *= w_now[j];
-                    ptx::named_sync(1, 32 * F::kEpi);
-                    uint32_t sp = ptx::smem_addr(scales + turn * kChunk * C + col0);
-                    const int n = min(kChunk, kb1 - kc);
-                    for (int i = 0; i < n; ++i, sp += 4 * C) {
-                        if (ok && !__all_sync(kFull, ptx::mbar_wait_sleep(acc_full + buf, bph, abortp))) {
-                            if (lane == 0) fail(4u);
-                            ok = false;
-                        }
-                        if (!ok) continue;
-                        ptx::tc_fence_after();
-                        uint32_t d[kPer];
-                        if constexpr (kPer == 32)
-                            tmem_ld32(taddr + buf * C, d);
-                        else
-                            ptx::tmem_ld16(taddr + buf * C, d);
-                        float4 s4[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s4[e] = ptx::lds_f4(sp + 16 * e);
-                        ptx::tmem_ld_wait();
-                        ptx::tc_fence_before();
-                        arrive_one(lane == 0, ptx::smem_addr(acc_empty + buf));
-#pragma unroll
-                        for (int e = 0; e < kPer / 4; ++e) {
-                            const float4 x = e < 4 ? s4[e & 3] : ptx::lds_f4(sp + 16 * e);
-                            acc[2 * e] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])),
-                                                   ptx::f2(x.x, x.y), acc[2 * e]);
-                            acc[2 * e + 1] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e + 2]), __uint_as_float(d[4 * e + 3])),
-                                                       ptx::f2(x.z, x.w), acc[2 * e + 1]);
-                        }
-                        if (++buf == kBufs) {
-                            buf = 0;
-                            bph ^= 1;
-                        }
+                    for (int e = 0; e < kPer / 4; ++e) {
+                        const float4 x = e < 4 ? s4[e & 3] : ptx::lds_f4(sp + 16 * e);
+                        acc[2 * e] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])),
+                                               ptx::f2(x.x, x.y), acc[2 * e]);
+                        acc[2 * e + 1] = ptx::fma2(ptx::f2(__uint_as_float(d[4 * e + 2]), __uint_as_float(d[4 * e + 3])),
+                                                   ptx::f2(x.z, x.w), acc[2 * e + 1]);
+                    }
+                    if (++buf == kBufs) {
+                        buf = 0;
+                        bph ^= 1;
                     }
                 }
-                cp_async_wait<0>();
-                const int cols = min(kPer, a.m - m0 - col0);
-                if (T.splits == 1) {
-                    if (ok && lrow < a.n) {
-                        if (a.type == MOE_F32)
-                            store_columns<float>(a, m0 + col0, lrow, cols, acc);
-                        else if (a.type == MOE_BF16)
-                            store_columns<__nv_bfloat16>(a, m0 + col0, lrow, cols, acc);
-                        else
-                            store_columns<__half>(a, m0 + col0, lrow, cols, acc);
-                    }
-                    ptx::named_sync(1, 32 * F::kEpi);  // this tile's scales are read before the next tile's come
-                } else if (ok) {
-                    // the ring is done with: the last accumulator's MMAs have read it
-                    float* part = reinterpret_cast<float*>(ring) + col0 * kLanes + 32 * q + lane;
+            }
+            cp_async_wait<0>();
+            const int cols = min(kPer, a.m - m0 - col0);
+            if (T.splits == 1) {
+                if (ok && lrow < a.n) {
+                    if (a.type == MOE_F32)
+                        store_columns<float>(a, m0 + col0, lrow, cols, acc);
+                    else if (a.type == MOE_BF16)
+                        store_columns<__nv_bfloat16>(a, m0 + col0, lrow, cols, acc);
+                    else
+                        store_columns<__half>(a, m0 + col0, lrow, cols, acc);
+                }
+                ptx::named_sync(1, 32 * F::kEpi);  // this tile's scales are read before the next tile's come
+            } else if (ok) {
+                // the ring is done with: the last accumulator's MMAs have read it
+                float* part = reinterpret_cast<float*>(ring) + col0 * kLanes + 32 * q + lane;
 #pragma unroll
-                    for (int c = 0; c < kPer / 2; ++c) {
-                        if (2 * c >= cols) break;
-                        const float2 v = ptx::f2(acc[c]);
-                        part[(2 * c) * kLanes] = v.x;
-                        part[(2 * c + 1) * kLanes] = v.y;
-                    }
+                for (int c = 0; c < kPer / 2; ++c) {
+                    if (2 * c >= cols) break;
+                    const float2 v = ptx::f2(acc[c]);
+                    part[(2 * c) * kLanes] = v.x;
+                    part[(2 * c + 1) * kLanes] = v.y;
                 }
             }
         }
     }
-    {
-        if (T.splits > 1) {  // one tile a cluster
-            __syncwarp();
-            cluster_sync();
-            int lt, ct;
-            place(first, lt, ct);
-            if (warp < F::kEpi && !*abortp) {
-                // a warp a column, a lane four weights; the loads of two columns before the first sum, as a peer's memory is far
-                const int n = lt * kLanes + 4 * lane, cols = min(C, a.m - ct * C);
-                const uint32_t at = ptx::smem_addr(ring) + 16 * lane;
-                for (int j = warp; rank + T.splits * j < cols; j += 2 * F::kEpi) {
-                    float4 v[2][8];
+    if (T.splits > 1) {  // one tile a cluster
+        __syncwarp();
+        cluster_sync();
+        int lt, ct;
+        place(first, lt, ct);
+        if (warp < F::kEpi && !*abortp) {
+            // a warp a column, a lane four weights; the loads of two columns before the first sum, as a peer's memory is far
+            const int n = lt * kLanes + 4 * lane, cols = min(C, a.m - ct * C);
+            const uint32_t at = ptx::smem_addr(ring) + 16 * lane;
+            for (int j = warp; rank + T.splits * j < cols; j += 2 * F::kEpi) {
+                float4 v[2][8];
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        const int c = rank + T.splits * (j + F::kEpi * d);
+                for (int d = 0; d < 2; ++d) {
+                    const int c = rank + T.splits * (j + F::kEpi * d);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            v[d][r] = r < T.splits && c < cols ? ld_peer4(at + c * (kLanes * 4), r) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    }
+                    for (int r = 0; r < 8; ++r)
+                        v[d][r] = r < T.splits && c < cols ? ld_peer4(at + c * (kLanes * 4), r) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        const int c = rank + T.splits * (j + F::kEpi * d);
-                        if (c >= cols) break;
-                        float4 x = v[d][0];
+                for (int d = 0; d < 2; ++d) {
+                    const int c = rank + T.splits * (j + F::kEpi * d);
+                    if (c >= cols) break;
+                    float4 x = v[d][0];
 #pragma unroll
-                        for (int r = 1; r < 8; ++r) x.x += v[d][r].x, x.y += v[d][r].y, x.z += v[d][r].z, x.w += v[d][r].w;
-                        store4(a, (int64_t)(ct * C + c) * a.out_stride + n, x, a.n - n);
-                    }
+                    for (int r = 1; r < 8; ++r) x.x += v[d][r].x, x.y += v[d][r].y, x.z += v[d][r].z, x.w += v[d][r].w;
+                    store4(a, (int64_t)(ct * C + c) * a.out_stride + n, x, a.n - n);
                 }
             }
-            __syncwarp();
-            cluster_sync();  // a CTA's part stays until its peers have read it
         }
+        __syncwarp();
+        cluster_sync();  // a CTA's part stays until its peers have read it
     }
     ptx::tc_fence_before();
     __syncthreads();
