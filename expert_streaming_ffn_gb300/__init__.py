@@ -234,13 +234,18 @@ def _new(shape, dtype, device, stream):
 # context and layer
 
 
+_ctx_devices = {}  # of the contexts created here
+
+
 def moe_ctx_create(device: int = 0) -> int:
     h = ctypes.c_void_p()
     _check(load().moe_ctx_create(device, ctypes.byref(h)), "moe_ctx_create")
+    _ctx_devices[h.value] = device
     return h.value
 
 
 def moe_ctx_destroy(ctx: int) -> None:
+    _ctx_devices.pop(ctx, None)
     load().moe_ctx_destroy(ctx)
 
 
@@ -748,10 +753,12 @@ def _dense_stream(stream, device: int):
     return getattr(stream, "cuda_stream", stream)
 
 
-def _cuda(t, what: str) -> int:
+def _cuda(ctx, t, what: str) -> int:
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
+    if _ctx_devices.get(ctx, device) != device:
+        raise ValueError(f"{what}: on {t.device}, the context on cuda:{_ctx_devices[ctx]}")
     return device
 
 
@@ -763,7 +770,7 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
     [n][d] and f32 scales [ceil(d / 128)][n] of the same rows (None, None without). Outputs given are filled."""
     torch = _torch or _kv_torch()
     shape, st = x.shape, x.stride()
-    device, where = _cuda(x, "x"), x.device
+    device, where = _cuda(ctx, x, "x"), x.device
     if len(st) == 3:
         shape = n, heads, d = tuple(shape)
         ht, tt = d, heads * d  # strides of a new tensor
@@ -829,7 +836,7 @@ def moe_rms_norm(ctx: int, x, weight=None, eps: float = 1e-6, residual=None, dty
 
 def _f8_quant(fn: str, ctx: int, x, weight: bool, codes, scales, stream):
     torch = _torch or _kv_torch()
-    device, where = _cuda(x, "x"), x.device
+    device, where = _cuda(ctx, x, "x"), x.device
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x: expected [n][k]")
@@ -869,7 +876,7 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
     """The product of 8-bit rows a [m][k] and weights w [n][k], each as moe_f8_quant_rows and moe_f8_quant_weight
     give them: out [m][n] of dtype (bf16 unless given)."""
     torch = _torch or _kv_torch()
-    device = _cuda(a, "a")
+    device = _cuda(ctx, a, "a")
     of_a, of_w = a.shape, w.shape
     if len(of_a) != 2 or len(of_w) != 2:
         raise ValueError("a and w: expected [m][k] and [n][k]")

@@ -576,3 +576,14 @@ def test_offsets_past_32_bits(ctx, dtype):
     y = torch.empty(((n - 1) * stride + 500,), dtype=T[dtype], device="cuda").as_strided((n, 500), (stride, 1))
     moe.moe_f8_matmul(ctx, c1, s1, *w, out=y)
     assert (y == moe.moe_f8_matmul(ctx, c1, s1, *w, dtype=T[dtype])).all()
+
+
+def test_tensors_on_another_device_than_the_context(ctx, monkeypatch):
+    """A context of another device is refused in the binding, before anything is launched."""
+    x = randn(rng(10), 4, 256)
+    a, w = moe.moe_f8_quant_rows(ctx, x), moe.moe_f8_quant_weight(ctx, x)
+    monkeypatch.setitem(moe._ctx_devices, ctx, 1)
+    for call in (lambda: moe.moe_rms_norm(ctx, x), lambda: moe.moe_f8_quant_rows(ctx, x),
+                 lambda: moe.moe_f8_quant_weight(ctx, x), lambda: moe.moe_f8_matmul(ctx, *a, *w)):
+        with pytest.raises(ValueError, match="context"):
+            call()
