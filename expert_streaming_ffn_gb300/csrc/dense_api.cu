@@ -29,6 +29,10 @@ bool rows_ok(const void* p, int64_t ts, int64_t hs, moe_dtype t) {
 
 int blocks(int n) { return (n - 1) / kF8Block + 1; }
 
+// Most rows, and most elements of a row: the launchers and kernels round these up to whole tiles and step past
+// the end by part of one in 32 bits.
+constexpr int32_t kMaxRows = 0x7FFFFFFF - 1023, kMaxK = 1 << 30;
+
 // Counts a launch; with profiling on, times it.
 struct Launch {
     void* rec = nullptr;
@@ -47,7 +51,8 @@ moe_status quant(const char* who, moe_ctx* C, const void* x, int64_t x_stride, m
                  void* codes, int64_t code_stride, float* scales, int64_t scale_stride, bool weight, void* stream) {
     if (!C) return set_error(MOE_EINVAL, "%s: ctx is NULL", who);
     if (!type_ok(dtype)) return set_error(MOE_EINVAL, "%s: dtype %d (MOE_F32, MOE_F16 or MOE_BF16)", who, (int)dtype);
-    if (n < 0 || k < 16 || k % 16) return set_error(MOE_EINVAL, "%s: n = %d, k = %d (k a multiple of 16)", who, n, k);
+    if (n < 0 || n > kMaxRows || k < 16 || k % 16 || k > kMaxK)
+        return set_error(MOE_EINVAL, "%s: n = %d, k = %d (n at most 2^31 - 1024; k a multiple of 16, 16 to 2^30)", who, n, k);
     if (n == 0) return MOE_OK;
     if ((int64_t)(weight ? blocks(n) : n) * blocks(k) >= ((int64_t)1 << 31) - 1024)
         return set_error(MOE_EINVAL, "%s: more than 2^31 - 1024 blocks", who);
@@ -142,7 +147,7 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
     if (!C || !p) return set_error(MOE_EINVAL, "%s: NULL argument", who);
     if (!type_ok(p->out_dtype))
         return set_error(MOE_EINVAL, "%s: out_dtype %d (MOE_F32, MOE_F16 or MOE_BF16)", who, (int)p->out_dtype);
-    if (p->m < 0 || p->n < 1 || p->k < 16 || p->k % 16 || p->k > 1 << 30)
+    if (p->m < 0 || p->n < 1 || p->k < 16 || p->k % 16 || p->k > kMaxK)
         return set_error(MOE_EINVAL, "%s: m = %d, n = %d, k = %d (k a multiple of 16, 16 to 2^30)", who, p->m, p->n, p->k);
     if (p->m == 0) return MOE_OK;
     if ((int64_t)blocks(p->m) * blocks(p->n) >= (int64_t)1 << 29)

@@ -648,8 +648,8 @@ typedef struct {
  * Errors: MOE_EINVAL, MOE_ECUDA. */
 moe_status moe_rms_norm(moe_ctx* ctx, const moe_norm_args* args, void* stream);
 
-/* Quantise rows x [n][k] (k a multiple of 16), for what no norm makes: attention's
- * output before its projection, say. code_stride is a multiple of 16.
+/* Quantise rows x [n][k] (n at most 2^31 - 1024; k a multiple of 16, at most 2^30; fewer than 2^31 - 1024
+ * blocks in all), for what no norm makes: attention's output before its projection, say. code_stride is a multiple of 16.
  * Errors: MOE_EINVAL, MOE_ECUDA. */
 moe_status moe_f8_quant_rows(moe_ctx* ctx, const void* x, int64_t x_stride, moe_dtype dtype, int32_t n, int32_t k,
                              void* codes, int64_t code_stride, float* scales, int64_t scale_stride, void* stream);

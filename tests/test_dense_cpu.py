@@ -94,3 +94,29 @@ def test_binding_refuses_host_tensors():
                  lambda: moe.moe_f8_matmul(0, c, s, c, s)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+TOP = (1 << 31) - 1024  # the most rows
+
+
+def taken(call):
+    """A call that is not refused, which must not find a device: its addresses are none."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("the call would be launched")
+    assert call() == moe.MOE_ECUDA
+
+
+@pytest.mark.parametrize("fn", ["moe_f8_quant_rows", "moe_f8_quant_weight"])
+@pytest.mark.parametrize("n,k", [(1, (1 << 31) - 16), (1, (1 << 31) - 112), (1, (1 << 31) - 128), (1, (1 << 30) + 16), ((1 << 31) - 1, 16),
+                                 ((1 << 31) - 128, 16), (TOP + 1, 16)])
+def test_quant_refuses_sizes_that_32_bits_do_not_hold_rounded_up(lib, fn, n, k):
+    """Rounded up to blocks and tiles, and a part of a tile further, sizes stay below 2^31."""
+    assert getattr(lib, fn)(CTX, P, k, moe.MOE_F16, n, k, P, k, P, n, None) == moe.MOE_EINVAL
+    assert "at most" in moe.moe_last_error()
+
+
+@pytest.mark.parametrize("fn", ["moe_f8_quant_rows", "moe_f8_quant_weight"])
+@pytest.mark.parametrize("n,k", [(1, 1 << 30), (3, 1 << 30)])
+def test_quant_takes_the_largest_rows(lib, fn, n, k):
+    taken(lambda: getattr(lib, fn)(CTX, P, k, moe.MOE_F16, n, k, P, k, P, k, None))
