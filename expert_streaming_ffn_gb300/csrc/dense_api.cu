@@ -147,8 +147,9 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
     if (!C || !p) return set_error(MOE_EINVAL, "%s: NULL argument", who);
     if (!type_ok(p->out_dtype))
         return set_error(MOE_EINVAL, "%s: out_dtype %d (MOE_F32, MOE_F16 or MOE_BF16)", who, (int)p->out_dtype);
-    if (p->m < 0 || p->n < 1 || p->k < 16 || p->k % 16 || p->k > kMaxK)
-        return set_error(MOE_EINVAL, "%s: m = %d, n = %d, k = %d (k a multiple of 16, 16 to 2^30)", who, p->m, p->n, p->k);
+    if (p->m < 0 || p->m > kMaxRows || p->n < 1 || p->n > kMaxRows || p->k < 16 || p->k % 16 || p->k > kMaxK)
+        return set_error(MOE_EINVAL, "%s: m = %d, n = %d, k = %d (m and n at most 2^31 - 1024; k a multiple of 16, 16 to 2^30)", who,
+                         p->m, p->n, p->k);
     if (p->m == 0) return MOE_OK;
     if ((int64_t)blocks(p->m) * blocks(p->n) >= (int64_t)1 << 29)
         return set_error(MOE_EINVAL, "%s: m = %d by n = %d is too large", who, p->m, p->n);

@@ -669,7 +669,8 @@ typedef struct {
     int64_t w_scale_stride;
     void* out; /* [m][n] of out_dtype, rows out_stride apart; any alignment and stride of elements */
     int64_t out_stride;
-    int32_t m, n, k; /* n >= 1; k a multiple of 16; any m >= 0 */
+    int32_t m, n, k; /* 0 <= m, 1 <= n, both at most 2^31 - 1024, and fewer than 2^29 blocks of out of 128 x 128;
+                        k a multiple of 16, at most 2^30 */
     moe_dtype out_dtype;
 } moe_f8_matmul_args;
 

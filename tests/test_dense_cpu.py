@@ -120,3 +120,19 @@ def test_quant_refuses_sizes_that_32_bits_do_not_hold_rounded_up(lib, fn, n, k):
 @pytest.mark.parametrize("n,k", [(1, 1 << 30), (3, 1 << 30)])
 def test_quant_takes_the_largest_rows(lib, fn, n, k):
     taken(lambda: getattr(lib, fn)(CTX, P, k, moe.MOE_F16, n, k, P, k, P, k, None))
+
+
+@pytest.mark.parametrize("size", [dict(m=(1 << 31) - 1), dict(m=(1 << 31) - 255), dict(m=TOP + 1), dict(n=(1 << 31) - 1),
+                                  dict(n=(1 << 31) - 15), dict(n=TOP + 1)])
+def test_matmul_refuses_sizes_that_32_bits_do_not_hold_rounded_up(lib, size):
+    big = 1 << 31
+    bad = dict(dict(m=1, n=1, k=16, a_stride=16, w_stride=16, a_scale_stride=big, w_scale_stride=big, out_stride=big), **size)
+    assert lib.moe_f8_matmul(CTX, ctypes.byref(matmul_args(**bad)), None) == moe.MOE_EINVAL
+    assert "at most" in moe.moe_last_error()
+
+
+@pytest.mark.parametrize("size", [dict(m=TOP), dict(n=TOP), dict(k=1 << 30, a_stride=1 << 30, w_stride=1 << 30, w_scale_stride=1 << 23)])
+def test_matmul_takes_the_largest_sizes(lib, size):
+    big = 1 << 31
+    args = dict(dict(m=1, n=1, k=16, a_stride=16, w_stride=16, a_scale_stride=big, w_scale_stride=big, out_stride=big), **size)
+    taken(lambda: lib.moe_f8_matmul(CTX, ctypes.byref(matmul_args(**args)), None))
