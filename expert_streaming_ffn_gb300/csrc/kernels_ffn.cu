@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < NT; ++q) row[q] = (q < nt ? list.pair[it.pb + q] : 0) / x_div;
         // ---- the unit's token rows as B fragments, unless staged already ----
+        // (read without a wait: the router lets this kernel start only once x is there)
         {
             bool same = staged_key[0] == nt;
 #pragma unroll

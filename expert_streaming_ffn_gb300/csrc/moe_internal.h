@@ -151,7 +151,8 @@ struct RouterParams {
 
 // pdl: launch as a programmatic dependent of the previous kernel on the
 // stream. The router then only prefetches its weights before it waits for
-// that kernel to finish; it lets the next kernel start early as well.
+// that kernel to finish, and then lets the next kernel, which may read x
+// without waiting, start early as well.
 cudaError_t launch_router(const RouterParams& p, cudaStream_t s, bool pdl = false);
 
 // The ordered decode combine: y[t][n] = S + O_0 + ... + O_{k-1}, where S is
