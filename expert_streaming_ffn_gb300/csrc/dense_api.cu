@@ -118,7 +118,6 @@ extern "C" moe_status moe_rms_norm(moe_ctx* C, const moe_norm_args* p, void* str
     a.inv_dim = 1.0f / (float)p->dim;
     a.by_head = FastDiv((uint32_t)p->n_heads);
     a.x_type = p->x_dtype, a.res_type = p->residual_dtype, a.weight_type = p->weight_dtype, a.out_type = p->out_dtype;
-    a.early = may_release_early(p->sum != nullptr, p->residual_dtype) && may_release_early(p->out != nullptr, p->out_dtype);
     double per = type_size(p->x_dtype);
     if (p->residual) per += type_size(p->residual_dtype);
     if (p->sum) per += type_size(p->residual_dtype);
@@ -175,7 +174,6 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
     a.m = p->m, a.n = p->n, a.k = p->k;
     a.type = p->out_dtype;
     a.err = ctx_f8_err(C);
-    a.early = may_release_early(true, p->out_dtype);
     cudaStream_t s = (cudaStream_t)stream;
     const double m = p->m, n = p->n, k = p->k;
     Launch l(C, K_F8_MATMUL, m * k + n * k + m * n * type_size(p->out_dtype) + 4.0 * blocks(p->k) * (m + blocks(p->n)),

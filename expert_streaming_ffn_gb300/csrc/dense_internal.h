@@ -9,11 +9,6 @@ namespace moe {
 constexpr int kF8Block = 128;  // elements (of a row; each way of a weight) that share a scale
 constexpr int kNormMaxDim = 32768;
 
-// Whether a kernel that writes outputs of these types may let the next one start before it is done. moe_forward's expert
-// kernel reads its bf16 rows x before it waits for what is in front of it (the router, which lets it start at once), so x
-// has to be there when the router starts: a kernel that may be writing x does not let it start early.
-inline bool may_release_early(bool writes, moe_dtype t) { return !writes || t != MOE_BF16; }
-
 struct NormArgs {
     const void* x;
     const void* res;     // or null
@@ -29,7 +24,6 @@ struct NormArgs {
     float eps, inv_dim;
     FastDiv by_head{1};
     moe_dtype x_type, res_type, weight_type, out_type;  // sum has res_type
-    bool early;  // may_release_early()
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int sms, cudaStream_t s);
 
@@ -55,7 +49,6 @@ struct MatmulArgs {
     int m, n, k;
     moe_dtype type;  // of out
     unsigned* err;   // mapped word: a bounded wait expired
-    bool early;      // may_release_early()
 };
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s);
 

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
         for (int kb = kb0; kb < min(kb1, kb0 + 2 * kStages); ++kb) prefetch_box(&map_lanes, kb * 128, lt * kLanes);
     }
     ptx::pdl_wait();
-    if (a.early) ptx::pdl_launch_dependents();
+    ptx::pdl_launch_dependents();
 
     if (warp >= F::kEpi) {
         if (warp == F::kEpi) {
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         abort_flag = 1;
     };
     ptx::pdl_wait();
-    if (a.early) ptx::pdl_launch_dependents();
+    ptx::pdl_launch_dependents();
 
     const int first = (int)blockIdx.x / (2 * splits), step = (int)gridDim.x / (2 * splits);
     const int kb0 = (int)((int64_t)T.kblocks * share / splits);
@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.w + n * a.w_stride), "r"(min(a.k, 16384)) : "memory");
     }
     ptx::pdl_wait();
-    if (a.early) ptx::pdl_launch_dependents();
+    ptx::pdl_launch_dependents();
     const uint8_t* ap[NT];
     bool ain[NT];
 #pragma unroll

@@ -150,7 +150,7 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], float s, float i
 template <int XB, int RB, int V, int U, bool kCta>
 __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a, const int group) {
     ptx::pdl_wait();
-    if (a.early) ptx::pdl_launch_dependents();
+    ptx::pdl_launch_dependents();
     const int G = kCta ? (int)blockDim.x : group;
     const unsigned per = kCta ? 1 : blockDim.x / (unsigned)group;
     const int i = kCta ? (int)threadIdx.x : (int)threadIdx.x & (G - 1);
