@@ -133,6 +133,18 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The same for a count that unrolling makes a constant.
+__device__ __forceinline__ void cp_async_wait_at_most(int n) {
+    if (n == 3)
+        cp_async_wait<3>();
+    else if (n == 2)
+        cp_async_wait<2>();
+    else if (n == 1)
+        cp_async_wait<1>();
+    else
+        cp_async_wait<0>();
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -919,15 +931,16 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
 // ---- a few rows ------------------------------------------------------------------
 //
 // Up to 16 rows are bound by the weights' way from memory, and short calls by latency. So there are no roles and no
-// tensor memory: a CTA takes 16 weights at a time, its warps take their K-blocks in turn, and the product is
+// tensor memory: a CTA takes 16 weights, its warps take their K-blocks in turn, and the product is
 // mma.sync's (m16n8k32, e4m3, the weights as the 16). The order of K within a block is free as long as both operands
 // share it, so a lane takes 16 consecutive bytes of a row, four words of which pairs feed two MMAs. A lane copies
-// exactly the weights that it will use itself (cp.async), so its shared memory is a queue of its own: nothing to
-// synchronise, no bank conflict, and kFewDeep K-blocks a warp in flight at no cost in registers. (Loads into registers, as
-// many in flight, left one CTA on an SM: 8.3 us below.)
-// 6,144 weights of 2,816 by one row, 17.3 MB: 5.6 us (floor 2.6); 1,024 of 1,024: 1.8 us, the launch.
+// exactly the weights that it will use itself (cp.async), so its shared memory is its own: nothing to
+// synchronise, no bank conflict, and all of a warp's K-blocks, kFewDeep at most, in flight at no cost in registers. (Loads into
+// registers, as many in flight, left one CTA on an SM: 8.3 us below.)
+// 6,144 weights of 2,816 by one row, 17.3 MB: 4.6 us (floor 2.6); 1,024 of 1,024: 1.5 us, the launch.
 
 constexpr int kFewWarps = 8, kFewDeep = 4, kFewLanes = 16;
+constexpr int kFewMaxK = kFewWarps * kFewDeep * kF8Block;
 constexpr int kFewSmem = kFewWarps * kFewDeep * 4 * 512;
 constexpr int few_ctas(int NT) { return NT == 1 ? 3 : 2; }  // resident on an SM
 
@@ -952,18 +965,15 @@ struct FewRows {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
-    f8_few_kernel(const __grid_constant__ MatmulArgs a, const int kblocks, const int groups) {
+__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT)) f8_few_kernel(const __grid_constant__ MatmulArgs a, const int kblocks) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ float part[2][kFewWarps][8 * NT][kFewLanes + 1];
+    __shared__ float part[kFewWarps][8 * NT][kFewLanes + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t queue = ptx::smem_addr(smem_raw) + warp * (kFewDeep * 4 * 512) + lane * 16;
-    {
-        // the weights may be what the kernel before writes, so they are only brought into L2 before the wait
-        const int64_t n = (int64_t)blockIdx.x * kFewLanes + threadIdx.x;
-        if (threadIdx.x < kFewLanes && n < a.n)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.w + n * a.w_stride), "r"(min(a.k, 16384)) : "memory");
-    }
+    const int64_t n0 = (int64_t)blockIdx.x * kFewLanes;  // the CTA's weights
+    const uint32_t own = ptx::smem_addr(smem_raw) + warp * (kFewDeep * 4 * 512) + lane * 16;
+    // the weights may be what the kernel before writes, so they are only brought into L2 before the wait
+    if (threadIdx.x < kFewLanes && n0 + threadIdx.x < a.n)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.w + (n0 + threadIdx.x) * a.w_stride), "r"(a.k) : "memory");
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const uint8_t* ap[NT];
@@ -973,32 +983,25 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
         ain[i] = 8 * i + g < a.m;
         ap[i] = a.a + (ain[i] ? (8 * i + g) * a.a_stride : 0) + 16 * t;
     }
-    // the next K-block to copy: of group pg, block pk
-    int pg = blockIdx.x, pk = warp, ps = 0;
-    auto copy = [&] {
-        if (pg < groups && pk < kblocks) {
-            const int k = pk * kF8Block + 16 * t;
+#pragma unroll
+    for (int d = 0; d < kFewDeep; ++d) {
+        const int kb = warp + kFewWarps * d, k = kb * kF8Block + 16 * t;
+        if (kb < kblocks) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t n = (int64_t)pg * kFewLanes + g + 8 * h;
+                const int64_t n = n0 + g + 8 * h;
                 const uint8_t* p = a.w + (n < a.n ? n * a.w_stride : 0);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const bool in = n < a.n && k + 64 * c < a.k;
-                    cp_async16(queue + ps * 2048 + (2 * h + c) * 512, p + (in ? k + 64 * c : 0), in);
+                    cp_async16(own + d * 2048 + (2 * h + c) * 512, p + (in ? k + 64 * c : 0), in);
                 }
             }
         }
         cp_async_commit();
-        ps = ps + 1 == kFewDeep ? 0 : ps + 1;
-        pk += kFewWarps;
-        if (pk >= kblocks) {
-            pk = warp;
-            pg += gridDim.x;
-        }
-    };
-    auto rows = [&](FewRows<NT>& r, int group, int kb) {
-        const bool in = group < groups && kb < kblocks;
+    }
+    auto rows = [&](FewRows<NT>& r, int kb) {
+        const bool in = kb < kblocks;
         const int k = kb * kF8Block;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -1009,73 +1012,65 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NT))
                 const int m = 8 * i + 2 * t + c;
                 r.s[i][c] = in && m < a.m ? a.sa[(int64_t)kb * a.sa_stride + m] : 0.0f;
             }
-        r.w = in ? a.sw[(int64_t)(group / (kF8Block / kFewLanes)) * a.sw_stride + kb] : 0.0f;
+        r.w = in ? a.sw[n0 / kF8Block * a.sw_stride + kb] : 0.0f;
     };
-#pragma unroll
-    for (int d = 0; d < kFewDeep; ++d) copy();
     FewRows<NT> next;
-    rows(next, blockIdx.x, warp);
-    int cs = 0, turn = 0;
-    for (int group = blockIdx.x; group < groups; group += gridDim.x, turn ^= 1) {
-        float acc[NT][4] = {};
-        for (int kb = warp; kb < kblocks; kb += kFewWarps) {
-            const FewRows<NT> r = next;
-            const bool last = kb + kFewWarps >= kblocks;
-            rows(next, last ? group + (int)gridDim.x : group, last ? warp : kb + kFewWarps);
-            cp_async_wait<kFewDeep - 1>();
-            uint4 w[2][2];
+    rows(next, warp);
+    float acc[NT][4] = {};
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+    for (int d = 0; d < kFewDeep; ++d) {
+        const int kb = warp + kFewWarps * d;
+        if (kb >= kblocks) break;
+        const FewRows<NT> r = next;
+        rows(next, kb + kFewWarps);
+        cp_async_wait_at_most(kFewDeep - 1 - d);
+        uint4 w[2][2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) w[h][c] = ptx::lds_u4(queue + cs * 2048 + (2 * h + c) * 512);
-            cs = cs + 1 == kFewDeep ? 0 : cs + 1;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                float s[4] = {};
+            for (int c = 0; c < 2; ++c) w[h][c] = ptx::lds_u4(own + d * 2048 + (2 * h + c) * 512);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint4 u = w[0][c], v = w[1][c], b = r.x[i][c];
-                    mma_e4m3(s, u.x, v.x, u.y, v.y, b.x, b.y);
-                    mma_e4m3(s, u.z, v.z, u.w, v.w, b.z, b.w);
-                }
-                // lanes hold rows 2t, 2t + 1 of weights g and g + 8
+        for (int i = 0; i < NT; ++i) {
+            float s[4] = {};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float sc = r.s[i][c] * r.w;
-                    acc[i][c] = fmaf(s[c], sc, acc[i][c]);
-                    acc[i][2 + c] = fmaf(s[2 + c], sc, acc[i][2 + c]);
-                }
+            for (int c = 0; c < 2; ++c) {
+                const uint4 u = w[0][c], v = w[1][c], b = r.x[i][c];
+                mma_e4m3(s, u.x, v.x, u.y, v.y, b.x, b.y);
+                mma_e4m3(s, u.z, v.z, u.w, v.w, b.z, b.w);
             }
-            copy();  // into the place just read
+            // lanes hold rows 2t, 2t + 1 of weights g and g + 8
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float sc = r.s[i][c] * r.w;
+                acc[i][c] = fmaf(s[c], sc, acc[i][c]);
+                acc[i][2 + c] = fmaf(s[2 + c], sc, acc[i][2 + c]);
+            }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[turn][warp][8 * i + 2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[i][e];
-        __syncthreads();
-        // (the other half of `part` is written meanwhile, and this one only after the next barrier)
-        if (threadIdx.x < 8 * NT * kFewLanes) {
-            const int r = threadIdx.x / kFewLanes, c = threadIdx.x % kFewLanes;
-            const int64_t n = (int64_t)group * kFewLanes + c;
-            float v = 0.0f;
+        for (int e = 0; e < 4; ++e) part[warp][8 * i + 2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[i][e];
+    __syncthreads();
+    if (threadIdx.x < 8 * NT * kFewLanes) {
+        const int r = threadIdx.x / kFewLanes, c = threadIdx.x % kFewLanes;
+        float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) v += part[turn][w][r][c];
-            if (r < a.m && n < a.n) store1(a.out, r * a.out_stride + n, v, a.type);
-        }
+        for (int w = 0; w < kFewWarps; ++w) v += part[w][r][c];
+        if (r < a.m && n0 + c < a.n) store1(a.out, r * a.out_stride + n0 + c, v, a.type);
     }
     cp_async_wait<0>();
 }
 
 template <int NT>
-cudaError_t launch_few(const MatmulArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_few(const MatmulArgs& a, cudaStream_t s) {
     static_assert(8 * NT * kFewLanes <= 32 * kFewWarps, "a thread an output");
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(f8_few_kernel<NT>), kFewSmem);
     if (e != cudaSuccess) return e;
-    const int groups = (a.n + kFewLanes - 1) / kFewLanes;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)std::min(groups, few_ctas(NT) * sms)), dim3(32 * kFewWarps), kFewSmem, s,
-                                                 true, &attr);
-    return cudaLaunchKernelEx(&cfg, f8_few_kernel<NT>, a, (a.k + kF8Block - 1) / kF8Block, groups);
+    const cudaLaunchConfig_t cfg =
+        launch_config(dim3((unsigned)((a.n + kFewLanes - 1) / kFewLanes)), dim3(32 * kFewWarps), kFewSmem, s, true, &attr);
+    return cudaLaunchKernelEx(&cfg, f8_few_kernel<NT>, a, (a.k + kF8Block - 1) / kF8Block);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1237,8 +1232,8 @@ double rows_form_us(const MatmulArgs& a, int sms, int* splits) {
 // mma.sync pays where each CTA's share is short: one round of CTAs, weights of up to 18 (9 to 16 rows: 6) million elements.
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
     const int64_t weights = (int64_t)a.n * a.k, groups = (a.n + kFewLanes - 1) / kFewLanes;
-    if (a.m <= 8 && weights <= 18000000 && a.k <= 4096 && groups <= few_ctas(1) * sms) return launch_few<1>(a, sms, s);
-    if (a.m <= 16 && weights <= 6000000 && a.k <= 2048 && groups <= few_ctas(2) * sms) return launch_few<2>(a, sms, s);
+    if (a.m <= 8 && weights <= 18000000 && a.k <= kFewMaxK && groups <= few_ctas(1) * sms) return launch_few<1>(a, s);
+    if (a.m <= 16 && weights <= 6000000 && a.k <= 2048 && groups <= few_ctas(2) * sms) return launch_few<2>(a, s);
     if (a.m <= 16) return launch_form<Form<16>>(a, sms, s);
     if (a.m <= 32) return launch_form<Form<32>>(a, sms, s);
     if (a.m <= 64) return launch_form<Form<64>>(a, sms, s);

@@ -1,0 +1,30 @@
+"""The forms of the 8-bit product at the ends of their ranges. Bounds and helpers are those of test_gpu_dense.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import expert_streaming_ffn_gb300 as moe  # noqa: E402
+import test_gpu_dense as dense  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = moe.moe_ctx_create(0)
+    yield c
+    moe.moe_ctx_destroy(c)
+
+
+def check(ctx, m, n, k, dtype):
+    ops = dense.operands(dense.rng(m + n + k), m, n, k)
+    dense.check_matmul(*ops, moe.moe_f8_matmul(ctx, *ops, dtype=dense.T[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 7, 8, 9, 16])
+@pytest.mark.parametrize("n,k", [(1, 16), (15, 128), (17, 144), (33, 1024), (129, 1040), (4864, 2048), (4865, 2048), (2000, 2064), (1000, 4096),
+                                 (1001, 4112), (4864, 4096), (4865, 4080), (7296, 2448), (7297, 2448), (7296, 4096)])
+def test_up_to_16_rows(ctx, m, n, k, dtype):
+    """A K-block a warp and fewer, up to as many as it holds, and one more; a round of CTAs of 16 weights, three or two
+    an SM, and one more."""
+    check(ctx, m, n, k, dtype)
