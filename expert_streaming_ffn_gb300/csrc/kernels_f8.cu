@@ -4,7 +4,7 @@
 //
 // The tensor cores multiply e4m3 codes and sum a K-block in fp32; as every K-block has scales of its own, scale * sum is
 // added in fp32 registers, K-block by K-block, in order. Three forms (launch_f8_matmul chooses):
-//   up to 16 rows and weights of no great size: mma.sync straight from each lane's own copies (f8_few_kernel);
+//   up to 16 rows and one round of CTAs, K up to 4,096: mma.sync straight from each lane's own copies (f8_few_kernel);
 //   weights form (f8_matmul_kernel): tcgen05.mma, 128 weights as its lanes, which share a scale, and 16, 32 or 64 rows as
 //     its columns, so that no tensor work or memory goes to rows that are not there;
 //   rows form (f8_rows_kernel): tcgen05.mma of CTA pairs, 256 rows as its lanes by 256 weights.
@@ -1224,16 +1224,20 @@ double rows_form_us(const MatmulArgs& a, int sms, int* splits) {
 }
 }  // namespace
 
-// Measured, us (columns: mma.sync, weights form of 16 / 32 / 64 rows, rows form):
-//   8 rows:   6,144 x 2,816: 5.6 7.7; 2,816 x 704: 2.2 3.4; 20,000 x 512: 4.7 3.6; 16,384 x 2,048: 9.2 8.8; 640 x 8,192: 6.5 5.1
-//   16 rows:  1,024 x 1,024: 2.0 3.6; 2,816 x 704: 2.7 3.4; 2,816 x 4,096: 6.3 5.2; 6,144 x 2,816: 8.5 7.7
-//   64 rows (of 32, of 64, rows): 2,816 x 4,096: 8.3 8.4 15.5; 8,192 x 8,192: 19.0 17.4 25.5; 6,144 x 2,816: 8.5 9.4 12.6
-//   128 rows (of 64, rows): 6,144 x 2,816: 9.7 14.9; 512 of them: 19.9 15.4; 192 of 16,384 x 2,048: 16.0 14.4
-// mma.sync pays where each CTA's share is short: one round of CTAs, weights of up to 18 (9 to 16 rows: 6) million elements.
+// Measured, us (columns: mma.sync, weights form of 16 rows):
+//   1 row, one round of CTAs: 1,024 x 1,024 1.5 3.1; 6,144 x 2,816 4.7 7.0; 7,168 x 4,096 7.1 9.2
+//   8 rows, one round: 7,296 x 512 2.3 3.1; 2,816 x 4,096 4.6 5.0; 7,296 x 4,096 7.8 9.3; more: 8,192 x 1,024 4.3 4.7; 8,192 x 4,096
+//     10.8 9.6; 14,592 x 1,024 5.2 4.6; 20,000 x 512 5.8 3.7
+//   16 rows, one round: 1,024 x 1,024 2.0 3.4; 4,864 x 2,048 4.1 5.5; 2,048 x 4,096 4.1 5.0; 4,864 x 4,096 6.4 8.0, but 2,816 x 4,096
+//     5.6 5.2; more: 9,728 x 1,024 5.1 4.9; 8,192 x 2,048 7.0 5.9; 20,000 x 512 8.9 3.7
+// and (weights form of 32 / 64 rows, rows form):
+//   64 rows: 2,816 x 4,096: 7.4 6.3 16.6; 8,192 x 8,192: 18.8 17.3 27.7; 6,144 x 2,816: 8.4 8.8 13.6
+//   128 rows (of 64, rows): 6,144 x 2,816: 9.2 13.9; 512 of them: 21.3 14.9; 192 of 16,384 x 2,048: 16.4 13.7
+// mma.sync pays where the CTAs, of 16 weights each, are one round and a warp holds all of its K-blocks.
 cudaError_t launch_f8_matmul(const MatmulArgs& a, int sms, cudaStream_t s) {
-    const int64_t weights = (int64_t)a.n * a.k, groups = (a.n + kFewLanes - 1) / kFewLanes;
-    if (a.m <= 8 && weights <= 18000000 && a.k <= kFewMaxK && groups <= few_ctas(1) * sms) return launch_few<1>(a, s);
-    if (a.m <= 16 && weights <= 6000000 && a.k <= 2048 && groups <= few_ctas(2) * sms) return launch_few<2>(a, s);
+    const int groups = (a.n + kFewLanes - 1) / kFewLanes;
+    if (a.m <= 8 && a.k <= kFewMaxK && groups <= few_ctas(1) * sms) return launch_few<1>(a, s);
+    if (a.m <= 16 && a.k <= kFewMaxK && groups <= few_ctas(2) * sms) return launch_few<2>(a, s);
     if (a.m <= 16) return launch_form<Form<16>>(a, sms, s);
     if (a.m <= 32) return launch_form<Form<32>>(a, sms, s);
     if (a.m <= 64) return launch_form<Form<64>>(a, sms, s);
