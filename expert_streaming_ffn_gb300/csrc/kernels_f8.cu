@@ -1133,23 +1133,23 @@ cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, 
 // the rows form, clusters of 4 fill 144, of 8 120.
 template <class F, class K>
 int resident_clusters(K* kernel, int n) {
+    constexpr int kDevices = 64;
     static std::mutex mu;
-    static int device = -1, held[9];
+    static int held[kDevices][9];  // [device][n]; [device][0]: known
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    if (dev != device) {
-        for (int i = 1; i <= 8; ++i) {
-            cudaLaunchAttribute attr[2];
-            const cudaLaunchConfig_t cfg = cluster_config(8u * i, F::kThreads, F::kSmem, nullptr, (unsigned)i, attr);
-            if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                held[i] = 0;
-            }
+    int(&of)[9] = held[dev];
+    for (int i = 1; !of[0] && i <= 8; ++i) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = cluster_config(8u * i, F::kThreads, F::kSmem, nullptr, (unsigned)i, attr);
+        if (cudaOccupancyMaxActiveClusters(&of[i], kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            of[i] = 0;
         }
-        device = dev;
     }
-    return held[n];
+    of[0] = 1;
+    return of[n];
 }
 
 // CTAs that share a tile's K-blocks: as many as find room at once, at least two K-blocks each. Only where tiles leave
