@@ -138,6 +138,7 @@ SIGNATURES = [
     ("moe_ctx_reset_kernel_times", _i32, [_vp]),
     ("moe_ctx_launches", _i32, [_vp, _P(ctypes.c_uint64)]),
     ("moe_ctx_inject_copy_failure", _i32, [_vp, _i64]),
+    ("moe_ctx_inject_f8_timeout", _i32, [_vp]),
     ("moe_store_expert_stride", _sz, [_P(moe_shapes)]),
     ("moe_store_write", _i32, [ctypes.c_char_p, _P(moe_shapes), _P(moe_host_weights)]),
     ("moe_store_open", _i32, [ctypes.c_char_p, _P(moe_shapes), _i32, _i32, _i32, _P(_vp)]),
@@ -165,6 +166,7 @@ SIGNATURES = [
     ("moe_f8_quant_rows", _i32, [_vp, _vp, _i64, ctypes.c_int, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     ("moe_f8_quant_weight", _i32, [_vp, _vp, _i64, ctypes.c_int, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     ("moe_f8_matmul", _i32, [_vp, _vp, _vp]),
+    ("moe_f8_check", _i32, [_vp]),
 ]
 
 
@@ -903,6 +905,11 @@ def moe_f8_matmul(ctx: int, a, a_scales, w, w_scales, dtype=None, out=None, stre
     return out
 
 
+def moe_f8_check(ctx: int) -> None:
+    """Raises if a bounded device wait expired in a finished product since the last check."""
+    _check(load().moe_f8_check(ctx), "moe_f8_check")
+
+
 # ---------------------------------------------------------------------------
 # diagnostics
 
@@ -942,3 +949,7 @@ def moe_ctx_launches(ctx: int) -> int:
 
 def moe_ctx_inject_copy_failure(ctx: int, nth: int) -> None:
     _check(load().moe_ctx_inject_copy_failure(ctx, nth), "moe_ctx_inject_copy_failure")
+
+
+def moe_ctx_inject_f8_timeout(ctx: int) -> None:
+    _check(load().moe_ctx_inject_f8_timeout(ctx), "moe_ctx_inject_f8_timeout")

@@ -163,8 +163,8 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
         return set_error(MOE_EINVAL, "%s: rows of scales overlap", who);
     if (p->out_stride < p->n && p->m > 1) return set_error(MOE_EINVAL, "%s: rows of out overlap", who);
     CUDA_TRY(cudaSetDevice(ctx_device(C)));
-    if (unsigned code = ctx_f8_expired(C))
-        return set_error(MOE_ETIMEOUT, "%s: a bounded device wait expired in an earlier product (code %u)", who, code);
+    if (const unsigned code = *ctx_f8_word(C))  // for moe_f8_check to take back: the call that failed may be another thread's
+        return set_error(MOE_ETIMEOUT, "%s: a bounded device wait expired in an earlier product (code %u; moe_f8_check)", who, code);
     MatmulArgs a{};
     a.a = static_cast<const uint8_t*>(p->a), a.w = static_cast<const uint8_t*>(p->w);
     a.sa = p->a_scales, a.sw = p->w_scales;
@@ -179,5 +179,18 @@ extern "C" moe_status moe_f8_matmul(moe_ctx* C, const moe_f8_matmul_args* p, voi
     Launch l(C, K_F8_MATMUL, m * k + n * k + m * n * type_size(p->out_dtype) + 4.0 * blocks(p->k) * (m + blocks(p->n)),
              2 * m * n * k, s);
     CUDA_TRY(launch_f8_matmul(a, ctx_sms(C), s));
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_f8_check(moe_ctx* C) {
+    if (!C) return set_error(MOE_EINVAL, "moe_f8_check: ctx is NULL");
+    if (const unsigned code = __atomic_exchange_n(const_cast<unsigned*>(ctx_f8_word(C)), 0u, __ATOMIC_RELAXED))
+        return set_error(MOE_ETIMEOUT, "a bounded device wait expired in an earlier product (code %u)", code);
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_ctx_inject_f8_timeout(moe_ctx* C) {
+    if (!C) return set_error(MOE_EINVAL, "moe_ctx_inject_f8_timeout: ctx is NULL");
+    *ctx_f8_word(C) = 1u;
     return MOE_OK;
 }

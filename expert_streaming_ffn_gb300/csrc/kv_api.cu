@@ -55,7 +55,7 @@ void kv_state_destroy(KvState* st) {
 }
 
 unsigned* ctx_f8_err(moe_ctx* C) { return ctx_kv(C)->bad_dev + 2; }
-unsigned ctx_f8_expired(moe_ctx* C) { return __atomic_exchange_n(ctx_kv(C)->bad_host + 2, 0u, __ATOMIC_RELAXED); }
+volatile unsigned* ctx_f8_word(moe_ctx* C) { return ctx_kv(C)->bad_host + 2; }
 
 // Most query columns a sequence (new tokens times query heads of a kv head) that the decode kernel
 // takes: it reads the cache once a tile of columns, the prompt kernel once for 256 (128 at head_dim

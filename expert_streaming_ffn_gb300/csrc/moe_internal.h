@@ -359,8 +359,8 @@ void kv_state_destroy(KvState* st);
 int ctx_device(const moe_ctx* C);
 KvState* ctx_kv(moe_ctx* C);
 int ctx_sms(const moe_ctx* C);
-unsigned* ctx_f8_err(moe_ctx* C);     // device address of the word that notes an expired wait of a matrix product
-unsigned ctx_f8_expired(moe_ctx* C);  // its value, which it takes back
+unsigned* ctx_f8_err(moe_ctx* C);  // device address of the word that notes an expired wait of a matrix product
+volatile unsigned* ctx_f8_word(moe_ctx* C);  // its host address
 std::mutex& ctx_kv_mutex(moe_ctx* C);  // held by a cache call while it enqueues
 bool ctx_profiling(const moe_ctx* C);
 void ctx_count_launch(moe_ctx* C);

@@ -677,8 +677,14 @@ typedef struct {
 /* out[i][j] = sum over blocks b of 128 of k: a_scales[b][i] * w_scales[j / 128][b] * sum of a[i][l] * w[j][l] in b,
  * products exact, all sums in fp32, rounded once to out_dtype (past fp16's range to infinity). The product of two
  * scales is to be within fp32's range. out overlaps no input.
- * Errors: MOE_EINVAL, MOE_ECUDA, MOE_ETIMEOUT (a bounded device wait expired in an earlier product). */
+ * Errors: MOE_EINVAL, MOE_ECUDA, MOE_ETIMEOUT (a bounded device wait expired in an earlier product of the context, and
+ * moe_f8_check has not been called since; nothing is launched). */
 moe_status moe_f8_matmul(moe_ctx* ctx, const moe_f8_matmul_args* args, void* stream);
+
+/* MOE_ETIMEOUT if a bounded device wait expired in a finished product of the context, a replayed one too, since the last
+ * check: what products have written since then is not to be used. Else MOE_OK. Does not wait: synchronise first for an answer
+ * on the products enqueued so far. */
+moe_status moe_f8_check(moe_ctx* ctx);
 
 /* ---- diagnostics -------------------------------------------------------- */
 
@@ -711,6 +717,9 @@ moe_status moe_ctx_launches(moe_ctx* ctx, uint64_t* out);
  * that hits it returns MOE_ECOPY and leaves the affected slots empty; later
  * calls proceed normally. nth < 0 disarms. No device fault is involved. */
 moe_status moe_ctx_inject_copy_failure(moe_ctx* ctx, int64_t nth);
+
+/* The same for products: notes an expired wait exactly as a product's kernel does. */
+moe_status moe_ctx_inject_f8_timeout(moe_ctx* ctx);
 
 #ifdef __cplusplus
 }

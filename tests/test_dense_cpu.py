@@ -136,3 +136,8 @@ def test_matmul_takes_the_largest_sizes(lib, size):
     big = 1 << 31
     args = dict(dict(m=1, n=1, k=16, a_stride=16, w_stride=16, a_scale_stride=big, w_scale_stride=big, out_stride=big), **size)
     taken(lambda: lib.moe_f8_matmul(CTX, ctypes.byref(matmul_args(**args)), None))
+
+
+def test_check_and_injection_refuse_no_context(lib):
+    assert lib.moe_f8_check(None) == moe.MOE_EINVAL
+    assert lib.moe_ctx_inject_f8_timeout(None) == moe.MOE_EINVAL

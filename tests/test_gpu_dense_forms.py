@@ -28,3 +28,36 @@ def test_up_to_16_rows(ctx, m, n, k, dtype):
     """A K-block a warp and fewer, up to as many as it holds, and one more; a round of CTAs of 16 weights, three or two
     an SM, and one more."""
     check(ctx, m, n, k, dtype)
+
+
+def test_an_expired_wait_is_reported_until_it_is_asked_for(ctx):
+    """By every product, to whatever thread, and by the check, which takes it back; the cache's check does not; also behind the last
+    call, as with a replayed graph. (The note is made on the host.)"""
+    import threading
+
+    ops = dense.operands(dense.rng(0), 3, 100, 256)
+    want = moe.moe_f8_matmul(ctx, *ops, dtype=torch.float32)
+    torch.cuda.synchronize()
+    moe.moe_f8_check(ctx)
+    moe.moe_ctx_inject_f8_timeout(ctx)
+    errors = []
+
+    def other():
+        try:
+            moe.moe_f8_matmul(ctx, *ops)
+        except moe.MoeError as e:
+            errors.append(e.status)
+
+    for _ in range(2):
+        t = threading.Thread(target=other)
+        t.start()
+        t.join()
+    moe.moe_kv_check(ctx)
+    n = moe.moe_ctx_launches(ctx)
+    other()
+    assert errors == [moe.MOE_ETIMEOUT] * 3 and moe.moe_ctx_launches(ctx) == n
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_f8_check(ctx)
+    assert e.value.status == moe.MOE_ETIMEOUT
+    moe.moe_f8_check(ctx)
+    assert torch.equal(moe.moe_f8_matmul(ctx, *ops, dtype=torch.float32), want)
