@@ -14,6 +14,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLeast = 448.0f * 1.17549435e-38f;  // a block's largest magnitude counts as at least this: no scale is subnormal
+constexpr float kSmallScale = 0x1p-90f, kUp = 0x1p64f;  // blocks of smaller scales are divided with both sides taken kUp times
 
 // Eight consecutive elements of B bytes each, as loaded.
 template <int B>
@@ -121,10 +122,12 @@ __device__ __forceinline__ float block_scale(float largest, float& inv) {
     return s;
 }
 
-// Eight values to codes, the nearest to f / s. t = f y with y = 1 / s is within two ulps of the quotient, and in
+// Eight values to codes, the fp32 quotients f / s rounded. t = f y with y = 1 / s is within two ulps of the quotient, and in
 // t + y (f - s t) the remainder is exact in a fused multiply-add, so that the sum before its rounding is within 2^-21 ulp of
 // the quotient: ties between codes, which are short numbers, come out as such. A plain product f y would move them, and
-// 16-bit inputs have many.
+// 16-bit inputs have many. (Exact as long as the remainder's last place is in fp32's range: for t of 2^-10, half the least
+// code, it is 2^-56 of s, which 2^-149 allows for s from 2^-93 on; for smaller ones the quantisers take small_codes8. The norm does
+// not: its values are products rounded before, so that a tie is chance, and two multiplies a pair took 2 % of 32,768 x 2,816 from bf16.)
 __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], float s, float inv) {
     uint32_t h[4];
     const uint64_t yy = ptx::f2(inv, inv), ns = ptx::f2(-s, -s);
@@ -293,9 +296,27 @@ cudaError_t launch_norm_of(const NormArgs& a, int sms, cudaStream_t s) {
                   : a.res_type == MOE_F32 ? launch_norm_of<XB, 4>(a, sms, s) : launch_norm_of<XB, 2>(a, sms, s);
 }
 
+// The codes of a block whose scale is below kSmallScale. The kernels below write these a second time, behind everything else and
+// from memory again, so that others pay one comparison a vector: with a branch for each vector 16,385 x 4,096 from fp16 took 40.7 us
+// in place of 34.8, from registers kept for it 38.4.
+__device__ __forceinline__ uint2 small_codes8(uint64_t (&f)[4], float s, float inv) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = ptx::mul2(f[i], ptx::f2(kUp, kUp));
+    return codes8(f, s * kUp, inv * (1.0f / kUp));
+}
+
+// A block's largest magnitude, from its 16 lanes; `mask` has all lanes that are here.
+template <int B>
+__device__ __forceinline__ float block_top(const Raw<B>& x, bool bf, unsigned mask) {
+    float top = largest8(x, bf);
+#pragma unroll
+    for (int m = 8; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(mask, top, m));
+    return top;
+}
+
 // Rows to codes: 16 lanes a block, eight elements each. V vectors a thread, a CTA's threads apart, so that 64 bytes a
 // thread are under way.
-// 16,385 rows of 4,096, fp16: 35.0 us, 5.75 TB/s, 0.86 of the copy bandwidth; issue slots 72 % busy. From fp32 47.9 us (1.05),
+// 16,385 rows of 4,096, fp16: 35.6 us, 5.66 TB/s, 0.85 of the copy bandwidth; issue slots 72 % busy. From fp32 47.8 us (1.05),
 // bound by HBM. 64 rows: 1.4 us, the launch.
 template <int B, int V>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
@@ -317,18 +338,37 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
         else
             x[v].zero();
     }
+    float least = kSmallScale;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float top = largest8(x[v], a.type == MOE_BF16);
-#pragma unroll
-        for (int m = 8; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, m));
+        const float top = block_top(x[v], a.type == MOE_BF16, kFull);
         float inv;
         const float s = block_scale(top, inv);
+        least = fminf(least, s);
         if (!in[v]) continue;
         uint64_t f[4];
         x[v].get(f, a.type == MOE_BF16);
         *reinterpret_cast<uint2*>(a.codes + (int64_t)row[v] * a.code_stride + 8 * vec[v]) = codes8(f, s, inv);
         if ((vec[v] & 15) == 0) a.scales[(int64_t)(vec[v] >> 4) * a.scale_stride + row[v]] = s;
+    }
+    if (least < kSmallScale) {  // of all 16 lanes of a block: its codes a second time
+        const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) {
+            const uint64_t at = first + 256 * v;
+            const int r = (int)a.by_row.div((uint32_t)(at >> 4)), j = (int)((at >> 4) - (uint64_t)r * per) * 16 + (int)(at & 15);
+            const bool live = r < a.n && 8 * j < a.dim;
+            Raw<B> again;
+            if (live)
+                again.load(a.x, (int64_t)r * a.x_stride + 8 * j);
+            else
+                again.zero();
+            float inv;
+            const float s = block_scale(block_top(again, a.type == MOE_BF16, lanes), inv);
+            uint64_t f[4];
+            again.get(f, a.type == MOE_BF16);
+            if (live && s < kSmallScale) *reinterpret_cast<uint2*>(a.codes + (int64_t)r * a.code_stride + 8 * j) = small_codes8(f, s, inv);
+        }
     }
 }
 
@@ -368,6 +408,17 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const __grid_constant
         uint64_t f[4];
         x[v].get(f, a.type == MOE_BF16);
         *reinterpret_cast<uint2*>(a.codes + (int64_t)(r0 + 16 * v) * a.code_stride + col) = codes8(f, s, inv);
+    }
+    if (s < kSmallScale) {
+#pragma unroll 1
+        for (int v = 0; v < 8; ++v) {
+            if (r0 + 16 * v >= a.n || col >= a.dim) continue;
+            Raw<B> again;
+            again.load(a.x, (int64_t)(r0 + 16 * v) * a.x_stride + col);
+            uint64_t f[4];
+            again.get(f, a.type == MOE_BF16);
+            *reinterpret_cast<uint2*>(a.codes + (int64_t)(r0 + 16 * v) * a.code_stride + col) = small_codes8(f, s, inv);
+        }
     }
 }
 

@@ -608,7 +608,7 @@ moe_status moe_kv_check(moe_ctx* ctx);
  *                   scale_stride + j / 128] that of element (i, j).
  * The last blocks may be smaller. An element's value is scale * code. Quantising:
  *   scale = max(largest magnitude of the block, 448 * 2^-126) / 448 in fp32,
- *   code = value / scale rounded to the nearest e4m3, ties to even,
+ *   code = value / scale in fp32, rounded to the nearest e4m3, ties to even,
  * so codes span +-448, and a value is off by at most 2^-4 of itself or 2^-10 of the
  * scale. An infinity or a NaN makes its whole block NaN, scale and codes.
  * Every tensor is in the memory of the context's device; rows of 16- and
@@ -640,8 +640,9 @@ typedef struct {
 
 /* Root-mean-square norm of each row:
  *   h = x + residual (x alone without one);  sum = h
- *   y = h / sqrt(mean(h^2) + eps) * weight;  out = y;  codes, scales = y quantised as rows
- * All arithmetic is fp32 (|h| below 2^55, so that its squares' sum stays finite), y comes from the
+ *   y = h / sqrt(mean(h^2) + eps) * weight;  out = y;  codes, scales = y quantised as rows (ties either way
+ * where a block's scale is below 2^-93)
+ * All arithmetic is fp32 (|h| below 2^55, so that its squares' sum stays finite; mean(h^2) + eps from 2^-126 on), y comes from the
  * unrounded h, and sum, out and codes are each rounded once. At least one of sum, out and codes is given. sum and out
  * may be x or residual themselves (the same pointer, type and strides); other overlaps are not allowed.
  * moe_forward's y (f32) is an x; its own x wants bf16 out with dim = d_model.

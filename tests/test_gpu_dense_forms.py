@@ -61,3 +61,32 @@ def test_an_expired_wait_is_reported_until_it_is_asked_for(ctx):
     assert e.value.status == moe.MOE_ETIMEOUT
     moe.moe_f8_check(ctx)
     assert torch.equal(moe.moe_f8_matmul(ctx, *ops, dtype=torch.float32), want)
+
+
+@pytest.mark.parametrize("weight", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quant_is_exact_near_the_least_scale(ctx, dtype, weight):
+    """Blocks whose scale is 2^-126 to 2^-60, of values at ties between codes and one step of the type beside them. The reference
+    divides on the CPU, by IEEE arithmetic with subnormals, and rounds the quotient."""
+    g = torch.Generator().manual_seed(7)
+    per = 128 if weight else 1  # rows that share a scale
+    exps = [-126, -125, -124, -122, -120, -117, -112, -104, -97, -94, -93, -92, -91, -90, -89, -88, -60]
+    reps = 4 if weight else 400
+    bits = 13 if dtype == "f32" else 3  # of the scale: 448 times it is exact
+    s = torch.cat([torch.ldexp(1.0 + torch.randint(0, 1 << bits, (reps,), generator=g) / (1 << bits), torch.tensor(float(e))) for e in exps])
+    s = s.double().repeat_interleave(per)
+    n = s.numel()
+    small = (2 * torch.randint(0, 8, (n, 128), generator=g) + 1) * 2.0 ** -10  # between subnormal codes
+    large = (17 + 2 * torch.randint(0, 8, (n, 128), generator=g)) * torch.ldexp(torch.tensor(1.0), torch.randint(-10, 4, (n, 128), generator=g).float())
+    tie = torch.where(torch.rand((n, 128), generator=g) < 0.6, small, large).double()
+    x = (tie * s[:, None]).to(dense.T[dtype])
+    step = torch.randint(-1, 2, (n, 128), generator=g)
+    as_int = x.view(torch.int32 if dtype == "f32" else torch.int16)
+    x = (as_int + step.to(as_int.dtype)).clamp(min=0).view(x.dtype)
+    x = torch.where(torch.rand((n, 128), generator=g) < 0.5, -x, x)
+    x[:, 0] = (448 * s).to(x.dtype)
+    codes, scales = (moe.moe_f8_quant_weight if weight else moe.moe_f8_quant_rows)(ctx, x.cuda())
+    want, ws = dense.quant_ref(x, weight)
+    assert (ws.double().flatten().repeat_interleave(per)[:n] == s).all()
+    assert (scales.cpu() == ws).all()
+    assert (codes.cpu().float() == want.float()).all()
