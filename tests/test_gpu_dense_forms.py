@@ -90,3 +90,58 @@ def test_quant_is_exact_near_the_least_scale(ctx, dtype, weight):
     assert (ws.double().flatten().repeat_interleave(per)[:n] == s).all()
     assert (scales.cpu() == ws).all()
     assert (codes.cpu().float() == want.float()).all()
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(4099, 2304, 2064, "bf16"), (4099, 2304, 2064, "f32"), (3000, 5001, 4096, "f16"), (5000, 2560, 4096, "bf16"),
+                                         (2560, 8200, 2832, "f32")])
+def test_more_tiles_than_pairs_of_sms(ctx, m, n, k, dtype):
+    """The rows form with two and more tiles of 256 x 256 a pair of CTAs, full and ragged ones: 17 x 9, 12 x 20, 20 x 10, 10 x 33."""
+    check(ctx, m, n, k, dtype)
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(5, 100003, 272, "f32"), (16, 50001, 1040, "bf16"), (13, 78000, 528, "f16"), (30, 45001, 400, "f32"),
+                                         (32, 90000, 272, "bf16"), (64, 41000, 784, "f16"), (100, 30011, 272, "f32")])
+def test_more_tiles_of_weights_than_ctas(ctx, m, n, k, dtype):
+    """The weights form of 16, 32 and 64 rows with two and more tiles a CTA (304 of them)."""
+    check(ctx, m, n, k, dtype)
+
+
+@pytest.mark.parametrize("m", [1, 9, 16, 30, 60, 128, 2000])
+def test_outputs_past_fp16(ctx, m):
+    """Sums past fp16's largest number, 65,504, become infinities of their sign: from 65,520 on, halfway to the next step."""
+    n, k = (2000, 4096) if m == 2000 else (300, 512)
+    a = torch.ones((m, k), device="cuda").to(dense.F8)
+    w = torch.ones((n, k), device="cuda").to(dense.F8)
+    sums = torch.tensor([65504.0, 65519.0, 65520.0, 65536.0, 1e6, -65504.0, -65520.0, -1e9, 3.0], device="cuda")
+    want = sums[torch.arange(m, device="cuda") % 9]
+    sa = torch.zeros((k // 128, m), device="cuda")
+    sa[0] = want / 128  # all exact
+    sw = torch.ones((-(-n // 128), k // 128), device="cuda")
+    out = moe.moe_f8_matmul(ctx, a, sa, w, sw, dtype=torch.float16)
+    assert torch.equal(out, want.half()[:, None].expand(m, n))
+    assert torch.isinf(out).any() == (m > 2)
+
+
+def test_norm_of_infinities(ctx):
+    """h / sqrt(inf) is NaN where h is infinite and 0 elsewhere: so are the outputs; a block with a NaN is NaN, others of the row
+    are zeros; other rows are as without."""
+    for n, d in ((6, 512), (6, 2816), (3000, 640), (2, 8208)):
+        x = torch.randn((n, d), generator=dense.rng(d), device="cuda")
+        r = torch.randn((n, d), generator=dense.rng(d + 1), device="cuda")
+        clean = moe.moe_rms_norm(ctx, x, residual=r, f8=True)
+        bad = x.clone()
+        bad[0, 130] = float("inf")
+        bad[1, d - 1] = float("-inf")
+        out, total, codes, scales = moe.moe_rms_norm(ctx, bad, residual=r, f8=True)
+        assert torch.equal(total, bad + r)
+        want = torch.zeros((2, d), device="cuda")
+        want[0, 130] = want[1, d - 1] = float("nan")
+        assert torch.equal(torch.isnan(out[:2]), torch.isnan(want)) and (out[:2][~torch.isnan(want)] == 0).all()
+        blocks = torch.zeros((2, -(-d // 128)), dtype=torch.bool, device="cuda")
+        blocks[0, 1] = blocks[1, -1] = True
+        assert torch.equal(torch.isnan(scales[:, :2].t()), blocks)
+        value = codes[:2].float() * scales[:, :2].t().repeat_interleave(128, 1)[:, :d]
+        nan = blocks.repeat_interleave(128, 1)[:, :d]
+        assert torch.isnan(value[nan]).all() and (value[~nan] == 0).all()
+        for a, b in zip((out, total, codes.float(), scales.t()), (clean[0], clean[1], clean[2].float(), clean[3].t())):
+            assert torch.equal(a[2:], b[2:])
