@@ -15,8 +15,8 @@
 // Weights form, warps: four or eight epilogue warps (warp w reads TMEM lanes 32 (w mod 4) on), one that loads both operands
 // by TMA into a ring of K-blocks (128 bytes a row, 128-byte swizzle), one that issues the MMAs.
 //   100,003 weights of 2,048 by 5 rows: 33.3 us, 6.2 TB/s, 0.92 of the copy bandwidth measured on this GPU, bound by HBM.
-//   2,816 of 4,096 by 77 rows 9 us (floor 1.8), 6,144 of 2,816 by 143 9.8 us (2.9): about 4 us of start, first loads
-//   and last stores, then 0.27 us a K-block for one CTA on an SM (0.41 for two): an epilogue warp's chain of barrier (120
+//   2,816 of 4,096 by 77 rows 8.4 us (floor 1.8), 6,144 of 2,816 by 143 9.2 us (2.9): 3 to 4 us of start, first loads
+//   and last stores (5 with a join), then 0.27 us a K-block for one CTA on an SM (0.41 for two): an epilogue warp's chain of barrier (120
 //   cycles when it is there), load from tensor memory (100), scales and sums. Deeper rings (one CTA on an SM) and sixteen
 //   epilogue warps of 16 columns were no faster.
 // Every wait is bounded; when one expires the kernel sets an error word, every other wait gives up, its own copies and
@@ -548,9 +548,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kCtas)
 // the end of a half until its buffer is needed again there are three halves, 768 cycles of tensor work, for the way to the
 // epilogue, its loads (eight warps a half, 64 columns each) and the way back.
 //
-// 8,192 rows of 8,192 by 8,192 weights: 368 us, 2.99 PFLOP/s, 1.53 times the bf16 rate that this GPU's library reaches (424 us
-// in a row of calls of a second or more, where the power cap brings the clock to about 1.7 GHz; all-zero codes, which draw
-// less, take 350 us at any length). 4,096 rows of 2,816 by 6,144: 70 us, 2.0 PFLOP/s, a last wave of tiles a twentieth full.
+// 8,192 rows of 8,192 by 8,192 weights: 367 us, 3.0 PFLOP/s, 1.57 times the bf16 rate that this GPU's library reaches (380 to
+// 400 us when warm, 428 to 434 in a row of calls of a second or more, where the power cap brings the clock to about 1.7 GHz; all-zero
+// codes, which draw less, take 350 us at any length). 4,096 rows of 2,816 by 6,144: 69 us, 2.1 PFLOP/s, a last wave of tiles a twentieth full.
 // A K-block of 256 x 256 takes 800 cycles, where its products take 512: the epilogue's 64 columns a warp cost two loads, 32
 // two-wide multiply-adds (128 a scheduler, two cycles each) and about 60 other instructions, and a buffer's way round is
 // longer than three halves. Eight epilogue warps of 128 columns, sixteen of 32 a half, single buffers of 256 and scalar
@@ -1128,9 +1128,9 @@ cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, 
     return cfg;
 }
 
-// How many clusters of n (1 .. 8) CTAs of the kernel are resident at once. A cluster lies within a GPC, so large ones leave
-// SMs idle: of 304 places for the weights form, clusters of 8 fill 288, of 7 266, of 6 276, of 5 290, of 4 296; of 152 for
-// the rows form, clusters of 4 fill 144, of 8 120.
+// How many clusters of n (2 .. 8) CTAs of the kernel the runtime counts as resident at once. A cluster lies within a GPC, so large
+// ones leave SMs idle: of 2 CTAs 76, of 3 46, of 4 36, of 5 28, of 6 23, of 7 and 8 15. For every form it counts one CTA an SM; the
+// weights form's run two where there are more.
 template <class F, class K>
 int resident_clusters(K* kernel, int n) {
     constexpr int kDevices = 64;
@@ -1152,10 +1152,11 @@ int resident_clusters(K* kernel, int n) {
     return of[n];
 }
 
-// CTAs that share a tile's K-blocks: as many as find room at once, at least two K-blocks each. Only where tiles leave
+// CTAs that share a tile's K-blocks: as many as find an SM each at once, at least two K-blocks each. Only where tiles leave
 // more than half of the SMs without one and there are some K-blocks to share, as joining the parts takes about 1 us. us for
-// 1, 2, 4 and (where they fit) 5, 6 or 8 CTAs: 32 rows, 22 tiles of 32 K-blocks 9.9 7.7 6.1 5.7; 48 tiles of 22: 8.4 8.1
-// 7.5 7.3 (6: 11.3, a second wave); 64 tiles of 64: 19.2 15.7 14.0; 128 tiles of 16: 9.0 9.4; 22 tiles of 6: 3.9 4.5.
+// 1, 2, 4, 6 and 8 CTAs, 32 rows: 22 tiles of 32 K-blocks 9.5 7.4 5.5 5.4 6.5; 48 tiles of 22 (where the rule says 2) 8.2 7.7 7.3
+// 11.1 (a second wave); 64 tiles of 64 (2) 18.4 15.7 13.9; 128 tiles of 16 9.0 9.2; 22 tiles of 6 3.7 4.2. 77 rows, 44 tiles of 32 (3),
+// for 2 to 6: 8.8 8.4 8.7 9.0 8.6.
 template <class F>
 int splits_of(const Tiles& T, int sms) {
     if (2 * T.total > sms || T.kblocks < 8) return 1;
@@ -1208,8 +1209,8 @@ double weights_form_us(const MatmulArgs& a, int sms) {
     return each == 1 ? 3.9 + 0.28 * T.kblocks : 3.5 + 0.41 * T.kblocks * ((each + 1) / 2);
 }
 
-// *splits: pairs of CTAs a tile. us for 1, 2 and 4: 1,052 rows of 7,536 by 1,154 weights (25 tiles) 31.7 20.6 30.9; 300 of
-// 16,384 by 300 (4 tiles) 51.8 29.3 20.2; 700 of 2,048 by 2,048 (24 tiles) 13.2 11.7 22.3.
+// *splits: pairs of CTAs a tile. us for 1, 2 and 4: 1,052 rows of 7,536 by 1,154 weights (25 tiles) 29.0 19.5 29.4; 300 of
+// 16,384 by 300 (4 tiles) 50.3 27.4 18.6; 700 of 2,048 by 2,048 (24 tiles) 11.6 10.7 20.9.
 double rows_form_us(const MatmulArgs& a, int sms, int* splits) {
     const Tiles T = tiles_of(a.m, a.n, 2 * Pair::kCtaRows, Pair::C, a.k);
     *splits = 1;

@@ -147,9 +147,11 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&f)[4], float s, float i
 // One pass: a row stays in registers between its sum of squares (exchanges in a warp, then through shared memory) and its
 // outputs, and a block of 128 elements is 16 neighbouring vectors, so its largest magnitude is an exchange of 16 lanes.
 //
-// Bound by HBM: 32,768 rows of 2,816, fp32 plus a bf16 residual into bf16 sums and 8 bits, 830 MB: 117.8 us, 7.05 TB/s, 1.05
-// of the copy bandwidth measured on this GPU; from bf16 101.8 us (0.95). 4,099 tokens of 32 heads of 128, 67 MB: 14.2 us
-// (0.71), of which about 3 are the launch and the ends. One row of 2,816 with four outputs: 2.1 us, the launch.
+// Bound by HBM: 32,768 rows of 2,816, fp32 plus a bf16 residual into bf16 sums and 8 bits, 833 MB: 117.5 us, 7.1 TB/s, 1.06
+// of the copy bandwidth measured on this GPU; from bf16 100.6 us (0.96). 4,099 tokens of 32 heads of 128, 67 MB: 13.0 us
+// (0.77), of which about 3 are the launch and the ends. One row of 2,816 with four outputs: 2.2 us, the launch. Bound by
+// instructions: bf16 into bf16 and codes, 32,768 of 640 25.6 us (15.7 of bytes), where 48 of a warp's 128 places hold no vector
+// and are computed all the same, and 20,000 of 1,008 18.5 us (15.1).
 template <int XB, int RB, int V, int U, bool kCta>
 __global__ void __launch_bounds__(!kCta ? 256 : V == 4 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a, const int group) {
     ptx::pdl_wait();
@@ -272,8 +274,8 @@ cudaError_t launch_norm(const NormArgs& a, unsigned threads, int group, cudaStre
 // Up to 512 elements a row goes to a warp or a part of one, more to a CTA; up to 1,024 to a warp too where rows are many.
 // Many rows: several vectors a thread, so that more loads are under way for as many exchanges between threads; few: one, as
 // a row's time counts. us, one and two (at 6,144 two and four) vectors a thread of a CTA: 32,768 rows of 2,816, fp32 into 8
-// bits with a bf16 residual 128 118, from bf16 118 102; 16,384 of 4,096, bf16: 53 46; of 2,048: 25.8 23.5; of 6,144: 69 66;
-// 64 rows of 4,096: 2.1 2.2. Rows of 128 by two a half warp: 14.2 (one 14.9, four 14.6).
+// bits with a bf16 residual 125 117, from bf16 114 96 (no weights); 16,384 of 4,096, bf16: 53.7 42.0; of 2,048: 25.0 21.2; of 6,144:
+// 63.9 60.5; 64 rows of 4,096: 1.9 1.7. Rows of 128 by two a half warp: 12.1 (one 14.0, four 12.3).
 template <int XB, int RB>
 cudaError_t launch_norm_of(const NormArgs& a, int sms, cudaStream_t s) {
     const int nv = a.dim >> 3;
@@ -316,7 +318,7 @@ __device__ __forceinline__ float block_top(const Raw<B>& x, bool bf, unsigned ma
 
 // Rows to codes: 16 lanes a block, eight elements each. V vectors a thread, a CTA's threads apart, so that 64 bytes a
 // thread are under way.
-// 16,385 rows of 4,096, fp16: 35.6 us, 5.66 TB/s, 0.85 of the copy bandwidth; issue slots 72 % busy. From fp32 47.8 us (1.05),
+// 16,385 rows of 4,096, fp16: 35.6 us, 5.66 TB/s, 0.85 of the copy bandwidth; issue slots 73 % busy. From fp32 47.8 us (1.05),
 // bound by HBM. 64 rows: 1.4 us, the launch.
 template <int B, int V>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
 }
 
 // A block of 128 x 128 weights a CTA, in registers between the pass for its largest magnitude and the pass for its codes.
-// 10,000 x 2,864, fp32: 24.7 us, 5.8 TB/s, 0.87 of the copy bandwidth; from bf16 15.8 us (0.81). What is left is a CTA's two
+// 10,000 x 2,864, fp32: 24.7 us, 5.8 TB/s, 0.87 of the copy bandwidth; from bf16 14.4 us (0.89). What is left is a CTA's two
 // passes one after the other, three (bf16: four) of them on an SM.
 template <int B>
 __global__ void __launch_bounds__(256) quant_weight_kernel(const __grid_constant__ QuantArgs a) {
